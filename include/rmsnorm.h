@@ -78,7 +78,8 @@ enum rmsn_status {
     RMSN_OK = 0,
     RMSN_EINVAL = -1,        /* null pointer, bad size, ld < D, negative/non-finite eps */
     RMSN_EALIGN = -2,        /* a pointer or row stride is not 16-byte aligned          */
-    RMSN_EUNSUPPORTED = -3,  /* D outside [8, 16384] or not a multiple of 8             */
+    RMSN_EUNSUPPORTED = -3,  /* D not a multiple of 8, or outside the call's range (8..16384;
+                                heads 8..512), or a rotated part it does not take  */
     RMSN_ECUDA = -4,         /* a CUDA runtime or driver call failed                    */
     RMSN_EWORKSPACE = -5     /* workspace missing or smaller than the query's answer    */
 };
@@ -317,6 +318,60 @@ int rmsnorm_gated_bwd_recompute_ex(const rmsn_act16* g, int64_t ldg, const rmsn_
                                    void* ws, size_t ws_bytes,
                                    int64_t T, int64_t D, int zero_centered_gamma, int gate, int dtype,
                                    rmsn_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Head RMSNorm of q and k fused with their rotary positions: one pass over q
+ * and k in place of a norm of each and a rotation. Every head of D values is a
+ * row of rmsnorm_fwd, with one weight wq [D] for all heads of q and one wk [D]
+ * for those of k; then, still in fp32, its first R values are turned as rope.h
+ * describes (layouts, angles, strides, positions, NULL k, calls in place):
+ *   r    = rsqrt( (sum_j x_j^2) / D + eps )       saved as fp32 rstd [T][H]
+ *   n_j  = (x_j * r) * w_eff_j
+ *   out  = round( turn(n) )                       one rounding, after the turn
+ * D is a multiple of 8 with 8 <= D <= 512.
+ * ------------------------------------------------------------------------ */
+enum rope_layout {
+    ROPE_HALF = 0,           /* pairs (i, i + R/2)   */
+    ROPE_INTERLEAVED = 1     /* pairs (2i, 2i + 1)   */
+};
+
+enum rope_pos_dtype {
+    ROPE_POS_I32 = 0,
+    ROPE_POS_I64 = 1
+};
+
+/* rstd_q [T][Hq] and rstd_k [T][Hk] are contiguous. */
+int rmsnorm_rope_fwd(const rmsn_act16* q, int64_t q_token, int64_t q_head,
+                     const rmsn_act16* k, int64_t k_token, int64_t k_head,
+                     const float* wq, const float* wk,
+                     const double* inv_freq, const void* positions, int pos_dtype,
+                     rmsn_act16* q_out, int64_t qo_token, int64_t qo_head,
+                     rmsn_act16* k_out, int64_t ko_token, int64_t ko_head,
+                     float* rstd_q, float* rstd_k,
+                     int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale, int layout,
+                     float eps, int zero_centered_gamma, int dtype, rmsn_stream stream);
+
+/* Bytes of workspace rmsnorm_rope_bwd needs (0 for T == 0 and unsupported sizes). */
+size_t rmsnorm_rope_bwd_workspace_bytes(int64_t T, int64_t Hq, int64_t Hk, int64_t D);
+
+/* Backward: the gradients gq, gk of q_out, k_out are turned back (by -a, same
+ * scale), then go through rmsnorm_bwd's formula at q and k (the forward's
+ * INPUTS: a forward in place has overwritten them) with the saved rstd.
+ * dwq_j and dwk_j are summed over tokens and heads in fp32, with no atomics, in
+ * an order that depends on T, Hq, Hk, D, R and the layout alone. dq, dk may be
+ * gq, gk themselves (same strides). T == 0 sets dwq and dwk to zero. */
+int rmsnorm_rope_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head,
+                     const rmsn_act16* gk, int64_t gk_token, int64_t gk_head,
+                     const rmsn_act16* q, int64_t q_token, int64_t q_head,
+                     const rmsn_act16* k, int64_t k_token, int64_t k_head,
+                     const float* wq, const float* wk,
+                     const double* inv_freq, const void* positions, int pos_dtype,
+                     const float* rstd_q, const float* rstd_k,
+                     rmsn_act16* dq, int64_t dq_token, int64_t dq_head,
+                     rmsn_act16* dk, int64_t dk_token, int64_t dk_head,
+                     float* dwq, float* dwk, void* ws, size_t ws_bytes,
+                     int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale, int layout,
+                     int zero_centered_gamma, int dtype, rmsn_stream stream);
 
 /* Weight-gradient pass 2 on its own: sums the per-chunk partials that a backward
  * call with a NULL dgamma/dw left in ws (same T, D and workspace), in the fixed

@@ -1,5 +1,5 @@
 """Python binding of the GB300 batch-invariant RMSNorm library (C ABI in
-``include/rmsnorm.h``).
+``include/rmsnorm.h``, ``layernorm.h`` and ``rope.h``).
 
 Argument marshalling only: every function here takes torch tensors that the
 caller allocated on a CUDA device, checks dtypes/shapes/devices, and passes raw
@@ -37,6 +37,9 @@ __all__ = [
     "rmsnorm_bwd_recompute_ex", "rmsnorm_gated_bwd_recompute_ex", "DTYPE_CODES", "GATE_CODES",
     "rmsnorm_residual_step_host", "rmsnorm_residual_step_host_work_bytes", "rmsnorm_selftest_wait_timeout",
     "DEVICE_ERR_WAIT_TIMEOUT", "rmsnorm_bwd_workspace_bytes_max",
+    "rmsnorm_rope_fwd", "rmsnorm_rope_bwd", "rmsnorm_rope_bwd_workspace_bytes",
+    "layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_bytes", "layernorm_bwd_workspace_bytes_max",
+    "rope_fwd", "rope_bwd", "rope_frequencies", "LAYERNORM_SYMBOLS", "ROPE_SYMBOLS", "ROPE_SCALINGS",
 ]
 
 EXPORTED_SYMBOLS = (
@@ -50,7 +53,13 @@ EXPORTED_SYMBOLS = (
     "rmsnorm_bwd_recompute_ex", "rmsnorm_gated_bwd_recompute_ex",
     "rmsnorm_residual_step_host_work_bytes", "rmsnorm_residual_step_host", "rmsnorm_selftest_wait_timeout",
     "rmsnorm_bwd_workspace_bytes_max",
+    "rmsnorm_rope_fwd", "rmsnorm_rope_bwd", "rmsnorm_rope_bwd_workspace_bytes",
 )
+
+# the entry points of include/layernorm.h and include/rope.h
+LAYERNORM_SYMBOLS = ("layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_bytes",
+                     "layernorm_bwd_workspace_bytes_max")
+ROPE_SYMBOLS = ("rope_frequencies", "rope_fwd", "rope_bwd")
 
 # RMSN_DEVICE_ERR_WAIT_TIMEOUT of include/rmsnorm.h: the flag a wait that ran out of time raises
 DEVICE_ERR_WAIT_TIMEOUT = 1
@@ -59,10 +68,14 @@ DEVICE_ERR_WAIT_TIMEOUT = 1
 DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1}
 GATE_CODES = {"silu": 0, "sigmoid": 1}
 
+# enum rope_scaling of include/rope.h
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp_turns": 3, "ramp_index": 4}
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _F = ctypes.c_float
+_DBL = ctypes.c_double
 _SZ = ctypes.c_size_t
 
 _SIGS = {
@@ -100,6 +113,22 @@ for _name in ("rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_residual_fwd", "rmsnorm_res
     _extra = [_INT, _INT] if "gated" in _name else [_INT]
     _SIGS[_name + "_ex"] = (_res, _args[:-1] + _extra + [_P])
 del _name, _res, _args, _extra
+
+# A heads tensor is its pointer, token stride and head stride.
+_HEADS = [_P, _I64, _I64]
+_SIGS["layernorm_fwd"] = (_INT, [_P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _I64, _F, _INT, _INT, _P])
+_SIGS["layernorm_bwd"] = (_INT, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _P, _SZ, _I64, _I64, _INT, _INT,
+                                 _P])
+_SIGS["layernorm_bwd_workspace_bytes"] = (_SZ, [_I64, _I64])
+_SIGS["layernorm_bwd_workspace_bytes_max"] = (_SZ, [_I64, _I64])
+_SIGS["rope_frequencies"] = (_INT, [_I64, _DBL, _INT, _DBL, _DBL, _DBL, _DBL, _P])
+_SIGS["rope_fwd"] = _SIGS["rope_bwd"] = (_INT, _HEADS * 2 + [_P, _P, _INT] + _HEADS * 2 + [_I64] * 5 +
+                                         [_F, _INT, _INT, _P])
+_SIGS["rmsnorm_rope_fwd"] = (_INT, _HEADS * 2 + [_P, _P, _P, _P, _INT] + _HEADS * 2 + [_P, _P] + [_I64] * 5 +
+                             [_F, _INT, _F, _INT, _INT, _P])
+_SIGS["rmsnorm_rope_bwd_workspace_bytes"] = (_SZ, [_I64] * 4)
+_SIGS["rmsnorm_rope_bwd"] = (_INT, _HEADS * 4 + [_P, _P, _P, _P, _INT, _P, _P] + _HEADS * 2 + [_P, _P, _P, _SZ] +
+                             [_I64] * 5 + [_F, _INT, _INT, _INT, _P])
 
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
@@ -499,6 +528,192 @@ def rmsnorm_gated_bwd_recompute_ex(g, x, z, w, rstd, dx, dz, dw, y, ws, zero_cen
         _ptr(g), ldg, _ptr(x), ldx, _ptr(z), ldz, _ptr(w), _ptr(rstd), _ptr(dx), lddx, _ptr(dz), lddz, _ptr(dw),
         _ptr(y), ldy, wp, wb, T, D, int(zero_centered_gamma), _gate_code(gate), _dtype_code(x),
         _stream(stream, x.device)))
+
+
+# --------------------------------------------------------------------------
+# LayerNorm, rotary positions, and the head RMSNorm fused with them
+# --------------------------------------------------------------------------
+class _On:
+    """Argument checks of one call: every tensor on the device of the first one;
+    ``call`` runs the entry point with that device current."""
+
+    __slots__ = ("index", "dtype", "code")
+
+    def __init__(self, x: torch.Tensor, name: str):
+        if not x.is_cuda:
+            raise TypeError(f"{name}: expected a CUDA tensor, got {x.device}")
+        self.index = x.get_device()
+        self.dtype = x.dtype
+        self.code = _dtype_code(x)
+
+    def rows(self, t, name: str, T: int, D: int):
+        if t.dtype is not self.dtype or t.get_device() != self.index or t.dim() != 2:
+            raise TypeError(f"{name}: expected a 2-D {self.dtype} tensor on cuda:{self.index}, got {t.dtype} "
+                            f"{t.device} {tuple(t.shape)}")
+        if t.shape != (T, D):
+            raise ValueError(f"{name}: expected shape {(T, D)}, got {tuple(t.shape)}")
+        if D > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: columns must be contiguous")
+        return t.data_ptr(), t.stride(0) if T > 1 else max(t.stride(0), D)
+
+    def heads(self, t, name: str, T: int, H: int, D: int):
+        if t is None and H == 0:
+            return None, 0, 0
+        if t is None or t.dtype is not self.dtype or t.get_device() != self.index or t.dim() != 3:
+            raise TypeError(f"{name}: expected a 3-D {self.dtype} tensor on cuda:{self.index}" +
+                            ("" if t is None else f", got {t.dtype} {t.device} {tuple(t.shape)}"))
+        if t.shape != (T, H, D):
+            raise ValueError(f"{name}: expected shape {(T, H, D)}, got {tuple(t.shape)}")
+        if H == 0:
+            return None, 0, 0
+        token, head, one = t.stride()
+        if D > 1 and one != 1:
+            raise ValueError(f"{name}: the values of a head must be contiguous")
+        # a stride that is never taken may be anything
+        return t.data_ptr(), token if T > 1 else 0, head if H > 1 else 0
+
+    def vec(self, t, name: str, shape, dtype: torch.dtype = torch.float32):
+        if t.dtype is not dtype or t.get_device() != self.index or t.shape != shape or not t.is_contiguous():
+            raise TypeError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                            f"cuda:{self.index}, got {t.dtype} {t.device} {tuple(t.shape)}")
+        return t.data_ptr()
+
+    def vec_of(self, t, name: str, H: int, shape):
+        """The vector of q or k: k has none where it has no heads."""
+        return self.vec(t, name, shape) if H else None
+
+    def bytes(self, t):
+        if t.get_device() != self.index or not t.is_contiguous():
+            raise TypeError(f"ws: expected a contiguous tensor on cuda:{self.index}")
+        return t.data_ptr(), t.numel() * t.element_size()
+
+    def positions(self, t, T: int):
+        if t is None:
+            return None, 1
+        if t.dtype is not torch.int64 and t.dtype is not torch.int32:
+            raise TypeError(f"positions: expected int32 or int64, got {t.dtype}")
+        return self.vec(t, "positions", (T,), t.dtype), 1 if t.dtype is torch.int64 else 0
+
+    def call(self, fn: str, stream, *args):
+        f = getattr(_lib or load(), fn)
+        if self.index == torch.cuda.current_device():
+            st = f(*args, _stream(stream, self.index))
+        else:
+            with torch.cuda.device(self.index):
+                st = f(*args, _stream(stream, self.index))
+        if st != 0:
+            raise RmsNormError(fn, st)
+
+
+def layernorm_fwd(x, w, b, y, mean, rstd, eps: float = 1e-5, zero_centered_gamma: bool = False, stream=None):
+    """``y = (x - mean) * rstd * w_eff + b`` by rows; writes ``y``, ``mean``, ``rstd``. ``b`` may be None.
+    The activation format (bf16 or fp16) is ``x``'s."""
+    on = _On(x, "x")
+    T, D = x.shape
+    xp, ldx = on.rows(x, "x", T, D)
+    yp, ldy = on.rows(y, "y", T, D)
+    on.call("layernorm_fwd", stream, xp, ldx, on.vec(w, "w", (D,)), None if b is None else on.vec(b, "b", (D,)), yp,
+            ldy, on.vec(mean, "mean", (T,)), on.vec(rstd, "rstd", (T,)), T, D, eps, 1 if zero_centered_gamma else 0,
+            on.code)
+
+
+def layernorm_bwd_workspace_bytes(T: int, D: int) -> int:
+    return int(load().layernorm_bwd_workspace_bytes(int(T), int(D)))
+
+
+def layernorm_bwd_workspace_bytes_max(T_max: int, D: int) -> int:
+    """Bytes of one workspace that serves every T up to T_max."""
+    return int(load().layernorm_bwd_workspace_bytes_max(int(T_max), int(D)))
+
+
+def layernorm_bwd(g, x, w, mean, rstd, dx, dw, db, ws, zero_centered_gamma: bool = False, stream=None):
+    """Writes ``dx``, ``dw`` and, unless it is None, ``db``."""
+    on = _On(x, "x")
+    T, D = x.shape
+    gp, ldg = on.rows(g, "g", T, D)
+    xp, ldx = on.rows(x, "x", T, D)
+    dp, ldd = on.rows(dx, "dx", T, D)
+    wp, wb = on.bytes(ws)
+    on.call("layernorm_bwd", stream, gp, ldg, xp, ldx, on.vec(w, "w", (D,)), on.vec(mean, "mean", (T,)),
+            on.vec(rstd, "rstd", (T,)), dp, ldd, on.vec(dw, "dw", (D,)),
+            None if db is None else on.vec(db, "db", (D,)), wp, wb, T, D, 1 if zero_centered_gamma else 0, on.code)
+
+
+def rope_frequencies(R: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0, low: float = 1.0,
+                     high: float = 32.0, length: float = 0.0) -> torch.Tensor:
+    """The R/2 rotary frequencies (radians a position) as a float64 CPU tensor: ``theta ** (-2 i / R)``,
+    scaled for contexts longer than those of training (the scalings of include/rope.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    out = torch.empty(max(int(R), 0) // 2, dtype=torch.float64)
+    _check("rope_frequencies", load().rope_frequencies(int(R), float(theta), ROPE_SCALINGS[scaling], float(factor),
+                                                       float(low), float(high), float(length), _ptr(out)))
+    return out
+
+
+def _q_k(on, q, k):
+    if q.dim() != 3:
+        raise TypeError(f"q: expected a 3-D tensor [T, heads, D], got {tuple(q.shape)}")
+    T, Hq, D = q.shape
+    return T, Hq, (0 if k is None else k.shape[1] if k.dim() == 3 else -1), D
+
+
+def _rope(fn, q, k, inv_freq, q_out, k_out, positions, scale, interleaved, stream):
+    on = _On(q, "q")
+    T, Hq, Hk, D = _q_k(on, q, k)
+    n = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+    on.call(fn, stream, *on.heads(q, "q", T, Hq, D), *on.heads(k, "k", T, Hk, D),
+            on.vec(inv_freq, "inv_freq", (n,), torch.float64), *on.positions(positions, T),
+            *on.heads(q_out, "q_out", T, Hq, D), *on.heads(k_out, "k_out", T, Hk, D), T, Hq, Hk, D, 2 * n, scale,
+            1 if interleaved else 0, on.code)
+
+
+def rope_fwd(q, k, inv_freq, q_out, k_out, positions=None, scale: float = 1.0, interleaved: bool = False, stream=None):
+    """Rotary positions of ``q`` [T, Hq, D] and ``k`` [T, Hk, D] (None: q alone): the first
+    ``2 * len(inv_freq)`` values of each head in pairs (halves, or neighbours if ``interleaved``), turned by
+    ``positions * inv_freq`` (float64 frequencies; positions None: 0, 1, 2, ...) and scaled by ``scale``.
+    ``q_out`` may be ``q`` and ``k_out`` may be ``k``."""
+    _rope("rope_fwd", q, k, inv_freq, q_out, k_out, positions, scale, interleaved, stream)
+
+
+def rope_bwd(gq, gk, inv_freq, dq, dk, positions=None, scale: float = 1.0, interleaved: bool = False, stream=None):
+    """Gradients of rope_fwd's inputs from those of its outputs (``dq`` may be ``gq``, ``dk`` may be ``gk``)."""
+    _rope("rope_bwd", gq, gk, inv_freq, dq, dk, positions, scale, interleaved, stream)
+
+
+def rmsnorm_rope_fwd(q, k, wq, wk, inv_freq, q_out, k_out, rstd_q, rstd_k, positions=None, scale: float = 1.0,
+                     interleaved: bool = False, eps: float = 1e-6, zero_centered_gamma: bool = False, stream=None):
+    """RMSNorm of every head of ``q`` (weight ``wq`` [D]) and of ``k`` (``wk``), then their rotary positions as
+    in ``rope_fwd``, in one pass; writes ``q_out``, ``k_out`` and the inverse RMS of every head, ``rstd_q`` [T, Hq]
+    and ``rstd_k`` [T, Hk]. ``k``, ``wk``, ``k_out`` and ``rstd_k`` may be None together."""
+    on = _On(q, "q")
+    T, Hq, Hk, D = _q_k(on, q, k)
+    n = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+    on.call("rmsnorm_rope_fwd", stream, *on.heads(q, "q", T, Hq, D), *on.heads(k, "k", T, Hk, D),
+            on.vec(wq, "wq", (D,)), on.vec_of(wk, "wk", Hk, (D,)), on.vec(inv_freq, "inv_freq", (n,), torch.float64),
+            *on.positions(positions, T), *on.heads(q_out, "q_out", T, Hq, D), *on.heads(k_out, "k_out", T, Hk, D),
+            on.vec(rstd_q, "rstd_q", (T, Hq)), on.vec_of(rstd_k, "rstd_k", Hk, (T, Hk)), T, Hq, Hk, D, 2 * n, scale,
+            1 if interleaved else 0, eps, 1 if zero_centered_gamma else 0, on.code)
+
+
+def rmsnorm_rope_bwd_workspace_bytes(T: int, Hq: int, Hk: int, D: int) -> int:
+    return int(load().rmsnorm_rope_bwd_workspace_bytes(int(T), int(Hq), int(Hk), int(D)))
+
+
+def rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, inv_freq, rstd_q, rstd_k, dq, dk, dwq, dwk, ws, positions=None,
+                     scale: float = 1.0, interleaved: bool = False, zero_centered_gamma: bool = False, stream=None):
+    """Gradients of rmsnorm_rope_fwd: ``dq``, ``dk`` (which may be ``gq``, ``gk``) and the weights' ``dwq``, ``dwk``."""
+    on = _On(q, "q")
+    T, Hq, Hk, D = _q_k(on, q, k)
+    n = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+    wp, wb = on.bytes(ws)
+    on.call("rmsnorm_rope_bwd", stream, *on.heads(gq, "gq", T, Hq, D), *on.heads(gk, "gk", T, Hk, D),
+            *on.heads(q, "q", T, Hq, D), *on.heads(k, "k", T, Hk, D), on.vec(wq, "wq", (D,)),
+            on.vec_of(wk, "wk", Hk, (D,)), on.vec(inv_freq, "inv_freq", (n,), torch.float64),
+            *on.positions(positions, T), on.vec(rstd_q, "rstd_q", (T, Hq)), on.vec_of(rstd_k, "rstd_k", Hk, (T, Hk)),
+            *on.heads(dq, "dq", T, Hq, D), *on.heads(dk, "dk", T, Hk, D), on.vec(dwq, "dwq", (D,)),
+            on.vec_of(dwk, "dwk", Hk, (D,)), wp, wb, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0,
+            1 if zero_centered_gamma else 0, on.code)
 
 
 def rmsnorm_dgamma_reduce(ws, T: int, D: int, dgamma, stream=None):

@@ -10,6 +10,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "checks.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -243,30 +244,6 @@ using namespace rmsn;
 // ---------------------------------------------------------------------------
 namespace {
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int check_shape(int64_t T, int64_t D) {
-    if (T < 0 || T >= (int64_t(1) << 31)) return RMSN_EINVAL;
-    if (D < 8 || D > kMaxD || (D % 8) != 0) return RMSN_EUNSUPPORTED;
-    return RMSN_OK;
-}
-
-// An activation matrix [T][ld] of bf16 (required = must be non-null).
-int check_act(const void* p, int64_t ld, int64_t D) {
-    if (p == nullptr) return RMSN_EINVAL;
-    if (ld < D || ld > (int64_t(1) << 40)) return RMSN_EINVAL;
-    if (!aligned16(p) || (ld % 8) != 0) return RMSN_EALIGN;
-    return RMSN_OK;
-}
-
-int check_vec(const void* p) {
-    if (p == nullptr) return RMSN_EINVAL;
-    if (!aligned16(p)) return RMSN_EALIGN;
-    return RMSN_OK;
-}
-
-int check_eps(float eps) { return (std::isfinite(eps) && eps >= 0.0f) ? RMSN_OK : RMSN_EINVAL; }
-
 int check_ws(const void* ws, size_t ws_bytes, int64_t T, int64_t D) {
     const size_t need = static_cast<size_t>(num_chunks(T, static_cast<int>(D))) * static_cast<size_t>(D) * 4u;
     if (ws == nullptr || ws_bytes < need) return RMSN_EWORKSPACE;
@@ -274,23 +251,9 @@ int check_ws(const void* ws, size_t ws_bytes, int64_t T, int64_t D) {
     return RMSN_OK;
 }
 
-#define RMSN_TRY(expr)                  \
-    do {                                \
-        const int _st = (expr);         \
-        if (_st != RMSN_OK) return _st; \
-    } while (0)
-
-inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? RMSN_OK : RMSN_ECUDA; }
-
 float inv_pow2(int D) { return (D & (D - 1)) == 0 ? 1.0f / static_cast<float>(D) : 0.0f; }
 
-// Variant flags of an activation dtype / gate argument (RMSN_EINVAL if unknown).
-int dtype_flags(int dtype, int* flags) {
-    if (dtype == RMSN_DTYPE_BF16) { *flags = 0; return RMSN_OK; }
-    if (dtype == RMSN_DTYPE_F16) { *flags = kFlagF16; return RMSN_OK; }
-    return RMSN_EINVAL;
-}
-
+// Variant flags of a gate argument (RMSN_EINVAL if unknown).
 int gate_flags(int gate, int* flags) {
     if (gate == RMSN_GATE_SILU) { *flags = 0; return RMSN_OK; }
     if (gate == RMSN_GATE_SIGMOID) { *flags = kFlagSigmoid; return RMSN_OK; }
@@ -616,7 +579,7 @@ const char* rmsnorm_status_string(int status) {
         case RMSN_OK: return "RMSN_OK";
         case RMSN_EINVAL: return "RMSN_EINVAL: invalid argument (null pointer, size, stride or eps)";
         case RMSN_EALIGN: return "RMSN_EALIGN: pointer or row stride not 16-byte aligned";
-        case RMSN_EUNSUPPORTED: return "RMSN_EUNSUPPORTED: D must be a multiple of 8 in [8, 16384]";
+        case RMSN_EUNSUPPORTED: return "RMSN_EUNSUPPORTED: D must be a multiple of 8 in [8, 16384] (heads: [8, 512], an even rotated part)";
         case RMSN_ECUDA: return "RMSN_ECUDA: a CUDA call failed";
         case RMSN_EWORKSPACE: return "RMSN_EWORKSPACE: workspace missing or too small";
         default: return "unknown rmsnorm status";
