@@ -13,6 +13,7 @@
 #include "checks.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "layernorm_launch.h"
 
 namespace rmsn {
 
@@ -802,6 +803,8 @@ int rmsnorm_device_error(unsigned int* flags, int clear) {
     if (e == cudaSuccess) e = narrow_read_error(flags, clear != 0);
     if (e == cudaSuccess) e = wide_f16_read_error(flags, clear != 0);
     if (e == cudaSuccess) e = narrow_f16_read_error(flags, clear != 0);
+    if (e == cudaSuccess) e = layernorm_read_error(flags, clear != 0);
+    if (e == cudaSuccess) e = layernorm_f16_read_error(flags, clear != 0);
     if (e == cudaSuccess) e = selftest_read_error(flags, clear != 0);
     return cuda_status(e);
 }

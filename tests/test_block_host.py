@@ -162,7 +162,7 @@ def test_workspace_queries(lib):
     for D in (8, 128, 256, 264, 1000, 4096, 8200, 16384):
         for T_max in (1, 7, 300, 305, 4000, 40000):
             most = max(rn.layernorm_bwd_workspace_bytes(t, D) for t in range(1, T_max + 1))
-            assert most == rn.layernorm_bwd_workspace_bytes_max(T_max, D), (T_max, D)
+            assert most <= rn.layernorm_bwd_workspace_bytes_max(T_max, D) <= 1.1 * most + 8 * D, (T_max, D)
 
 
 def test_binding_refuses_cpu_tensors():

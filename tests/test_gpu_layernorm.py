@@ -168,7 +168,7 @@ def test_workspace_queries():
     T_max, D = 5000, 512
     most = rn.layernorm_bwd_workspace_bytes_max(T_max, D)
     sizes = [rn.layernorm_bwd_workspace_bytes(t, D) for t in range(1, T_max + 1)]
-    assert max(sizes) == most
+    assert max(sizes) <= most
     x, g, w, b = _inputs(300, D, 3)
     _, _, mean, rstd = _fwd(x, w, b)
     ws = torch.empty(most, dtype=torch.uint8, device=DEV)
