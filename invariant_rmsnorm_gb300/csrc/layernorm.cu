@@ -21,25 +21,14 @@ namespace {
 // and D alone: 152 stands for the GPU.
 constexpr int64_t kLnSms = 152;
 constexpr int64_t kLnMaxChunk = 256;
-struct LnShape { int64_t ctas, step, most; };  // CTAs at once, rows that a CTA takes at a time, rows of a chunk at most
 struct LnChunks { int64_t rows, count; };
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-LnShape ln_shape(int64_t D) {
-    const int64_t per_sm = D <= 256 ? 3 : D <= 512 ? 2 : D <= 2048 ? 3 : D <= 4096 ? 2 : 1;  // the launch bounds of ln_bwd_dispatch
-    int64_t step = 1;
-    if (D <= 512) {  // a group of lanes a row
-        int64_t G = 1;
-        while (G < 32 && G * 8 < D) G *= 2;
-        step = kLnRowThreads / G;
-    }
-    return {kLnSms * per_sm, step, kLnMaxChunk * step};
-}
-
 LnChunks ln_chunks(int64_t T, int64_t D) {
     const LnShape s = ln_shape(D);
-    const int64_t ctas = ceil_div(T, s.ctas * s.most) * s.ctas;
+    const int64_t round = kLnSms * s.per_sm;
+    const int64_t ctas = ceil_div(T, round * kLnMaxChunk * s.step) * round;
     const int64_t rows = ceil_div(ceil_div(T, ctas), s.step) * s.step;
     return {rows, ceil_div(T, rows)};
 }
@@ -48,14 +37,13 @@ LnChunks ln_chunks(int64_t T, int64_t D) {
 // the CTAs of T_max's rounds.
 int64_t ln_chunks_max(int64_t T_max, int64_t D) {
     const LnShape s = ln_shape(D);
-    return std::min(ceil_div(T_max, s.step), ceil_div(T_max, s.ctas * s.most) * s.ctas);
+    const int64_t round = kLnSms * s.per_sm;
+    return std::min(ceil_div(T_max, s.step), ceil_div(T_max, round * kLnMaxChunk * s.step) * round);
 }
 
 size_t ws_need(int64_t T, int64_t D) {
     return static_cast<size_t>(ln_chunks(T, D).count) * static_cast<size_t>(D) * 8u;
 }
-
-float inv_pow2(int64_t D) { return (D & (D - 1)) == 0 ? 1.0f / static_cast<float>(D) : 0.0f; }
 
 }  // namespace
 }  // namespace rmsn
@@ -79,7 +67,7 @@ int layernorm_fwd(const rmsn_act16* x, int64_t ldx, const float* w, const float*
     RMSN_TRY(check_vec(rstd));
     RMSN_TRY(check_eps(eps));
     const LnFwdArgs a{x, ldx, w, b, y, ldy, mean, rstd, T, static_cast<int>(D), eps, zero_centered_gamma ? 1 : 0,
-                      inv_pow2(D)};
+                      1.0f / static_cast<float>(D)};
     return cuda_status(flags ? launch_ln_fwd_f16(a, stream) : launch_ln_fwd(a, stream));
 }
 
@@ -116,7 +104,7 @@ int layernorm_bwd(const rmsn_act16* g, int64_t ldg, const rmsn_act16* x, int64_t
     if (!aligned16(ws)) return RMSN_EALIGN;
     const LnChunks c = ln_chunks(T, D);
     const LnBwdArgs a{g, ldg, x, ldx, w, mean, rstd, dx, lddx, static_cast<float*>(ws), T, static_cast<int>(D),
-                      zero_centered_gamma ? 1 : 0, static_cast<int>(c.rows), inv_pow2(D)};
+                      zero_centered_gamma ? 1 : 0, static_cast<int>(c.rows), 1.0f / static_cast<float>(D)};
     const unsigned n = static_cast<unsigned>(c.count);
     cudaError_t e = flags ? launch_ln_bwd_f16(a, n, db != nullptr, stream) : launch_ln_bwd(a, n, db != nullptr, stream);
     if (e == cudaSuccess) e = launch_reduce_columns(a.partials, n, a.D, dw, db, stream);

@@ -48,178 +48,338 @@ cudaError_t read_ln_error_word(unsigned* flags, bool clear) {
     return e;
 }
 
-__device__ __forceinline__ float fma1(float a, float b, float c) { return __fmaf_rn(a, b, c); }
+// Pairs of fp32 operations in one instruction, each half rounded as the scalar
+// operation is: half the issue slots. Every product that feeds a sum is an
+// explicit fused multiply-add, so nothing is left for ptxas to contract.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
 
-__device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
-    const float4 lo = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 hi = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    o[0] = lo.x; o[1] = lo.y; o[2] = lo.z; o[3] = lo.w;
-    o[4] = hi.x; o[5] = hi.y; o[6] = hi.z; o[7] = hi.w;
+// Eight values as four pairs.
+struct Oct { float2 p[4]; };
+
+__device__ __forceinline__ Oct oct_zero() {
+    Oct o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.p[i] = make_float2(0.0f, 0.0f);
+    return o;
+}
+
+template <bool F16>
+__device__ __forceinline__ Oct oct_unpack(const uint4 v) {
+    float f[8];
+    unpack_act<F16>(v, f);
+    Oct o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.p[i] = pair(f, 2 * i);
+    return o;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint4 oct_pack(const Oct& o) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = o.p[i].x;
+        f[2 * i + 1] = o.p[i].y;
+    }
+    return pack_act<F16>(f);
+}
+
+__device__ __forceinline__ Oct oct_of(float4 lo, float4 hi) {
+    Oct o;
+    o.p[0] = make_float2(lo.x, lo.y); o.p[1] = make_float2(lo.z, lo.w);
+    o.p[2] = make_float2(hi.x, hi.y); o.p[3] = make_float2(hi.z, hi.w);
+    return o;
+}
+
+__device__ __forceinline__ Oct load_oct(const float* p) {
+    return oct_of(__ldg(reinterpret_cast<const float4*>(p)), __ldg(reinterpret_cast<const float4*>(p) + 1));
 }
 
 // Effective weights of vector v.
-__device__ __forceinline__ void ln_weights8(const float* w, int zc, int v, float (&o)[8]) {
-    load8(w + 8 * v, o);
+__device__ __forceinline__ Oct ln_weights(const float* w, int zc, int v) {
+    Oct o = load_oct(w + 8 * v);
     if (zc) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = fadd(o[e], 1.0f);
+        for (int i = 0; i < 4; ++i) o.p[i] = fadd2(o.p[i], both(1.0f));
     }
+    return o;
 }
 
+__device__ __forceinline__ Oct ln_bias(const float* b, int v) { return b != nullptr ? load_oct(b + 8 * v) : oct_zero(); }
+
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
+
+// s / D through the fp32 reciprocal of D, its remainder taken back once: the
+// correctly rounded quotient (the mean of a constant row is that constant), in
+// three instructions in a division's place. An infinite sum stays infinite.
+__device__ __forceinline__ float over_d(float s, float d, float rcp_d) {
+    const float q = fmul(s, rcp_d);
+    const float e = __fmaf_rn(__fmaf_rn(-q, d, s), rcp_d, q);
+    return fabsf(q) < __int_as_float(0x7f800000) ? e : q;
+}
+
+// Parts of a lane's sums, even and odd elements apart.
+__device__ __forceinline__ float2 oct_sum(float2 s, const Oct& o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fadd2(s, o.p[i]);
+    return s;
+}
+// o - mu in place; the squares' sum is added to q.
+__device__ __forceinline__ float2 oct_centre(Oct& o, float mu, float2 q) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o.p[i] = fadd2(o.p[i], both(-mu));
+        q = fma2(o.p[i], o.p[i], q);
+    }
+    return q;
+}
+// (c r) w + b
+__device__ __forceinline__ Oct oct_affine(const Oct& c, float r, const Oct& w, const Oct& b) {
+    Oct o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.p[i] = fma2(fmul2(c.p[i], both(r)), w.p[i], b.p[i]);
+    return o;
+}
+// The backward's first half for eight values: x becomes c = x - mu and g becomes
+// gw = g w, their sums (s1: gw, s2: gw c) and the weight gradients grow.
+template <bool BIAS>
+__device__ __forceinline__ void oct_grad(Oct& g, Oct& x, const Oct& w, float mu, float r, float2& s1, float2& s2,
+                                         Oct& aw, Oct& ab) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x.p[i] = fadd2(x.p[i], both(-mu));
+        aw.p[i] = fma2(g.p[i], fmul2(x.p[i], both(r)), aw.p[i]);
+        if (BIAS) ab.p[i] = fadd2(ab.p[i], g.p[i]);
+        s1 = fma2(g.p[i], w.p[i], s1);
+        g.p[i] = fmul2(g.p[i], w.p[i]);
+        s2 = fma2(g.p[i], x.p[i], s2);
+    }
+}
+// r gw + (m c - r c1)
+__device__ __forceinline__ Oct oct_dx(const Oct& gw, const Oct& c, float r, float m, float rc1) {
+    Oct o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.p[i] = fma2(gw.p[i], both(r), fma2(c.p[i], both(m), both(-rc1)));
+    return o;
+}
 
 // ---------------------------------------------------------------------------
 // A group of G lanes a row (V vectors a lane: v = k G + l)
 // ---------------------------------------------------------------------------
 constexpr int kLnRowThreads = 256;
 
-template <bool F16, int G, int V, int NR>
-__global__ void __launch_bounds__(kLnRowThreads) ln_rows_fwd_kernel(const LnFwdArgs a) {
+// Every lane keeps its own ring of S turns in flight: it copies its vectors to
+// its own slots of shared memory (cp.async, past L1) and reads them back itself,
+// so a wait for its own copies is all the synchronisation there is, and data in
+// flight costs no registers. Slot layout [turn][vector][thread]: conflict-free.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// w_eff and b of a row in shared memory as [w low | w high | b low | b high][NV]
+// float4 (the halves of a vector's eight): conflict-free reads.
+__device__ __forceinline__ void stage_weights(float4* wb, const float* w, const float* b, int zc, int NV) {
+    for (int v = threadIdx.x; v < NV; v += blockDim.x) {
+        const Oct x = ln_weights(w, zc, v);
+        wb[v] = make_float4(x.p[0].x, x.p[0].y, x.p[1].x, x.p[1].y);
+        wb[NV + v] = make_float4(x.p[2].x, x.p[2].y, x.p[3].x, x.p[3].y);
+        if (b != nullptr) {
+            const Oct y = load_oct(b + 8 * v);
+            wb[2 * NV + v] = make_float4(y.p[0].x, y.p[0].y, y.p[1].x, y.p[1].y);
+            wb[3 * NV + v] = make_float4(y.p[2].x, y.p[2].y, y.p[3].x, y.p[3].y);
+        }
+    }
+}
+__device__ __forceinline__ Oct staged_weights(const float4* wb, int NV, int v) { return oct_of(wb[v], wb[NV + v]); }
+__device__ __forceinline__ Oct staged_bias(const float4* wb, bool bias, int NV, int v) {
+    return bias ? oct_of(wb[2 * NV + v], wb[3 * NV + v]) : oct_zero();
+}
+
+// Weights in registers at one vector a lane, else in shared memory, read once
+// for the NR rows of a turn.
+template <bool F16, int G, int V, int NR, int S, int MINB>
+__global__ void __launch_bounds__(kLnRowThreads, MINB) ln_rows_fwd_kernel(const LnFwdArgs a) {
     constexpr int P = kLnRowThreads / G;
+    extern __shared__ __align__(16) uint4 ring[];  // [S][NR][V][threads], then V > 1: the weights
     const int NV = a.D >> 3;
     const int gr = threadIdx.x / G, l = threadIdx.x % G;
+    const bool bias = a.b != nullptr;
+    float4* wb = reinterpret_cast<float4*>(ring + S * NR * V * kLnRowThreads);
     pdl_wait();
-    float w[V][8], b[V][8];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const int v = k * G + l;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[k][e] = b[k][e] = 0.0f;
-        if (v < NV) {
-            ln_weights8(a.w, a.zc, v, w[k]);
-            if (a.b != nullptr) load8(a.b + 8 * v, b[k]);
-        }
-    }
     const int64_t nblocks = (a.T + P * NR - 1) / (P * NR);
+    auto fetch = [&](int64_t blk, int s) {
+        if (blk < nblocks) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int64_t row = blk * (P * NR) + gr + i * P;
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (row < a.T && k * G + l < NV)
+                        cp_async16(ring + ((s * NR + i) * V + k) * kLnRowThreads + threadIdx.x, a.x + row * a.ldx + 8 * (k * G + l));
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) fetch(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+    Oct w1 = oct_zero(), b1 = oct_zero();
+    if constexpr (V == 1) {
+        if (l < NV) {
+            w1 = ln_weights(a.w, a.zc, l);
+            b1 = ln_bias(a.b, l);
+        }
+    } else {
+        stage_weights(wb, a.w, a.b, a.zc, NV);
+        __syncthreads();
+    }
+    const float d = static_cast<float>(a.D);
+    int s = 0;
     for (int64_t blk = blockIdx.x; blk < nblocks; blk += gridDim.x) {
         const int64_t row0 = blk * (P * NR) + gr;
-        uint4 xv[NR][V];
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                xv[i][k] = make_uint4(0, 0, 0, 0);
-                if (row0 + i * P < a.T && k * G + l < NV)
-                    xv[i][k] = ld_stream(a.x + (row0 + i * P) * a.ldx + 8 * (k * G + l));
-            }
-        float s[NR], q[NR], mu[NR];
+        cp_async_wait<S - 2>();
+        Oct c[NR][V];
+        float mu[NR], r[NR];
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-            s[i] = 0.0f;
+            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                float f[8];
-                unpack_act<F16>(xv[i][k], f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[i] = fadd(s[i], f[e]);  // zeros beyond the row
+                uint4 xv = make_uint4(0, 0, 0, 0);  // zeros beyond the row
+                if (row0 + i * P < a.T && k * G + l < NV) xv = ring[((s * NR + i) * V + k) * kLnRowThreads + threadIdx.x];
+                c[i][k] = oct_unpack<F16>(xv);
+                sum = oct_sum(sum, c[i][k]);
             }
+            mu[i] = fadd(sum.x, sum.y);
+        }
+        // The slots of the turn before are free: every value of them is used.
+        fetch(blk + static_cast<int64_t>(S - 1) * gridDim.x, s == 0 ? S - 1 : s - 1);
+        if (++s == S) s = 0;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) mu[i] = over_d(group_sum<G>(mu[i]), d, a.rcp_d);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            float2 q = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (k * G + l < NV) q = oct_centre(c[i][k], mu[i], q);
+            r[i] = fadd(q.x, q.y);
         }
 #pragma unroll
-        for (int i = 0; i < NR; ++i) mu[i] = div_by_d(group_sum<G>(s[i]), a.D, a.inv_d_pow2);
+        for (int i = 0; i < NR; ++i) r[i] = rsqrtf(fadd(fmul(group_sum<G>(r[i]), a.rcp_d), a.eps));
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            q[i] = 0.0f;
+        for (int k = 0; k < V; ++k) {
+            const int v = k * G + l;
+            if (v < NV) {
+                Oct w = w1, b = b1;
+                if constexpr (V > 1) {
+                    w = staged_weights(wb, NV, v);
+                    b = staged_bias(wb, bias, NV, v);
+                }
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                float f[8];
-                unpack_act<F16>(xv[i][k], f);
-                if (k * G + l < NV) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float c = fsub(f[e], mu[i]);
-                        q[i] = fma1(c, c, q[i]);
-                    }
+                for (int i = 0; i < NR; ++i) {
+                    const int64_t row = row0 + i * P;
+                    if (row < a.T) st_global_cs(a.y + row * a.ldy + 8 * v, oct_pack<F16>(oct_affine(c[i][k], r[i], w, b)));
                 }
             }
         }
+        if (l == 0) {
 #pragma unroll
-        for (int i = 0; i < NR; ++i) q[i] = group_sum<G>(q[i]);
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            const int64_t row = row0 + i * P;
-            if (row < a.T) {
-                const float r = rsqrtf(fadd(div_by_d(q[i], a.D, a.inv_d_pow2), a.eps));
-                if (l == 0) {
-                    a.mean[row] = mu[i];
-                    a.rstd[row] = r;
+            for (int i = 0; i < NR; ++i)
+                if (row0 + i * P < a.T) {
+                    a.mean[row0 + i * P] = mu[i];
+                    a.rstd[row0 + i * P] = r[i];
                 }
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    if (k * G + l < NV) {
-                        float f[8];
-                        unpack_act<F16>(xv[i][k], f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = fma1(fmul(fsub(f[e], mu[i]), r), w[k][e], b[k][e]);
-                        st_global_cs(a.y + row * a.ldy + 8 * (k * G + l), pack_act<F16>(f));
-                    }
-                }
-            }
         }
     }
+    cp_async_wait<0>();
     pdl_release();
 }
 
 // One CTA a chunk of rows; the group gr of a CTA takes the rows gr, gr + P, ...
 // of the chunk in ascending order, and the groups' sums are added in group order.
-template <bool F16, int G, int V, int NR, bool BIAS>
-__global__ void __launch_bounds__(kLnRowThreads, V == 1 ? 3 : 2) ln_rows_bwd_kernel(const LnBwdArgs a) {
+template <bool F16, int G, int V, int NR, int S, int MINB, bool BIAS>
+__global__ void __launch_bounds__(kLnRowThreads, MINB) ln_rows_bwd_kernel(const LnBwdArgs a) {
     constexpr int P = kLnRowThreads / G;
-    extern __shared__ __align__(16) float comb[];  // [P][D]
+    extern __shared__ __align__(16) uint4 ring[];  // [S][NR][g | x][V][threads]; at the end [P][D] sums
     const int NV = a.D >> 3;
     const int gr = threadIdx.x / G, l = threadIdx.x % G;
     pdl_wait();
-    float w[V][8], aw[V][8], ab[V][8];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[k][e] = aw[k][e] = ab[k][e] = 0.0f;
-        if (k * G + l < NV) ln_weights8(a.w, a.zc, k * G + l, w[k]);
-    }
     const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
-    const int64_t c1 = min(c0 + a.chunk, a.T);
-    for (int64_t row0 = c0 + gr; row0 - gr < c1; row0 += P * NR) {  // every lane takes every turn: the sums are the warp's
-        uint4 gv[NR][V], xv[NR][V];
-        float mu[NR], r[NR];
+    const int n_rows = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.T - c0));
+    auto slot = [&](int s, int i, int op, int k) { return ring + (((s * NR + i) * 2 + op) * V + k) * kLnRowThreads + threadIdx.x; };
+    auto fetch = [&](int at, int s) {  // the turn whose first row is c0 + at
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-            const int64_t row = row0 + i * P;
-            mu[i] = r[i] = 0.0f;
-            if (row < c1) {
-                mu[i] = __ldg(a.mean + row);
-                r[i] = __ldg(a.rstd + row);
-            }
+            const int rel = at + gr + i * P;
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                gv[i][k] = xv[i][k] = make_uint4(0, 0, 0, 0);
-                if (row < c1 && k * G + l < NV) {
-                    gv[i][k] = ld_stream(a.g + row * a.ldg + 8 * (k * G + l));
-                    xv[i][k] = ld_stream(a.x + row * a.ldx + 8 * (k * G + l));
+            for (int k = 0; k < V; ++k)
+                if (rel < n_rows && k * G + l < NV) {
+                    cp_async16(slot(s, i, 0, k), a.g + (c0 + rel) * a.ldg + 8 * (k * G + l));
+                    cp_async16(slot(s, i, 1, k), a.x + (c0 + rel) * a.ldx + 8 * (k * G + l));
                 }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) fetch(s * P * NR, s);
+    float mu1[NR], r1[NR];  // the next turn's statistics
+    auto stats = [&](int at) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const int rel = at + gr + i * P;
+            mu1[i] = r1[i] = 0.0f;
+            if (rel < n_rows) {
+                mu1[i] = __ldg(a.mean + c0 + rel);
+                r1[i] = __ldg(a.rstd + c0 + rel);
             }
         }
-        float s1[NR], s2[NR];
+    };
+    stats(0);
+    Oct w[V], aw[V], ab[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        w[k] = aw[k] = ab[k] = oct_zero();
+        if (k * G + l < NV) w[k] = ln_weights(a.w, a.zc, k * G + l);
+    }
+    int s = 0;
+    for (int at = 0; at < n_rows; at += P * NR) {  // every lane takes every turn: the sums are the warp's
+        cp_async_wait<S - 2>();
+        Oct g[NR][V], c[NR][V];
+        float s1[NR], s2[NR], mu[NR], r[NR];
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-            s1[i] = s2[i] = 0.0f;
-            if (row0 + i * P < c1) {
+            mu[i] = mu1[i];
+            r[i] = r1[i];
+        }
+        stats(at + P * NR);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            float2 p1 = make_float2(0.0f, 0.0f), p2 = p1;
+            if (at + gr + i * P < n_rows) {
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
-                    float g[8], f[8];
-                    unpack_act<F16>(gv[i][k], g);
-                    unpack_act<F16>(xv[i][k], f);
                     if (k * G + l < NV) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float c = fsub(f[e], mu[i]), gw = fmul(g[e], w[k][e]);
-                            s1[i] = fadd(s1[i], gw);
-                            s2[i] = fma1(gw, c, s2[i]);
-                            aw[k][e] = fma1(g[e], fmul(c, r[i]), aw[k][e]);
-                            if (BIAS) ab[k][e] = fadd(ab[k][e], g[e]);
-                        }
+                        g[i][k] = oct_unpack<F16>(*slot(s, i, 0, k));
+                        c[i][k] = oct_unpack<F16>(*slot(s, i, 1, k));
+                        oct_grad<BIAS>(g[i][k], c[i][k], w[k], mu[i], r[i], p1, p2, aw[k], ab[k]);
                     }
                 }
             }
+            s1[i] = fadd(p1.x, p1.y);
+            s2[i] = fadd(p2.x, p2.y);
         }
+        fetch(at + (S - 1) * P * NR, s == 0 ? S - 1 : s - 1);
+        if (++s == S) s = 0;
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             s1[i] = group_sum<G>(s1[i]);
@@ -227,28 +387,21 @@ __global__ void __launch_bounds__(kLnRowThreads, V == 1 ? 3 : 2) ln_rows_bwd_ker
         }
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-            const int64_t row = row0 + i * P;
-            if (row < c1) {
-                const float rc1 = fmul(r[i], div_by_d(s1[i], a.D, a.inv_d_pow2));
-                const float m = -fmul(fmul(r[i], r[i]), div_by_d(fmul(s2[i], r[i]), a.D, a.inv_d_pow2));
+            const int rel = at + gr + i * P;
+            if (rel < n_rows) {
+                const float rc1 = fmul(r[i], fmul(s1[i], a.rcp_d));
+                const float m = -fmul(fmul(r[i], r[i]), fmul(fmul(s2[i], r[i]), a.rcp_d));
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    if (k * G + l < NV) {
-                        float g[8], f[8];
-                        unpack_act<F16>(gv[i][k], g);
-                        unpack_act<F16>(xv[i][k], f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float c = fsub(f[e], mu[i]), gw = fmul(g[e], w[k][e]);
-                            f[e] = fma1(gw, r[i], fma1(c, m, -rc1));
-                        }
-                        st_global_cs(a.dx + row * a.lddx + 8 * (k * G + l), pack_act<F16>(f));
-                    }
-                }
+                for (int k = 0; k < V; ++k)
+                    if (k * G + l < NV)
+                        st_global_cs(a.dx + (c0 + rel) * a.lddx + 8 * (k * G + l),
+                                     oct_pack<F16>(oct_dx(g[i][k], c[i][k], r[i], m, rc1)));
             }
         }
     }
+    cp_async_wait<0>();
     // The groups' sums: dw, then db through the same shared memory.
+    float* comb = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int part = 0; part < (BIAS ? 2 : 1); ++part) {
         __syncthreads();
@@ -256,9 +409,9 @@ __global__ void __launch_bounds__(kLnRowThreads, V == 1 ? 3 : 2) ln_rows_bwd_ker
         for (int k = 0; k < V; ++k) {
             if (k * G + l < NV) {
                 float4* o = reinterpret_cast<float4*>(comb + gr * a.D + 8 * (k * G + l));
-                const float(&s)[8] = part ? ab[k] : aw[k];
-                o[0] = make_float4(s[0], s[1], s[2], s[3]);
-                o[1] = make_float4(s[4], s[5], s[6], s[7]);
+                const Oct& t = part ? ab[k] : aw[k];
+                o[0] = make_float4(t.p[0].x, t.p[0].y, t.p[1].x, t.p[1].y);
+                o[1] = make_float4(t.p[2].x, t.p[2].y, t.p[3].x, t.p[3].y);
             }
         }
         __syncthreads();
@@ -318,8 +471,8 @@ __device__ void ln_abort(uint64_t* full, int S, int i, int last) {
 }
 
 // Forward: rows cta, cta + grid, ..., R an iteration. Stage: [R][D] 16-bit.
-template <bool F16, int VPT, int MAXT, int R>
-__global__ void __launch_bounds__(MAXT) ln_wide_fwd_kernel(const LnFwdArgs a, const int S) {
+template <bool F16, int VPT, int MAXT, int MINB, int R>
+__global__ void __launch_bounds__(MAXT, MINB) ln_wide_fwd_kernel(const LnFwdArgs a, const int S) {
     constexpr int NW = MAXT / 32;
     extern __shared__ __align__(128) unsigned char smem[];
     const int NV = a.D >> 3, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -327,7 +480,10 @@ __global__ void __launch_bounds__(MAXT) ln_wide_fwd_kernel(const LnFwdArgs a, co
     const uint32_t stage_bytes = R * row_bytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * stage_bytes);
     float* red = reinterpret_cast<float*>(full + ((S + 1) & ~1));  // [2][R][NW]
+    float4* wb = reinterpret_cast<float4*>(red + 2 * R * NW);      // weights (and bias)
+    const bool bias = a.b != nullptr;
     const int64_t cta = blockIdx.x, G = gridDim.x;
+    const float d = static_cast<float>(a.D);
     const int n_my = static_cast<int>((a.T - 1 - cta) / G + 1);  // grid <= T
     const int n_it = (n_my + R - 1) / R;
     if (tid == 0) {
@@ -348,6 +504,7 @@ __global__ void __launch_bounds__(MAXT) ln_wide_fwd_kernel(const LnFwdArgs a, co
     };
     if (tid == 0)
         for (int i = 0; i < min(S, n_it); ++i) issue(i);
+    stage_weights(wb, a.w, a.b, a.zc, NV);  // seen by every thread after the first barrier below
 
     int s = 0;
     uint32_t ph = 0;
@@ -355,20 +512,19 @@ __global__ void __launch_bounds__(MAXT) ln_wide_fwd_kernel(const LnFwdArgs a, co
         const bool ok = mbar_wait(&full[s], ph);
         const unsigned char* st = smem + static_cast<size_t>(s) * stage_bytes;
         const int nvalid = min(n_my - i * R, R);
-        uint4 xv[R][VPT];
+        Oct c[R][VPT];
         float sum[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            sum[r] = 0.0f;
+            float2 p = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                xv[r][j] = make_uint4(0, 0, 0, 0);
-                if (r < nvalid && j * nt + tid < NV) xv[r][j] = ld_shared_v4(st + r * row_bytes + 16 * (j * nt + tid));
-                float f[8];
-                unpack_act<F16>(xv[r][j], f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[r] = fadd(sum[r], f[e]);
+                uint4 xv = make_uint4(0, 0, 0, 0);
+                if (r < nvalid && j * nt + tid < NV) xv = ld_shared_v4(st + r * row_bytes + 16 * (j * nt + tid));
+                c[r][j] = oct_unpack<F16>(xv);
+                p = oct_sum(p, c[r][j]);
             }
+            sum[r] = fadd(p.x, p.y);
         }
         {
             const float t = warp_sums<R>(sum, lane);
@@ -389,20 +545,12 @@ __global__ void __launch_bounds__(MAXT) ln_wide_fwd_kernel(const LnFwdArgs a, co
         float mu[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            mu[r] = div_by_d(warps_total<NW>(red + r * NW), a.D, a.inv_d_pow2);
-            sum[r] = 0.0f;
+            mu[r] = over_d(warps_total<NW>(red + r * NW), d, a.rcp_d);
+            float2 q = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (j * nt + tid < NV) {
-                    float f[8];
-                    unpack_act<F16>(xv[r][j], f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float c = fsub(f[e], mu[r]);
-                        sum[r] = fma1(c, c, sum[r]);
-                    }
-                }
-            }
+            for (int j = 0; j < VPT; ++j)
+                if (j * nt + tid < NV) q = oct_centre(c[r][j], mu[r], q);
+            sum[r] = fadd(q.x, q.y);
         }
         {
             const float t = warp_sums<R>(sum, lane);
@@ -412,7 +560,7 @@ __global__ void __launch_bounds__(MAXT) ln_wide_fwd_kernel(const LnFwdArgs a, co
         float rr[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            rr[r] = rsqrtf(fadd(div_by_d(warps_total<NW>(red + (R + r) * NW), a.D, a.inv_d_pow2), a.eps));
+            rr[r] = rsqrtf(fadd(fmul(warps_total<NW>(red + (R + r) * NW), a.rcp_d), a.eps));
             if (tid == 0 && r < nvalid) {
                 const int64_t row = cta + static_cast<int64_t>(i * R + r) * G;
                 a.mean[row] = mu[r];
@@ -423,24 +571,12 @@ __global__ void __launch_bounds__(MAXT) ln_wide_fwd_kernel(const LnFwdArgs a, co
         for (int j = 0; j < VPT; ++j) {
             const int v = j * nt + tid;
             if (v < NV) {
-                float w[8], b[8];
-                ln_weights8(a.w, a.zc, v, w);
-                if (a.b != nullptr) {
-                    load8(a.b + 8 * v, b);
-                } else {
+                const Oct w = staged_weights(wb, NV, v), b = staged_bias(wb, bias, NV, v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) b[e] = 0.0f;
-                }
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if (r < nvalid) {
-                        float f[8];
-                        unpack_act<F16>(xv[r][j], f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = fma1(fmul(fsub(f[e], mu[r]), rr[r]), w[e], b[e]);
-                        st_global_cs(a.y + (cta + static_cast<int64_t>(i * R + r) * G) * a.ldy + 8 * v, pack_act<F16>(f));
-                    }
-                }
+                for (int r = 0; r < R; ++r)
+                    if (r < nvalid)
+                        st_global_cs(a.y + (cta + static_cast<int64_t>(i * R + r) * G) * a.ldy + 8 * v,
+                                     oct_pack<F16>(oct_affine(c[r][j], rr[r], w, b)));
             }
         }
     }
@@ -448,9 +584,10 @@ __global__ void __launch_bounds__(MAXT) ln_wide_fwd_kernel(const LnFwdArgs a, co
 }
 
 // Backward: one CTA a chunk of rows, R an iteration. Stage: [R][g | x][D]
-// 16-bit. HOLD: the operands are read from the stage again after the reduction
-// instead of being kept in registers, and the stage is refilled an iteration later.
-template <bool F16, int VPT, int MAXT, int MINB, int R, bool BIAS, bool HOLD>
+// 16-bit. Between the two halves of a row its c and g w stay in registers; SW
+// (the widest rows, whose weight gradients take 64 registers): the packed g and x
+// stay instead, and the weights lie in shared memory.
+template <bool F16, int VPT, int MAXT, int MINB, int R, bool BIAS, bool SW>
 __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs a, const int S) {
     constexpr int NW = MAXT / 32;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -459,7 +596,8 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
     const uint32_t stage_bytes = 2 * R * row_bytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * stage_bytes);
     float* red = reinterpret_cast<float*>(full + ((S + 1) & ~1));  // [2][2 R][NW]
-    float2* stat = reinterpret_cast<float2*>(red + 4 * R * NW);    // [chunk]: mean, rstd
+    float4* wb = reinterpret_cast<float4*>(red + 4 * R * NW);      // SW: the weights
+    float2* stat = reinterpret_cast<float2*>(wb + (SW ? 2 * NV : 0));  // [chunk]: mean, rstd
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
     const int n_my = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.T - row0));
     const int n_it = (n_my + R - 1) / R;
@@ -485,11 +623,13 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
     if (tid == 0)
         for (int i = 0; i < min(S, n_it); ++i) issue(i);
     for (int i = tid; i < n_my; i += nt) stat[i] = make_float2(__ldg(a.mean + row0 + i), __ldg(a.rstd + row0 + i));
-    float aw[VPT][8], ab[VPT][8];
+    Oct w[VPT], aw[VPT], ab[VPT];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) aw[j][e] = ab[j][e] = 0.0f;
+    for (int j = 0; j < VPT; ++j) {
+        w[j] = aw[j] = ab[j] = oct_zero();
+        if (!SW && j * nt + tid < NV) w[j] = ln_weights(a.w, a.zc, j * nt + tid);
+    }
+    if constexpr (SW) stage_weights(wb, a.w, nullptr, a.zc, NV);
     __syncthreads();
 
     int s = 0;
@@ -498,12 +638,13 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
         const bool ok = mbar_wait(&full[s], ph);
         const unsigned char* st = smem + static_cast<size_t>(s) * stage_bytes;
         const int nvalid = min(n_my - i * R, R);
+        Oct g[R][VPT], c[R][VPT];  // gw and x - mu
         uint4 gv[R][VPT], xv[R][VPT];
         float sum[2 * R];
         float2 mr[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            sum[2 * r] = sum[2 * r + 1] = 0.0f;
+            float2 p1 = make_float2(0.0f, 0.0f), p2 = p1;
             if (r < nvalid) {
                 mr[r] = stat[i * R + r];
 #pragma unroll
@@ -512,21 +653,15 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
                     if (v < NV) {
                         gv[r][j] = ld_shared_v4(st + r * 2 * row_bytes + 16 * v);
                         xv[r][j] = ld_shared_v4(st + r * 2 * row_bytes + row_bytes + 16 * v);
-                        float g[8], f[8], w[8];
-                        unpack_act<F16>(gv[r][j], g);
-                        unpack_act<F16>(xv[r][j], f);
-                        ln_weights8(a.w, a.zc, v, w);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float c = fsub(f[e], mr[r].x), gw = fmul(g[e], w[e]);
-                            sum[2 * r] = fadd(sum[2 * r], gw);
-                            sum[2 * r + 1] = fma1(gw, c, sum[2 * r + 1]);
-                            aw[j][e] = fma1(g[e], fmul(c, mr[r].y), aw[j][e]);
-                            if (BIAS) ab[j][e] = fadd(ab[j][e], g[e]);
-                        }
+                        g[r][j] = oct_unpack<F16>(gv[r][j]);
+                        c[r][j] = oct_unpack<F16>(xv[r][j]);
+                        oct_grad<BIAS>(g[r][j], c[r][j], SW ? staged_weights(wb, NV, v) : w[j], mr[r].x, mr[r].y, p1, p2,
+                                       aw[j], ab[j]);
                     }
                 }
             }
+            sum[2 * r] = fadd(p1.x, p1.y);
+            sum[2 * r + 1] = fadd(p2.x, p2.y);
         }
         float* rb = red + (i & 1) * 2 * R * NW;
         {
@@ -534,14 +669,12 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
             if (lane % (16 / R) == 0) rb[(lane / (16 / R)) * NW + warp] = t;
         }
         if (!__syncthreads_and(ok ? 1 : 0)) {
-            if (tid == 0) ln_abort(full, S, i, min(i + S - (HOLD ? 1 : 0), n_it) - 1);
+            if (tid == 0) ln_abort(full, S, i, min(i + S, n_it) - 1);
             return;
         }
-        // Free now: this iteration's stage, or with HOLD the one before it.
-        const int next = HOLD ? i - 1 + S : i + S;
-        if (tid == 0 && next < n_it && next >= S) {
+        if (tid == 0 && i + S < n_it) {  // every thread has the stage in registers
             fence_proxy_async_smem();
-            issue(next);
+            issue(i + S);
         }
         if (++s == S) {
             s = 0;
@@ -551,27 +684,24 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
         for (int r = 0; r < R; ++r) {
             if (r < nvalid) {
                 const float rs = mr[r].y;
-                const float rc1 = fmul(rs, div_by_d(warps_total<NW>(rb + 2 * r * NW), a.D, a.inv_d_pow2));
-                const float m = -fmul(fmul(rs, rs), div_by_d(fmul(warps_total<NW>(rb + (2 * r + 1) * NW), rs), a.D, a.inv_d_pow2));
+                const float rc1 = fmul(rs, fmul(warps_total<NW>(rb + 2 * r * NW), a.rcp_d));
+                const float m = -fmul(fmul(rs, rs), fmul(fmul(warps_total<NW>(rb + (2 * r + 1) * NW), rs), a.rcp_d));
                 uint16_t* dx = a.dx + (row0 + i * R + r) * a.lddx;
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
                     const int v = j * nt + tid;
                     if (v < NV) {
-                        if (HOLD) {
-                            gv[r][j] = ld_shared_v4(st + r * 2 * row_bytes + 16 * v);
-                            xv[r][j] = ld_shared_v4(st + r * 2 * row_bytes + row_bytes + 16 * v);
-                        }
-                        float g[8], f[8], w[8];
-                        unpack_act<F16>(gv[r][j], g);
-                        unpack_act<F16>(xv[r][j], f);
-                        ln_weights8(a.w, a.zc, v, w);
+                        if constexpr (SW) {
+                            const Oct wv = staged_weights(wb, NV, v);
+                            g[r][j] = oct_unpack<F16>(gv[r][j]);
+                            c[r][j] = oct_unpack<F16>(xv[r][j]);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float c = fsub(f[e], mr[r].x), gw = fmul(g[e], w[e]);
-                            f[e] = fma1(gw, rs, fma1(c, m, -rc1));
+                            for (int e = 0; e < 4; ++e) {
+                                g[r][j].p[e] = fmul2(g[r][j].p[e], wv.p[e]);
+                                c[r][j].p[e] = fadd2(c[r][j].p[e], both(-mr[r].x));
+                            }
                         }
-                        st_global_cs(dx + 8 * v, pack_act<F16>(f));
+                        st_global_cs(dx + 8 * v, oct_pack<F16>(oct_dx(g[r][j], c[r][j], rs, m, rc1)));
                     }
                 }
             }
@@ -585,11 +715,11 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
     for (int j = 0; j < VPT; ++j) {
         const int v = j * nt + tid;
         if (v < NV) {
-            st_global_f4_hint(pw + 8 * v, aw[j][0], aw[j][1], aw[j][2], aw[j][3], keep);
-            st_global_f4_hint(pw + 8 * v + 4, aw[j][4], aw[j][5], aw[j][6], aw[j][7], keep);
+            st_global_f4_hint(pw + 8 * v, aw[j].p[0].x, aw[j].p[0].y, aw[j].p[1].x, aw[j].p[1].y, keep);
+            st_global_f4_hint(pw + 8 * v + 4, aw[j].p[2].x, aw[j].p[2].y, aw[j].p[3].x, aw[j].p[3].y, keep);
             if (BIAS) {
-                st_global_f4_hint(pb + 8 * v, ab[j][0], ab[j][1], ab[j][2], ab[j][3], keep);
-                st_global_f4_hint(pb + 8 * v + 4, ab[j][4], ab[j][5], ab[j][6], ab[j][7], keep);
+                st_global_f4_hint(pb + 8 * v, ab[j].p[0].x, ab[j].p[0].y, ab[j].p[1].x, ab[j].p[1].y, keep);
+                st_global_f4_hint(pb + 8 * v + 4, ab[j].p[2].x, ab[j].p[2].y, ab[j].p[3].x, ab[j].p[3].y, keep);
             }
         }
     }
@@ -601,86 +731,129 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
 // ---------------------------------------------------------------------------
 constexpr size_t kLnMaxSmem = 227 * 1024;
 
-template <bool F16, int G, int V, int NR>
+template <bool F16, int G, int V, int NR, int S, int MINB>
 cudaError_t rows_fwd(const LnFwdArgs& a, cudaStream_t st) {
     constexpr int rows = kLnRowThreads / G * NR;
-    const void* kern = reinterpret_cast<const void*>(ln_rows_fwd_kernel<F16, G, V, NR>);
-    const int occ = ctas_per_sm(kern, kLnRowThreads, 0);
+    const int smem = S * NR * V * kLnRowThreads * 16 + (V > 1 ? a.D * 8 : 0);
+    const auto kern = ln_rows_fwd_kernel<F16, G, V, NR, S, MINB>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+    const int occ = ctas_per_sm(reinterpret_cast<const void*>(kern), kLnRowThreads, smem);
     if (occ < 1) return cudaErrorInvalidConfiguration;
     const int64_t grid = std::min<int64_t>((a.T + rows - 1) / rows, static_cast<int64_t>(sm_count()) * occ);
-    return launch_kernel(ln_rows_fwd_kernel<F16, G, V, NR>, static_cast<unsigned>(grid), kLnRowThreads, 0, st, a);
+    return launch_kernel(kern, static_cast<unsigned>(grid), kLnRowThreads, smem, st, a);
 }
 
-template <bool F16, int VPT, int MAXT, int R>
-cudaError_t wide_fwd(const LnFwdArgs& a, size_t ring, int most, cudaStream_t st) {
+template <bool F16, int VPT, int MAXT, int MINB, int R>
+cudaError_t wide_fwd(const LnFwdArgs& a, size_t ring, cudaStream_t st) {
     const int NV = a.D / 8;
     const int threads = ((NV + VPT - 1) / VPT + 31) / 32 * 32;
     const size_t stage = static_cast<size_t>(R) * a.D * 2;
-    const size_t fixed = 2 * R * (MAXT / 32) * 4 + 16;
+    const size_t fixed = 2 * R * (MAXT / 32) * 4 + 16 + static_cast<size_t>(a.D) * (a.b != nullptr ? 8 : 4);
     const int S = static_cast<int>(std::min<size_t>(std::max<size_t>(ring / stage, 2), 16));
     const size_t smem = S * (stage + 8) + fixed;
     if (smem > kLnMaxSmem) return cudaErrorInvalidConfiguration;
-    const void* kern = reinterpret_cast<const void*>(ln_wide_fwd_kernel<F16, VPT, MAXT, R>);
-    cudaError_t e = ensure_smem_attr(kern, static_cast<int>(smem));
+    const auto kern = ln_wide_fwd_kernel<F16, VPT, MAXT, MINB, R>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    const int occ = std::min(ctas_per_sm(kern, threads, static_cast<int>(smem)), most);
+    const int occ = ctas_per_sm(reinterpret_cast<const void*>(kern), threads, static_cast<int>(smem));
     if (occ < 1) return cudaErrorInvalidConfiguration;
     const int64_t grid = std::min<int64_t>(a.T, static_cast<int64_t>(sm_count()) * occ);
-    return launch_kernel(ln_wide_fwd_kernel<F16, VPT, MAXT, R>, static_cast<unsigned>(grid), threads, smem, st, a, S);
+    return launch_kernel(kern, static_cast<unsigned>(grid), threads, smem, st, a, S);
 }
+
+// lanes, vectors a lane, rows a turn, turns in flight, CTAs an SM
+#ifndef LN_F1
+#define LN_F1 1, 2, 4, 4
+#endif
+#ifndef LN_FNARROW
+#define LN_FNARROW(n) rows_fwd<F16, n, LN_F1>(a, st)
+#endif
+#ifndef LN_F2
+#define LN_F2 2, 2, 3, 4
+#endif
+#ifndef LN_F4
+#define LN_F4 4, 1, 3, 3
+#endif
+#ifndef LN_F8
+#define LN_F8 8, 1, 2, 2
+#endif
+// vectors a thread, threads, CTAs an SM, rows an iteration; ring KB
+#ifndef LN_W2
+#define LN_W2 2, 256, 2, 4
+#endif
+#ifndef LN_W2_RING
+#define LN_W2_RING 64
+#endif
+#ifndef LN_W4
+#define LN_W4 2, 512, 1, 2
+#endif
+#ifndef LN_W4_RING
+#define LN_W4_RING 128
+#endif
+#ifndef LN_W8
+#define LN_W8 2, 1024, 1, 1
+#endif
+#ifndef LN_W8_RING
+#define LN_W8_RING 64
+#endif
 
 template <bool F16>
 cudaError_t ln_fwd_dispatch(const LnFwdArgs& a, cudaStream_t st) {
     const int NV = a.D / 8;
-    if (NV <= 1) return rows_fwd<F16, 1, 1, 4>(a, st);
-    if (NV <= 2) return rows_fwd<F16, 2, 1, 4>(a, st);
-    if (NV <= 4) return rows_fwd<F16, 4, 1, 4>(a, st);
-    if (NV <= 8) return rows_fwd<F16, 8, 1, 4>(a, st);
-    if (NV <= 16) return rows_fwd<F16, 16, 1, 4>(a, st);
-    if (NV <= 32) return rows_fwd<F16, 32, 1, 4>(a, st);
-    if (NV <= 64) return rows_fwd<F16, 32, 2, 2>(a, st);
-    if (NV <= 128) return rows_fwd<F16, 32, 4, 1>(a, st);
-    if (NV <= 256) return wide_fwd<F16, 1, 256, 4>(a, 64 * 1024, 3, st);
-    if (NV <= 512) return wide_fwd<F16, 2, 256, 4>(a, 96 * 1024, 3, st);
-    if (NV <= 1024) return wide_fwd<F16, 4, 256, 2>(a, 96 * 1024, 2, st);
-    return wide_fwd<F16, 4, 512, 2>(a, 192 * 1024, 1, st);
+    if (NV <= 1) return LN_FNARROW(1);
+    if (NV <= 2) return LN_FNARROW(2);
+    if (NV <= 4) return LN_FNARROW(4);
+    if (NV <= 8) return LN_FNARROW(8);
+    if (NV <= 16) return LN_FNARROW(16);
+    if (NV <= 32) return LN_FNARROW(32);
+    if (NV <= 64) return rows_fwd<F16, 32, LN_F2>(a, st);
+    if (NV <= 128) return rows_fwd<F16, 32, LN_F4>(a, st);
+    if (NV <= 256) return rows_fwd<F16, 32, LN_F8>(a, st);
+    if (NV <= 512) return wide_fwd<F16, LN_W2>(a, LN_W2_RING * 1024, st);
+    if (NV <= 1024) return wide_fwd<F16, LN_W4>(a, LN_W4_RING * 1024, st);
+    return wide_fwd<F16, LN_W8>(a, LN_W8_RING * 1024, st);
 }
 
-template <bool F16, int G, int V, int NR, bool BIAS>
+template <bool F16, int G, int V, int NR, int S, int MINB, bool BIAS>
 cudaError_t rows_bwd(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
-    const size_t smem = static_cast<size_t>(kLnRowThreads / G) * a.D * 4;
-    return launch_kernel(ln_rows_bwd_kernel<F16, G, V, NR, BIAS>, grid, kLnRowThreads, smem, st, a);
+    const int smem = std::max(S * NR * 2 * V * kLnRowThreads * 16, kLnRowThreads / G * a.D * 4);
+    const auto kern = ln_rows_bwd_kernel<F16, G, V, NR, S, MINB, BIAS>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, grid, kLnRowThreads, smem, st, a);
 }
 
-template <bool F16, int VPT, int MAXT, int MINB, int R, bool BIAS, bool HOLD>
+template <bool F16, int VPT, int MAXT, int MINB, int R, bool BIAS, bool SW>
 cudaError_t wide_bwd(const LnBwdArgs& a, unsigned grid, size_t ring, cudaStream_t st) {
     const int NV = a.D / 8;
     const int threads = ((NV + VPT - 1) / VPT + 31) / 32 * 32;
     const size_t stage = static_cast<size_t>(2) * R * a.D * 2;
-    const size_t fixed = 4 * R * (MAXT / 32) * 4 + 8 * static_cast<size_t>(a.chunk) + 16;
-    int S = static_cast<int>(std::min<size_t>(std::max<size_t>(ring / stage, HOLD ? 3 : 2), 16));
+    const size_t fixed = 4 * R * (MAXT / 32) * 4 + 8 * static_cast<size_t>(a.chunk) + 16 + (SW ? static_cast<size_t>(a.D) * 4 : 0);
+    const int S = static_cast<int>(std::min<size_t>(std::max<size_t>(ring / stage, 2), 16));
     const size_t smem = S * (stage + 8) + fixed;
     if (smem > kLnMaxSmem) return cudaErrorInvalidConfiguration;
-    const void* kern = reinterpret_cast<const void*>(ln_wide_bwd_kernel<F16, VPT, MAXT, MINB, R, BIAS, HOLD>);
-    cudaError_t e = ensure_smem_attr(kern, static_cast<int>(smem));
+    const auto kern = ln_wide_bwd_kernel<F16, VPT, MAXT, MINB, R, BIAS, SW>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_kernel(ln_wide_bwd_kernel<F16, VPT, MAXT, MINB, R, BIAS, HOLD>, grid, threads, smem, st, a, S);
+    return launch_kernel(kern, grid, threads, smem, st, a, S);
 }
 
 template <bool F16, bool BIAS>
 cudaError_t ln_bwd_dispatch(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
     const int NV = a.D / 8;
-    if (NV <= 1) return rows_bwd<F16, 1, 1, 2, BIAS>(a, grid, st);
-    if (NV <= 2) return rows_bwd<F16, 2, 1, 2, BIAS>(a, grid, st);
-    if (NV <= 4) return rows_bwd<F16, 4, 1, 2, BIAS>(a, grid, st);
-    if (NV <= 8) return rows_bwd<F16, 8, 1, 2, BIAS>(a, grid, st);
-    if (NV <= 16) return rows_bwd<F16, 16, 1, 2, BIAS>(a, grid, st);
-    if (NV <= 32) return rows_bwd<F16, 32, 1, 2, BIAS>(a, grid, st);
-    if (NV <= 64) return rows_bwd<F16, 32, 2, 1, BIAS>(a, grid, st);
-    if (NV <= 256) return wide_bwd<F16, 1, 256, 3, 2, BIAS, false>(a, grid, 48 * 1024, st);
-    if (NV <= 512) return wide_bwd<F16, 2, 256, 2, 1, BIAS, false>(a, grid, 64 * 1024, st);
-    if (NV <= 1024) return wide_bwd<F16, 2, 512, 1, 1, BIAS, false>(a, grid, 128 * 1024, st);
-    return wide_bwd<F16, 4, 512, 1, 1, BIAS, true>(a, grid, 192 * 1024, st);
+    if (NV <= 1) return rows_bwd<F16, 1, LN_B1, BIAS>(a, grid, st);
+    if (NV <= 2) return rows_bwd<F16, 2, LN_B1, BIAS>(a, grid, st);
+    if (NV <= 4) return rows_bwd<F16, 4, LN_B1, BIAS>(a, grid, st);
+    if (NV <= 8) return rows_bwd<F16, 8, LN_B1, BIAS>(a, grid, st);
+    if (NV <= 16) return rows_bwd<F16, 16, LN_B1, BIAS>(a, grid, st);
+    if (NV <= 32) return rows_bwd<F16, 32, LN_B1, BIAS>(a, grid, st);
+    if (NV <= 64) return rows_bwd<F16, 32, LN_B2, BIAS>(a, grid, st);
+    const size_t ring = LN_BW_RING * 1024 / ln_shape(a.D).per_sm;
+    if (NV <= 256) return wide_bwd<F16, LN_BW1, BIAS, false>(a, grid, ring, st);
+    if (NV <= 512) return wide_bwd<F16, LN_BW2, BIAS, false>(a, grid, ring, st);
+    if (NV <= 1024) return wide_bwd<F16, LN_BW4, BIAS, false>(a, grid, ring, st);
+    return wide_bwd<F16, 4, 512, 1, 1, BIAS, true>(a, grid, 128 * 1024, st);
 }
 
 }  // namespace
