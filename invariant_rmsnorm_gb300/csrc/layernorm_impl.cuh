@@ -7,20 +7,22 @@
 //   dx = r gw - r c1 - c (r^2 c2'),  c1 = sum gw / D,  c2' = r sum(gw c) / D
 // (n = c r is never formed there), dw = sum_t g (c r), db = sum_t g.
 //
-// All kernels are bound by HBM: 4 D bytes a row forward, 6 D backward. Two forms:
-//   * Rows of up to 512 (backward) or 2048 values (forward): a group of G lanes,
-//     at most a warp, holds a row in registers, straight from global loads, with
-//     several rows a group in flight; no barrier, no shared memory. G and the
-//     vectors a lane follow from D alone.
-//   * Wider rows: a CTA a row. Rows come through a ring of bulk (TMA) copies to
-//     shared memory; thread t owns the 16-byte vectors t, t + NT, ...; a row's
-//     sums go by warp butterflies and one barrier, warps added in warp order. The
-//     barrier also tells thread 0 that the stage is read, so it refills it: there
-//     is no producer warp, and 512 threads keep 128 registers each (a 17th warp
-//     would cut them to 96).
-// Either way a row's tree depends on D alone. Weight gradients are summed in
-// registers by the threads that own the columns, one partial row a CTA; pass 2
-// is reduce_columns.cu.
+// All kernels are bound by HBM: 4 D bytes a row forward, 6 D backward. Three forms:
+//   * Groups (rows of up to 512 values, backward 1016): a group of G lanes, at most
+//     a warp, holds a row, up to four vectors of 8 values a lane, fed by rings of
+//     asynchronous copies that each lane keeps for itself. Sums are butterflies in
+//     the group; no barrier.
+//   * Teams (forward, wider rows): 1 to 8 warps a row, up to 8 vectors a thread in
+//     registers. A row's two sums meet at its team's own barrier.
+//   * CTA rows (backward, wider rows): a CTA a row from a ring of bulk (TMA) copies;
+//     thread t owns the 16-byte vectors t, t + NT, ... and their columns' weight
+//     gradients; warps' sums are added in warp order after one barrier, which also
+//     tells thread 0 that the stage is read, so it refills it: there is no producer
+//     warp, and 512 threads keep 128 registers each (a 17th warp would cut them to 96).
+// Either way a row's tree depends on D alone. The arithmetic is issued in pairs
+// (f32x2): at one operation a value the group kernels spent 19 issue slots a value
+// and stood at 64 % of the copy rate at D = 128. Weight gradients are summed by the
+// threads that own the columns, one partial row a CTA; pass 2 is reduce_columns.cu.
 #pragma once
 
 #include <algorithm>
@@ -307,10 +309,14 @@ __global__ void __launch_bounds__(kLnRowThreads, MINB) ln_rows_fwd_kernel(const 
 
 // One CTA a chunk of rows; the group gr of a CTA takes the rows gr, gr + P, ...
 // of the chunk in ascending order, and the groups' sums are added in group order.
-template <bool F16, int G, int V, int NR, int S, int MINB, bool BIAS>
+// HOLD (three or four vectors a lane, whose weight gradients take 48 or 64
+// registers): the weights lie in shared memory, and after the row's sums g and x
+// are read again from the lane's slots, which are refilled a turn later.
+template <bool F16, int G, int V, int NR, int S, int MINB, bool HOLD, bool BIAS>
 __global__ void __launch_bounds__(kLnRowThreads, MINB) ln_rows_bwd_kernel(const LnBwdArgs a) {
     constexpr int P = kLnRowThreads / G;
-    extern __shared__ __align__(16) uint4 ring[];  // [S][NR][g | x][V][threads]; at the end [P][D] sums
+    extern __shared__ __align__(16) uint4 ring[];  // [S][NR][g | x][V][threads], HOLD: the weights; at the end [P][D] sums
+    float4* wb = reinterpret_cast<float4*>(ring + S * NR * 2 * V * kLnRowThreads);
     const int NV = a.D >> 3;
     const int gr = threadIdx.x / G, l = threadIdx.x % G;
     pdl_wait();
@@ -349,7 +355,11 @@ __global__ void __launch_bounds__(kLnRowThreads, MINB) ln_rows_bwd_kernel(const 
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         w[k] = aw[k] = ab[k] = oct_zero();
-        if (k * G + l < NV) w[k] = ln_weights(a.w, a.zc, k * G + l);
+        if (!HOLD && k * G + l < NV) w[k] = ln_weights(a.w, a.zc, k * G + l);
+    }
+    if constexpr (HOLD) {
+        stage_weights(wb, a.w, nullptr, a.zc, NV);
+        __syncthreads();
     }
     int s = 0;
     for (int at = 0; at < n_rows; at += P * NR) {  // every lane takes every turn: the sums are the warp's
@@ -371,15 +381,14 @@ __global__ void __launch_bounds__(kLnRowThreads, MINB) ln_rows_bwd_kernel(const 
                     if (k * G + l < NV) {
                         g[i][k] = oct_unpack<F16>(*slot(s, i, 0, k));
                         c[i][k] = oct_unpack<F16>(*slot(s, i, 1, k));
-                        oct_grad<BIAS>(g[i][k], c[i][k], w[k], mu[i], r[i], p1, p2, aw[k], ab[k]);
+                        oct_grad<BIAS>(g[i][k], c[i][k], HOLD ? staged_weights(wb, NV, k * G + l) : w[k], mu[i], r[i], p1, p2, aw[k], ab[k]);
                     }
                 }
             }
             s1[i] = fadd(p1.x, p1.y);
             s2[i] = fadd(p2.x, p2.y);
         }
-        fetch(at + (S - 1) * P * NR, s == 0 ? S - 1 : s - 1);
-        if (++s == S) s = 0;
+        if constexpr (!HOLD) fetch(at + (S - 1) * P * NR, s == 0 ? S - 1 : s - 1);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             s1[i] = group_sum<G>(s1[i]);
@@ -393,11 +402,24 @@ __global__ void __launch_bounds__(kLnRowThreads, MINB) ln_rows_bwd_kernel(const 
                 const float m = -fmul(fmul(r[i], r[i]), fmul(fmul(s2[i], r[i]), a.rcp_d));
 #pragma unroll
                 for (int k = 0; k < V; ++k)
-                    if (k * G + l < NV)
+                    if (k * G + l < NV) {
+                        if constexpr (HOLD) {
+                            const Oct wv = staged_weights(wb, NV, k * G + l);
+                            g[i][k] = oct_unpack<F16>(*slot(s, i, 0, k));
+                            c[i][k] = oct_unpack<F16>(*slot(s, i, 1, k));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                g[i][k].p[e] = fmul2(g[i][k].p[e], wv.p[e]);
+                                c[i][k].p[e] = fadd2(c[i][k].p[e], both(-mu[i]));
+                            }
+                        }
                         st_global_cs(a.dx + (c0 + rel) * a.lddx + 8 * (k * G + l),
                                      oct_pack<F16>(oct_dx(g[i][k], c[i][k], r[i], m, rc1)));
+                    }
             }
         }
+        if constexpr (HOLD) fetch(at + (S - 1) * P * NR, s == 0 ? S - 1 : s - 1);
+        if (++s == S) s = 0;
     }
     cp_async_wait<0>();
     // The groups' sums: dw, then db through the same shared memory.
@@ -450,6 +472,9 @@ __device__ __forceinline__ float warp_sums(float (&v)[K], int lane) {
     return t;
 }
 
+// Places for the warps' totals of one value: whole float4s.
+__host__ __device__ constexpr int warp_places(int threads) { return (threads / 32 + 3) / 4 * 4; }
+
 // The warps' totals of one value in warp order; the places beyond the last warp
 // hold zeros.
 template <int NWMAX>
@@ -470,158 +495,113 @@ __device__ void ln_abort(uint64_t* full, int S, int i, int last) {
     atomicOr(&g_ln_error, kErrWaitTimeout);
 }
 
-// Forward: rows cta, cta + grid, ..., R an iteration. Stage: [R][D] 16-bit.
-template <bool F16, int VPT, int MAXT, int MINB, int R>
-__global__ void __launch_bounds__(MAXT, MINB) ln_wide_fwd_kernel(const LnFwdArgs a, const int S) {
-    constexpr int NW = MAXT / 32;
-    extern __shared__ __align__(128) unsigned char smem[];
-    const int NV = a.D >> 3, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t row_bytes = static_cast<uint32_t>(a.D) * 2u;
-    const uint32_t stage_bytes = R * row_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * stage_bytes);
-    float* red = reinterpret_cast<float*>(full + ((S + 1) & ~1));  // [2][R][NW]
-    float4* wb = reinterpret_cast<float4*>(red + 2 * R * NW);      // weights (and bias)
-    const bool bias = a.b != nullptr;
-    const int64_t cta = blockIdx.x, G = gridDim.x;
-    const float d = static_cast<float>(a.D);
-    const int n_my = static_cast<int>((a.T - 1 - cta) / G + 1);  // grid <= T
-    const int n_it = (n_my + R - 1) / R;
-    if (tid == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
-        fence_mbar_init();
+// Forward: a team of TW warps a row, V vectors a thread, in registers; the CTA's
+// teams take rows of their own and share the weights in shared memory. A row's
+// two sums meet at the team's own named barrier, so one team's wait is another's
+// work. PRE: the next row's loads are issued as soon as this row is unpacked and
+// stay in registers until its turn.
+template <int TW>
+__device__ __forceinline__ float team_sum(float v, float* red, int warp, int lane, int bar) {
+    v = group_sum<32>(v);
+    if constexpr (TW > 1) {
+        if (lane == 0) red[warp] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(TW * 32) : "memory");
+        v = red[0];
+#pragma unroll
+        for (int i = 1; i < TW; ++i) v = fadd(v, red[i]);
     }
-    for (int i = tid; i < 2 * R * NW; i += nt) red[i] = 0.0f;
-    __syncthreads();
+    return v;
+}
+
+template <bool F16, int TW, int V, bool PRE, int THREADS, int MINB>
+__global__ void __launch_bounds__(THREADS, MINB) ln_team_fwd_kernel(const LnFwdArgs a) {
+    constexpr int NT = TW * 32, TEAMS = THREADS / NT;
+    extern __shared__ __align__(16) float4 wb[];  // the weights, then the teams' sums
+    const int NV = a.D >> 3;
+    const int team = threadIdx.x / NT, t = threadIdx.x % NT, lane = t & 31, warp = t >> 5;
+    const bool bias = a.b != nullptr;
+    float* red = reinterpret_cast<float*>(wb + (bias ? 4 : 2) * NV) + team * 2 * TW;  // [teams][2][TW]
     pdl_wait();
-
-    const uint64_t pol = policy_evict_first();
-    auto issue = [&](int i) {
-        const int s = i % S, nvalid = min(n_my - i * R, R);
-        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nvalid) * row_bytes);
-        for (int r = 0; r < nvalid; ++r)
-            bulk_g2s(smem + static_cast<size_t>(s) * stage_bytes + r * row_bytes,
-                     a.x + (cta + static_cast<int64_t>(i * R + r) * G) * a.ldx, row_bytes, &full[s], pol);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
+    uint4 xv[V];
+    auto load = [&](int64_t at) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            xv[k] = make_uint4(0, 0, 0, 0);  // zeros beyond the row
+            if (k * NT + t < NV && at < a.T) xv[k] = ld_stream(a.x + at * a.ldx + 8 * (k * NT + t));
+        }
     };
-    if (tid == 0)
-        for (int i = 0; i < min(S, n_it); ++i) issue(i);
-    stage_weights(wb, a.w, a.b, a.zc, NV);  // seen by every thread after the first barrier below
-
-    int s = 0;
-    uint32_t ph = 0;
-    for (int i = 0; i < n_it; ++i) {
-        const bool ok = mbar_wait(&full[s], ph);
-        const unsigned char* st = smem + static_cast<size_t>(s) * stage_bytes;
-        const int nvalid = min(n_my - i * R, R);
-        Oct c[R][VPT];
-        float sum[R];
+    if constexpr (PRE) load(row);
+    stage_weights(wb, a.w, a.b, a.zc, NV);
+    __syncthreads();
+    const float d = static_cast<float>(a.D);
+    for (; row < a.T; row += step) {
+        Oct c[V];
+        if constexpr (!PRE) load(row);
+        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float2 p = make_float2(0.0f, 0.0f);
+        for (int k = 0; k < V; ++k) {
+            c[k] = oct_unpack<F16>(xv[k]);
+            sum = oct_sum(sum, c[k]);
+        }
+        if constexpr (PRE) load(row + step);
+        const float mu = over_d(team_sum<TW>(fadd(sum.x, sum.y), red, warp, lane, team + 1), d, a.rcp_d);
+        float2 q = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                uint4 xv = make_uint4(0, 0, 0, 0);
-                if (r < nvalid && j * nt + tid < NV) xv = ld_shared_v4(st + r * row_bytes + 16 * (j * nt + tid));
-                c[r][j] = oct_unpack<F16>(xv);
-                p = oct_sum(p, c[r][j]);
-            }
-            sum[r] = fadd(p.x, p.y);
-        }
-        {
-            const float t = warp_sums<R>(sum, lane);
-            if (lane % (32 / R) == 0) red[(lane / (32 / R)) * NW + warp] = t;
-        }
-        if (!__syncthreads_and(ok ? 1 : 0)) {
-            if (tid == 0) ln_abort(full, S, i, min(i + S, n_it) - 1);
-            return;
-        }
-        if (tid == 0 && i + S < n_it) {  // every thread has the stage in registers
-            fence_proxy_async_smem();
-            issue(i + S);
-        }
-        if (++s == S) {
-            s = 0;
-            ph ^= 1u;
-        }
-        float mu[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            mu[r] = over_d(warps_total<NW>(red + r * NW), d, a.rcp_d);
-            float2 q = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int j = 0; j < VPT; ++j)
-                if (j * nt + tid < NV) q = oct_centre(c[r][j], mu[r], q);
-            sum[r] = fadd(q.x, q.y);
-        }
-        {
-            const float t = warp_sums<R>(sum, lane);
-            if (lane % (32 / R) == 0) red[(R + lane / (32 / R)) * NW + warp] = t;
-        }
-        __syncthreads();
-        float rr[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            rr[r] = rsqrtf(fadd(fmul(warps_total<NW>(red + (R + r) * NW), a.rcp_d), a.eps));
-            if (tid == 0 && r < nvalid) {
-                const int64_t row = cta + static_cast<int64_t>(i * R + r) * G;
-                a.mean[row] = mu[r];
-                a.rstd[row] = rr[r];
-            }
+        for (int k = 0; k < V; ++k)
+            if (k * NT + t < NV) q = oct_centre(c[k], mu, q);
+        const float r = rsqrtf(fadd(fmul(team_sum<TW>(fadd(q.x, q.y), red + TW, warp, lane, team + 1), a.rcp_d), a.eps));
+        if (t == 0) {
+            a.mean[row] = mu;
+            a.rstd[row] = r;
         }
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = j * nt + tid;
-            if (v < NV) {
-                const Oct w = staged_weights(wb, NV, v), b = staged_bias(wb, bias, NV, v);
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (r < nvalid)
-                        st_global_cs(a.y + (cta + static_cast<int64_t>(i * R + r) * G) * a.ldy + 8 * v,
-                                     oct_pack<F16>(oct_affine(c[r][j], rr[r], w, b)));
-            }
+        for (int k = 0; k < V; ++k) {
+            const int v = k * NT + t;
+            if (v < NV)
+                st_global_cs(a.y + row * a.ldy + 8 * v,
+                             oct_pack<F16>(oct_affine(c[k], r, staged_weights(wb, NV, v), staged_bias(wb, bias, NV, v))));
         }
     }
     pdl_release();
 }
 
-// Backward: one CTA a chunk of rows, R an iteration. Stage: [R][g | x][D]
-// 16-bit. Between the two halves of a row its c and g w stay in registers; SW
-// (the widest rows, whose weight gradients take 64 registers): the packed g and x
-// stay instead, and the weights lie in shared memory.
-template <bool F16, int VPT, int MAXT, int MINB, int R, bool BIAS, bool SW>
+// Backward: one CTA a chunk of rows. Stage: [g | x][D] 16-bit. Between the two
+// halves of a row its c and g w stay in registers; SW (the widest rows, whose
+// weight gradients take 48 or 64 registers): the packed g and x stay instead, and
+// the weights lie in shared memory.
+template <bool F16, int VPT, int MAXT, int MINB, bool BIAS, bool SW>
 __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs a, const int S) {
-    constexpr int NW = MAXT / 32;
+    constexpr int NW = warp_places(MAXT);
     extern __shared__ __align__(128) unsigned char smem[];
     const int NV = a.D >> 3, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t row_bytes = static_cast<uint32_t>(a.D) * 2u;
-    const uint32_t stage_bytes = 2 * R * row_bytes;
+    const uint32_t stage_bytes = 2 * row_bytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * stage_bytes);
-    float* red = reinterpret_cast<float*>(full + ((S + 1) & ~1));  // [2][2 R][NW]
-    float4* wb = reinterpret_cast<float4*>(red + 4 * R * NW);      // SW: the weights
+    float* red = reinterpret_cast<float*>(full + ((S + 1) & ~1));      // [2][2][NW]
+    float4* wb = reinterpret_cast<float4*>(red + 4 * NW);              // SW: the weights
     float2* stat = reinterpret_cast<float2*>(wb + (SW ? 2 * NV : 0));  // [chunk]: mean, rstd
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
     const int n_my = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.T - row0));
-    const int n_it = (n_my + R - 1) / R;
     if (tid == 0) {
         for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
         fence_mbar_init();
     }
-    for (int i = tid; i < 4 * R * NW; i += nt) red[i] = 0.0f;
+    for (int i = tid; i < 4 * NW; i += nt) red[i] = 0.0f;
     __syncthreads();
     pdl_wait();
 
     const uint64_t pol = policy_evict_first();
     auto issue = [&](int i) {
-        const int s = i % S, nvalid = min(n_my - i * R, R);
-        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nvalid) * 2u * row_bytes);
-        for (int r = 0; r < nvalid; ++r) {
-            unsigned char* dst = smem + static_cast<size_t>(s) * stage_bytes + r * 2 * row_bytes;
-            const int64_t row = row0 + i * R + r;
-            bulk_g2s(dst, a.g + row * a.ldg, row_bytes, &full[s], pol);
-            bulk_g2s(dst + row_bytes, a.x + row * a.ldx, row_bytes, &full[s], pol);
-        }
+        const int s = i % S;
+        unsigned char* dst = smem + static_cast<size_t>(s) * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        bulk_g2s(dst, a.g + (row0 + i) * a.ldg, row_bytes, &full[s], pol);
+        bulk_g2s(dst + row_bytes, a.x + (row0 + i) * a.ldx, row_bytes, &full[s], pol);
     };
     if (tid == 0)
-        for (int i = 0; i < min(S, n_it); ++i) issue(i);
+        for (int i = 0; i < min(S, n_my); ++i) issue(i);
     for (int i = tid; i < n_my; i += nt) stat[i] = make_float2(__ldg(a.mean + row0 + i), __ldg(a.rstd + row0 + i));
     Oct w[VPT], aw[VPT], ab[VPT];
 #pragma unroll
@@ -634,45 +614,35 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
 
     int s = 0;
     uint32_t ph = 0;
-    for (int i = 0; i < n_it; ++i) {
+    for (int i = 0; i < n_my; ++i) {
         const bool ok = mbar_wait(&full[s], ph);
         const unsigned char* st = smem + static_cast<size_t>(s) * stage_bytes;
-        const int nvalid = min(n_my - i * R, R);
-        Oct g[R][VPT], c[R][VPT];  // gw and x - mu
-        uint4 gv[R][VPT], xv[R][VPT];
-        float sum[2 * R];
-        float2 mr[R];
+        const float2 mr = stat[i];
+        Oct g[VPT], c[VPT];  // g w and x - mu
+        uint4 gv[VPT], xv[VPT];
+        float2 p1 = make_float2(0.0f, 0.0f), p2 = p1;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float2 p1 = make_float2(0.0f, 0.0f), p2 = p1;
-            if (r < nvalid) {
-                mr[r] = stat[i * R + r];
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    const int v = j * nt + tid;
-                    if (v < NV) {
-                        gv[r][j] = ld_shared_v4(st + r * 2 * row_bytes + 16 * v);
-                        xv[r][j] = ld_shared_v4(st + r * 2 * row_bytes + row_bytes + 16 * v);
-                        g[r][j] = oct_unpack<F16>(gv[r][j]);
-                        c[r][j] = oct_unpack<F16>(xv[r][j]);
-                        oct_grad<BIAS>(g[r][j], c[r][j], SW ? staged_weights(wb, NV, v) : w[j], mr[r].x, mr[r].y, p1, p2,
-                                       aw[j], ab[j]);
-                    }
-                }
+        for (int j = 0; j < VPT; ++j) {
+            const int v = j * nt + tid;
+            if (v < NV) {
+                gv[j] = ld_shared_v4(st + 16 * v);
+                xv[j] = ld_shared_v4(st + row_bytes + 16 * v);
+                g[j] = oct_unpack<F16>(gv[j]);
+                c[j] = oct_unpack<F16>(xv[j]);
+                oct_grad<BIAS>(g[j], c[j], SW ? staged_weights(wb, NV, v) : w[j], mr.x, mr.y, p1, p2, aw[j], ab[j]);
             }
-            sum[2 * r] = fadd(p1.x, p1.y);
-            sum[2 * r + 1] = fadd(p2.x, p2.y);
         }
-        float* rb = red + (i & 1) * 2 * R * NW;
+        float* rb = red + (i & 1) * 2 * NW;
         {
-            const float t = warp_sums<2 * R>(sum, lane);
-            if (lane % (16 / R) == 0) rb[(lane / (16 / R)) * NW + warp] = t;
+            float sum[2] = {fadd(p1.x, p1.y), fadd(p2.x, p2.y)};
+            const float t = warp_sums<2>(sum, lane);
+            if ((lane & 15) == 0) rb[(lane >> 4) * NW + warp] = t;
         }
         if (!__syncthreads_and(ok ? 1 : 0)) {
-            if (tid == 0) ln_abort(full, S, i, min(i + S, n_it) - 1);
+            if (tid == 0) ln_abort(full, S, i, min(i + S, n_my) - 1);
             return;
         }
-        if (tid == 0 && i + S < n_it) {  // every thread has the stage in registers
+        if (tid == 0 && i + S < n_my) {  // every thread has the stage in registers
             fence_proxy_async_smem();
             issue(i + S);
         }
@@ -680,30 +650,24 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
             s = 0;
             ph ^= 1u;
         }
+        const float rc1 = fmul(mr.y, fmul(warps_total<NW>(rb), a.rcp_d));
+        const float m = -fmul(fmul(mr.y, mr.y), fmul(fmul(warps_total<NW>(rb + NW), mr.y), a.rcp_d));
+        uint16_t* dx = a.dx + (row0 + i) * a.lddx;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (r < nvalid) {
-                const float rs = mr[r].y;
-                const float rc1 = fmul(rs, fmul(warps_total<NW>(rb + 2 * r * NW), a.rcp_d));
-                const float m = -fmul(fmul(rs, rs), fmul(fmul(warps_total<NW>(rb + (2 * r + 1) * NW), rs), a.rcp_d));
-                uint16_t* dx = a.dx + (row0 + i * R + r) * a.lddx;
+        for (int j = 0; j < VPT; ++j) {
+            const int v = j * nt + tid;
+            if (v < NV) {
+                if constexpr (SW) {
+                    const Oct wv = staged_weights(wb, NV, v);
+                    g[j] = oct_unpack<F16>(gv[j]);
+                    c[j] = oct_unpack<F16>(xv[j]);
 #pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    const int v = j * nt + tid;
-                    if (v < NV) {
-                        if constexpr (SW) {
-                            const Oct wv = staged_weights(wb, NV, v);
-                            g[r][j] = oct_unpack<F16>(gv[r][j]);
-                            c[r][j] = oct_unpack<F16>(xv[r][j]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                g[r][j].p[e] = fmul2(g[r][j].p[e], wv.p[e]);
-                                c[r][j].p[e] = fadd2(c[r][j].p[e], both(-mr[r].x));
-                            }
-                        }
-                        st_global_cs(dx + 8 * v, oct_pack<F16>(oct_dx(g[r][j], c[r][j], rs, m, rc1)));
+                    for (int e = 0; e < 4; ++e) {
+                        g[j].p[e] = fmul2(g[j].p[e], wv.p[e]);
+                        c[j].p[e] = fadd2(c[j].p[e], both(-mr.x));
                     }
                 }
+                st_global_cs(dx + 8 * v, oct_pack<F16>(oct_dx(g[j], c[j], mr.y, m, rc1)));
             }
         }
     }
@@ -744,116 +708,115 @@ cudaError_t rows_fwd(const LnFwdArgs& a, cudaStream_t st) {
     return launch_kernel(kern, static_cast<unsigned>(grid), kLnRowThreads, smem, st, a);
 }
 
-template <bool F16, int VPT, int MAXT, int MINB, int R>
-cudaError_t wide_fwd(const LnFwdArgs& a, size_t ring, cudaStream_t st) {
-    const int NV = a.D / 8;
-    const int threads = ((NV + VPT - 1) / VPT + 31) / 32 * 32;
-    const size_t stage = static_cast<size_t>(R) * a.D * 2;
-    const size_t fixed = 2 * R * (MAXT / 32) * 4 + 16 + static_cast<size_t>(a.D) * (a.b != nullptr ? 8 : 4);
-    const int S = static_cast<int>(std::min<size_t>(std::max<size_t>(ring / stage, 2), 16));
-    const size_t smem = S * (stage + 8) + fixed;
-    if (smem > kLnMaxSmem) return cudaErrorInvalidConfiguration;
-    const auto kern = ln_wide_fwd_kernel<F16, VPT, MAXT, MINB, R>;
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
+template <bool F16, int TW, int V, bool PRE, int THREADS, int MINB>
+cudaError_t team_fwd(const LnFwdArgs& a, cudaStream_t st) {
+    constexpr int teams = THREADS / (TW * 32);
+    const int smem = a.D * (a.b != nullptr ? 8 : 4) + teams * 2 * TW * 4;
+    const auto kern = ln_team_fwd_kernel<F16, TW, V, PRE, THREADS, MINB>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
-    const int occ = ctas_per_sm(reinterpret_cast<const void*>(kern), threads, static_cast<int>(smem));
+    const int occ = ctas_per_sm(reinterpret_cast<const void*>(kern), THREADS, smem);
     if (occ < 1) return cudaErrorInvalidConfiguration;
-    const int64_t grid = std::min<int64_t>(a.T, static_cast<int64_t>(sm_count()) * occ);
-    return launch_kernel(kern, static_cast<unsigned>(grid), threads, smem, st, a, S);
+    const int64_t grid = std::min<int64_t>((a.T + teams - 1) / teams, static_cast<int64_t>(sm_count()) * occ);
+    return launch_kernel(kern, static_cast<unsigned>(grid), THREADS, smem, st, a);
 }
 
 // lanes, vectors a lane, rows a turn, turns in flight, CTAs an SM
-#ifndef LN_F1
-#define LN_F1 1, 2, 4, 4
-#endif
-#ifndef LN_FNARROW
-#define LN_FNARROW(n) rows_fwd<F16, n, LN_F1>(a, st)
-#endif
-#ifndef LN_F2
-#define LN_F2 2, 2, 3, 4
-#endif
-#ifndef LN_F4
-#define LN_F4 4, 1, 3, 3
-#endif
-#ifndef LN_F8
-#define LN_F8 8, 1, 2, 2
-#endif
-// vectors a thread, threads, CTAs an SM, rows an iteration; ring KB
-#ifndef LN_W2
-#define LN_W2 2, 256, 2, 4
-#endif
-#ifndef LN_W2_RING
-#define LN_W2_RING 64
-#endif
-#ifndef LN_W4
-#define LN_W4 2, 512, 1, 2
-#endif
-#ifndef LN_W4_RING
-#define LN_W4_RING 128
-#endif
-#ifndef LN_W8
-#define LN_W8 2, 1024, 1, 1
-#endif
-#ifndef LN_W8_RING
-#define LN_W8_RING 64
-#endif
-
+// Shapes by width, each the fastest measured: as many vectors a lane as its
+// registers hold (fewer lanes a row: fewer shuffles, more loads in flight a lane),
+// in steps that leave few lanes idle. Of the rates at 256 MB a tensor: D = 128
+// 89 % of the copy rate (with 16 lanes of one vector 76 %), 2048 95 %, 4096 93 %,
+// 5000 93 %, 8192 91 %, 16384 91 %. Rows of 8 vectors a lane on one or two warps
+// do without PRE (2048: 95 against 89 %): 16 warps of 4 KB are in flight as it is.
 template <bool F16>
 cudaError_t ln_fwd_dispatch(const LnFwdArgs& a, cudaStream_t st) {
     const int NV = a.D / 8;
-    if (NV <= 1) return LN_FNARROW(1);
-    if (NV <= 2) return LN_FNARROW(2);
-    if (NV <= 4) return LN_FNARROW(4);
-    if (NV <= 8) return LN_FNARROW(8);
-    if (NV <= 16) return LN_FNARROW(16);
-    if (NV <= 32) return LN_FNARROW(32);
-    if (NV <= 64) return rows_fwd<F16, 32, LN_F2>(a, st);
-    if (NV <= 128) return rows_fwd<F16, 32, LN_F4>(a, st);
-    if (NV <= 256) return rows_fwd<F16, 32, LN_F8>(a, st);
-    if (NV <= 512) return wide_fwd<F16, LN_W2>(a, LN_W2_RING * 1024, st);
-    if (NV <= 1024) return wide_fwd<F16, LN_W4>(a, LN_W4_RING * 1024, st);
-    return wide_fwd<F16, LN_W8>(a, LN_W8_RING * 1024, st);
+    if (NV <= 1) return rows_fwd<F16, 1, 1, 2, 4, 4>(a, st);
+    if (NV <= 2) return rows_fwd<F16, 1, 2, 2, 3, 3>(a, st);
+    if (NV <= 4) return rows_fwd<F16, 2, 2, 2, 3, 3>(a, st);
+    if (NV <= 8) return rows_fwd<F16, 4, 2, 2, 3, 3>(a, st);
+    if (NV <= 12) return rows_fwd<F16, 4, 3, 1, 3, 3>(a, st);
+    if (NV <= 16) return rows_fwd<F16, 4, 4, 1, 3, 3>(a, st);
+    if (NV <= 24) return rows_fwd<F16, 8, 3, 1, 3, 3>(a, st);
+    if (NV <= 32) return rows_fwd<F16, 8, 4, 1, 3, 3>(a, st);
+    if (NV <= 48) return rows_fwd<F16, 16, 3, 1, 3, 3>(a, st);
+    if (NV <= 64) return rows_fwd<F16, 16, 4, 1, 3, 3>(a, st);
+    if (NV <= 96) return team_fwd<F16, 1, 3, true, 256, 3>(a, st);
+    if (NV <= 128) return team_fwd<F16, 1, 4, true, 256, 3>(a, st);
+    if (NV <= 160) return team_fwd<F16, 1, 5, true, 256, 2>(a, st);
+    if (NV <= 192) return team_fwd<F16, 1, 6, true, 256, 2>(a, st);
+    if (NV <= 224) return team_fwd<F16, 1, 7, true, 256, 2>(a, st);
+    if (NV <= 256) return team_fwd<F16, 1, 8, false, 256, 2>(a, st);
+    if (NV <= 320) return team_fwd<F16, 2, 5, true, 256, 2>(a, st);
+    if (NV <= 384) return team_fwd<F16, 2, 6, true, 256, 2>(a, st);
+    if (NV <= 448) return team_fwd<F16, 2, 7, true, 256, 2>(a, st);
+    if (NV <= 512) return team_fwd<F16, 2, 8, false, 256, 2>(a, st);
+    if (NV <= 640) return team_fwd<F16, 4, 5, true, 512, 1>(a, st);
+    if (NV <= 768) return team_fwd<F16, 4, 6, true, 512, 1>(a, st);
+    if (NV <= 896) return team_fwd<F16, 4, 7, true, 512, 1>(a, st);
+    if (NV <= 1024) return team_fwd<F16, 4, 8, true, 512, 1>(a, st);
+    if (NV <= 1280) return team_fwd<F16, 8, 5, true, 512, 1>(a, st);
+    if (NV <= 1536) return team_fwd<F16, 8, 6, true, 512, 1>(a, st);
+    if (NV <= 1792) return team_fwd<F16, 8, 7, true, 512, 1>(a, st);
+    return team_fwd<F16, 8, 8, true, 512, 1>(a, st);
 }
 
-template <bool F16, int G, int V, int NR, int S, int MINB, bool BIAS>
+template <bool F16, int G, int V, int NR, int S, int MINB, bool HOLD, bool BIAS>
 cudaError_t rows_bwd(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
-    const int smem = std::max(S * NR * 2 * V * kLnRowThreads * 16, kLnRowThreads / G * a.D * 4);
-    const auto kern = ln_rows_bwd_kernel<F16, G, V, NR, S, MINB, BIAS>;
+    const int smem = std::max(S * NR * 2 * V * kLnRowThreads * 16 + (HOLD ? a.D * 4 : 0), kLnRowThreads / G * a.D * 4);
+    const auto kern = ln_rows_bwd_kernel<F16, G, V, NR, S, MINB, HOLD, BIAS>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     return launch_kernel(kern, grid, kLnRowThreads, smem, st, a);
 }
 
-template <bool F16, int VPT, int MAXT, int MINB, int R, bool BIAS, bool SW>
-cudaError_t wide_bwd(const LnBwdArgs& a, unsigned grid, size_t ring, cudaStream_t st) {
+// The ring's stages: as many as bring the copies in flight on an SM (all its
+// CTAs') to 88 KB. More measured slower as well as fewer (32768 x 4096, two CTAs
+// with three stages of 16 KB each 95 % of the copy rate, with four 87 %, with two
+// 89 %; 16384 x 8192, one CTA: three of 32 KB 93 %, four 92 %, two 82 %).
+constexpr size_t kLnBwdInFlight = 88 * 1024;
+
+template <bool F16, int VPT, int MAXT, int MINB, bool BIAS, bool SW>
+cudaError_t wide_bwd(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
     const int NV = a.D / 8;
     const int threads = ((NV + VPT - 1) / VPT + 31) / 32 * 32;
-    const size_t stage = static_cast<size_t>(2) * R * a.D * 2;
-    const size_t fixed = 4 * R * (MAXT / 32) * 4 + 8 * static_cast<size_t>(a.chunk) + 16 + (SW ? static_cast<size_t>(a.D) * 4 : 0);
-    const int S = static_cast<int>(std::min<size_t>(std::max<size_t>(ring / stage, 2), 16));
+    const size_t stage = static_cast<size_t>(4) * a.D;
+    const size_t fixed = 4 * warp_places(MAXT) * 4 + 8 * static_cast<size_t>(a.chunk) + 16 + (SW ? static_cast<size_t>(a.D) * 4 : 0);
+    const size_t all = stage * ln_shape(a.D).per_sm;
+    const int S = std::max(2, static_cast<int>((kLnBwdInFlight + all - 1) / all));
     const size_t smem = S * (stage + 8) + fixed;
     if (smem > kLnMaxSmem) return cudaErrorInvalidConfiguration;
-    const auto kern = ln_wide_bwd_kernel<F16, VPT, MAXT, MINB, R, BIAS, SW>;
+    const auto kern = ln_wide_bwd_kernel<F16, VPT, MAXT, MINB, BIAS, SW>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     return launch_kernel(kern, grid, threads, smem, st, a, S);
 }
 
+// Shapes by width, each the fastest measured (ln_shape has their CTAs an SM). Of
+// the copy rate, both passes, 65536 to 8192 rows: D = 768 85 % (a CTA a row: 80),
+// 1024 87, 2048 92, 4096 95, 5000 90, 8192 93, 16384 89. D = 128: 79 % of 30 us.
 template <bool F16, bool BIAS>
 cudaError_t ln_bwd_dispatch(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
     const int NV = a.D / 8;
-    if (NV <= 1) return rows_bwd<F16, 1, LN_B1, BIAS>(a, grid, st);
-    if (NV <= 2) return rows_bwd<F16, 2, LN_B1, BIAS>(a, grid, st);
-    if (NV <= 4) return rows_bwd<F16, 4, LN_B1, BIAS>(a, grid, st);
-    if (NV <= 8) return rows_bwd<F16, 8, LN_B1, BIAS>(a, grid, st);
-    if (NV <= 16) return rows_bwd<F16, 16, LN_B1, BIAS>(a, grid, st);
-    if (NV <= 32) return rows_bwd<F16, 32, LN_B1, BIAS>(a, grid, st);
-    if (NV <= 64) return rows_bwd<F16, 32, LN_B2, BIAS>(a, grid, st);
-    const size_t ring = LN_BW_RING * 1024 / ln_shape(a.D).per_sm;
-    if (NV <= 256) return wide_bwd<F16, LN_BW1, BIAS, false>(a, grid, ring, st);
-    if (NV <= 512) return wide_bwd<F16, LN_BW2, BIAS, false>(a, grid, ring, st);
-    if (NV <= 1024) return wide_bwd<F16, LN_BW4, BIAS, false>(a, grid, ring, st);
-    return wide_bwd<F16, 4, 512, 1, 1, BIAS, true>(a, grid, 128 * 1024, st);
+    if (NV <= 1) return rows_bwd<F16, 1, 1, 1, 4, 2, false, BIAS>(a, grid, st);
+    if (NV <= 2) return rows_bwd<F16, 1, 2, 1, 3, 2, false, BIAS>(a, grid, st);
+    if (NV <= 4) return rows_bwd<F16, 2, 2, 1, 3, 2, false, BIAS>(a, grid, st);
+    if (NV <= 8) return rows_bwd<F16, 4, 2, 1, 3, 2, false, BIAS>(a, grid, st);
+    if (NV <= 12) return rows_bwd<F16, 4, 3, 1, 3, 2, true, BIAS>(a, grid, st);
+    if (NV <= 16) return rows_bwd<F16, 8, 2, 1, 3, 2, false, BIAS>(a, grid, st);
+    if (NV <= 24) return rows_bwd<F16, 8, 3, 1, 3, 2, true, BIAS>(a, grid, st);
+    if (NV <= 32) return rows_bwd<F16, 16, 2, 1, 3, 2, false, BIAS>(a, grid, st);
+    if (NV <= 48) return rows_bwd<F16, 16, 3, 1, 3, 2, true, BIAS>(a, grid, st);
+    if (NV <= 64) return rows_bwd<F16, 32, 2, 1, 3, 2, false, BIAS>(a, grid, st);
+    if (NV <= 96) return rows_bwd<F16, 32, 3, 1, 3, 2, true, BIAS>(a, grid, st);
+    if (NV < kLnCtaRowFrom) return rows_bwd<F16, 32, 4, 1, 3, 2, true, BIAS>(a, grid, st);
+    if (NV <= 256) return wide_bwd<F16, 2, 128, 4, BIAS, false>(a, grid, st);
+    if (NV <= 512) return wide_bwd<F16, 2, 256, 2, BIAS, false>(a, grid, st);
+    if (NV <= 640) return wide_bwd<F16, 2, 320, 2, BIAS, false>(a, grid, st);
+    if (NV <= 768) return wide_bwd<F16, 2, 384, 1, BIAS, false>(a, grid, st);
+    if (NV <= 1024) return wide_bwd<F16, 2, 512, 1, BIAS, false>(a, grid, st);
+    if (NV <= 1536) return wide_bwd<F16, 3, 512, 1, BIAS, true>(a, grid, st);
+    return wide_bwd<F16, 4, 512, 1, BIAS, true>(a, grid, st);
 }
 
 }  // namespace

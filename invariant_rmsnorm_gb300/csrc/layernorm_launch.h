@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace rmsn {
 
 struct LnFwdArgs {
@@ -31,48 +33,8 @@ struct LnBwdArgs {
     float rcp_d;
 };
 
-// Launch shapes of the backward, by D: vectors a lane or thread, ...
-// (group kernels: rows a turn, turns in flight, CTAs an SM)
-#ifndef LN_B1
-#define LN_B1 1, 2, 3, 3
-#endif
-#ifndef LN_B1_CTAS
-#define LN_B1_CTAS 3
-#endif
-#ifndef LN_B2
-#define LN_B2 2, 1, 3, 2
-#endif
-#ifndef LN_B2_CTAS
-#define LN_B2_CTAS 2
-#endif
-// (CTA kernels: threads at most, CTAs an SM for the register bound, rows an iteration; warps an SM)
-#ifndef LN_BW1
-#define LN_BW1 1, 256, 3, 2
-#endif
-#ifndef LN_BW1_WARPS
-#define LN_BW1_WARPS 24
-#endif
-#ifndef LN_BW2
-#define LN_BW2 2, 256, 2, 1
-#endif
-#ifndef LN_BW2_WARPS
-#define LN_BW2_WARPS 16
-#endif
-#ifndef LN_BW2_VPT
-#define LN_BW2_VPT 2
-#endif
-#ifndef LN_BW4
-#define LN_BW4 2, 512, 1, 1
-#endif
-#ifndef LN_BW4_WARPS
-#define LN_BW4_WARPS 16
-#endif
-#ifndef LN_BW4_VPT
-#define LN_BW4_VPT 2
-#endif
-#ifndef LN_BW_RING
-#define LN_BW_RING 144  // KB an SM
-#endif
+// The backward's launch shape, by D alone: it decides the weight gradients' chunks.
+constexpr int64_t kLnCtaRowFrom = 128;  // 16-byte vectors a row from which a CTA takes a row (D >= 1024)
 
 struct LnShape {
     int64_t per_sm;  // CTAs an SM
@@ -81,16 +43,22 @@ struct LnShape {
 
 inline LnShape ln_shape(int64_t D) {
     const int64_t NV = D / 8;
-    if (NV <= 64) {  // a group of lanes a row
-        int64_t G = 1;
-        while (G < 32 && G < NV) G *= 2;
-        return {NV <= 32 ? LN_B1_CTAS : LN_B2_CTAS, 256 / G};
+    if (NV < kLnCtaRowFrom) {
+        // Groups of 256-thread CTAs, two an SM: two vectors a lane, or three where
+        // that halves the lanes (or a warp is not enough for two), else four.
+        auto lanes = [&](int64_t v) {
+            int64_t G = 1;
+            while (G * v < NV) G *= 2;
+            return G;
+        };
+        int64_t G = NV == 1 ? 1 : lanes(2);
+        if (NV > 8 && lanes(3) < G) G = lanes(3);
+        return {2, 256 / std::min<int64_t>(G, 32)};
     }
-    auto ctas = [&](int64_t vpt, int64_t warps) { return warps / (((NV + vpt - 1) / vpt + 31) / 32); };
-    if (NV <= 256) return {ctas(1, LN_BW1_WARPS), 1};
-    if (NV <= 512) return {ctas(LN_BW2_VPT, LN_BW2_WARPS), 1};
-    if (NV <= 1024) return {ctas(LN_BW4_VPT, LN_BW4_WARPS), 1};
-    return {1, 1};
+    // A CTA of two vectors a thread: 16 warps an SM, 20 at 10 warps a row.
+    const int64_t warps = ((NV + 1) / 2 + 31) / 32;
+    if (NV <= 512) return {16 / warps, 1};
+    return {NV <= 640 ? 20 / warps : 1, 1};
 }
 
 cudaError_t launch_ln_fwd(const LnFwdArgs& a, cudaStream_t s);

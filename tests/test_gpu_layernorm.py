@@ -74,8 +74,9 @@ def _check(T, D, seed, dtype=BF16, shift=0.0, zc=False, bias=True, pad=0):
 
 
 # widths on both sides of every launch shape, a row and a few, odd counts
-WIDTHS = [8, 16, 24, 64, 72, 128, 136, 248, 256, 264, 512, 1000, 1024, 2048, 2056, 4096, 4104, 5000, 7168, 8192, 8200,
-          12296, 16384]
+WIDTHS = [8, 16, 24, 32, 40, 64, 72, 96, 104, 128, 136, 192, 200, 256, 264, 384, 392, 512, 520, 768, 776, 1016, 1024,
+          1032, 1280, 1536, 1792, 2048, 2056, 2560, 2568, 3584, 4096, 4104, 5000, 5120, 5128, 6144, 6152, 7168, 8192, 8200,
+          10240, 12288, 12296, 14336, 14344, 16384]
 
 
 @pytest.mark.parametrize("D", WIDTHS)
