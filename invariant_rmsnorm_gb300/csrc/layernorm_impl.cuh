@@ -27,7 +27,7 @@
 
 #include <algorithm>
 
-#include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "layernorm.h"
 #include "layernorm_launch.h"
@@ -48,70 +48,6 @@ cudaError_t read_ln_error_word(unsigned* flags, bool clear) {
         e = cudaMemcpyToSymbol(g_ln_error, &zero, sizeof(zero));
     }
     return e;
-}
-
-// Pairs of fp32 operations in one instruction, each half rounded as the scalar
-// operation is: half the issue slots. Every product that feeds a sum is an
-// explicit fused multiply-add, so nothing is left for ptxas to contract.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
-// Eight values as four pairs.
-struct Oct { float2 p[4]; };
-
-__device__ __forceinline__ Oct oct_zero() {
-    Oct o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o.p[i] = make_float2(0.0f, 0.0f);
-    return o;
-}
-
-template <bool F16>
-__device__ __forceinline__ Oct oct_unpack(const uint4 v) {
-    float f[8];
-    unpack_act<F16>(v, f);
-    Oct o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o.p[i] = pair(f, 2 * i);
-    return o;
-}
-
-template <bool F16>
-__device__ __forceinline__ uint4 oct_pack(const Oct& o) {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = o.p[i].x;
-        f[2 * i + 1] = o.p[i].y;
-    }
-    return pack_act<F16>(f);
-}
-
-__device__ __forceinline__ Oct oct_of(float4 lo, float4 hi) {
-    Oct o;
-    o.p[0] = make_float2(lo.x, lo.y); o.p[1] = make_float2(lo.z, lo.w);
-    o.p[2] = make_float2(hi.x, hi.y); o.p[3] = make_float2(hi.z, hi.w);
-    return o;
-}
-
-__device__ __forceinline__ Oct load_oct(const float* p) {
-    return oct_of(__ldg(reinterpret_cast<const float4*>(p)), __ldg(reinterpret_cast<const float4*>(p) + 1));
-}
-
-// Effective weights of vector v.
-__device__ __forceinline__ Oct ln_weights(const float* w, int zc, int v) {
-    Oct o = load_oct(w + 8 * v);
-    if (zc) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o.p[i] = fadd2(o.p[i], both(1.0f));
-    }
-    return o;
 }
 
 __device__ __forceinline__ Oct ln_bias(const float* b, int v) { return b != nullptr ? load_oct(b + 8 * v) : oct_zero(); }
@@ -181,18 +117,11 @@ constexpr int kLnRowThreads = 256;
 // its own slots of shared memory (cp.async, past L1) and reads them back itself,
 // so a wait for its own copies is all the synchronisation there is, and data in
 // flight costs no registers. Slot layout [turn][vector][thread]: conflict-free.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // w_eff and b of a row in shared memory as [w low | w high | b low | b high][NV]
 // float4 (the halves of a vector's eight): conflict-free reads.
 __device__ __forceinline__ void stage_weights(float4* wb, const float* w, const float* b, int zc, int NV) {
     for (int v = threadIdx.x; v < NV; v += blockDim.x) {
-        const Oct x = ln_weights(w, zc, v);
+        const Oct x = oct_weights(w, zc, v);
         wb[v] = make_float4(x.p[0].x, x.p[0].y, x.p[1].x, x.p[1].y);
         wb[NV + v] = make_float4(x.p[2].x, x.p[2].y, x.p[3].x, x.p[3].y);
         if (b != nullptr) {
@@ -237,7 +166,7 @@ __global__ void __launch_bounds__(kLnRowThreads, MINB) ln_rows_fwd_kernel(const 
     Oct w1 = oct_zero(), b1 = oct_zero();
     if constexpr (V == 1) {
         if (l < NV) {
-            w1 = ln_weights(a.w, a.zc, l);
+            w1 = oct_weights(a.w, a.zc, l);
             b1 = ln_bias(a.b, l);
         }
     } else {
@@ -355,7 +284,7 @@ __global__ void __launch_bounds__(kLnRowThreads, MINB) ln_rows_bwd_kernel(const 
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         w[k] = aw[k] = ab[k] = oct_zero();
-        if (!HOLD && k * G + l < NV) w[k] = ln_weights(a.w, a.zc, k * G + l);
+        if (!HOLD && k * G + l < NV) w[k] = oct_weights(a.w, a.zc, k * G + l);
     }
     if constexpr (HOLD) {
         stage_weights(wb, a.w, nullptr, a.zc, NV);
@@ -607,7 +536,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         w[j] = aw[j] = ab[j] = oct_zero();
-        if (!SW && j * nt + tid < NV) w[j] = ln_weights(a.w, a.zc, j * nt + tid);
+        if (!SW && j * nt + tid < NV) w[j] = oct_weights(a.w, a.zc, j * nt + tid);
     }
     if constexpr (SW) stage_weights(wb, a.w, nullptr, a.zc, NV);
     __syncthreads();

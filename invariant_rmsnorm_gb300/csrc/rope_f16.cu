@@ -1,0 +1,8 @@
+// Rotary kernels with fp16 activations: the instantiations of rope_impl.cuh.
+#include "rope_impl.cuh"
+
+namespace rmsn {
+
+cudaError_t launch_rope_f16(RopeMode mode, const RopeArgs& a, cudaStream_t s) { return rope_mode<true>(mode, a, s); }
+
+}  // namespace rmsn
