@@ -50,11 +50,13 @@ __device__ __forceinline__ long long position(const RopeArgs& a, int64_t t) {
     return a.pos64 ? static_cast<const long long*>(a.pos)[t] : static_cast<const int*>(a.pos)[t];
 }
 
-// A warp's contiguous range of the turns (t, b): token t, b-th turn of its heads.
-// (A warp's own turns fit an int: 2^31 of them would be 2^35 bytes a warp.)
+// A warp's contiguous range of the turns (t, b): token t, b-th turn of its heads,
+// q's first, then k's (a turn has heads of one of them only, so all that depends on
+// which is the same for the whole warp). (A warp's own turns fit an int: 2^31 of
+// them would be 2^35 bytes a warp.)
 struct Turns {
-    int left, t, b, nb;
-    __device__ __forceinline__ Turns(int64_t T, int nb_, int64_t warp, int64_t warps) : nb(nb_) {
+    int left, t, b, nb, nq;
+    __device__ __forceinline__ Turns(int64_t T, int nb_, int nq_, int64_t warp, int64_t warps) : nb(nb_), nq(nq_) {
         const int64_t all = T * nb, first = all * warp / warps;
         left = static_cast<int>(all * (warp + 1) / warps - first);
         t = static_cast<int>(first / nb);
@@ -67,6 +69,8 @@ struct Turns {
             ++t;
         }
     }
+    __device__ __forceinline__ int tensor() const { return b >= nq; }
+    __device__ __forceinline__ int turn_of_tensor() const { return b >= nq ? b - nq : b; }
 };
 
 __device__ __forceinline__ float lanes_sum(float v, int G) {  // over aligned groups of G lanes
@@ -97,32 +101,37 @@ __device__ __forceinline__ void turn_halves(Oct& A, Oct& B, const Oct& c, const 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 u = A.p[i], v = B.p[i];
-        A.p[i] = fma2(make_float2(-v.x, -v.y), s.p[i], fmul2(u, c.p[i]));
+        const float2 uc = fmul2(u, c.p[i]);
+        A.p[i] = make_float2(__fmaf_rn(-v.x, s.p[i].x, uc.x), __fmaf_rn(-v.y, s.p[i].y, uc.y));
         B.p[i] = fma2(u, s.p[i], fmul2(v, c.p[i]));
     }
 }
-// A's neighbours turned; pairs from `n` on are not.
+// The first n of A's neighbours turned (n may pass 4).
 __device__ __forceinline__ void turn_neighbours(Oct& A, const float4 c, const float4 s, int n) {
     const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    const Oct was = A;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 u = A.p[i];
-        const float2 o = fma2(make_float2(-u.y, u.x), both(ss[i]), fmul2(u, both(cc[i])));
-        A.p[i] = i < n ? o : u;
+        const float2 u = A.p[i], uc = fmul2(u, both(cc[i]));
+        A.p[i] = make_float2(__fmaf_rn(-u.y, ss[i], uc.x), __fmaf_rn(u.x, ss[i], uc.y));
+    }
+    if (n < 4) {
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+            if (i >= n) A.p[i] = was.p[i];
     }
 }
 
 // ---------------------------------------------------------------------------
 // Units: NU of two vectors a lane
 // ---------------------------------------------------------------------------
-template <int MODE, bool F16, int NU, int S, int MINB>
+template <int MODE, bool INTER, bool F16, int NU, int S, int MINB>
 __global__ void __launch_bounds__(kRopeThreads, MINB) rope_units_kernel(const RopeArgs a, const int lgG) {
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
     constexpr int OPS = BWD ? 2 : 1;
     extern __shared__ __align__(16) unsigned char smem[];
     const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     const int D = a.D, NC = D >> 3, half = a.R >> 1, hp = (half + 7) & ~7;
-    const bool inter = a.layout == ROPE_INTERLEAVED;
     const int G = 1 << lgG, l = lane & (G - 1), head = lane >> lgG, per = 32 >> lgG;
     uint4* ring = reinterpret_cast<uint4*>(smem);                                   // [S][OPS][2 NU][threads]
     float* ring_r = reinterpret_cast<float*>(ring + S * OPS * 2 * NU * nt);         // BWD: [S][threads]
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_units_kernel(const Ro
     unsigned long long* F = reinterpret_cast<unsigned long long*>(reinterpret_cast<float*>(wb + (NORM ? 4 * NC : 0)) + nw * 2 * hp);
 
     // This lane's vectors: unit u = j G + l is a vector and its partner.
-    const int NP = inter ? 0 : half >> 3;               // units of the halves
+    const int NP = INTER ? 0 : half >> 3;               // units of the halves
     const int rest = (NC - 2 * NP + 1) >> 1;            // other units: two vectors `rest` apart
     int c0[NU], c1[NU];
 #pragma unroll
@@ -157,33 +166,32 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_units_kernel(const Ro
     __syncthreads();
 
     auto slot = [&](int s, int op, int k) { return ring + ((s * OPS + op) * 2 * NU + k) * nt + tid; };
-    // Forward: one pass over q's and k's heads. Backward: q, then k, each with its own weight gradient.
+    // Forward: one pass over the turns of q and of k. Backward: q, then k, each with its own weight gradient.
     for (int pass = 0; pass < (BWD ? 2 : 1); ++pass) {
-        const int H = BWD ? a.H[pass] : a.H[0] + a.H[1];
-        if (H == 0) continue;
-        Turns now(a.T, (H + per - 1) / per, static_cast<int64_t>(blockIdx.x) * nw + warp, static_cast<int64_t>(gridDim.x) * nw);
+        const int nq = (a.H[0] + per - 1) >> (5 - lgG), nk = (a.H[1] + per - 1) >> (5 - lgG);
+        const int nb = BWD ? (pass ? nk : nq) : nq + nk;
+        if (nb == 0) continue;
+        Turns now(a.T, nb, BWD && pass ? 0 : nq, static_cast<int64_t>(blockIdx.x) * nw + warp, static_cast<int64_t>(gridDim.x) * nw);
         Turns ahead = now;
         int fs = 0;
         auto fetch = [&]() {
             if (ahead.left > 0) {
-                const int h = ahead.b * per + head;
-                if (h < H) {
-                    const int s = BWD ? pass : h >= a.H[0];
-                    const int hh = BWD || !s ? h : h - a.H[0];
-                    const uint16_t* p = a.in[s].p + static_cast<int64_t>(ahead.t) * a.in[s].token + hh * a.in[s].head;
+                const int s = ahead.tensor(), h = ahead.turn_of_tensor() * per + head;
+                if (h < a.H[s]) {
+                    const uint16_t* p = a.in[s].p + ahead.t * a.in[s].token + h * a.in[s].head;
 #pragma unroll
                     for (int j = 0; j < NU; ++j) {
                         if (c0[j] < NC) cp_async16(slot(fs, 0, 2 * j), p + 8 * c0[j]);
                         if (c1[j] < NC) cp_async16(slot(fs, 0, 2 * j + 1), p + 8 * c1[j]);
                     }
                     if constexpr (BWD) {
-                        const uint16_t* x = a.x[s].p + static_cast<int64_t>(ahead.t) * a.x[s].token + hh * a.x[s].head;
+                        const uint16_t* x = a.x[s].p + ahead.t * a.x[s].token + h * a.x[s].head;
 #pragma unroll
                         for (int j = 0; j < NU; ++j) {
                             if (c0[j] < NC) cp_async16(slot(fs, 1, 2 * j), x + 8 * c0[j]);
                             if (c1[j] < NC) cp_async16(slot(fs, 1, 2 * j + 1), x + 8 * c1[j]);
                         }
-                        cp_async4(ring_r + fs * nt + tid, a.rstd[s] + static_cast<int64_t>(ahead.t) * a.H[s] + hh);
+                        cp_async4(ring_r + fs * nt + tid, a.rstd[s] + static_cast<int64_t>(ahead.t) * a.H[s] + h);
                     }
                 }
                 ahead.next();
@@ -208,10 +216,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_units_kernel(const Ro
                 if (t_angles + 1 < a.T) p_next = position(a, t_angles + 1);
             }
             cp_async_wait<S - 2>();
-            const int h = now.b * per + head;
-            const bool have = h < H;
-            const int s = BWD ? pass : h >= a.H[0];
-            const int hh = BWD || !s ? h : h - a.H[0];
+            const int s = now.tensor(), h = now.turn_of_tensor() * per + head;
+            const bool have = h < a.H[s];
             const float4* ws = wb + 2 * s * NC;
             Oct o[NU][2], x[NU][2];
             uint4 raw[NU][2];
@@ -221,17 +227,12 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_units_kernel(const Ro
                 if (have) r = ring_r[cur * nt + tid];
             }
             auto turn = [&](int j) {
-                if (inter) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = i ? c1[j] : c0[j];
-                        if (4 * c < half && c < NC) {
-                            const float4* q = reinterpret_cast<const float4*>(cs);
-                            turn_neighbours(o[j][i], q[c], q[(hp >> 2) + c], half - 4 * c);
-                        }
-                    }
-                } else if (c0[j] < NP) {
-                    turn_halves(o[j][0], o[j][1], oct_at(cs + 8 * c0[j]), oct_at(cs + hp + 8 * c0[j]));
+                if constexpr (INTER) {
+                    const float4* q = reinterpret_cast<const float4*>(cs);
+                    if (4 * c0[j] < half) turn_neighbours(o[j][0], q[c0[j]], q[(hp >> 2) + c0[j]], half - 4 * c0[j]);
+                    if (4 * c1[j] < half) turn_neighbours(o[j][1], q[c1[j]], q[(hp >> 2) + c1[j]], half - 4 * c1[j]);
+                } else {
+                    if (c0[j] < NP) turn_halves(o[j][0], o[j][1], oct_at(cs + 8 * c0[j]), oct_at(cs + hp + 8 * c0[j]));
                 }
             };
 #pragma unroll
@@ -273,11 +274,11 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_units_kernel(const Ro
                     coef = -fmul(fmul(fmul(fmul(r, r), r), a.rcp_d), sum);
                 } else {
                     r = rsqrtf(fadd(fmul(sum, a.rcp_d), a.eps));
-                    if (have && l == 0) a.rstd[s][static_cast<int64_t>(now.t) * a.H[s] + hh] = r;
+                    if (have && l == 0) a.rstd[s][static_cast<int64_t>(now.t) * a.H[s] + h] = r;
                 }
             }
             if (have) {
-                uint16_t* out = a.out[s].p + static_cast<int64_t>(now.t) * a.out[s].token + hh * a.out[s].head;
+                uint16_t* out = a.out[s].p + now.t * a.out[s].token + h * a.out[s].head;
                 const bool in_place = MODE == kTurn && a.out[s].p == a.in[s].p;
 #pragma unroll
                 for (int j = 0; j < NU; ++j) {
@@ -292,33 +293,37 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_units_kernel(const Ro
                                 st_global_cs(out + 8 * c, oct_pack<F16>(o[j][i]));
                             }
                         }
-                    } else {
-                        if constexpr (NORM) {
+                    } else if constexpr (NORM) {
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int c = i ? c1[j] : c0[j];
-                                if (c < NC) {
-                                    const Oct w = oct_of(ws[c], ws[NC + c]);
+                        for (int i = 0; i < 2; ++i) {
+                            const int c = i ? c1[j] : c0[j];
+                            if (c < NC) {
+                                const Oct w = oct_of(ws[c], ws[NC + c]);
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) o[j][i].p[e] = fmul2(fmul2(o[j][i].p[e], both(r)), w.p[e]);
-                                }
+                                for (int e = 0; e < 4; ++e) o[j][i].p[e] = fmul2(fmul2(o[j][i].p[e], both(r)), w.p[e]);
                             }
                         }
+                        turn(j);
+                        if (c0[j] < NC) st_global_cs(out + 8 * c0[j], oct_pack<F16>(o[j][0]));
+                        if (c1[j] < NC) st_global_cs(out + 8 * c1[j], oct_pack<F16>(o[j][1]));
+                    } else {
                         turn(j);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int c = i ? c1[j] : c0[j];
-                            // Pairs of this vector that are turned (4: all).
-                            const int n = inter ? half - 4 * c : c0[j] < NP ? 4 : 0;
-                            if (c >= NC || (in_place && n <= 0)) continue;
-                            uint4 q = oct_pack<F16>(o[j][i]);
-                            if constexpr (!NORM) {  // the rest of the head keeps its bits
-                                if (n < 1) q.x = raw[j][i].x;
-                                if (n < 2) q.y = raw[j][i].y;
-                                if (n < 3) q.z = raw[j][i].z;
-                                if (n < 4) q.w = raw[j][i].w;
+                            if (c >= NC) continue;
+                            const int n = INTER ? half - 4 * c : c0[j] < NP ? 4 : 0;  // pairs of this vector that are turned
+                            if (n > 0) {
+                                uint4 q = oct_pack<F16>(o[j][i]);
+                                if (INTER && n < 4) {  // the rest of the head keeps its bits
+                                    if (n < 2) q.y = raw[j][i].y;
+                                    if (n < 3) q.z = raw[j][i].z;
+                                    q.w = raw[j][i].w;
+                                }
+                                st_global_cs(out + 8 * c, q);
+                            } else if (!in_place) {
+                                st_global_cs(out + 8 * c, raw[j][i]);
                             }
-                            st_global_cs(out + 8 * c, q);
                         }
                     }
                 }
@@ -390,22 +395,21 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const RopeArgs
     __syncthreads();
 
     for (int pass = 0; pass < (BWD ? 2 : 1); ++pass) {
-        const int H = BWD ? a.H[pass] : a.H[0] + a.H[1];
-        if (H == 0) continue;
-        Turns now(a.T, (H + per - 1) / per, static_cast<int64_t>(blockIdx.x) * nw + warp, static_cast<int64_t>(gridDim.x) * nw);
+        const int nq = (a.H[0] + per - 1) >> (5 - lgG), nk = (a.H[1] + per - 1) >> (5 - lgG);
+        const int nb = BWD ? (pass ? nk : nq) : nq + nk;
+        if (nb == 0) continue;
+        Turns now(a.T, nb, BWD && pass ? 0 : nq, static_cast<int64_t>(blockIdx.x) * nw + warp, static_cast<int64_t>(gridDim.x) * nw);
         Turns ahead = now;
         int fs = 0;
         auto fetch = [&]() {
             if (ahead.left > 0) {
-                const int h = ahead.b * per + head;
-                if (h < H) {
-                    const int s = BWD ? pass : h >= a.H[0];
-                    const int hh = BWD || !s ? h : h - a.H[0];
-                    const uint16_t* p = a.in[s].p + static_cast<int64_t>(ahead.t) * a.in[s].token + hh * a.in[s].head;
+                const int s = ahead.tensor(), h = ahead.turn_of_tensor() * per + head;
+                if (h < a.H[s]) {
+                    const uint16_t* p = a.in[s].p + static_cast<int64_t>(ahead.t) * a.in[s].token + h * a.in[s].head;
                     uint16_t* to = rows + fs * OPS * stride;
                     for (int v = l; v < NC; v += G) cp_async16(to + 8 * v, p + 8 * v);
                     if constexpr (BWD) {
-                        const uint16_t* x = a.x[s].p + static_cast<int64_t>(ahead.t) * a.x[s].token + hh * a.x[s].head;
+                        const uint16_t* x = a.x[s].p + static_cast<int64_t>(ahead.t) * a.x[s].token + h * a.x[s].head;
                         for (int v = l; v < NC; v += G) cp_async16(to + stride + 8 * v, x + 8 * v);
                     }
                 }
@@ -428,13 +432,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const RopeArgs
                 token_angles(cs, hp, half, F, p_next, a.scale, BWD || a.back, lane);
                 if (t_angles + 1 < a.T) p_next = position(a, t_angles + 1);
             }
-            const int h = now.b * per + head;
-            const bool have = h < H;
-            const int s = BWD ? pass : h >= a.H[0];
-            const int hh = BWD || !s ? h : h - a.H[0];
+            const int s = now.tensor(), h = now.turn_of_tensor() * per + head;
+            const bool have = h < a.H[s];
             float r = 0.0f, coef = 0.0f, sum = 0.0f;
             if constexpr (BWD) {
-                if (have) r = __ldg(a.rstd[s] + static_cast<int64_t>(now.t) * a.H[s] + hh);
+                if (have) r = __ldg(a.rstd[s] + static_cast<int64_t>(now.t) * a.H[s] + h);
             }
             cp_async_wait<S - 2>();
             __syncwarp();  // the other lanes' copies too
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const RopeArgs
                     coef = -fmul(fmul(fmul(fmul(r, r), r), a.rcp_d), sum);
                 } else {
                     r = rsqrtf(fadd(fmul(sum, a.rcp_d), a.eps));
-                    if (have && l == 0) a.rstd[s][static_cast<int64_t>(now.t) * a.H[s] + hh] = r;
+                    if (have && l == 0) a.rstd[s][static_cast<int64_t>(now.t) * a.H[s] + h] = r;
                 }
             }
             __syncwarp();  // every lane has its values: the row is overwritten with the results
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const RopeArgs
             }
             __syncwarp();
             if (have) {
-                uint16_t* out = a.out[s].p + static_cast<int64_t>(now.t) * a.out[s].token + hh * a.out[s].head;
+                uint16_t* out = a.out[s].p + static_cast<int64_t>(now.t) * a.out[s].token + h * a.out[s].head;
                 const int n = MODE == kTurn && a.out[s].p == a.in[s].p ? (a.R + 7) >> 3 : NC;  // in place: what is turned
                 for (int v = l; v < n; v += G) st_global_cs(out + 8 * v, reinterpret_cast<const uint4*>(ri)[v]);
             }
@@ -564,10 +566,10 @@ cudaError_t rope_launch_free(Kern kern, const RopeArgs& a, int lgG, int64_t turn
     return launch_kernel(kern, static_cast<unsigned>(grid), threads, static_cast<size_t>(smem), st, a, lgG);
 }
 
-template <int MODE, bool F16, int NU, int S, int MINB>
+template <int MODE, bool INTER, bool F16, int NU, int S, int MINB>
 cudaError_t rope_units(const RopeArgs& a, int lgG, int64_t turns, cudaStream_t st) {
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
-    const auto kern = rope_units_kernel<MODE, F16, NU, S, MINB>;
+    const auto kern = rope_units_kernel<MODE, INTER, F16, NU, S, MINB>;
     const int half = a.R / 2, hp = (half + 7) & ~7;
     const size_t thread = static_cast<size_t>(S) * (BWD ? 2 : 1) * 2 * NU * 16 + (BWD ? S * 4 : 0);
     const size_t fixed = (NORM ? static_cast<size_t>(a.D) * 8 : 0) + static_cast<size_t>(half) * 8;
@@ -603,24 +605,41 @@ cudaError_t rope_pairs(const RopeArgs& a, int lgG, int64_t turns, cudaStream_t s
     }
 }
 
+#ifndef RP_F1
+#define RP_F1 1, 3, 4
+#endif
+#ifndef RP_F2
+#define RP_F2 2, 3, 3
+#endif
+#ifndef RP_F3
+#define RP_F3 3, 3, 2
+#endif
+#ifndef RP_B1
+#define RP_B1 1, 3, 2
+#endif
+
+template <int MODE, bool INTER, bool F16>
+cudaError_t rope_units_of(const RopeArgs& a, cudaStream_t st) {
+    const RopeShape s = rope_shape(a.D, MODE == kNormTurnBwd);
+    const int64_t turns = a.T * (rope_turns_of(a.H[0], s) + rope_turns_of(a.H[1], s));
+    if constexpr (MODE == kNormTurnBwd) {
+        return rope_units<MODE, INTER, F16, RP_B1>(a, s.lgG, turns, st);
+    } else {
+        if (s.NU == 1) return rope_units<MODE, INTER, F16, RP_F1>(a, s.lgG, turns, st);
+        if (s.NU == 2) return rope_units<MODE, INTER, F16, RP_F2>(a, s.lgG, turns, st);
+        return rope_units<MODE, INTER, F16, RP_F3>(a, s.lgG, turns, st);
+    }
+}
+
 template <int MODE, bool F16>
 cudaError_t rope_dispatch(const RopeArgs& a, cudaStream_t st) {
-    const int64_t H = a.H[0] + a.H[1];
-    if (a.layout == ROPE_HALF && a.R % 16 != 0) {
-        int lg = 0;
-        while (lg < 5 && (8 << lg) < a.D) ++lg;  // four slots a lane, eight beyond D = 256
-        const int64_t per = 32 >> lg, turns = a.T * ((H + per - 1) / per);
-        return a.D <= 256 ? rope_pairs<MODE, F16, 4, 3>(a, lg, turns, st) : rope_pairs<MODE, F16, 8, 3>(a, lg, turns, st);
-    }
-    const RopeShape s = rope_shape(a.D, MODE == kNormTurnBwd);
-    const int64_t turns = a.T * rope_turns_of(H, s);
-    if constexpr (MODE == kNormTurnBwd) {
-        return rope_units<MODE, F16, 1, 3, 2>(a, s.lgG, turns, st);
-    } else {
-        if (s.NU == 1) return rope_units<MODE, F16, 1, 3, 4>(a, s.lgG, turns, st);
-        if (s.NU == 2) return rope_units<MODE, F16, 2, 3, 3>(a, s.lgG, turns, st);
-        return rope_units<MODE, F16, 3, 3, 2>(a, s.lgG, turns, st);
-    }
+    if (a.layout == ROPE_INTERLEAVED) return rope_units_of<MODE, true, F16>(a, st);
+    if (a.R % 16 == 0) return rope_units_of<MODE, false, F16>(a, st);
+    int lg = 0;
+    while (lg < 5 && (8 << lg) < a.D) ++lg;  // four slots a lane, eight beyond D = 256
+    const RopeShape s{lg, 0};
+    const int64_t turns = a.T * (rope_turns_of(a.H[0], s) + rope_turns_of(a.H[1], s));
+    return a.D <= 256 ? rope_pairs<MODE, F16, 4, 3>(a, lg, turns, st) : rope_pairs<MODE, F16, 8, 3>(a, lg, turns, st);
 }
 
 template <bool F16>

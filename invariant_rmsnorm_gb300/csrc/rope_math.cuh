@@ -17,14 +17,32 @@ __device__ __forceinline__ unsigned long long rope_turns(double inv_freq) {
     return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
 }
 
-// scale (cos, sin) of position p at the frequency F. The phase, a signed 64-bit
-// number of half turns / 2^63, keeps 24 bits as a float: an error of at most
-// pi 2^-25 in the angle.
+// scale (cos, sin) of position p at the frequency F. Of the phase (64 bits of a
+// turn) the upper 32 are kept, an angle's error below 2^-33 turns; its nearest
+// quarter turn is taken off in integers, and what is left, |y| <= pi / 4, goes
+// through the Taylor series of sine (to y^9, remainder below 2^-29) and cosine
+// (to y^10, below 2^-31) in fp32.
 __device__ __forceinline__ float2 rope_cos_sin(long long p, unsigned long long F, float scale) {
-    const long long phase = static_cast<long long>(static_cast<unsigned long long>(p) * F);
-    float s, c;
-    sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &s, &c);  // 2^-63
-    return make_float2(fmul(c, scale), fmul(s, scale));
+    const uint32_t pl = static_cast<uint32_t>(p), ph = static_cast<uint32_t>(static_cast<unsigned long long>(p) >> 32);
+    const uint32_t fl = static_cast<uint32_t>(F), fh = static_cast<uint32_t>(F >> 32);
+    const uint32_t turn = pl * fh + ph * fl + __umulhi(pl, fl);  // upper half of p F modulo 2^64
+    const uint32_t quarter = (turn + 0x20000000u) >> 30;
+    const float y = fmul(static_cast<float>(static_cast<int>(turn - (quarter << 30))), 1.4629180792671596e-9f);  // 2 pi / 2^32
+    const float z = fmul(y, y);
+    float s = __fmaf_rn(z, 2.7557319223985893e-6f, -1.9841269841269841e-4f);  // 1/9!, -1/7!
+    s = __fmaf_rn(s, z, 8.3333333333333333e-3f);
+    s = __fmaf_rn(s, z, -1.6666666666666667e-1f);
+    s = __fmaf_rn(fmul(s, z), y, y);
+    float c = __fmaf_rn(z, -2.7557319223985891e-7f, 2.4801587301587302e-5f);  // -1/10!, 1/8!
+    c = __fmaf_rn(c, z, -1.3888888888888889e-3f);
+    c = __fmaf_rn(c, z, 4.1666666666666667e-2f);
+    c = __fmaf_rn(c, z, -0.5f);
+    c = __fmaf_rn(c, z, 1.0f);
+    const bool odd = quarter & 1u;
+    float cq = odd ? s : c, sq = odd ? c : s;  // quarter turns: (c, s), (-s, c), (-c, -s), (s, -c)
+    cq = ((quarter + 1u) & 2u) ? -cq : cq;
+    sq = (quarter & 2u) ? -sq : sq;
+    return make_float2(fmul(cq, scale), fmul(sq, scale));
 }
 
 // (u, v) turned by the angle of cs = scale (cos, sin); backward: by minus it.

@@ -393,3 +393,20 @@ def test_on_a_stream_of_its_own():
     rn.rope_fwd(q, k, f, o1, k1, stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(_bits(o0), _bits(o1)) and torch.equal(_bits(k0), _bits(k1))
+
+
+def test_infinity_beside_the_turned_part():
+    """An infinite value whose 16-byte vector also holds turned pairs touches its own place alone: its head's
+    inverse RMS is zero, so the others are zeros, and its own place is NaN."""
+    q, _ = _heads(3, 2, 0, 128, 91)
+    q[1, 0, 7] = float("inf")
+    w, _ = _weights(128, 0, 92, False)
+    for R, inter in ((6, True), (2, True), (6, False)):
+        (_, o, r), _ = _norm_fwd(q, None, w, None, _freq(R), None, inter)
+        assert float(r[1, 0]) == 0.0
+        want = torch.zeros(128, dtype=torch.bool, device=DEV)
+        want[7] = True
+        assert torch.equal(o[1, 0].isnan(), want) and bool((o[1, 0][~want] == 0).all())
+        rest = o.isfinite().all(2)
+        rest[1, 0] = True
+        assert bool(rest.all())
