@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "layernorm_launch.h"
+#include "rope_launch.h"
 
 namespace rmsn {
 
@@ -805,6 +806,8 @@ int rmsnorm_device_error(unsigned int* flags, int clear) {
     if (e == cudaSuccess) e = narrow_f16_read_error(flags, clear != 0);
     if (e == cudaSuccess) e = layernorm_read_error(flags, clear != 0);
     if (e == cudaSuccess) e = layernorm_f16_read_error(flags, clear != 0);
+    if (e == cudaSuccess) e = rope_read_error(flags, clear != 0);
+    if (e == cudaSuccess) e = rope_f16_read_error(flags, clear != 0);
     if (e == cudaSuccess) e = selftest_read_error(flags, clear != 0);
     return cuda_status(e);
 }

@@ -10,12 +10,17 @@
 
 namespace rmsn {
 
+cudaError_t rope_read_error(unsigned* flags, bool clear) { return read_rope_error_word(flags, clear); }
 cudaError_t launch_rope(RopeMode mode, const RopeArgs& a, cudaStream_t s) { return rope_mode<false>(mode, a, s); }
 
 namespace {
 
 int rope_run(RopeMode mode, RopeArgs& a, int flags, cudaStream_t s) {
     a.rcp_d = 1.0f / static_cast<float>(a.D);
+    for (int i = 0; i < 2; ++i) {
+        const bool in_place = mode == kTurn && a.out[i].p == a.in[i].p;
+        a.row_bytes[i] = static_cast<uint32_t>(in_place ? (a.R + 7) / 8 * 16 : a.D * 2);
+    }
     return cuda_status(flags ? launch_rope_f16(mode, a, s) : launch_rope(mode, a, s));
 }
 

@@ -3,6 +3,7 @@
 
 namespace rmsn {
 
+cudaError_t rope_f16_read_error(unsigned* flags, bool clear) { return read_rope_error_word(flags, clear); }
 cudaError_t launch_rope_f16(RopeMode mode, const RopeArgs& a, cudaStream_t s) { return rope_mode<true>(mode, a, s); }
 
 }  // namespace rmsn

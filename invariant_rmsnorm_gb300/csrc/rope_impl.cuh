@@ -11,19 +11,22 @@
 // angles (rope_math.cuh) are computed once a token by the warp that has it, a few
 // percent of its work.
 //
-// A warp takes a turn of 32 / G heads of one token at a time, G lanes a head. The
-// turns of a launch are split among its warps in contiguous ranges, so a warp
-// computes a token's cosines once for all its heads, in its own part of shared
-// memory. Every warp keeps a ring of S turns in flight through asynchronous
-// copies. Warps never wait for one another; dw is summed in registers and
-// joined over the CTA's groups at the end, in group order, one partial row a CTA.
+// A warp takes a turn of up to NR x 32 / G heads of one token at a time, G lanes a
+// head (the smallest power of two that holds its units). The turns of a launch are
+// split among its warps in contiguous ranges, so a warp computes a token's cosines
+// once for all its heads and keeps those of its lanes' pairs in registers. Rows come
+// and go by bulk (TMA) copies between HBM and a ring of S stages in the warp's own
+// shared memory: lanes read their values there, overwrite them with the results,
+// and one lane sends the stage back. Warps never wait for one another; dw is
+// summed in registers and joined over the CTA's groups at the end, in group order,
+// one partial row a CTA.
 //
-// Two kernels, by how pairs lie in 16-byte vectors:
-//   * units: each lane holds whole vectors whose pairs are complete (a vector and
-//     its partner R/2 values on, or a vector of neighbours), copied and read back
-//     by the lane itself. ROPE_HALF with R a multiple of 16, ROPE_INTERLEAVED.
-//   * pairs: any other R of ROPE_HALF. A head is copied vector by vector to
-//     shared memory and read value by value, lane by lane in order.
+// A lane's unit is two times eight values, A and B:
+//   * kHalves (ROPE_HALF, R a multiple of 16): a 16-byte vector of the first half
+//     and the vector of its partners R/2 values on; beyond the turned part two vectors.
+//   * kNeighbours (ROPE_INTERLEAVED): two vectors.
+//   * kHalvesAny (ROPE_HALF, any R): as kHalves, but B (and, beyond the turned part,
+//     A) lies at any even number of bytes and may be cut short by the half's end.
 #pragma once
 
 #include <algorithm>
@@ -36,42 +39,125 @@
 namespace rmsn {
 namespace {
 
-template <bool F16>
-__device__ __forceinline__ float widen(uint16_t v) {
-    return F16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(static_cast<uint32_t>(v) << 16);
-}
-template <bool F16>
-__device__ __forceinline__ uint16_t narrow(float v) {
-    return F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
 __device__ __forceinline__ long long position(const RopeArgs& a, int64_t t) {
     if (a.pos == nullptr) return t;
     return a.pos64 ? static_cast<const long long*>(a.pos)[t] : static_cast<const int*>(a.pos)[t];
 }
 
-// A warp's contiguous range of the turns (t, b): token t, b-th turn of its heads,
-// q's first, then k's (a turn has heads of one of them only, so all that depends on
-// which is the same for the whole warp). (A warp's own turns fit an int: 2^31 of
-// them would be 2^35 bytes a warp.)
-struct Turns {
-    int left, t, b, nb, nq;
-    __device__ __forceinline__ Turns(int64_t T, int nb_, int nq_, int64_t warp, int64_t warps) : nb(nb_), nq(nq_) {
-        const int64_t all = T * nb, first = all * warp / warps;
-        left = static_cast<int>(all * (warp + 1) / warps - first);
-        t = static_cast<int>(first / nb);
-        b = static_cast<int>(first - static_cast<int64_t>(t) * nb);
+// Device error word of the including translation unit.
+__device__ unsigned int g_rope_error;
+
+cudaError_t read_rope_error_word(unsigned* flags, bool clear) {
+    unsigned v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_rope_error, sizeof(v));
+    if (e != cudaSuccess) return e;
+    *flags |= v;
+    if (clear && v) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(g_rope_error, &zero, sizeof(zero));
     }
-    __device__ __forceinline__ void next() {
+    return e;
+}
+
+// A warp's contiguous range of the turns: token t, heads h .. h + step - 1 of
+// tensor s, q's heads first, then k's (a turn has heads of one of them only, so
+// all that depends on which is the same for the whole warp). (A warp's own turns
+// fit an int: 2^31 of them would be 2^35 bytes a warp.)
+struct Turns {
+    int left, t, s, h;
+    __device__ __forceinline__ Turns(int64_t T, int nq, int nk, int step, int64_t warp, int64_t warps) {
+        const int64_t all = T * (nq + nk), first = all * warp / warps;
+        left = static_cast<int>(all * (warp + 1) / warps - first);
+        t = static_cast<int>(first / (nq + nk));
+        const int b = static_cast<int>(first - static_cast<int64_t>(t) * (nq + nk));
+        s = b >= nq;
+        h = (s ? b - nq : b) * step;
+    }
+    // Hq, Hk: the heads that the walk covers (0: none of that tensor).
+    __device__ __forceinline__ void next(int Hq, int Hk, int step) {
         --left;
-        if (++b == nb) {
-            b = 0;
-            ++t;
+        h += step;
+        if (h >= (s ? Hk : Hq)) {
+            h = 0;
+            if (s == 0 && Hk > 0) {
+                s = 1;
+            } else {
+                s = Hq > 0 ? 0 : 1;
+                ++t;
+            }
         }
     }
-    __device__ __forceinline__ int tensor() const { return b >= nq; }
-    __device__ __forceinline__ int turn_of_tensor() const { return b >= nq ? b - nq : b; }
 };
+
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t p) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t p, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t p, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(p), "r"(v) : "memory"); }
+__device__ __forceinline__ void sts16(uint32_t p, uint32_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(p), "h"(static_cast<uint16_t>(v)) : "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ float widen(uint32_t v) {
+    return F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(v))) : __uint_as_float(v << 16);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t narrow(float v) {
+    return F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Sixteen bytes at any even address, through the words that hold them (n <= 8
+// values are wanted; no word without one of them is read).
+__device__ __forceinline__ uint4 lds_window(uint32_t p, int n) {
+    const bool odd = p & 2u;
+    const uint32_t q = p & ~3u;
+    uint32_t w[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = 2 * i < n + (odd ? 1 : 0) ? lds32(q + 4 * i) : 0u;
+    uint4 v;
+    v.x = odd ? __funnelshift_r(w[0], w[1], 16) : w[0];
+    v.y = odd ? __funnelshift_r(w[1], w[2], 16) : w[1];
+    v.z = odd ? __funnelshift_r(w[2], w[3], 16) : w[2];
+    v.w = odd ? __funnelshift_r(w[3], w[4], 16) : w[3];
+    return v;
+}
+// The first n of eight values to any even address.
+__device__ __forceinline__ void sts_window(uint32_t p, uint4 v, int n) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if ((p & 2u) == 0 && n == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sts32(p + 4 * i, w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) sts16(p + 2 * i, i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+    }
+}
+
+// 1-D bulk copy shared -> global, in the thread's current bulk group.
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All but the N newest of the thread's bulk groups have read their shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ float lanes_sum(float v, int G) {  // over aligned groups of G lanes
     for (int o = G >> 1; o > 0; o >>= 1) v = fadd(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -91,11 +177,6 @@ __device__ __forceinline__ void token_angles(float* cs, int hp, int half, const 
     __syncwarp();
 }
 
-__device__ __forceinline__ Oct oct_at(const float* p) {
-    const float4* q = reinterpret_cast<const float4*>(p);
-    return oct_of(q[0], q[1]);
-}
-
 // (A, B) turned, pair by pair: halves.
 __device__ __forceinline__ void turn_halves(Oct& A, Oct& B, const Oct& c, const Oct& s) {
 #pragma unroll
@@ -107,8 +188,8 @@ __device__ __forceinline__ void turn_halves(Oct& A, Oct& B, const Oct& c, const 
     }
 }
 // The first n of A's neighbours turned (n may pass 4).
-__device__ __forceinline__ void turn_neighbours(Oct& A, const float4 c, const float4 s, int n) {
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+__device__ __forceinline__ void turn_neighbours(Oct& A, const float2 (&c)[2], const float2 (&s)[2], int n) {
+    const float cc[4] = {c[0].x, c[0].y, c[1].x, c[1].y}, ss[4] = {s[0].x, s[0].y, s[1].x, s[1].y};
     const Oct was = A;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -117,270 +198,75 @@ __device__ __forceinline__ void turn_neighbours(Oct& A, const float4 c, const fl
     }
     if (n < 4) {
 #pragma unroll
-        for (int i = 1; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
             if (i >= n) A.p[i] = was.p[i];
     }
 }
-
-// ---------------------------------------------------------------------------
-// Units: NU of two vectors a lane
-// ---------------------------------------------------------------------------
-template <int MODE, bool INTER, bool F16, int NU, int S, int MINB>
-__global__ void __launch_bounds__(kRopeThreads, MINB) rope_units_kernel(const RopeArgs a, const int lgG) {
-    constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
-    constexpr int OPS = BWD ? 2 : 1;
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-    const int D = a.D, NC = D >> 3, half = a.R >> 1, hp = (half + 7) & ~7;
-    const int G = 1 << lgG, l = lane & (G - 1), head = lane >> lgG, per = 32 >> lgG;
-    uint4* ring = reinterpret_cast<uint4*>(smem);                                   // [S][OPS][2 NU][threads]
-    float* ring_r = reinterpret_cast<float*>(ring + S * OPS * 2 * NU * nt);         // BWD: [S][threads]
-    float4* wb = reinterpret_cast<float4*>(ring_r + (BWD ? S * nt : 0));            // NORM: [q | k][low | high][NC]
-    float* cs = reinterpret_cast<float*>(wb + (NORM ? 4 * NC : 0)) + warp * 2 * hp;  // [warps][cos | sin][hp]
-    unsigned long long* F = reinterpret_cast<unsigned long long*>(reinterpret_cast<float*>(wb + (NORM ? 4 * NC : 0)) + nw * 2 * hp);
-
-    // This lane's vectors: unit u = j G + l is a vector and its partner.
-    const int NP = INTER ? 0 : half >> 3;               // units of the halves
-    const int rest = (NC - 2 * NP + 1) >> 1;            // other units: two vectors `rest` apart
-    int c0[NU], c1[NU];
+// Values from place n on become zero.
+__device__ __forceinline__ void cut(Oct& A, int n) {
+    if (n < 8) {
 #pragma unroll
-    for (int j = 0; j < NU; ++j) {
-        const int u = (j << lgG) + l;
-        c0[j] = u < NP ? u : u + NP;                     // 2 NP + (u - NP)
-        c1[j] = u < NP ? u + NP : c0[j] + rest;
-        if (u >= NP + rest) c0[j] = NC;                  // none
-        if (c1[j] >= NC) c1[j] = NC;
-    }
-    pdl_wait();
-    for (int i = tid; i < half; i += nt) F[i] = rope_turns(a.inv_freq[i]);
-    if constexpr (NORM) {
-        for (int i = tid; i < 2 * NC; i += nt) {
-            const int s = i >= NC, v = s ? i - NC : i;
-            if (a.H[s] > 0) {
-                const Oct w = oct_weights(a.w[s], a.zc, v);
-                wb[2 * s * NC + v] = make_float4(w.p[0].x, w.p[0].y, w.p[1].x, w.p[1].y);
-                wb[(2 * s + 1) * NC + v] = make_float4(w.p[2].x, w.p[2].y, w.p[3].x, w.p[3].y);
-            }
+        for (int i = 0; i < 4; ++i) {
+            if (2 * i >= n) A.p[i].x = 0.0f;
+            if (2 * i + 1 >= n) A.p[i].y = 0.0f;
         }
     }
-    __syncthreads();
-
-    auto slot = [&](int s, int op, int k) { return ring + ((s * OPS + op) * 2 * NU + k) * nt + tid; };
-    // Forward: one pass over the turns of q and of k. Backward: q, then k, each with its own weight gradient.
-    for (int pass = 0; pass < (BWD ? 2 : 1); ++pass) {
-        const int nq = (a.H[0] + per - 1) >> (5 - lgG), nk = (a.H[1] + per - 1) >> (5 - lgG);
-        const int nb = BWD ? (pass ? nk : nq) : nq + nk;
-        if (nb == 0) continue;
-        Turns now(a.T, nb, BWD && pass ? 0 : nq, static_cast<int64_t>(blockIdx.x) * nw + warp, static_cast<int64_t>(gridDim.x) * nw);
-        Turns ahead = now;
-        int fs = 0;
-        auto fetch = [&]() {
-            if (ahead.left > 0) {
-                const int s = ahead.tensor(), h = ahead.turn_of_tensor() * per + head;
-                if (h < a.H[s]) {
-                    const uint16_t* p = a.in[s].p + ahead.t * a.in[s].token + h * a.in[s].head;
-#pragma unroll
-                    for (int j = 0; j < NU; ++j) {
-                        if (c0[j] < NC) cp_async16(slot(fs, 0, 2 * j), p + 8 * c0[j]);
-                        if (c1[j] < NC) cp_async16(slot(fs, 0, 2 * j + 1), p + 8 * c1[j]);
-                    }
-                    if constexpr (BWD) {
-                        const uint16_t* x = a.x[s].p + ahead.t * a.x[s].token + h * a.x[s].head;
-#pragma unroll
-                        for (int j = 0; j < NU; ++j) {
-                            if (c0[j] < NC) cp_async16(slot(fs, 1, 2 * j), x + 8 * c0[j]);
-                            if (c1[j] < NC) cp_async16(slot(fs, 1, 2 * j + 1), x + 8 * c1[j]);
-                        }
-                        cp_async4(ring_r + fs * nt + tid, a.rstd[s] + static_cast<int64_t>(ahead.t) * a.H[s] + h);
-                    }
-                }
-                ahead.next();
-            }
-            cp_async_commit();
-            fs = fs + 1 == S ? 0 : fs + 1;
-        };
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i) fetch();
-        long long p_next = now.left > 0 ? position(a, now.t) : 0;
-        Oct acc[NU][2];
-        if constexpr (BWD) {
-#pragma unroll
-            for (int j = 0; j < NU; ++j) acc[j][0] = acc[j][1] = oct_zero();
-        }
-        int t_angles = -1;
-        int cur = 0;
-        while (now.left > 0) {
-            if (now.t != t_angles) {
-                t_angles = now.t;
-                token_angles(cs, hp, half, F, p_next, a.scale, BWD || a.back, lane);
-                if (t_angles + 1 < a.T) p_next = position(a, t_angles + 1);
-            }
-            cp_async_wait<S - 2>();
-            const int s = now.tensor(), h = now.turn_of_tensor() * per + head;
-            const bool have = h < a.H[s];
-            const float4* ws = wb + 2 * s * NC;
-            Oct o[NU][2], x[NU][2];
-            uint4 raw[NU][2];
-            float2 sum2 = make_float2(0.0f, 0.0f);
-            float r = 0.0f;
-            if constexpr (BWD) {
-                if (have) r = ring_r[cur * nt + tid];
-            }
-            auto turn = [&](int j) {
-                if constexpr (INTER) {
-                    const float4* q = reinterpret_cast<const float4*>(cs);
-                    if (4 * c0[j] < half) turn_neighbours(o[j][0], q[c0[j]], q[(hp >> 2) + c0[j]], half - 4 * c0[j]);
-                    if (4 * c1[j] < half) turn_neighbours(o[j][1], q[c1[j]], q[(hp >> 2) + c1[j]], half - 4 * c1[j]);
-                } else {
-                    if (c0[j] < NP) turn_halves(o[j][0], o[j][1], oct_at(cs + 8 * c0[j]), oct_at(cs + hp + 8 * c0[j]));
-                }
-            };
-#pragma unroll
-            for (int j = 0; j < NU; ++j) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    raw[j][i] = make_uint4(0, 0, 0, 0);
-                    if (have && (i ? c1[j] : c0[j]) < NC) raw[j][i] = *slot(cur, 0, 2 * j + i);
-                    o[j][i] = oct_unpack<F16>(raw[j][i]);
-                }
-                if constexpr (BWD) {
-                    turn(j);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = i ? c1[j] : c0[j];
-                        if (have && c < NC) {
-                            x[j][i] = oct_unpack<F16>(*slot(cur, 1, 2 * j + i));
-                            const Oct w = oct_of(ws[c], ws[NC + c]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                acc[j][i].p[e] = fma2(o[j][i].p[e], fmul2(x[j][i].p[e], both(r)), acc[j][i].p[e]);
-                                o[j][i].p[e] = fmul2(o[j][i].p[e], w.p[e]);
-                                sum2 = fma2(o[j][i].p[e], x[j][i].p[e], sum2);
-                            }
-                        }
-                    }
-                } else if constexpr (NORM) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sum2 = fma2(o[j][i].p[e], o[j][i].p[e], sum2);
-                }
-            }
-            fetch();
-            float coef = 0.0f;
-            if constexpr (NORM) {
-                const float sum = lanes_sum(fadd(sum2.x, sum2.y), G);
-                if constexpr (BWD) {
-                    coef = -fmul(fmul(fmul(fmul(r, r), r), a.rcp_d), sum);
-                } else {
-                    r = rsqrtf(fadd(fmul(sum, a.rcp_d), a.eps));
-                    if (have && l == 0) a.rstd[s][static_cast<int64_t>(now.t) * a.H[s] + h] = r;
-                }
-            }
-            if (have) {
-                uint16_t* out = a.out[s].p + now.t * a.out[s].token + h * a.out[s].head;
-                const bool in_place = MODE == kTurn && a.out[s].p == a.in[s].p;
-#pragma unroll
-                for (int j = 0; j < NU; ++j) {
-                    if constexpr (BWD) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int c = i ? c1[j] : c0[j];
-                            if (c < NC) {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    o[j][i].p[e] = fma2(o[j][i].p[e], both(r), fmul2(x[j][i].p[e], both(coef)));
-                                st_global_cs(out + 8 * c, oct_pack<F16>(o[j][i]));
-                            }
-                        }
-                    } else if constexpr (NORM) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int c = i ? c1[j] : c0[j];
-                            if (c < NC) {
-                                const Oct w = oct_of(ws[c], ws[NC + c]);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) o[j][i].p[e] = fmul2(fmul2(o[j][i].p[e], both(r)), w.p[e]);
-                            }
-                        }
-                        turn(j);
-                        if (c0[j] < NC) st_global_cs(out + 8 * c0[j], oct_pack<F16>(o[j][0]));
-                        if (c1[j] < NC) st_global_cs(out + 8 * c1[j], oct_pack<F16>(o[j][1]));
-                    } else {
-                        turn(j);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int c = i ? c1[j] : c0[j];
-                            if (c >= NC) continue;
-                            const int n = INTER ? half - 4 * c : c0[j] < NP ? 4 : 0;  // pairs of this vector that are turned
-                            if (n > 0) {
-                                uint4 q = oct_pack<F16>(o[j][i]);
-                                if (INTER && n < 4) {  // the rest of the head keeps its bits
-                                    if (n < 2) q.y = raw[j][i].y;
-                                    if (n < 3) q.z = raw[j][i].z;
-                                    q.w = raw[j][i].w;
-                                }
-                                st_global_cs(out + 8 * c, q);
-                            } else if (!in_place) {
-                                st_global_cs(out + 8 * c, raw[j][i]);
-                            }
-                        }
-                    }
-                }
-            }
-            cur = cur + 1 == S ? 0 : cur + 1;
-            now.next();
-        }
-        cp_async_wait<0>();
-        if constexpr (BWD) {
-            // The groups' sums in group order, through the rings' memory.
-            float* part = reinterpret_cast<float*>(smem);  // [groups][D]
-            const int groups = nt >> lgG;
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < NU; ++j)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int c = i ? c1[j] : c0[j];
-                    if (c < NC) {
-                        float4* q = reinterpret_cast<float4*>(part + (tid >> lgG) * D + 8 * c);
-                        const Oct& v = acc[j][i];
-                        q[0] = make_float4(v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y);
-                        q[1] = make_float4(v.p[2].x, v.p[2].y, v.p[3].x, v.p[3].y);
-                    }
-                }
-            __syncthreads();
-            float* row = a.partials + (static_cast<int64_t>(pass) * gridDim.x + blockIdx.x) * D;
-            for (int col = tid; col < D; col += nt) {
-                float v = part[col];
-                for (int g = 1; g < groups; ++g) v = fadd(v, part[g * D + col]);
-                row[col] = v;
-            }
-            __syncthreads();  // before the next pass fills the rings
-        }
-    }
-    pdl_release();
 }
 
+enum RopeKind : int { kHalves = 0, kNeighbours = 1, kHalvesAny = 2 };
+
 // ---------------------------------------------------------------------------
-// Pairs: G lanes a head; lane l has the slots q = l, l + G, ... of D/2. Slot q is
-// two values: the pair (q, q + R/2) of the rotation, or from R/2 on two neighbours
-// of the rest. NJ slots a lane at most, NV vectors a lane to copy.
+// The kernel
 // ---------------------------------------------------------------------------
-template <int MODE, bool F16, int NJ, int S>
-__global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const RopeArgs a, const int lgG) {
+template <int MODE, int KIND, bool F16, int NR, int S, int MINB>
+__global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs a, const int lgG) {
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
     constexpr int OPS = BWD ? 2 : 1;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(128) unsigned char smem[];
     const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-    const int D = a.D, NC = D >> 3, half = a.R >> 1, hp = (half + 7) & ~7;
-    const int G = 1 << lgG, l = lane & (G - 1), head = lane >> lgG, per = 32 >> lgG;
-    const int groups = nt >> lgG, group = tid >> lgG;
-    uint16_t* rows = reinterpret_cast<uint16_t*>(smem) + group * D;               // [S][OPS][groups][D]
-    const int stride = groups * D;
-    float* wsm = reinterpret_cast<float*>(smem + static_cast<size_t>(S) * OPS * stride * 2);  // NORM: [q | k][D]
-    float* cs = wsm + (NORM ? 2 * D : 0) + warp * 2 * hp;                           // [warps][cos | sin][hp]
-    unsigned long long* F = reinterpret_cast<unsigned long long*>(wsm + (NORM ? 2 * D : 0) + nw * 2 * hp);
+    const int D = a.D, half = a.R >> 1, hp = (half + 7) & ~7;
+    const int l = lane & ((1 << lgG) - 1), head = lane >> lgG, per = 32 >> lgG, step = per * NR;
+    const uint32_t pitch = static_cast<uint32_t>(D) * 2u;
+    const uint32_t op_bytes = static_cast<uint32_t>(step) * pitch, stage_bytes = OPS * op_bytes;
+    // Shared memory: every warp's stages; weights [q | k][D]; every warp's [cos | sin][hp];
+    // BWD: every warp's inverse RMS [S][step]; barriers; frequencies.
+    float* wsm = reinterpret_cast<float*>(smem + static_cast<size_t>(nw) * S * stage_bytes);
+    float* cs = wsm + (NORM ? 2 * D : 0) + warp * 2 * hp;
+    float* rs = wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (BWD ? warp * S * step : 0);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (BWD ? nw * S * step : 0));
+    unsigned long long* F = reinterpret_cast<unsigned long long*>(bars + nw * S);
+    uint64_t* full = bars + warp * S;
+    const uint32_t ring = smem_u32(smem) + warp * S * stage_bytes;
+
+    // This lane's unit: where A and B lie in a row (bytes), how many of their eight
+    // values there are, and of what pairs they are.
+    const int NC = D >> 3;
+    const int NP = KIND == kNeighbours ? 0 : KIND == kHalves ? half >> 3 : (half + 7) >> 3;  // units of the halves
+    const bool turned = l < NP;
+    int atA, atB, nA = 8, nB = 8;
+    if (turned) {
+        atA = 8 * l;
+        atB = half + 8 * l;
+        if constexpr (KIND == kHalvesAny) nA = nB = min(8, half - 8 * l);
+    } else if constexpr (KIND == kHalvesAny) {
+        atA = a.R + 16 * (l - NP);
+        atB = atA + 8;
+        nA = max(0, min(8, D - atA));
+        nB = max(0, min(8, D - atB));
+    } else {
+        const int rest = (NC - 2 * NP + 1) >> 1, c = l + NP;  // 2 NP + (l - NP)
+        atA = 8 * c;
+        atB = 8 * (c + rest);
+        if (l >= NP + rest) nA = 0;
+        if (nA == 0 || c + rest >= NC) nB = 0;
+    }
+    // kHalvesAny: a value beyond the units of 32 lanes, if there is one for this lane.
+    const int atX = KIND == kHalvesAny && NORM ? a.R + 16 * ((1 << lgG) - NP) + l : D;
+    const bool hasX = KIND == kHalvesAny && NORM && atX < D;
+    const uint32_t rowA = head * pitch + 2u * atA, rowB = head * pitch + 2u * atB;
+
+    for (int i = tid; i < nw * S; i += nt) mbar_init(&bars[i], 1);
+    fence_mbar_init();
     pdl_wait();
     for (int i = tid; i < half; i += nt) F[i] = rope_turns(a.inv_freq[i]);
     if constexpr (NORM) {
@@ -394,143 +280,276 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const RopeArgs
     }
     __syncthreads();
 
+    const uint64_t pol = policy_evict_first();
+    auto load = [&](uint32_t at, int n) -> uint4 {
+        if constexpr (KIND == kHalvesAny) return lds_window(at, n);
+        return lds128(at);
+    };
+    auto store = [&](uint32_t at, const Oct& o, int n) {
+        const uint4 v = oct_pack<F16>(o);
+        if constexpr (KIND == kHalvesAny) sts_window(at, v, n);
+        else sts128(at, v);
+    };
+    uint32_t phase = 0;  // of the stage that comes next
+    int cur = 0;
+    // Forward: one pass over the turns of q and of k. Backward: q, then k, each with its own weight gradient.
     for (int pass = 0; pass < (BWD ? 2 : 1); ++pass) {
-        const int nq = (a.H[0] + per - 1) >> (5 - lgG), nk = (a.H[1] + per - 1) >> (5 - lgG);
-        const int nb = BWD ? (pass ? nk : nq) : nq + nk;
-        if (nb == 0) continue;
-        Turns now(a.T, nb, BWD && pass ? 0 : nq, static_cast<int64_t>(blockIdx.x) * nw + warp, static_cast<int64_t>(gridDim.x) * nw);
+        const int Hq = BWD && pass ? 0 : a.H[0], Hk = BWD && !pass ? 0 : a.H[1];
+        const int nq = (Hq + step - 1) / step, nk = (Hk + step - 1) / step;
+        if (nq + nk == 0) continue;
+        Turns now(a.T, nq, nk, step, static_cast<int64_t>(blockIdx.x) * nw + warp, static_cast<int64_t>(gridDim.x) * nw);
         Turns ahead = now;
-        int fs = 0;
+        int fs = cur;
         auto fetch = [&]() {
             if (ahead.left > 0) {
-                const int s = ahead.tensor(), h = ahead.turn_of_tensor() * per + head;
-                if (h < a.H[s]) {
-                    const uint16_t* p = a.in[s].p + static_cast<int64_t>(ahead.t) * a.in[s].token + h * a.in[s].head;
-                    uint16_t* to = rows + fs * OPS * stride;
-                    for (int v = l; v < NC; v += G) cp_async16(to + 8 * v, p + 8 * v);
-                    if constexpr (BWD) {
-                        const uint16_t* x = a.x[s].p + static_cast<int64_t>(ahead.t) * a.x[s].token + h * a.x[s].head;
-                        for (int v = l; v < NC; v += G) cp_async16(to + stride + 8 * v, x + 8 * v);
+                const int s = ahead.s, n = min(step, a.H[s] - ahead.h);
+                const uint32_t to = ring + fs * stage_bytes;
+                if (lane == 0) {
+                    const uint32_t bytes = a.row_bytes[s];
+                    mbar_arrive_expect_tx(&full[fs], static_cast<uint32_t>(n) * OPS * bytes);
+#pragma unroll
+                    for (int op = 0; op < OPS; ++op) {
+                        const HeadsIn& in = op ? a.x[s] : a.in[s];
+                        const uint16_t* p = in.p + ahead.t * in.token + ahead.h * in.head;
+                        // Heads side by side come in one copy.
+                        const bool one = in.head == D && bytes == pitch;
+                        const int copies = one ? 1 : n;
+                        for (int i = 0; i < copies; ++i)
+                            bulk_g2s(smem + (to - smem_u32(smem)) + op * op_bytes + i * pitch, p + i * in.head,
+                                     one ? n * pitch : bytes, &full[fs], pol);
                     }
                 }
-                ahead.next();
+                if constexpr (BWD) {
+                    for (int i = lane; i < n; i += 32)
+                        cp_async4(rs + fs * step + i, a.rstd[s] + static_cast<int64_t>(ahead.t) * a.H[s] + ahead.h + i);
+                }
+                ahead.next(Hq, Hk, step);
             }
-            cp_async_commit();
+            if constexpr (BWD) cp_async_commit();
             fs = fs + 1 == S ? 0 : fs + 1;
         };
 #pragma unroll
         for (int i = 0; i < S - 1; ++i) fetch();
         long long p_next = now.left > 0 ? position(a, now.t) : 0;
-        float acc[NJ][2];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[j][0] = acc[j][1] = 0.0f;
-        int t_angles = -1;
-        int cur = 0;
+        Oct accA = oct_zero(), accB = oct_zero(), wA = oct_zero(), wB = oct_zero();
+        float accX = 0.0f, wX = 0.0f;
+        float2 c[4], sn[4];  // cos and sin of this lane's pairs
+        int t_have = -1, s_have = -1;
         while (now.left > 0) {
-            if (now.t != t_angles) {
-                t_angles = now.t;
+            if (now.t != t_have) {
+                t_have = now.t;
                 token_angles(cs, hp, half, F, p_next, a.scale, BWD || a.back, lane);
-                if (t_angles + 1 < a.T) p_next = position(a, t_angles + 1);
-            }
-            const int s = now.tensor(), h = now.turn_of_tensor() * per + head;
-            const bool have = h < a.H[s];
-            float r = 0.0f, coef = 0.0f, sum = 0.0f;
-            if constexpr (BWD) {
-                if (have) r = __ldg(a.rstd[s] + static_cast<int64_t>(now.t) * a.H[s] + h);
-            }
-            cp_async_wait<S - 2>();
-            __syncwarp();  // the other lanes' copies too
-            uint16_t* ri = rows + cur * OPS * stride;
-            const uint16_t* rx = ri + stride;
-            const float* w = wsm + s * D;
-            float u[NJ][2], x[NJ][2];
+                if (t_have + 1 < a.T) p_next = position(a, t_have + 1);
+                if constexpr (KIND == kNeighbours) {
+                    const float4* q = reinterpret_cast<const float4*>(cs);
+                    const int iA = min(atA >> 3, (hp >> 2) - 1), iB = min(atB >> 3, (hp >> 2) - 1);
+                    const float4 ca = q[iA], cb = q[iB], sa = q[(hp >> 2) + iA], sb = q[(hp >> 2) + iB];
+                    c[0] = make_float2(ca.x, ca.y); c[1] = make_float2(ca.z, ca.w); c[2] = make_float2(cb.x, cb.y); c[3] = make_float2(cb.z, cb.w);
+                    sn[0] = make_float2(sa.x, sa.y); sn[1] = make_float2(sa.z, sa.w); sn[2] = make_float2(sb.x, sb.y); sn[3] = make_float2(sb.z, sb.w);
+                } else if (turned) {
+                    const float2* q = reinterpret_cast<const float2*>(cs + atA);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int q = l + (j << lgG);
-                if (have && 2 * q < D) {
-                    const bool turn = q < half;
-                    const int i0 = turn ? q : 2 * q, i1 = turn ? q + half : 2 * q + 1;
-                    u[j][0] = widen<F16>(ri[i0]);
-                    u[j][1] = widen<F16>(ri[i1]);
-                    if constexpr (BWD) {
-                        x[j][0] = widen<F16>(rx[i0]);
-                        x[j][1] = widen<F16>(rx[i1]);
-                        if (turn) {
-                            const float2 o = rope_turn(u[j][0], u[j][1], make_float2(cs[q], cs[hp + q]));
-                            u[j][0] = o.x;
-                            u[j][1] = o.y;
-                        }
-                        acc[j][0] = __fmaf_rn(u[j][0], fmul(x[j][0], r), acc[j][0]);
-                        acc[j][1] = __fmaf_rn(u[j][1], fmul(x[j][1], r), acc[j][1]);
-                        u[j][0] = fmul(u[j][0], w[i0]);
-                        u[j][1] = fmul(u[j][1], w[i1]);
-                        sum = __fmaf_rn(u[j][0], x[j][0], sum);
-                        sum = __fmaf_rn(u[j][1], x[j][1], sum);
-                    } else if constexpr (NORM) {
-                        sum = __fmaf_rn(u[j][0], u[j][0], sum);
-                        sum = __fmaf_rn(u[j][1], u[j][1], sum);
+                    for (int i = 0; i < 4; ++i) {
+                        c[i] = q[i];
+                        sn[i] = q[(hp >> 1) + i];
                     }
                 }
             }
-            if constexpr (NORM) {
-                sum = lanes_sum(sum, G);
-                if constexpr (BWD) {
-                    coef = -fmul(fmul(fmul(fmul(r, r), r), a.rcp_d), sum);
-                } else {
-                    r = rsqrtf(fadd(fmul(sum, a.rcp_d), a.eps));
-                    if (have && l == 0) a.rstd[s][static_cast<int64_t>(now.t) * a.H[s] + h] = r;
-                }
-            }
-            __syncwarp();  // every lane has its values: the row is overwritten with the results
+            const int s = now.s;
+            if (NORM && s != s_have) {
+                s_have = s;
+                const float* w = wsm + s * D;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int q = l + (j << lgG);
-                if (have && 2 * q < D) {
-                    const bool turn = q < half;
-                    const int i0 = turn ? q : 2 * q, i1 = turn ? q + half : 2 * q + 1;
-                    if constexpr (BWD) {
-                        u[j][0] = __fmaf_rn(u[j][0], r, fmul(x[j][0], coef));
-                        u[j][1] = __fmaf_rn(u[j][1], r, fmul(x[j][1], coef));
+                for (int i = 0; i < 4; ++i) {
+                    if (KIND != kHalvesAny) {
+                        if (nA > 0) wA.p[i] = reinterpret_cast<const float2*>(w + atA)[i];
+                        if (nB > 0) wB.p[i] = reinterpret_cast<const float2*>(w + atB)[i];
                     } else {
-                        if constexpr (NORM) {
-                            u[j][0] = fmul(fmul(u[j][0], r), w[i0]);
-                            u[j][1] = fmul(fmul(u[j][1], r), w[i1]);
-                        }
-                        if (turn) {
-                            const float2 o = rope_turn(u[j][0], u[j][1], make_float2(cs[q], cs[hp + q]));
-                            u[j][0] = o.x;
-                            u[j][1] = o.y;
-                        }
-                    }
-                    if (NORM || turn) {  // the rest of a rotation alone keeps its bits
-                        ri[i0] = narrow<F16>(u[j][0]);
-                        ri[i1] = narrow<F16>(u[j][1]);
+                        wA.p[i] = make_float2(2 * i < nA ? w[atA + 2 * i] : 0.0f, 2 * i + 1 < nA ? w[atA + 2 * i + 1] : 0.0f);
+                        wB.p[i] = make_float2(2 * i < nB ? w[atB + 2 * i] : 0.0f, 2 * i + 1 < nB ? w[atB + 2 * i + 1] : 0.0f);
                     }
                 }
+                if (hasX) wX = w[atX];
             }
+            if constexpr (BWD) cp_async_wait<S - 2>();
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[cur], phase))) {
+                // Give up: wait (bounded) for the copies in flight, and leave the turns.
+                if (lane == 0) {
+                    for (int i = 1, f = cur, ph = phase; i < S; ++i) {
+                        if (++f == S) {
+                            f = 0;
+                            ph ^= 1u;
+                        }
+                        if (i < now.left) (void)mbar_wait(&full[f], ph);
+                    }
+                    atomicOr(&g_rope_error, kErrWaitTimeout);
+                }
+                break;
+            }
+            __syncwarp();  // BWD: the other lanes' inverse RMS
+            const uint32_t st = ring + cur * stage_bytes;
+            const int n = min(step, a.H[s] - now.h);
+            auto turn = [&](Oct& A, Oct& B) {
+                if constexpr (KIND == kNeighbours) {
+                    const int tA = half - (atA >> 1), tB = half - (atB >> 1);  // pairs of A and of B that are turned
+                    const float2 c0[2] = {c[0], c[1]}, c1[2] = {c[2], c[3]}, s0[2] = {sn[0], sn[1]}, s1[2] = {sn[2], sn[3]};
+                    if (tA > 0) turn_neighbours(A, c0, s0, tA);
+                    if (tB > 0) turn_neighbours(B, c1, s1, tB);
+                } else if (turned) {
+                    Oct co, so;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        co.p[i] = c[i];
+                        so.p[i] = sn[i];
+                    }
+                    turn_halves(A, B, co, so);
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                if (i * per >= n) break;  // the same for all lanes
+                const bool have = i * per + head < n;
+                const uint32_t at = st + i * per * pitch;
+                if constexpr (MODE == kTurn) {
+                    // What is not turned stays where it is.
+                    if constexpr (KIND == kNeighbours) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int n_turn = half - ((k ? atB : atA) >> 1);
+                            const uint32_t p = at + (k ? rowB : rowA);
+                            if (have && (k ? nB : nA) > 0 && n_turn > 0) {
+                                const uint4 raw = lds128(p);
+                                Oct A = oct_unpack<F16>(raw);
+                                const float2 ck[2] = {c[2 * k], c[2 * k + 1]}, sk[2] = {sn[2 * k], sn[2 * k + 1]};
+                                turn_neighbours(A, ck, sk, 4);
+                                uint4 v = oct_pack<F16>(A);
+                                if (n_turn < 4) {  // the rest of the vector keeps its bits
+                                    if (n_turn < 2) v.y = raw.y;
+                                    if (n_turn < 3) v.z = raw.z;
+                                    v.w = raw.w;
+                                }
+                                sts128(p, v);
+                            }
+                        }
+                    } else {
+                        Oct A, B;
+                        if (have && turned) {
+                            A = oct_unpack<F16>(load(at + rowA, nA));
+                            B = oct_unpack<F16>(load(at + rowB, nB));
+                        }
+                        if (KIND == kHalvesAny) __syncwarp();  // all are read before any is written
+                        if (have && turned) {
+                            turn(A, B);
+                            store(at + rowA, A, nA);
+                            store(at + rowB, B, nB);
+                        }
+                    }
+                } else {
+                    Oct A = oct_zero(), B = oct_zero(), xA = oct_zero(), xB = oct_zero();
+                    float2 sum2 = make_float2(0.0f, 0.0f);
+                    float r = 0.0f, coef = 0.0f, X = 0.0f, xX = 0.0f, sumX = 0.0f;
+                    const uint32_t pX = at + head * pitch + 2u * atX;
+                    if (have && hasX) X = widen<F16>(lds16(pX));
+                    if (have && nA > 0) A = oct_unpack<F16>(load(at + rowA, nA));
+                    if (have && nB > 0) B = oct_unpack<F16>(load(at + rowB, nB));
+                    if constexpr (KIND == kHalvesAny) {
+                        cut(A, nA);
+                        cut(B, nB);
+                    }
+                    if constexpr (BWD) {
+                        if (have && nA > 0) xA = oct_unpack<F16>(load(at + op_bytes + rowA, nA));
+                        if (have && nB > 0) xB = oct_unpack<F16>(load(at + op_bytes + rowB, nB));
+                        if constexpr (KIND == kHalvesAny) {
+                            cut(xA, nA);
+                            cut(xB, nB);
+                        }
+                        if (have) r = rs[cur * step + i * per + head];
+                        if (have && hasX) {
+                            xX = widen<F16>(lds16(pX + op_bytes));
+                            accX = __fmaf_rn(X, fmul(xX, r), accX);
+                            X = fmul(X, wX);
+                            sumX = fmul(X, xX);
+                        }
+                        turn(A, B);
+                        if constexpr (KIND == kHalvesAny) {  // what the cosines beyond the half's end made of zeros
+                            cut(A, nA);
+                            cut(B, nB);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            accA.p[e] = fma2(A.p[e], fmul2(xA.p[e], both(r)), accA.p[e]);
+                            accB.p[e] = fma2(B.p[e], fmul2(xB.p[e], both(r)), accB.p[e]);
+                            A.p[e] = fmul2(A.p[e], wA.p[e]);
+                            B.p[e] = fmul2(B.p[e], wB.p[e]);
+                            sum2 = fma2(A.p[e], xA.p[e], sum2);
+                            sum2 = fma2(B.p[e], xB.p[e], sum2);
+                        }
+                    } else {
+                        if (KIND == kHalvesAny) sumX = fmul(X, X);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            sum2 = fma2(A.p[e], A.p[e], sum2);
+                            sum2 = fma2(B.p[e], B.p[e], sum2);
+                        }
+                    }
+                    float mine = fadd(sum2.x, sum2.y);
+                    if constexpr (KIND == kHalvesAny) mine = fadd(mine, sumX);
+                    const float sum = lanes_sum(mine, 1 << lgG);  // every lane of the group has read its values
+                    if constexpr (BWD) {
+                        coef = -fmul(fmul(fmul(fmul(r, r), r), a.rcp_d), sum);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            A.p[e] = fma2(A.p[e], both(r), fmul2(xA.p[e], both(coef)));
+                            B.p[e] = fma2(B.p[e], both(r), fmul2(xB.p[e], both(coef)));
+                        }
+                    } else {
+                        r = rsqrtf(fadd(fmul(sum, a.rcp_d), a.eps));
+                        if (have && l == 0) a.rstd[s][static_cast<int64_t>(now.t) * a.H[s] + now.h + i * per + head] = r;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            A.p[e] = fmul2(fmul2(A.p[e], both(r)), wA.p[e]);
+                            B.p[e] = fmul2(fmul2(B.p[e], both(r)), wB.p[e]);
+                        }
+                        turn(A, B);
+                    }
+                    if (have && nA > 0) store(at + rowA, A, nA);
+                    if (have && nB > 0) store(at + rowB, B, nB);
+                    if (have && hasX) sts16(pX, narrow<F16>(BWD ? __fmaf_rn(X, r, fmul(xX, coef)) : fmul(fmul(X, r), wX)));
+                }
+            }
+            fence_proxy_async_smem();  // the results, before the copy that sends them and the one that refills the stage
             __syncwarp();
-            if (have) {
-                uint16_t* out = a.out[s].p + static_cast<int64_t>(now.t) * a.out[s].token + h * a.out[s].head;
-                const int n = MODE == kTurn && a.out[s].p == a.in[s].p ? (a.R + 7) >> 3 : NC;  // in place: what is turned
-                for (int v = l; v < n; v += G) st_global_cs(out + 8 * v, reinterpret_cast<const uint4*>(ri)[v]);
+            if (lane == 0) {
+                const HeadsOut& o = a.out[s];
+                uint16_t* p = o.p + now.t * o.token + now.h * o.head;
+                const uint32_t bytes = a.row_bytes[s];
+                const bool one = o.head == D && bytes == pitch;
+                const int copies = one ? 1 : n;
+                for (int i = 0; i < copies; ++i) bulk_s2g(p + i * o.head, st + i * pitch, one ? n * pitch : bytes);
+                bulk_commit();
+                bulk_wait_read<1>();  // the stage of the turn before is sent: it is filled next
             }
-            __syncwarp();  // before the row's slot is filled again
+            if (++cur == S) {
+                cur = 0;
+                phase ^= 1u;
+            }
+            now.next(Hq, Hk, step);
             fetch();
-            cur = cur + 1 == S ? 0 : cur + 1;
-            now.next();
         }
-        cp_async_wait<0>();
+        if (lane == 0) bulk_wait_all();
         if constexpr (BWD) {
+            cp_async_wait<0>();
+            // The groups' sums in group order, through the stages' memory.
             float* part = reinterpret_cast<float*>(smem);  // [groups][D]
+            const int groups = nt >> lgG, group = tid >> lgG;
+            fence_proxy_async_smem();
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int q = l + (j << lgG);
-                if (2 * q < D) {
-                    part[group * D + (q < half ? q : 2 * q)] = acc[j][0];
-                    part[group * D + (q < half ? q + half : 2 * q + 1)] = acc[j][1];
-                }
+            for (int e = 0; e < 8; ++e) {
+                if (e < nA) part[group * D + atA + e] = e & 1 ? accA.p[e / 2].y : accA.p[e / 2].x;
+                if (e < nB) part[group * D + atB + e] = e & 1 ? accB.p[e / 2].y : accB.p[e / 2].x;
             }
+            if (hasX) part[group * D + atX] = accX;
             __syncthreads();
             float* row = a.partials + (static_cast<int64_t>(pass) * gridDim.x + blockIdx.x) * D;
             for (int col = tid; col < D; col += nt) {
@@ -538,7 +557,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const RopeArgs
                 for (int g = 1; g < groups; ++g) v = fadd(v, part[g * D + col]);
                 row[col] = v;
             }
-            __syncthreads();
+            fence_proxy_async_smem();
+            __syncthreads();  // before the next pass fills the stages
         }
     }
     pdl_release();
@@ -547,99 +567,59 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const RopeArgs
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
+#ifndef RP_T
+#define RP_T 2, 3, 3
+#endif
+#ifndef RP_F
+#define RP_F 2, 3, 3
+#endif
+#ifndef RP_B
+#define RP_B 2, 3, 2
+#endif
 
-// CTAs of a launch whose order of sums does not matter: all that fit, in smaller
-// CTAs where there are few turns of warps, so that they spread over the SMs.
-template <typename Kern>
-cudaError_t rope_launch_free(Kern kern, const RopeArgs& a, int lgG, int64_t turns, size_t smem_thread, size_t smem_warp,
-                             size_t smem_fixed, cudaStream_t st) {
+template <int MODE, int KIND, bool F16, int NR, int S, int MINB>
+cudaError_t rope_run_kernel(const RopeArgs& a, cudaStream_t st) {
+    constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
+    const auto kern = rope_kernel<MODE, KIND, F16, NR, S, MINB>;
+    const int lgG = rope_lanes_log2(a.D, a.R, KIND == kHalvesAny, NORM);
+    const int step = (32 >> lgG) * NR, hp = (a.R / 2 + 7) & ~7;
+    const size_t warp_bytes = static_cast<size_t>(S) * (BWD ? 2 : 1) * step * a.D * 2 + hp * 8 + (BWD ? S * step * 4 : 0) + S * 8;
+    const size_t fixed = (NORM ? static_cast<size_t>(a.D) * 8 : 0) + static_cast<size_t>(a.R / 2) * 8;
+    const int64_t turns = a.T * ((a.H[0] + step - 1) / step + (a.H[1] + step - 1) / step);
     const int64_t sms = sm_count();
+    // Threads: few turns spread over the SMs in smaller CTAs. The backward's CTAs
+    // are a function of the problem (rope_bwd_ctas).
     int threads = kRopeThreads;
-    while (threads > 32 && turns * 32 < sms * threads) threads /= 2;
-    const int smem = static_cast<int>(smem_thread * threads + smem_warp * (threads / 32) + smem_fixed);
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+    if (!BWD)
+        while (threads > 32 && turns * 32 < sms * threads) threads /= 2;
+    size_t smem = warp_bytes * (threads / 32) + fixed;
+    if (BWD) smem = std::max(smem, static_cast<size_t>(threads >> lgG) * a.D * 4);
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    const int occ = ctas_per_sm(reinterpret_cast<const void*>(kern), threads, smem);
-    if (occ < 1) return cudaErrorInvalidConfiguration;
-    const int64_t warps = threads / 32;
-    const int64_t grid = std::min<int64_t>((turns + warps - 1) / warps, sms * occ);
-    return launch_kernel(kern, static_cast<unsigned>(grid), threads, static_cast<size_t>(smem), st, a, lgG);
-}
-
-template <int MODE, bool INTER, bool F16, int NU, int S, int MINB>
-cudaError_t rope_units(const RopeArgs& a, int lgG, int64_t turns, cudaStream_t st) {
-    constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
-    const auto kern = rope_units_kernel<MODE, INTER, F16, NU, S, MINB>;
-    const int half = a.R / 2, hp = (half + 7) & ~7;
-    const size_t thread = static_cast<size_t>(S) * (BWD ? 2 : 1) * 2 * NU * 16 + (BWD ? S * 4 : 0);
-    const size_t fixed = (NORM ? static_cast<size_t>(a.D) * 8 : 0) + static_cast<size_t>(half) * 8;
-    if constexpr (!BWD) {
-        return rope_launch_free(kern, a, lgG, turns, thread, static_cast<size_t>(hp) * 8, fixed, st);
-    } else {
-        const size_t smem = std::max<size_t>(thread * kRopeThreads + static_cast<size_t>(hp) * 8 * (kRopeThreads / 32) + fixed,
-                                             static_cast<size_t>(kRopeThreads >> lgG) * a.D * 4);
-        cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-        const unsigned grid = static_cast<unsigned>(rope_bwd_ctas(a.T, a.H[0], a.H[1], a.D));
-        return launch_kernel(kern, grid, kRopeThreads, smem, st, a, lgG);
+    int64_t grid = rope_bwd_ctas(a.T, a.H[0], a.H[1], a.D);
+    if (!BWD) {
+        const int occ = ctas_per_sm(reinterpret_cast<const void*>(kern), threads, static_cast<int>(smem));
+        if (occ < 1) return cudaErrorInvalidConfiguration;
+        grid = std::min<int64_t>((turns + threads / 32 - 1) / (threads / 32), sms * occ);
     }
-}
-
-template <int MODE, bool F16, int NJ, int S>
-cudaError_t rope_pairs(const RopeArgs& a, int lgG, int64_t turns, cudaStream_t st) {
-    constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
-    const auto kern = rope_pairs_kernel<MODE, F16, NJ, S>;
-    const int half = a.R / 2, hp = (half + 7) & ~7;
-    // a head's row for each group of lanes: bytes a thread, of whole warps
-    const size_t warp_rows = static_cast<size_t>(S) * (BWD ? 2 : 1) * (32 >> lgG) * a.D * 2;
-    const size_t fixed = (NORM ? static_cast<size_t>(a.D) * 8 : 0) + static_cast<size_t>(half) * 8;
-    if constexpr (!BWD) {
-        return rope_launch_free(kern, a, lgG, turns, 0, warp_rows + static_cast<size_t>(hp) * 8, fixed, st);
-    } else {
-        const size_t smem = std::max<size_t>((warp_rows + static_cast<size_t>(hp) * 8) * (kRopeThreads / 32) + fixed,
-                                             static_cast<size_t>(kRopeThreads >> lgG) * a.D * 4);
-        cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-        const unsigned grid = static_cast<unsigned>(rope_bwd_ctas(a.T, a.H[0], a.H[1], a.D));
-        return launch_kernel(kern, grid, kRopeThreads, smem, st, a, lgG);
-    }
-}
-
-#ifndef RP_F1
-#define RP_F1 1, 3, 4
-#endif
-#ifndef RP_F2
-#define RP_F2 2, 3, 3
-#endif
-#ifndef RP_F3
-#define RP_F3 3, 3, 2
-#endif
-#ifndef RP_B1
-#define RP_B1 1, 3, 2
-#endif
-
-template <int MODE, bool INTER, bool F16>
-cudaError_t rope_units_of(const RopeArgs& a, cudaStream_t st) {
-    const RopeShape s = rope_shape(a.D, MODE == kNormTurnBwd);
-    const int64_t turns = a.T * (rope_turns_of(a.H[0], s) + rope_turns_of(a.H[1], s));
-    if constexpr (MODE == kNormTurnBwd) {
-        return rope_units<MODE, INTER, F16, RP_B1>(a, s.lgG, turns, st);
-    } else {
-        if (s.NU == 1) return rope_units<MODE, INTER, F16, RP_F1>(a, s.lgG, turns, st);
-        if (s.NU == 2) return rope_units<MODE, INTER, F16, RP_F2>(a, s.lgG, turns, st);
-        return rope_units<MODE, INTER, F16, RP_F3>(a, s.lgG, turns, st);
-    }
+    return launch_kernel(kern, static_cast<unsigned>(grid), threads, smem, st, a, lgG);
 }
 
 template <int MODE, bool F16>
 cudaError_t rope_dispatch(const RopeArgs& a, cudaStream_t st) {
-    if (a.layout == ROPE_INTERLEAVED) return rope_units_of<MODE, true, F16>(a, st);
-    if (a.R % 16 == 0) return rope_units_of<MODE, false, F16>(a, st);
-    int lg = 0;
-    while (lg < 5 && (8 << lg) < a.D) ++lg;  // four slots a lane, eight beyond D = 256
-    const RopeShape s{lg, 0};
-    const int64_t turns = a.T * (rope_turns_of(a.H[0], s) + rope_turns_of(a.H[1], s));
-    return a.D <= 256 ? rope_pairs<MODE, F16, 4, 3>(a, lg, turns, st) : rope_pairs<MODE, F16, 8, 3>(a, lg, turns, st);
+    if constexpr (MODE == kTurn) {
+        if (a.layout == ROPE_INTERLEAVED) return rope_run_kernel<MODE, kNeighbours, F16, RP_T>(a, st);
+        if (a.R % 16 == 0) return rope_run_kernel<MODE, kHalves, F16, RP_T>(a, st);
+        return rope_run_kernel<MODE, kHalvesAny, F16, RP_T>(a, st);
+    } else if constexpr (MODE == kNormTurn) {
+        if (a.layout == ROPE_INTERLEAVED) return rope_run_kernel<MODE, kNeighbours, F16, RP_F>(a, st);
+        if (a.R % 16 == 0) return rope_run_kernel<MODE, kHalves, F16, RP_F>(a, st);
+        return rope_run_kernel<MODE, kHalvesAny, F16, RP_F>(a, st);
+    } else {
+        if (a.layout == ROPE_INTERLEAVED) return rope_run_kernel<MODE, kNeighbours, F16, RP_B>(a, st);
+        if (a.R % 16 == 0) return rope_run_kernel<MODE, kHalves, F16, RP_B>(a, st);
+        return rope_run_kernel<MODE, kHalvesAny, F16, RP_B>(a, st);
+    }
 }
 
 template <bool F16>

@@ -33,43 +33,36 @@ struct RopeArgs {
     int D, R, layout, pos64, back, zc;
     float scale, eps;
     float rcp_d;         // 1/D rounded to fp32
+    uint32_t row_bytes[2];  // of a head's row to copy: all of it, or in place what is turned
 };
-
-// How heads lie in warps: G lanes a head, NU units of two 16-byte vectors a
-// lane. A function of D alone, so a row's reduction tree is too (with R and the
-// layout, which say which vectors make a unit).
-struct RopeShape { int lgG, NU; };
-
-inline RopeShape rope_shape(int D, bool bwd) {
-    const int U = (D / 8 + 1) / 2;
-    int lg = 0;
-    while ((1 << lg) < U) ++lg;
-    RopeShape s{lg, 1};
-    if (!bwd) {  // more values a lane where that leaves no more lanes idle
-        for (int nu = 2; nu <= 3; ++nu) {
-            int l = 0;
-            while ((nu << l) < U) ++l;
-            if (U > 2 && (nu << l) <= (s.NU << s.lgG)) s = {l, nu};
-        }
-    }
-    return s;
-}
-
-// Warps' turns of a token: 32 / G heads a turn.
-inline int64_t rope_turns_of(int64_t H, const RopeShape& s) { return (H + (32 >> s.lgG) - 1) / (32 >> s.lgG); }
 
 constexpr int kRopeThreads = 256;
 
+// log2 of the lanes a head: the smallest power of two that holds its units of two
+// times eight values. Where R is no multiple of 16 the halves' last unit is cut
+// short and the rest of a head that is normalised has units of its own: one more
+// than a head's 16th at most, and at 32 lanes the few values beyond the last unit
+// are taken one a lane. A function of D, R and the layout alone, so a row's
+// reduction tree is too.
+inline int rope_lanes_log2(int D, int R, bool any_halves, bool norm) {
+    int units = (D / 8 + 1) / 2;
+    if (any_halves && norm) units = std::max(units, (R / 2 + 7) / 8 + (D - R + 15) / 16);
+    int lg = 0;
+    while (lg < 5 && (1 << lg) < units) ++lg;
+    return lg;
+}
+
 // CTAs of the norm backward, each with one partial row of dwq and of dwk: two an
-// SM of a GPU of 152, fewer where there are fewer turns of warps. A function of
-// T, Hq, Hk and D alone.
+// SM of a GPU of 152, fewer where there are few heads. A function of T, Hq, Hk
+// and D alone.
 inline int64_t rope_bwd_ctas(int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
-    const RopeShape s = rope_shape(static_cast<int>(D), true);
-    const int64_t turns = T * std::max(rope_turns_of(Hq, s), rope_turns_of(Hk, s));
-    return std::max<int64_t>(1, std::min<int64_t>(304, (turns + kRopeThreads / 32 - 1) / (kRopeThreads / 32)));
+    const int64_t values = T * std::max(Hq, Hk) * D;  // of a warp's turn: about 1024
+    return std::max<int64_t>(1, std::min<int64_t>(304, (values + 8191) / 8192));
 }
 
 cudaError_t launch_rope(RopeMode mode, const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_rope_f16(RopeMode mode, const RopeArgs& a, cudaStream_t s);
+cudaError_t rope_read_error(unsigned* flags, bool clear);
+cudaError_t rope_f16_read_error(unsigned* flags, bool clear);
 
 }  // namespace rmsn

@@ -63,7 +63,8 @@ def _freq(R, theta=10000.0, **kw):
 # (D, R): whole heads and parts, pairs that fill 16-byte vectors and pairs that do not
 SHAPES = [(8, 2), (8, 8), (16, 16), (24, 24), (64, 64), (64, 32), (72, 72), (80, 32), (96, 24), (96, 96), (128, 128),
           (128, 64), (128, 78), (128, 126), (128, 2), (192, 192), (192, 64), (256, 64), (256, 256), (256, 250),
-          (264, 264), (320, 320), (512, 512), (512, 64), (512, 510), (40, 36)]
+          (264, 264), (320, 320), (512, 512), (512, 64), (512, 510), (512, 2),
+          (512, 34), (496, 490), (40, 36), (160, 160), (128, 36), (128, 44)]
 
 
 @pytest.mark.parametrize("D,R", SHAPES)
