@@ -804,10 +804,10 @@ int rmsnorm_device_error(unsigned int* flags, int clear) {
     if (e == cudaSuccess) e = narrow_read_error(flags, clear != 0);
     if (e == cudaSuccess) e = wide_f16_read_error(flags, clear != 0);
     if (e == cudaSuccess) e = narrow_f16_read_error(flags, clear != 0);
-    if (e == cudaSuccess) e = layernorm_read_error(flags, clear != 0);
-    if (e == cudaSuccess) e = layernorm_f16_read_error(flags, clear != 0);
-    if (e == cudaSuccess) e = rope_read_error(flags, clear != 0);
-    if (e == cudaSuccess) e = rope_f16_read_error(flags, clear != 0);
+    for (auto read : {layernorm_read_error, layernorm_f16_read_error, rope_turn_read_error, rope_turn_f16_read_error,
+                      rope_norm_read_error, rope_norm_f16_read_error, rope_norm_bwd_read_error,
+                      rope_norm_bwd_f16_read_error})
+        if (e == cudaSuccess) e = read(flags, clear != 0);
     if (e == cudaSuccess) e = selftest_read_error(flags, clear != 0);
     return cuda_status(e);
 }

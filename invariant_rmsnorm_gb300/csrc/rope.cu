@@ -1,17 +1,13 @@
 // Rotary positions of q and k, alone and fused with the heads' RMSNorm, forward
-// and backward: the bf16 kernels (the instantiations of rope_impl.cuh) and the
-// C-ABI entry points for both formats.
+// and backward: the C-ABI entry points.
 #include <algorithm>
 #include <cmath>
 
 #include "checks.h"
 #include "reduce_columns.h"
-#include "rope_impl.cuh"
+#include "rope_launch.h"
 
 namespace rmsn {
-
-cudaError_t rope_read_error(unsigned* flags, bool clear) { return read_rope_error_word(flags, clear); }
-cudaError_t launch_rope(RopeMode mode, const RopeArgs& a, cudaStream_t s) { return rope_mode<false>(mode, a, s); }
 
 namespace {
 
@@ -20,8 +16,16 @@ int rope_run(RopeMode mode, RopeArgs& a, int flags, cudaStream_t s) {
     for (int i = 0; i < 2; ++i) {
         const bool in_place = mode == kTurn && a.out[i].p == a.in[i].p;
         a.row_bytes[i] = static_cast<uint32_t>(in_place ? (a.R + 7) / 8 * 16 : a.D * 2);
+        const bool whole = a.row_bytes[i] == static_cast<uint32_t>(a.D) * 2u;
+        a.dense[0][i] = whole && a.in[i].head == a.D;
+        a.dense[1][i] = whole && a.x[i].head == a.D;
+        a.dense[2][i] = whole && a.out[i].head == a.D;
     }
-    return cuda_status(flags ? launch_rope_f16(mode, a, s) : launch_rope(mode, a, s));
+    switch (mode) {
+        case kTurn: return cuda_status(flags ? launch_rope_turn_f16(a, s) : launch_rope_turn(a, s));
+        case kNormTurn: return cuda_status(flags ? launch_rope_norm_f16(a, s) : launch_rope_norm(a, s));
+        default: return cuda_status(flags ? launch_rope_norm_bwd_f16(a, s) : launch_rope_norm_bwd(a, s));
+    }
 }
 
 // ---------------------------------------------------------------------------

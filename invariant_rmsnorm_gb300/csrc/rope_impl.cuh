@@ -159,11 +159,6 @@ template <int N>
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-__device__ __forceinline__ float lanes_sum(float v, int G) {  // over aligned groups of G lanes
-    for (int o = G >> 1; o > 0; o >>= 1) v = fadd(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
-
 // scale (cos, sin) of every pair of a token, by its warp: [cos | sin][hp]
 // floats. Backward: of minus the angle.
 __device__ __forceinline__ void token_angles(float* cs, int hp, int half, const unsigned long long* F, long long p, float scale,
@@ -212,43 +207,48 @@ __device__ __forceinline__ void cut(Oct& A, int n) {
         }
     }
 }
+__device__ __forceinline__ uint4 keep_if(bool k, uint4 v) {
+    return make_uint4(k ? v.x : 0u, k ? v.y : 0u, k ? v.z : 0u, k ? v.w : 0u);
+}
 
 enum RopeKind : int { kHalves = 0, kNeighbours = 1, kHalvesAny = 2 };
 
 // ---------------------------------------------------------------------------
-// The kernel
+// The kernel: 2^LG lanes a head, NR heads a group and turn, RB of them at a time.
+// FULL: every lane has a whole unit (D = 16 x 2^LG, no unit cut short).
 // ---------------------------------------------------------------------------
-template <int MODE, int KIND, bool F16, int NR, int S, int MINB>
-__global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs a, const int lgG) {
-    constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
-    constexpr int OPS = BWD ? 2 : 1;
+template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
+__global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs a) {
+    constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd, ANY = KIND == kHalvesAny;
+    constexpr int OPS = BWD ? 2 : 1, per = 32 >> LG, step = per * NR;
+    static_assert(NR % RB == 0 && !(FULL && ANY), "whole batches; cut units are not full");
     extern __shared__ __align__(128) unsigned char smem[];
     const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-    const int D = a.D, half = a.R >> 1, hp = (half + 7) & ~7;
-    const int l = lane & ((1 << lgG) - 1), head = lane >> lgG, per = 32 >> lgG, step = per * NR;
+    const int D = FULL ? 16 << LG : a.D, half = a.R >> 1, hp = (half + 7) & ~7;
+    const int l = lane & ((1 << LG) - 1), head = lane >> LG;
     const uint32_t pitch = static_cast<uint32_t>(D) * 2u;
-    const uint32_t op_bytes = static_cast<uint32_t>(step) * pitch, stage_bytes = OPS * op_bytes;
+    const uint32_t op_bytes = step * pitch, stage_bytes = OPS * op_bytes;
     // Shared memory: every warp's stages; weights [q | k][D]; every warp's [cos | sin][hp];
-    // BWD: every warp's inverse RMS [S][step]; barriers; frequencies.
+    // every warp's inverse RMS [S][step] (read backward, gathered forward); barriers; frequencies.
     float* wsm = reinterpret_cast<float*>(smem + static_cast<size_t>(nw) * S * stage_bytes);
     float* cs = wsm + (NORM ? 2 * D : 0) + warp * 2 * hp;
-    float* rs = wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (BWD ? warp * S * step : 0);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (BWD ? nw * S * step : 0));
+    float* rs = wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (NORM ? warp * S * step : 0);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (NORM ? nw * S * step : 0));
     unsigned long long* F = reinterpret_cast<unsigned long long*>(bars + nw * S);
     uint64_t* full = bars + warp * S;
     const uint32_t ring = smem_u32(smem) + warp * S * stage_bytes;
 
-    // This lane's unit: where A and B lie in a row (bytes), how many of their eight
-    // values there are, and of what pairs they are.
+    // This lane's unit: where A and B lie in a row (in values), and how many of
+    // their eight values there are.
     const int NC = D >> 3;
-    const int NP = KIND == kNeighbours ? 0 : KIND == kHalves ? half >> 3 : (half + 7) >> 3;  // units of the halves
+    const int NP = KIND == kNeighbours ? 0 : ANY ? (half + 7) >> 3 : half >> 3;  // units of the halves
     const bool turned = l < NP;
     int atA, atB, nA = 8, nB = 8;
     if (turned) {
         atA = 8 * l;
         atB = half + 8 * l;
-        if constexpr (KIND == kHalvesAny) nA = nB = min(8, half - 8 * l);
-    } else if constexpr (KIND == kHalvesAny) {
+        if constexpr (ANY) nA = nB = min(8, half - 8 * l);
+    } else if constexpr (ANY) {
         atA = a.R + 16 * (l - NP);
         atB = atA + 8;
         nA = max(0, min(8, D - atA));
@@ -257,13 +257,22 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         const int rest = (NC - 2 * NP + 1) >> 1, c = l + NP;  // 2 NP + (l - NP)
         atA = 8 * c;
         atB = 8 * (c + rest);
-        if (l >= NP + rest) nA = 0;
-        if (nA == 0 || c + rest >= NC) nB = 0;
+        if constexpr (!FULL) {
+            if (l >= NP + rest) nA = 0;
+            if (nA == 0 || c + rest >= NC) nB = 0;
+        }
     }
+    if constexpr (!FULL) {  // no address of a unit that is not there
+        if (nA == 0) atA = 0;
+        if (nB == 0) atB = 0;
+    }
+    const bool hasA = FULL || nA > 0, hasB = FULL || nB > 0;
     // kHalvesAny: a value beyond the units of 32 lanes, if there is one for this lane.
-    const int atX = KIND == kHalvesAny && NORM ? a.R + 16 * ((1 << lgG) - NP) + l : D;
-    const bool hasX = KIND == kHalvesAny && NORM && atX < D;
-    const uint32_t rowA = head * pitch + 2u * atA, rowB = head * pitch + 2u * atB;
+    const int atX = ANY && NORM ? a.R + 16 * ((1 << LG) - NP) + l : D;
+    const bool hasX = ANY && NORM && atX < D;
+    const uint32_t rowA = head * pitch + 2u * atA, rowB = head * pitch + 2u * atB, rowX = head * pitch + 2u * atX;
+    // kNeighbours: pairs of A and of B that are turned (past 4: all).
+    const int tA = hasA ? half - (atA >> 1) : 0, tB = hasB ? half - (atB >> 1) : 0;
 
     for (int i = tid; i < nw * S; i += nt) mbar_init(&bars[i], 1);
     fence_mbar_init();
@@ -281,14 +290,15 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     __syncthreads();
 
     const uint64_t pol = policy_evict_first();
-    auto load = [&](uint32_t at, int n) -> uint4 {
-        if constexpr (KIND == kHalvesAny) return lds_window(at, n);
-        return lds128(at);
+    auto load = [&](uint32_t at, bool has, int n) -> uint4 {
+        if constexpr (ANY) return lds_window(at, n);
+        else if constexpr (FULL) return lds128(at);
+        else return keep_if(has, lds128(at));
     };
-    auto store = [&](uint32_t at, const Oct& o, int n) {
+    auto store = [&](uint32_t at, bool has, const Oct& o, int n) {
         const uint4 v = oct_pack<F16>(o);
-        if constexpr (KIND == kHalvesAny) sts_window(at, v, n);
-        else sts128(at, v);
+        if constexpr (ANY) sts_window(at, v, n);
+        else if (has) sts128(at, v);
     };
     uint32_t phase = 0;  // of the stage that comes next
     int cur = 0;
@@ -303,25 +313,26 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         auto fetch = [&]() {
             if (ahead.left > 0) {
                 const int s = ahead.s, n = min(step, a.H[s] - ahead.h);
-                const uint32_t to = ring + fs * stage_bytes;
                 if (lane == 0) {
                     const uint32_t bytes = a.row_bytes[s];
+                    unsigned char* to = smem + static_cast<size_t>(warp * S + fs) * stage_bytes;
                     mbar_arrive_expect_tx(&full[fs], static_cast<uint32_t>(n) * OPS * bytes);
 #pragma unroll
                     for (int op = 0; op < OPS; ++op) {
                         const HeadsIn& in = op ? a.x[s] : a.in[s];
                         const uint16_t* p = in.p + ahead.t * in.token + ahead.h * in.head;
-                        // Heads side by side come in one copy.
-                        const bool one = in.head == D && bytes == pitch;
-                        const int copies = one ? 1 : n;
-                        for (int i = 0; i < copies; ++i)
-                            bulk_g2s(smem + (to - smem_u32(smem)) + op * op_bytes + i * pitch, p + i * in.head,
-                                     one ? n * pitch : bytes, &full[fs], pol);
+                        if (a.dense[op][s]) {  // heads side by side come in one copy
+                            bulk_g2s(to + op * op_bytes, p, n * pitch, &full[fs], pol);
+                        } else {
+                            for (int i = 0; i < n; ++i, p += in.head) bulk_g2s(to + op * op_bytes + i * pitch, p, bytes, &full[fs], pol);
+                        }
                     }
                 }
                 if constexpr (BWD) {
-                    for (int i = lane; i < n; i += 32)
-                        cp_async4(rs + fs * step + i, a.rstd[s] + static_cast<int64_t>(ahead.t) * a.H[s] + ahead.h + i);
+                    const float* p = a.rstd[s] + static_cast<int64_t>(ahead.t) * a.H[s] + ahead.h;
+#pragma unroll
+                    for (int i = 0; i < step; i += 32)
+                        if (i + lane < n) cp_async4(rs + fs * step + i + lane, p + i + lane);
                 }
                 ahead.next(Hq, Hk, step);
             }
@@ -333,7 +344,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         long long p_next = now.left > 0 ? position(a, now.t) : 0;
         Oct accA = oct_zero(), accB = oct_zero(), wA = oct_zero(), wB = oct_zero();
         float accX = 0.0f, wX = 0.0f;
-        float2 c[4], sn[4];  // cos and sin of this lane's pairs
+        Oct c = oct_zero(), sn = oct_zero();  // cos and sin of this lane's pairs (kNeighbours: four of A, four of B)
         int t_have = -1, s_have = -1;
         while (now.left > 0) {
             if (now.t != t_have) {
@@ -343,33 +354,30 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                 if constexpr (KIND == kNeighbours) {
                     const float4* q = reinterpret_cast<const float4*>(cs);
                     const int iA = min(atA >> 3, (hp >> 2) - 1), iB = min(atB >> 3, (hp >> 2) - 1);
-                    const float4 ca = q[iA], cb = q[iB], sa = q[(hp >> 2) + iA], sb = q[(hp >> 2) + iB];
-                    c[0] = make_float2(ca.x, ca.y); c[1] = make_float2(ca.z, ca.w); c[2] = make_float2(cb.x, cb.y); c[3] = make_float2(cb.z, cb.w);
-                    sn[0] = make_float2(sa.x, sa.y); sn[1] = make_float2(sa.z, sa.w); sn[2] = make_float2(sb.x, sb.y); sn[3] = make_float2(sb.z, sb.w);
+                    c = oct_of(q[iA], q[iB]);
+                    sn = oct_of(q[(hp >> 2) + iA], q[(hp >> 2) + iB]);
                 } else if (turned) {
-                    const float2* q = reinterpret_cast<const float2*>(cs + atA);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        c[i] = q[i];
-                        sn[i] = q[(hp >> 1) + i];
-                    }
+                    const float4* q = reinterpret_cast<const float4*>(cs + atA);
+                    c = oct_of(q[0], q[1]);
+                    sn = oct_of(q[hp >> 2], q[(hp >> 2) + 1]);
                 }
             }
             const int s = now.s;
             if (NORM && s != s_have) {
                 s_have = s;
                 const float* w = wsm + s * D;
+                if constexpr (!ANY) {
+                    const float4 *p = reinterpret_cast<const float4*>(w + atA), *q = reinterpret_cast<const float4*>(w + atB);
+                    wA = oct_of(p[0], p[1]);
+                    wB = oct_of(q[0], q[1]);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (KIND != kHalvesAny) {
-                        if (nA > 0) wA.p[i] = reinterpret_cast<const float2*>(w + atA)[i];
-                        if (nB > 0) wB.p[i] = reinterpret_cast<const float2*>(w + atB)[i];
-                    } else {
+                    for (int i = 0; i < 4; ++i) {
                         wA.p[i] = make_float2(2 * i < nA ? w[atA + 2 * i] : 0.0f, 2 * i + 1 < nA ? w[atA + 2 * i + 1] : 0.0f);
                         wB.p[i] = make_float2(2 * i < nB ? w[atB + 2 * i] : 0.0f, 2 * i + 1 < nB ? w[atB + 2 * i + 1] : 0.0f);
                     }
+                    if (hasX) wX = w[atX];
                 }
-                if (hasX) wX = w[atX];
             }
             if constexpr (BWD) cp_async_wait<S - 2>();
             if (!__all_sync(0xffffffffu, mbar_wait(&full[cur], phase))) {
@@ -388,133 +396,140 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
             }
             __syncwarp();  // BWD: the other lanes' inverse RMS
             const uint32_t st = ring + cur * stage_bytes;
-            const int n = min(step, a.H[s] - now.h);
+            const int n = min(step, a.H[s] - now.h);  // heads of this turn; what is computed of others is sent nowhere
             auto turn = [&](Oct& A, Oct& B) {
                 if constexpr (KIND == kNeighbours) {
-                    const int tA = half - (atA >> 1), tB = half - (atB >> 1);  // pairs of A and of B that are turned
-                    const float2 c0[2] = {c[0], c[1]}, c1[2] = {c[2], c[3]}, s0[2] = {sn[0], sn[1]}, s1[2] = {sn[2], sn[3]};
+                    const float2 c0[2] = {c.p[0], c.p[1]}, c1[2] = {c.p[2], c.p[3]}, s0[2] = {sn.p[0], sn.p[1]}, s1[2] = {sn.p[2], sn.p[3]};
                     if (tA > 0) turn_neighbours(A, c0, s0, tA);
                     if (tB > 0) turn_neighbours(B, c1, s1, tB);
                 } else if (turned) {
-                    Oct co, so;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        co.p[i] = c[i];
-                        so.p[i] = sn[i];
-                    }
-                    turn_halves(A, B, co, so);
+                    turn_halves(A, B, c, sn);
                 }
             };
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                if (i * per >= n) break;  // the same for all lanes
-                const bool have = i * per + head < n;
-                const uint32_t at = st + i * per * pitch;
-                if constexpr (MODE == kTurn) {
-                    // What is not turned stays where it is.
-                    if constexpr (KIND == kNeighbours) {
+            for (int i0 = 0; i0 < NR; i0 += RB) {
+                if (i0 * per >= n) break;  // the same for all lanes
+                const uint32_t at = st + i0 * per * pitch;
+                uint4 rawA[RB], rawB[RB];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int n_turn = half - ((k ? atB : atA) >> 1);
-                            const uint32_t p = at + (k ? rowB : rowA);
-                            if (have && (k ? nB : nA) > 0 && n_turn > 0) {
-                                const uint4 raw = lds128(p);
-                                Oct A = oct_unpack<F16>(raw);
-                                const float2 ck[2] = {c[2 * k], c[2 * k + 1]}, sk[2] = {sn[2 * k], sn[2 * k + 1]};
-                                turn_neighbours(A, ck, sk, 4);
-                                uint4 v = oct_pack<F16>(A);
-                                if (n_turn < 4) {  // the rest of the vector keeps its bits
-                                    if (n_turn < 2) v.y = raw.y;
-                                    if (n_turn < 3) v.z = raw.z;
+                for (int i = 0; i < RB; ++i) {
+                    const uint32_t p = at + i * per * pitch;
+                    if (NORM || KIND == kNeighbours || turned) {
+                        rawA[i] = load(p + rowA, hasA, nA);
+                        rawB[i] = load(p + rowB, hasB, nB);
+                    }
+                }
+                if constexpr (MODE == kTurn) {
+                    if constexpr (ANY) __syncwarp();  // windows share words: all are read before any is written
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) {
+                        const uint32_t p = at + i * per * pitch;
+                        if constexpr (KIND == kNeighbours) {
+                            // What is not turned stays where it is, or keeps its bits.
+                            Oct A = oct_unpack<F16>(rawA[i]), B = oct_unpack<F16>(rawB[i]);
+                            turn(A, B);
+                            auto put = [&](uint32_t q, const Oct& o, const uint4& raw, int t) {
+                                uint4 v = oct_pack<F16>(o);
+                                if (t < 4) {
+                                    if (t < 2) v.y = raw.y;
+                                    if (t < 3) v.z = raw.z;
                                     v.w = raw.w;
                                 }
-                                sts128(p, v);
-                            }
-                        }
-                    } else {
-                        Oct A, B;
-                        if (have && turned) {
-                            A = oct_unpack<F16>(load(at + rowA, nA));
-                            B = oct_unpack<F16>(load(at + rowB, nB));
-                        }
-                        if (KIND == kHalvesAny) __syncwarp();  // all are read before any is written
-                        if (have && turned) {
+                                if (t > 0) sts128(q, v);
+                            };
+                            put(p + rowA, A, rawA[i], tA);
+                            put(p + rowB, B, rawB[i], tB);
+                        } else if (turned) {
+                            Oct A = oct_unpack<F16>(rawA[i]), B = oct_unpack<F16>(rawB[i]);
                             turn(A, B);
-                            store(at + rowA, A, nA);
-                            store(at + rowB, B, nB);
+                            store(p + rowA, true, A, nA);
+                            store(p + rowB, true, B, nB);
                         }
                     }
                 } else {
-                    Oct A = oct_zero(), B = oct_zero(), xA = oct_zero(), xB = oct_zero();
-                    float2 sum2 = make_float2(0.0f, 0.0f);
-                    float r = 0.0f, coef = 0.0f, X = 0.0f, xX = 0.0f, sumX = 0.0f;
-                    const uint32_t pX = at + head * pitch + 2u * atX;
-                    if (have && hasX) X = widen<F16>(lds16(pX));
-                    if (have && nA > 0) A = oct_unpack<F16>(load(at + rowA, nA));
-                    if (have && nB > 0) B = oct_unpack<F16>(load(at + rowB, nB));
-                    if constexpr (KIND == kHalvesAny) {
-                        cut(A, nA);
-                        cut(B, nB);
+                    Oct A[RB], B[RB], xA[RB], xB[RB];
+                    float sum[RB], r[RB], X[RB], xX[RB];
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) {
+                        const uint32_t p = at + i * per * pitch;
+                        const int row = (i0 + i) * per + head;
+                        float2 sum2 = make_float2(0.0f, 0.0f);
+                        X[i] = xX[i] = r[i] = 0.0f;
+                        if (hasX) X[i] = widen<F16>(lds16(p + rowX));
+                        if constexpr (BWD) {  // a row that is not there adds nothing to the weight gradients
+                            const bool have = row < n;
+                            A[i] = oct_unpack<F16>(keep_if(have, rawA[i]));
+                            B[i] = oct_unpack<F16>(keep_if(have, rawB[i]));
+                            xA[i] = oct_unpack<F16>(keep_if(have, load(p + op_bytes + rowA, hasA, nA)));
+                            xB[i] = oct_unpack<F16>(keep_if(have, load(p + op_bytes + rowB, hasB, nB)));
+                            if (have) r[i] = rs[cur * step + row];
+                            turn(A[i], B[i]);
+                            if constexpr (ANY) {  // cosines beyond the half's end
+                                cut(A[i], nA);
+                                cut(B[i], nB);
+                                cut(xA[i], nA);
+                                cut(xB[i], nB);
+                                if (hasX && have) {
+                                    xX[i] = widen<F16>(lds16(p + op_bytes + rowX));
+                                    accX = __fmaf_rn(X[i], fmul(xX[i], r[i]), accX);
+                                    X[i] = fmul(X[i], wX);
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                accA.p[e] = fma2(A[i].p[e], fmul2(xA[i].p[e], both(r[i])), accA.p[e]);
+                                accB.p[e] = fma2(B[i].p[e], fmul2(xB[i].p[e], both(r[i])), accB.p[e]);
+                                A[i].p[e] = fmul2(A[i].p[e], wA.p[e]);
+                                B[i].p[e] = fmul2(B[i].p[e], wB.p[e]);
+                                sum2 = fma2(A[i].p[e], xA[i].p[e], sum2);
+                                sum2 = fma2(B[i].p[e], xB[i].p[e], sum2);
+                            }
+                            sum[i] = fadd(sum2.x, sum2.y);
+                            if constexpr (ANY) sum[i] = __fmaf_rn(X[i], xX[i], sum[i]);
+                        } else {
+                            A[i] = oct_unpack<F16>(rawA[i]);
+                            B[i] = oct_unpack<F16>(rawB[i]);
+                            if constexpr (ANY) {
+                                cut(A[i], nA);
+                                cut(B[i], nB);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                sum2 = fma2(A[i].p[e], A[i].p[e], sum2);
+                                sum2 = fma2(B[i].p[e], B[i].p[e], sum2);
+                            }
+                            sum[i] = fadd(sum2.x, sum2.y);
+                            if constexpr (ANY) sum[i] = __fmaf_rn(X[i], X[i], sum[i]);
+                        }
                     }
-                    if constexpr (BWD) {
-                        if (have && nA > 0) xA = oct_unpack<F16>(load(at + op_bytes + rowA, nA));
-                        if (have && nB > 0) xB = oct_unpack<F16>(load(at + op_bytes + rowB, nB));
-                        if constexpr (KIND == kHalvesAny) {
-                            cut(xA, nA);
-                            cut(xB, nB);
-                        }
-                        if (have) r = rs[cur * step + i * per + head];
-                        if (have && hasX) {
-                            xX = widen<F16>(lds16(pX + op_bytes));
-                            accX = __fmaf_rn(X, fmul(xX, r), accX);
-                            X = fmul(X, wX);
-                            sumX = fmul(X, xX);
-                        }
-                        turn(A, B);
-                        if constexpr (KIND == kHalvesAny) {  // what the cosines beyond the half's end made of zeros
-                            cut(A, nA);
-                            cut(B, nB);
-                        }
+                    if constexpr (ANY) __syncwarp();  // windows share words: all are read before any is written
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            accA.p[e] = fma2(A.p[e], fmul2(xA.p[e], both(r)), accA.p[e]);
-                            accB.p[e] = fma2(B.p[e], fmul2(xB.p[e], both(r)), accB.p[e]);
-                            A.p[e] = fmul2(A.p[e], wA.p[e]);
-                            B.p[e] = fmul2(B.p[e], wB.p[e]);
-                            sum2 = fma2(A.p[e], xA.p[e], sum2);
-                            sum2 = fma2(B.p[e], xB.p[e], sum2);
-                        }
-                    } else {
-                        if (KIND == kHalvesAny) sumX = fmul(X, X);
+                    for (int i = 0; i < RB; ++i) sum[i] = group_sum<(1 << LG)>(sum[i]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            sum2 = fma2(A.p[e], A.p[e], sum2);
-                            sum2 = fma2(B.p[e], B.p[e], sum2);
+                    for (int i = 0; i < RB; ++i) {
+                        const uint32_t p = at + i * per * pitch;
+                        if constexpr (BWD) {
+                            const float coef = -fmul(fmul(fmul(fmul(r[i], r[i]), r[i]), a.rcp_d), sum[i]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                A[i].p[e] = fma2(A[i].p[e], both(r[i]), fmul2(xA[i].p[e], both(coef)));
+                                B[i].p[e] = fma2(B[i].p[e], both(r[i]), fmul2(xB[i].p[e], both(coef)));
+                            }
+                            if (hasX) sts16(p + rowX, narrow<F16>(__fmaf_rn(X[i], r[i], fmul(xX[i], coef))));
+                        } else {
+                            r[i] = rsqrtf(fadd(fmul(sum[i], a.rcp_d), a.eps));
+                            if (l == 0) rs[cur * step + (i0 + i) * per + head] = r[i];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                A[i].p[e] = fmul2(fmul2(A[i].p[e], both(r[i])), wA.p[e]);
+                                B[i].p[e] = fmul2(fmul2(B[i].p[e], both(r[i])), wB.p[e]);
+                            }
+                            turn(A[i], B[i]);
+                            if (hasX) sts16(p + rowX, narrow<F16>(fmul(fmul(X[i], r[i]), wX)));
                         }
+                        store(p + rowA, hasA, A[i], nA);
+                        store(p + rowB, hasB, B[i], nB);
                     }
-                    float mine = fadd(sum2.x, sum2.y);
-                    if constexpr (KIND == kHalvesAny) mine = fadd(mine, sumX);
-                    const float sum = lanes_sum(mine, 1 << lgG);  // every lane of the group has read its values
-                    if constexpr (BWD) {
-                        coef = -fmul(fmul(fmul(fmul(r, r), r), a.rcp_d), sum);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            A.p[e] = fma2(A.p[e], both(r), fmul2(xA.p[e], both(coef)));
-                            B.p[e] = fma2(B.p[e], both(r), fmul2(xB.p[e], both(coef)));
-                        }
-                    } else {
-                        r = rsqrtf(fadd(fmul(sum, a.rcp_d), a.eps));
-                        if (have && l == 0) a.rstd[s][static_cast<int64_t>(now.t) * a.H[s] + now.h + i * per + head] = r;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            A.p[e] = fmul2(fmul2(A.p[e], both(r)), wA.p[e]);
-                            B.p[e] = fmul2(fmul2(B.p[e], both(r)), wB.p[e]);
-                        }
-                        turn(A, B);
-                    }
-                    if (have && nA > 0) store(at + rowA, A, nA);
-                    if (have && nB > 0) store(at + rowB, B, nB);
-                    if (have && hasX) sts16(pX, narrow<F16>(BWD ? __fmaf_rn(X, r, fmul(xX, coef)) : fmul(fmul(X, r), wX)));
                 }
             }
             fence_proxy_async_smem();  // the results, before the copy that sends them and the one that refills the stage
@@ -522,12 +537,20 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
             if (lane == 0) {
                 const HeadsOut& o = a.out[s];
                 uint16_t* p = o.p + now.t * o.token + now.h * o.head;
-                const uint32_t bytes = a.row_bytes[s];
-                const bool one = o.head == D && bytes == pitch;
-                const int copies = one ? 1 : n;
-                for (int i = 0; i < copies; ++i) bulk_s2g(p + i * o.head, st + i * pitch, one ? n * pitch : bytes);
+                if (a.dense[2][s]) {
+                    bulk_s2g(p, st, n * pitch);
+                } else {
+                    const uint32_t bytes = a.row_bytes[s];
+                    for (int i = 0; i < n; ++i, p += o.head) bulk_s2g(p, st + i * pitch, bytes);
+                }
                 bulk_commit();
                 bulk_wait_read<1>();  // the stage of the turn before is sent: it is filled next
+            }
+            if constexpr (NORM && !BWD) {
+                float* p = a.rstd[s] + static_cast<int64_t>(now.t) * a.H[s] + now.h;
+#pragma unroll
+                for (int i = 0; i < step; i += 32)
+                    if (i + lane < n) p[i + lane] = rs[cur * step + i + lane];
             }
             if (++cur == S) {
                 cur = 0;
@@ -541,7 +564,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
             cp_async_wait<0>();
             // The groups' sums in group order, through the stages' memory.
             float* part = reinterpret_cast<float*>(smem);  // [groups][D]
-            const int groups = nt >> lgG, group = tid >> lgG;
+            const int groups = nt >> LG, group = tid >> LG;
             fence_proxy_async_smem();
             __syncthreads();
 #pragma unroll
@@ -567,23 +590,24 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
+// heads a group and turn, of them at a time, stages, CTAs an SM
 #ifndef RP_T
-#define RP_T 2, 3, 3
+#define RP_T 4, 2, 3, 3
 #endif
 #ifndef RP_F
-#define RP_F 2, 3, 3
+#define RP_F 4, 2, 3, 2
 #endif
 #ifndef RP_B
-#define RP_B 2, 3, 2
+#define RP_B 2, 1, 3, 2
 #endif
 
-template <int MODE, int KIND, bool F16, int NR, int S, int MINB>
+template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
 cudaError_t rope_run_kernel(const RopeArgs& a, cudaStream_t st) {
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
-    const auto kern = rope_kernel<MODE, KIND, F16, NR, S, MINB>;
-    const int lgG = rope_lanes_log2(a.D, a.R, KIND == kHalvesAny, NORM);
-    const int step = (32 >> lgG) * NR, hp = (a.R / 2 + 7) & ~7;
-    const size_t warp_bytes = static_cast<size_t>(S) * (BWD ? 2 : 1) * step * a.D * 2 + hp * 8 + (BWD ? S * step * 4 : 0) + S * 8;
+    constexpr int step = (32 >> LG) * NR;
+    const auto kern = rope_kernel<MODE, KIND, F16, LG, FULL, NR, RB, S, MINB>;
+    const int hp = (a.R / 2 + 7) & ~7;
+    const size_t warp_bytes = static_cast<size_t>(S) * (BWD ? 2 : 1) * step * a.D * 2 + hp * 8 + (NORM ? S * step * 4 : 0) + S * 8;
     const size_t fixed = (NORM ? static_cast<size_t>(a.D) * 8 : 0) + static_cast<size_t>(a.R / 2) * 8;
     const int64_t turns = a.T * ((a.H[0] + step - 1) / step + (a.H[1] + step - 1) / step);
     const int64_t sms = sm_count();
@@ -593,7 +617,7 @@ cudaError_t rope_run_kernel(const RopeArgs& a, cudaStream_t st) {
     if (!BWD)
         while (threads > 32 && turns * 32 < sms * threads) threads /= 2;
     size_t smem = warp_bytes * (threads / 32) + fixed;
-    if (BWD) smem = std::max(smem, static_cast<size_t>(threads >> lgG) * a.D * 4);
+    if (BWD) smem = std::max(smem, static_cast<size_t>(threads >> LG) * a.D * 4);
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     int64_t grid = rope_bwd_ctas(a.T, a.H[0], a.H[1], a.D);
@@ -602,33 +626,38 @@ cudaError_t rope_run_kernel(const RopeArgs& a, cudaStream_t st) {
         if (occ < 1) return cudaErrorInvalidConfiguration;
         grid = std::min<int64_t>((turns + threads / 32 - 1) / (threads / 32), sms * occ);
     }
-    return launch_kernel(kern, static_cast<unsigned>(grid), threads, smem, st, a, lgG);
+    return launch_kernel(kern, static_cast<unsigned>(grid), threads, smem, st, a);
+}
+
+template <int MODE, int KIND, bool F16, int LG, bool FULL>
+cudaError_t rope_shape_of(const RopeArgs& a, cudaStream_t st) {
+    if constexpr (MODE == kTurn) return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_T>(a, st);
+    else if constexpr (MODE == kNormTurn) return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_F>(a, st);
+    else return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_B>(a, st);
+}
+
+template <int MODE, int KIND, bool F16, int LG>
+cudaError_t rope_full(const RopeArgs& a, cudaStream_t st) {
+    if constexpr (KIND != kHalvesAny)
+        if (a.D == 16 << LG) return rope_shape_of<MODE, KIND, F16, LG, true>(a, st);
+    return rope_shape_of<MODE, KIND, F16, LG, false>(a, st);
+}
+
+template <int MODE, int KIND, bool F16>
+cudaError_t rope_lanes(const RopeArgs& a, cudaStream_t st) {
+    switch (rope_lanes_log2(a.D, a.R, KIND == kHalvesAny, MODE != kTurn)) {
+        case 2: return rope_full<MODE, KIND, F16, 2>(a, st);
+        case 3: return rope_full<MODE, KIND, F16, 3>(a, st);
+        case 4: return rope_full<MODE, KIND, F16, 4>(a, st);
+        default: return rope_full<MODE, KIND, F16, 5>(a, st);
+    }
 }
 
 template <int MODE, bool F16>
-cudaError_t rope_dispatch(const RopeArgs& a, cudaStream_t st) {
-    if constexpr (MODE == kTurn) {
-        if (a.layout == ROPE_INTERLEAVED) return rope_run_kernel<MODE, kNeighbours, F16, RP_T>(a, st);
-        if (a.R % 16 == 0) return rope_run_kernel<MODE, kHalves, F16, RP_T>(a, st);
-        return rope_run_kernel<MODE, kHalvesAny, F16, RP_T>(a, st);
-    } else if constexpr (MODE == kNormTurn) {
-        if (a.layout == ROPE_INTERLEAVED) return rope_run_kernel<MODE, kNeighbours, F16, RP_F>(a, st);
-        if (a.R % 16 == 0) return rope_run_kernel<MODE, kHalves, F16, RP_F>(a, st);
-        return rope_run_kernel<MODE, kHalvesAny, F16, RP_F>(a, st);
-    } else {
-        if (a.layout == ROPE_INTERLEAVED) return rope_run_kernel<MODE, kNeighbours, F16, RP_B>(a, st);
-        if (a.R % 16 == 0) return rope_run_kernel<MODE, kHalves, F16, RP_B>(a, st);
-        return rope_run_kernel<MODE, kHalvesAny, F16, RP_B>(a, st);
-    }
-}
-
-template <bool F16>
-cudaError_t rope_mode(RopeMode mode, const RopeArgs& a, cudaStream_t st) {
-    switch (mode) {
-        case kTurn: return rope_dispatch<kTurn, F16>(a, st);
-        case kNormTurn: return rope_dispatch<kNormTurn, F16>(a, st);
-        default: return rope_dispatch<kNormTurnBwd, F16>(a, st);
-    }
+cudaError_t rope_kinds(const RopeArgs& a, cudaStream_t st) {
+    if (a.layout == ROPE_INTERLEAVED) return rope_lanes<MODE, kNeighbours, F16>(a, st);
+    if (a.R % 16 == 0) return rope_lanes<MODE, kHalves, F16>(a, st);
+    return rope_lanes<MODE, kHalvesAny, F16>(a, st);
 }
 
 }  // namespace

@@ -33,6 +33,7 @@ struct RopeArgs {
     int D, R, layout, pos64, back, zc;
     float scale, eps;
     float rcp_d;         // 1/D rounded to fp32
+    bool dense[3][2];    // [in | x | out]: a token's heads lie side by side and are copied whole
     uint32_t row_bytes[2];  // of a head's row to copy: all of it, or in place what is turned
 };
 
@@ -47,7 +48,7 @@ constexpr int kRopeThreads = 256;
 inline int rope_lanes_log2(int D, int R, bool any_halves, bool norm) {
     int units = (D / 8 + 1) / 2;
     if (any_halves && norm) units = std::max(units, (R / 2 + 7) / 8 + (D - R + 15) / 16);
-    int lg = 0;
+    int lg = 2;
     while (lg < 5 && (1 << lg) < units) ++lg;
     return lg;
 }
@@ -60,9 +61,18 @@ inline int64_t rope_bwd_ctas(int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
     return std::max<int64_t>(1, std::min<int64_t>(304, (values + 8191) / 8192));
 }
 
-cudaError_t launch_rope(RopeMode mode, const RopeArgs& a, cudaStream_t s);
-cudaError_t launch_rope_f16(RopeMode mode, const RopeArgs& a, cudaStream_t s);
-cudaError_t rope_read_error(unsigned* flags, bool clear);
-cudaError_t rope_f16_read_error(unsigned* flags, bool clear);
+// The kernels by mode and format, each in a translation unit of its own.
+cudaError_t launch_rope_turn(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_norm(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_norm_bwd(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_turn_f16(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_norm_f16(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_norm_bwd_f16(const RopeArgs& a, cudaStream_t s);
+cudaError_t rope_turn_read_error(unsigned* flags, bool clear);
+cudaError_t rope_norm_read_error(unsigned* flags, bool clear);
+cudaError_t rope_norm_bwd_read_error(unsigned* flags, bool clear);
+cudaError_t rope_turn_f16_read_error(unsigned* flags, bool clear);
+cudaError_t rope_norm_f16_read_error(unsigned* flags, bool clear);
+cudaError_t rope_norm_bwd_f16_read_error(unsigned* flags, bool clear);
 
 }  // namespace rmsn

@@ -1,0 +1,10 @@
+// The head norm fused with rotary positions, backward, fp16 activations: the
+// instantiations of rope_impl.cuh.
+#include "rope_impl.cuh"
+
+namespace rmsn {
+
+cudaError_t rope_norm_bwd_f16_read_error(unsigned* flags, bool clear) { return read_rope_error_word(flags, clear); }
+cudaError_t launch_rope_norm_bwd_f16(const RopeArgs& a, cudaStream_t s) { return rope_kinds<kNormTurnBwd, true>(a, s); }
+
+}  // namespace rmsn
