@@ -27,15 +27,13 @@ reduce_columns_kernel(const float* __restrict__ partials, int64_t n, int D, floa
     const int64_t c0 = w * per, c1 = min(c0 + per, n);
     const float* p = partials + (static_cast<int64_t>(blockIdx.y) * n) * D + col;
     float acc = 0.0f;
-    int64_t c = c0;
-    for (; c + kUnroll <= c1; c += kUnroll) {
+    for (int64_t c = c0; c < c1; c += kUnroll) {  // all of a batch in flight, a place without a chunk adds zero
         float v[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) v[i] = __ldcs(p + (c + i) * D);
+        for (int i = 0; i < kUnroll; ++i) v[i] = c + i < c1 ? __ldcg(p + (c + i) * D) : 0.0f;
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) acc = fadd(acc, v[i]);
     }
-    for (; c < c1; ++c) acc = fadd(acc, __ldcs(p + c * D));
     pdl_release();
     tot[w][k] = acc;
     __syncthreads();

@@ -341,7 +341,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         };
 #pragma unroll
         for (int i = 0; i < S - 1; ++i) fetch();
-        long long p_next = now.left > 0 ? position(a, now.t) : 0;
+        long long p32 = 0;  // lane i: the position of token t32 + i
+        int t32 = -32;
         Oct accA = oct_zero(), accB = oct_zero(), wA = oct_zero(), wB = oct_zero();
         float accX = 0.0f, wX = 0.0f;
         Oct c = oct_zero(), sn = oct_zero();  // cos and sin of this lane's pairs (kNeighbours: four of A, four of B)
@@ -349,8 +350,11 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         while (now.left > 0) {
             if (now.t != t_have) {
                 t_have = now.t;
-                token_angles(cs, hp, half, F, p_next, a.scale, BWD || a.back, lane);
-                if (t_have + 1 < a.T) p_next = position(a, t_have + 1);
+                if (t_have - t32 >= 32) {
+                    t32 = t_have;
+                    if (t32 + lane < a.T) p32 = position(a, t32 + lane);
+                }
+                token_angles(cs, hp, half, F, __shfl_sync(0xffffffffu, p32, t_have - t32), a.scale, BWD || a.back, lane);
                 if constexpr (KIND == kNeighbours) {
                     const float4* q = reinterpret_cast<const float4*>(cs);
                     const int iA = min(atA >> 3, (hp >> 2) - 1), iB = min(atB >> 3, (hp >> 2) - 1);
@@ -397,6 +401,17 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
             __syncwarp();  // BWD: the other lanes' inverse RMS
             const uint32_t st = ring + cur * stage_bytes;
             const int n = min(step, a.H[s] - now.h);  // heads of this turn; what is computed of others is sent nowhere
+            if constexpr (BWD) {  // a head that is not there adds zeros to the weight gradients
+                if (n < step) {
+                    const int last = min(step, (n + per * RB - 1) / (per * RB) * (per * RB));
+                    for (int i = n * (D >> 3) + lane; i < last * (D >> 3); i += 32) {
+                        sts128(st + 16 * i, make_uint4(0, 0, 0, 0));
+                        sts128(st + op_bytes + 16 * i, make_uint4(0, 0, 0, 0));
+                    }
+                    for (int i = n + lane; i < last; i += 32) rs[cur * step + i] = 0.0f;
+                    __syncwarp();
+                }
+            }
             auto turn = [&](Oct& A, Oct& B) {
                 if constexpr (KIND == kNeighbours) {
                     const float2 c0[2] = {c.p[0], c.p[1]}, c1[2] = {c.p[2], c.p[3]}, s0[2] = {sn.p[0], sn.p[1]}, s1[2] = {sn.p[2], sn.p[3]};
@@ -456,20 +471,19 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                         float2 sum2 = make_float2(0.0f, 0.0f);
                         X[i] = xX[i] = r[i] = 0.0f;
                         if (hasX) X[i] = widen<F16>(lds16(p + rowX));
-                        if constexpr (BWD) {  // a row that is not there adds nothing to the weight gradients
-                            const bool have = row < n;
-                            A[i] = oct_unpack<F16>(keep_if(have, rawA[i]));
-                            B[i] = oct_unpack<F16>(keep_if(have, rawB[i]));
-                            xA[i] = oct_unpack<F16>(keep_if(have, load(p + op_bytes + rowA, hasA, nA)));
-                            xB[i] = oct_unpack<F16>(keep_if(have, load(p + op_bytes + rowB, hasB, nB)));
-                            if (have) r[i] = rs[cur * step + row];
+                        if constexpr (BWD) {
+                            A[i] = oct_unpack<F16>(rawA[i]);
+                            B[i] = oct_unpack<F16>(rawB[i]);
+                            xA[i] = oct_unpack<F16>(load(p + op_bytes + rowA, hasA, nA));
+                            xB[i] = oct_unpack<F16>(load(p + op_bytes + rowB, hasB, nB));
+                            r[i] = rs[cur * step + row];
                             turn(A[i], B[i]);
                             if constexpr (ANY) {  // cosines beyond the half's end
                                 cut(A[i], nA);
                                 cut(B[i], nB);
                                 cut(xA[i], nA);
                                 cut(xB[i], nB);
-                                if (hasX && have) {
+                                if (hasX) {
                                     xX[i] = widen<F16>(lds16(p + op_bytes + rowX));
                                     accX = __fmaf_rn(X[i], fmul(xX[i], r[i]), accX);
                                     X[i] = fmul(X[i], wX);
@@ -592,13 +606,13 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
 // ---------------------------------------------------------------------------
 // heads a group and turn, of them at a time, stages, CTAs an SM
 #ifndef RP_T
-#define RP_T 4, 2, 3, 3
+#define RP_T 4, 2, 2, 3
 #endif
 #ifndef RP_F
 #define RP_F 4, 2, 3, 2
 #endif
 #ifndef RP_B
-#define RP_B 2, 1, 3, 2
+#define RP_B 3, 1, 2, 2
 #endif
 
 template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
