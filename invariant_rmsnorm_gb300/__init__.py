@@ -533,88 +533,108 @@ def rmsnorm_gated_bwd_recompute_ex(g, x, z, w, rstd, dx, dz, dw, y, ws, zero_cen
 # --------------------------------------------------------------------------
 # LayerNorm, rotary positions, and the head RMSNorm fused with them
 # --------------------------------------------------------------------------
-class _On:
-    """Argument checks of one call: every tensor on the device of the first one;
-    ``call`` runs the entry point with that device current."""
+# The calls of this section are short enough on the GPU for their checks to count,
+# so these are plain functions of a tensor and the device's index, the passing case
+# first, and each returns what the entry point takes.
+_F32, _F64 = torch.float32, torch.float64
 
-    __slots__ = ("index", "dtype", "code")
 
-    def __init__(self, x: torch.Tensor, name: str):
-        if not x.is_cuda:
-            raise TypeError(f"{name}: expected a CUDA tensor, got {x.device}")
-        self.index = x.get_device()
-        self.dtype = x.dtype
-        self.code = _dtype_code(x)
+def _index_and_code(x: torch.Tensor, name: str):
+    """The device of a call (its first tensor's) and the activation format's code."""
+    code = DTYPE_CODES.get(x.dtype)
+    if code is None or not x.is_cuda:
+        raise TypeError(f"{name}: expected a bf16 or fp16 CUDA tensor, got {x.dtype} {x.device}")
+    return x.get_device(), code
 
-    def rows(self, t, name: str, T: int, D: int):
-        if t.dtype is not self.dtype or t.get_device() != self.index or t.dim() != 2:
-            raise TypeError(f"{name}: expected a 2-D {self.dtype} tensor on cuda:{self.index}, got {t.dtype} "
-                            f"{t.device} {tuple(t.shape)}")
-        if t.shape != (T, D):
-            raise ValueError(f"{name}: expected shape {(T, D)}, got {tuple(t.shape)}")
-        if D > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name}: columns must be contiguous")
-        return t.data_ptr(), t.stride(0) if T > 1 else max(t.stride(0), D)
 
-    def heads(self, t, name: str, T: int, H: int, D: int):
-        if t is None and H == 0:
+def _rows(t, name: str, shape, dtype, index: int):
+    """Pointer and row stride of an activation matrix."""
+    if t.dtype is dtype and t.get_device() == index and t.shape == shape:
+        ld, one = t.stride()
+        if one == 1 or shape[1] <= 1:
+            return t.data_ptr(), ld if shape[0] > 1 else max(ld, shape[1])
+        raise ValueError(f"{name}: columns must be contiguous")
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 2:
+        raise TypeError(f"{name}: expected a 2-D {dtype} tensor on cuda:{index}, got {t.dtype} {t.device} {tuple(t.shape)}")
+    raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _heads(t, name: str, shape, dtype, index: int):
+    """Pointer, token stride and head stride of [T, heads, D] (None: of no heads)."""
+    if t is None:
+        if shape[1] == 0:
             return None, 0, 0
-        if t is None or t.dtype is not self.dtype or t.get_device() != self.index or t.dim() != 3:
-            raise TypeError(f"{name}: expected a 3-D {self.dtype} tensor on cuda:{self.index}" +
-                            ("" if t is None else f", got {t.dtype} {t.device} {tuple(t.shape)}"))
-        if t.shape != (T, H, D):
-            raise ValueError(f"{name}: expected shape {(T, H, D)}, got {tuple(t.shape)}")
-        if H == 0:
-            return None, 0, 0
+        raise TypeError(f"{name}: expected a tensor of shape {shape}")
+    if t.dtype is dtype and t.get_device() == index and t.shape == shape:
         token, head, one = t.stride()
-        if D > 1 and one != 1:
-            raise ValueError(f"{name}: the values of a head must be contiguous")
-        # a stride that is never taken may be anything
-        return t.data_ptr(), token if T > 1 else 0, head if H > 1 else 0
+        if one == 1 or shape[2] <= 1:
+            # a stride that is never taken may be anything
+            return t.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else 0
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 3:
+        raise TypeError(f"{name}: expected a 3-D {dtype} tensor on cuda:{index}, got {t.dtype} {t.device} {tuple(t.shape)}")
+    raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
 
-    def vec(self, t, name: str, shape, dtype: torch.dtype = torch.float32):
-        if t.dtype is not dtype or t.get_device() != self.index or t.shape != shape or not t.is_contiguous():
-            raise TypeError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                            f"cuda:{self.index}, got {t.dtype} {t.device} {tuple(t.shape)}")
+
+def _vec(t, name: str, shape, index: int, dtype: torch.dtype = _F32):
+    """Pointer of a contiguous tensor of fp32 (or ``dtype``) values."""
+    if t is not None and t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
+    raise TypeError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}" +
+                    ("" if t is None else f", got {t.dtype} {t.device} {tuple(t.shape)}"))
 
-    def vec_of(self, t, name: str, H: int, shape):
-        """The vector of q or k: k has none where it has no heads."""
-        return self.vec(t, name, shape) if H else None
 
-    def bytes(self, t):
-        if t.get_device() != self.index or not t.is_contiguous():
-            raise TypeError(f"ws: expected a contiguous tensor on cuda:{self.index}")
-        return t.data_ptr(), t.numel() * t.element_size()
+def _bytes_of(ws, index: int):
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise TypeError(f"ws: expected a contiguous tensor on cuda:{index}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
-    def positions(self, t, T: int):
-        if t is None:
-            return None, 1
-        if t.dtype is not torch.int64 and t.dtype is not torch.int32:
-            raise TypeError(f"positions: expected int32 or int64, got {t.dtype}")
-        return self.vec(t, "positions", (T,), t.dtype), 1 if t.dtype is torch.int64 else 0
 
-    def call(self, fn: str, stream, *args):
-        f = getattr(_lib or load(), fn)
-        if self.index == torch.cuda.current_device():
-            st = f(*args, _stream(stream, self.index))
-        else:
-            with torch.cuda.device(self.index):
-                st = f(*args, _stream(stream, self.index))
-        if st != 0:
-            raise RmsNormError(fn, st)
+def _positions(t, T: int, index: int):
+    """Pointer and enum rope_pos_dtype (None: 0, 1, 2, ...)."""
+    if t is None:
+        return None, 1
+    if t.dtype is torch.int64:
+        return _vec(t, "positions", (T,), index, torch.int64), 1
+    if t.dtype is torch.int32:
+        return _vec(t, "positions", (T,), index, torch.int32), 0
+    raise TypeError(f"positions: expected int32 or int64, got {t.dtype}")
+
+
+# The current stream's handle and the current device without the objects around
+# them, where torch has these (as of 2.x); the public calls otherwise.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _handle(stream, index: int) -> int:
+    if stream is None:
+        return _raw_stream(index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _call(name: str, index: int, stream, *args):
+    """The entry point ``name`` on ``stream``, with the tensors' device current."""
+    fn = getattr(_lib or load(), name)
+    if _device_now() == index:
+        st = fn(*args, _handle(stream, index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _handle(stream, index))
+    if st != 0:
+        raise RmsNormError(name, st)
 
 
 def layernorm_fwd(x, w, b, y, mean, rstd, eps: float = 1e-5, zero_centered_gamma: bool = False, stream=None):
     """``y = (x - mean) * rstd * w_eff + b`` by rows; writes ``y``, ``mean``, ``rstd``. ``b`` may be None.
     The activation format (bf16 or fp16) is ``x``'s."""
-    on = _On(x, "x")
-    T, D = x.shape
-    xp, ldx = on.rows(x, "x", T, D)
-    yp, ldy = on.rows(y, "y", T, D)
-    on.call("layernorm_fwd", stream, xp, ldx, on.vec(w, "w", (D,)), None if b is None else on.vec(b, "b", (D,)), yp,
-            ldy, on.vec(mean, "mean", (T,)), on.vec(rstd, "rstd", (T,)), T, D, eps, 1 if zero_centered_gamma else 0,
-            on.code)
+    i, code = _index_and_code(x, "x")
+    dt, shape = x.dtype, x.shape
+    T, D = shape
+    xp, ldx = _rows(x, "x", shape, dt, i)
+    yp, ldy = _rows(y, "y", shape, dt, i)
+    _call("layernorm_fwd", i, stream, xp, ldx, _vec(w, "w", (D,), i), None if b is None else _vec(b, "b", (D,), i), yp, ldy,
+          _vec(mean, "mean", (T,), i), _vec(rstd, "rstd", (T,), i), T, D, eps, 1 if zero_centered_gamma else 0, code)
 
 
 def layernorm_bwd_workspace_bytes(T: int, D: int) -> int:
@@ -627,16 +647,18 @@ def layernorm_bwd_workspace_bytes_max(T_max: int, D: int) -> int:
 
 
 def layernorm_bwd(g, x, w, mean, rstd, dx, dw, db, ws, zero_centered_gamma: bool = False, stream=None):
-    """Writes ``dx``, ``dw`` and, unless it is None, ``db``."""
-    on = _On(x, "x")
-    T, D = x.shape
-    gp, ldg = on.rows(g, "g", T, D)
-    xp, ldx = on.rows(x, "x", T, D)
-    dp, ldd = on.rows(dx, "dx", T, D)
-    wp, wb = on.bytes(ws)
-    on.call("layernorm_bwd", stream, gp, ldg, xp, ldx, on.vec(w, "w", (D,)), on.vec(mean, "mean", (T,)),
-            on.vec(rstd, "rstd", (T,)), dp, ldd, on.vec(dw, "dw", (D,)),
-            None if db is None else on.vec(db, "db", (D,)), wp, wb, T, D, 1 if zero_centered_gamma else 0, on.code)
+    """Writes ``dx``, ``dw`` and, unless it is None, ``db``. ``ws`` is a workspace of
+    ``layernorm_bwd_workspace_bytes(T, D)`` bytes."""
+    i, code = _index_and_code(x, "x")
+    dt, shape = x.dtype, x.shape
+    T, D = shape
+    gp, ldg = _rows(g, "g", shape, dt, i)
+    xp, ldx = _rows(x, "x", shape, dt, i)
+    dp, ldd = _rows(dx, "dx", shape, dt, i)
+    wp, wb = _bytes_of(ws, i)
+    _call("layernorm_bwd", i, stream, gp, ldg, xp, ldx, _vec(w, "w", (D,), i), _vec(mean, "mean", (T,), i),
+          _vec(rstd, "rstd", (T,), i), dp, ldd, _vec(dw, "dw", (D,), i), None if db is None else _vec(db, "db", (D,), i), wp,
+          wb, T, D, 1 if zero_centered_gamma else 0, code)
 
 
 def rope_frequencies(R: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0, low: float = 1.0,
@@ -651,21 +673,29 @@ def rope_frequencies(R: int, theta: float = 10000.0, scaling: str = "none", fact
     return out
 
 
-def _q_k(on, q, k):
-    if q.dim() != 3:
-        raise TypeError(f"q: expected a 3-D tensor [T, heads, D], got {tuple(q.shape)}")
-    T, Hq, D = q.shape
-    return T, Hq, (0 if k is None else k.shape[1] if k.dim() == 3 else -1), D
+def _q_k(q, k, inv_freq):
+    """Shapes of q and k and the number of frequencies."""
+    shape = q.shape
+    if len(shape) != 3:
+        raise TypeError(f"q: expected a 3-D tensor [T, heads, D], got {tuple(shape)}")
+    if inv_freq.dim() != 1:
+        raise TypeError(f"inv_freq: expected a 1-D tensor, got {tuple(inv_freq.shape)}")
+    T, _, D = shape
+    if k is None:
+        return shape, (T, 0, D), inv_freq.shape[0]
+    if k.dim() != 3:
+        raise TypeError(f"k: expected a 3-D tensor [T, heads, D], got {tuple(k.shape)}")
+    return shape, (T, k.shape[1], D), inv_freq.shape[0]
 
 
-def _rope(fn, q, k, inv_freq, q_out, k_out, positions, scale, interleaved, stream):
-    on = _On(q, "q")
-    T, Hq, Hk, D = _q_k(on, q, k)
-    n = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
-    on.call(fn, stream, *on.heads(q, "q", T, Hq, D), *on.heads(k, "k", T, Hk, D),
-            on.vec(inv_freq, "inv_freq", (n,), torch.float64), *on.positions(positions, T),
-            *on.heads(q_out, "q_out", T, Hq, D), *on.heads(k_out, "k_out", T, Hk, D), T, Hq, Hk, D, 2 * n, scale,
-            1 if interleaved else 0, on.code)
+def _rope(name, q, k, inv_freq, q_out, k_out, positions, scale, interleaved, stream):
+    i, code = _index_and_code(q, "q")
+    dt = q.dtype
+    sq, sk, n = _q_k(q, k, inv_freq)
+    T, Hq, D = sq
+    _call(name, i, stream, *_heads(q, "q", sq, dt, i), *_heads(k, "k", sk, dt, i), _vec(inv_freq, "inv_freq", (n,), i, _F64),
+          *_positions(positions, T, i), *_heads(q_out, "q_out", sq, dt, i), *_heads(k_out, "k_out", sk, dt, i), T, Hq, sk[1],
+          D, 2 * n, scale, 1 if interleaved else 0, code)
 
 
 def rope_fwd(q, k, inv_freq, q_out, k_out, positions=None, scale: float = 1.0, interleaved: bool = False, stream=None):
@@ -686,14 +716,16 @@ def rmsnorm_rope_fwd(q, k, wq, wk, inv_freq, q_out, k_out, rstd_q, rstd_k, posit
     """RMSNorm of every head of ``q`` (weight ``wq`` [D]) and of ``k`` (``wk``), then their rotary positions as
     in ``rope_fwd``, in one pass; writes ``q_out``, ``k_out`` and the inverse RMS of every head, ``rstd_q`` [T, Hq]
     and ``rstd_k`` [T, Hk]. ``k``, ``wk``, ``k_out`` and ``rstd_k`` may be None together."""
-    on = _On(q, "q")
-    T, Hq, Hk, D = _q_k(on, q, k)
-    n = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
-    on.call("rmsnorm_rope_fwd", stream, *on.heads(q, "q", T, Hq, D), *on.heads(k, "k", T, Hk, D),
-            on.vec(wq, "wq", (D,)), on.vec_of(wk, "wk", Hk, (D,)), on.vec(inv_freq, "inv_freq", (n,), torch.float64),
-            *on.positions(positions, T), *on.heads(q_out, "q_out", T, Hq, D), *on.heads(k_out, "k_out", T, Hk, D),
-            on.vec(rstd_q, "rstd_q", (T, Hq)), on.vec_of(rstd_k, "rstd_k", Hk, (T, Hk)), T, Hq, Hk, D, 2 * n, scale,
-            1 if interleaved else 0, eps, 1 if zero_centered_gamma else 0, on.code)
+    i, code = _index_and_code(q, "q")
+    dt = q.dtype
+    sq, sk, n = _q_k(q, k, inv_freq)
+    T, Hq, D = sq
+    Hk = sk[1]
+    _call("rmsnorm_rope_fwd", i, stream, *_heads(q, "q", sq, dt, i), *_heads(k, "k", sk, dt, i), _vec(wq, "wq", (D,), i),
+          _vec(wk, "wk", (D,), i) if Hk else None, _vec(inv_freq, "inv_freq", (n,), i, _F64), *_positions(positions, T, i),
+          *_heads(q_out, "q_out", sq, dt, i), *_heads(k_out, "k_out", sk, dt, i), _vec(rstd_q, "rstd_q", (T, Hq), i),
+          _vec(rstd_k, "rstd_k", (T, Hk), i) if Hk else None, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0, eps,
+          1 if zero_centered_gamma else 0, code)
 
 
 def rmsnorm_rope_bwd_workspace_bytes(T: int, Hq: int, Hk: int, D: int) -> int:
@@ -702,18 +734,21 @@ def rmsnorm_rope_bwd_workspace_bytes(T: int, Hq: int, Hk: int, D: int) -> int:
 
 def rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, inv_freq, rstd_q, rstd_k, dq, dk, dwq, dwk, ws, positions=None,
                      scale: float = 1.0, interleaved: bool = False, zero_centered_gamma: bool = False, stream=None):
-    """Gradients of rmsnorm_rope_fwd: ``dq``, ``dk`` (which may be ``gq``, ``gk``) and the weights' ``dwq``, ``dwk``."""
-    on = _On(q, "q")
-    T, Hq, Hk, D = _q_k(on, q, k)
-    n = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
-    wp, wb = on.bytes(ws)
-    on.call("rmsnorm_rope_bwd", stream, *on.heads(gq, "gq", T, Hq, D), *on.heads(gk, "gk", T, Hk, D),
-            *on.heads(q, "q", T, Hq, D), *on.heads(k, "k", T, Hk, D), on.vec(wq, "wq", (D,)),
-            on.vec_of(wk, "wk", Hk, (D,)), on.vec(inv_freq, "inv_freq", (n,), torch.float64),
-            *on.positions(positions, T), on.vec(rstd_q, "rstd_q", (T, Hq)), on.vec_of(rstd_k, "rstd_k", Hk, (T, Hk)),
-            *on.heads(dq, "dq", T, Hq, D), *on.heads(dk, "dk", T, Hk, D), on.vec(dwq, "dwq", (D,)),
-            on.vec_of(dwk, "dwk", Hk, (D,)), wp, wb, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0,
-            1 if zero_centered_gamma else 0, on.code)
+    """Gradients of rmsnorm_rope_fwd: ``dq``, ``dk`` (which may be ``gq``, ``gk``) and the weights' ``dwq``, ``dwk``.
+    ``ws`` is a workspace of ``rmsnorm_rope_bwd_workspace_bytes(T, Hq, Hk, D)`` bytes."""
+    i, code = _index_and_code(q, "q")
+    dt = q.dtype
+    sq, sk, n = _q_k(q, k, inv_freq)
+    T, Hq, D = sq
+    Hk = sk[1]
+    wp, wb = _bytes_of(ws, i)
+    _call("rmsnorm_rope_bwd", i, stream, *_heads(gq, "gq", sq, dt, i), *_heads(gk, "gk", sk, dt, i),
+          *_heads(q, "q", sq, dt, i), *_heads(k, "k", sk, dt, i), _vec(wq, "wq", (D,), i),
+          _vec(wk, "wk", (D,), i) if Hk else None, _vec(inv_freq, "inv_freq", (n,), i, _F64), *_positions(positions, T, i),
+          _vec(rstd_q, "rstd_q", (T, Hq), i), _vec(rstd_k, "rstd_k", (T, Hk), i) if Hk else None,
+          *_heads(dq, "dq", sq, dt, i), *_heads(dk, "dk", sk, dt, i), _vec(dwq, "dwq", (D,), i),
+          _vec(dwk, "dwk", (D,), i) if Hk else None, wp, wb, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0,
+          1 if zero_centered_gamma else 0, code)
 
 
 def rmsnorm_dgamma_reduce(ws, T: int, D: int, dgamma, stream=None):

@@ -30,6 +30,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "f32x2.cuh"
 #include "kernels.h"
@@ -99,11 +100,6 @@ __device__ __forceinline__ uint32_t lds32(uint32_t p) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t p) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p) : "memory");
-    return v;
-}
 __device__ __forceinline__ void sts128(uint32_t p, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -112,13 +108,18 @@ __device__ __forceinline__ void sts16(uint32_t p, uint32_t v) {
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(p), "h"(static_cast<uint16_t>(v)) : "memory");
 }
 
+// Two values of a word.
 template <bool F16>
-__device__ __forceinline__ float widen(uint32_t v) {
-    return F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(v))) : __uint_as_float(v << 16);
+__device__ __forceinline__ float2 widen2(uint32_t v) {
+    if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&v));
+    else return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 template <bool F16>
-__device__ __forceinline__ uint32_t narrow(float v) {
-    return F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+__device__ __forceinline__ uint32_t narrow2(float2 v) {
+    uint32_t w;
+    if constexpr (F16) *reinterpret_cast<__half2*>(&w) = __floats2half2_rn(v.x, v.y);
+    else *reinterpret_cast<__nv_bfloat162*>(&w) = __floats2bfloat162_rn(v.x, v.y);
+    return w;
 }
 
 // Sixteen bytes at any even address, through the words that hold them (n <= 8
@@ -136,16 +137,24 @@ __device__ __forceinline__ uint4 lds_window(uint32_t p, int n) {
     v.w = odd ? __funnelshift_r(w[3], w[4], 16) : w[3];
     return v;
 }
-// The first n of eight values to any even address.
+
+// The first n of eight values to any even address: whole words, and the half words
+// at the ends, which may share theirs with another lane's values.
 __device__ __forceinline__ void sts_window(uint32_t p, uint4 v, int n) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if ((p & 2u) == 0 && n == 8) {
+    const uint32_t w[5] = {v.x, v.y, v.z, v.w, 0u};
+    if ((p & 2u) == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sts32(p + 4 * i, w[i]);
+        for (int i = 0; i < 4; ++i) {
+            if (2 * i + 1 < n) sts32(p + 4 * i, w[i]);
+            else if (2 * i < n) sts16(p + 4 * i, w[i]);
+        }
     } else {
+        if (n > 0) sts16(p, w[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) sts16(p + 2 * i, i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+        for (int i = 0; i < 4; ++i) {  // values 2 i + 1 and 2 i + 2
+            if (2 * i + 2 < n) sts32(p + 4 * i + 2, __funnelshift_r(w[i], w[i + 1], 16));
+            else if (2 * i + 1 < n) sts16(p + 4 * i + 2, w[i] >> 16);
+        }
     }
 }
 
@@ -218,11 +227,11 @@ enum RopeKind : int { kHalves = 0, kNeighbours = 1, kHalvesAny = 2 };
 // The kernel: 2^LG lanes a head, NR heads a group and turn, RB of them at a time.
 // FULL: every lane has a whole unit (D = 16 x 2^LG, no unit cut short).
 // ---------------------------------------------------------------------------
-template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
+template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RBATCH, int S, int MINB>
 __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs a) {
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd, ANY = KIND == kHalvesAny;
     constexpr int OPS = BWD ? 2 : 1, per = 32 >> LG, step = per * NR;
-    static_assert(NR % RB == 0 && !(FULL && ANY), "whole batches; cut units are not full");
+    static_assert(NR % RBATCH == 0 && !(FULL && ANY), "whole batches; cut units are not full");
     extern __shared__ __align__(128) unsigned char smem[];
     const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     const int D = FULL ? 16 << LG : a.D, half = a.R >> 1, hp = (half + 7) & ~7;
@@ -268,8 +277,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         if (nB == 0) atB = 0;
     }
     const bool hasA = FULL || nA > 0, hasB = FULL || nB > 0;
-    // kHalvesAny: a value beyond the units of 32 lanes, if there is one for this lane.
-    const int atX = ANY && NORM ? a.R + 16 * ((1 << LG) - NP) + l : D;
+    // kHalvesAny: two values beyond the lanes' units, if there are any for this lane.
+    const int atX = ANY && NORM ? a.R + 16 * ((1 << LG) - NP) + 2 * l : D;
     const bool hasX = ANY && NORM && atX < D;
     const uint32_t rowA = head * pitch + 2u * atA, rowB = head * pitch + 2u * atB, rowX = head * pitch + 2u * atX;
     // kNeighbours: pairs of A and of B that are turned (past 4: all).
@@ -350,7 +359,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         long long p32 = 0;  // lane i: the position of token t32 + i
         int t32 = -32;
         Oct accA = oct_zero(), accB = oct_zero(), wA = oct_zero(), wB = oct_zero();
-        float accX = 0.0f, wX = 0.0f;
+        float2 accX = make_float2(0.0f, 0.0f), wX = accX;
         Oct c = oct_zero(), sn = oct_zero();  // cos and sin of this lane's pairs (kNeighbours: four of A, four of B)
         int t_have = -1, s_have = -1;
         while (now.left > 0) {
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                         wA.p[i] = make_float2(2 * i < nA ? w[atA + 2 * i] : 0.0f, 2 * i + 1 < nA ? w[atA + 2 * i + 1] : 0.0f);
                         wB.p[i] = make_float2(2 * i < nB ? w[atB + 2 * i] : 0.0f, 2 * i + 1 < nB ? w[atB + 2 * i + 1] : 0.0f);
                     }
-                    if (hasX) wX = w[atX];
+                    if (hasX) wX = *reinterpret_cast<const float2*>(w + atX);
                 }
             }
             if constexpr (BWD) cp_async_wait<S - 2>();
@@ -409,7 +418,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
             const int n = min(step, a.H[s] - now.h);  // heads of this turn; what is computed of others is sent nowhere
             if constexpr (BWD) {  // a head that is not there adds zeros to the weight gradients
                 if (n < step) {
-                    const int last = min(step, (n + per * RB - 1) / (per * RB) * (per * RB));
+                    const int last = min(step, (n + per * RBATCH - 1) / (per * RBATCH) * (per * RBATCH));
                     for (int i = n * (D >> 3) + lane; i < last * (D >> 3); i += 32) {
                         sts128(st + 16 * i, make_uint4(0, 0, 0, 0));
                         sts128(st + op_bytes + 16 * i, make_uint4(0, 0, 0, 0));
@@ -427,9 +436,9 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                     turn_halves(A, B, c, sn);
                 }
             };
-#pragma unroll
-            for (int i0 = 0; i0 < NR; i0 += RB) {
-                if (i0 * per >= n) break;  // the same for all lanes
+            // A batch of RB heads a group, from the i0-th on.
+            auto batch = [&](auto count, const int i0) {
+                constexpr int RB = decltype(count)::value;
                 const uint32_t at = st + i0 * per * pitch;
                 uint4 rawA[RB], rawB[RB];
 #pragma unroll
@@ -469,14 +478,16 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                     }
                 } else {
                     Oct A[RB], B[RB], xA[RB], xB[RB];
-                    float sum[RB], r[RB], X[RB], xX[RB];
+                    float sum[RB], r[RB];
+                    float2 X[RB], xX[RB];
 #pragma unroll
                     for (int i = 0; i < RB; ++i) {
                         const uint32_t p = at + i * per * pitch;
                         const int row = (i0 + i) * per + head;
                         float2 sum2 = make_float2(0.0f, 0.0f);
-                        X[i] = xX[i] = r[i] = 0.0f;
-                        if (hasX) X[i] = widen<F16>(lds16(p + rowX));
+                        r[i] = 0.0f;
+                        X[i] = xX[i] = make_float2(0.0f, 0.0f);
+                        if (hasX) X[i] = widen2<F16>(lds32(p + rowX));
                         if constexpr (BWD) {
                             A[i] = oct_unpack<F16>(rawA[i]);
                             B[i] = oct_unpack<F16>(rawB[i]);
@@ -490,9 +501,9 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                                 cut(xA[i], nA);
                                 cut(xB[i], nB);
                                 if (hasX) {
-                                    xX[i] = widen<F16>(lds16(p + op_bytes + rowX));
-                                    accX = __fmaf_rn(X[i], fmul(xX[i], r[i]), accX);
-                                    X[i] = fmul(X[i], wX);
+                                    xX[i] = widen2<F16>(lds32(p + op_bytes + rowX));
+                                    accX = fma2(X[i], fmul2(xX[i], both(r[i])), accX);
+                                    X[i] = fmul2(X[i], wX);
                                 }
                             }
 #pragma unroll
@@ -504,8 +515,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                                 sum2 = fma2(A[i].p[e], xA[i].p[e], sum2);
                                 sum2 = fma2(B[i].p[e], xB[i].p[e], sum2);
                             }
+                            if constexpr (ANY) sum2 = fma2(X[i], xX[i], sum2);
                             sum[i] = fadd(sum2.x, sum2.y);
-                            if constexpr (ANY) sum[i] = __fmaf_rn(X[i], xX[i], sum[i]);
                         } else {
                             A[i] = oct_unpack<F16>(rawA[i]);
                             B[i] = oct_unpack<F16>(rawB[i]);
@@ -518,8 +529,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                                 sum2 = fma2(A[i].p[e], A[i].p[e], sum2);
                                 sum2 = fma2(B[i].p[e], B[i].p[e], sum2);
                             }
+                            if constexpr (ANY) sum2 = fma2(X[i], X[i], sum2);
                             sum[i] = fadd(sum2.x, sum2.y);
-                            if constexpr (ANY) sum[i] = __fmaf_rn(X[i], X[i], sum[i]);
                         }
                     }
                     if constexpr (ANY) __syncwarp();  // windows share words: all are read before any is written
@@ -535,7 +546,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                                 A[i].p[e] = fma2(A[i].p[e], both(r[i]), fmul2(xA[i].p[e], both(coef)));
                                 B[i].p[e] = fma2(B[i].p[e], both(r[i]), fmul2(xB[i].p[e], both(coef)));
                             }
-                            if (hasX) sts16(p + rowX, narrow<F16>(__fmaf_rn(X[i], r[i], fmul(xX[i], coef))));
+                            if (hasX) sts32(p + rowX, narrow2<F16>(fma2(X[i], both(r[i]), fmul2(xX[i], both(coef)))));
                         } else {
                             r[i] = rsqrtf(fadd(fmul(sum[i], a.rcp_d), a.eps));
                             if (l == 0) rs[cur * step + (i0 + i) * per + head] = r[i];
@@ -545,12 +556,19 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                                 B[i].p[e] = fmul2(fmul2(B[i].p[e], both(r[i])), wB.p[e]);
                             }
                             turn(A[i], B[i]);
-                            if (hasX) sts16(p + rowX, narrow<F16>(fmul(fmul(X[i], r[i]), wX)));
+                            if (hasX) sts32(p + rowX, narrow2<F16>(fmul2(fmul2(X[i], both(r[i])), wX)));
                         }
                         store(p + rowA, hasA, A[i], nA);
                         store(p + rowB, hasB, B[i], nB);
                     }
                 }
+            };
+#pragma unroll
+            for (int i0 = 0; i0 < NR; i0 += RBATCH) {
+                const int rest = n - i0 * per;
+                if (rest <= 0) break;  // the same for all lanes
+                if (RBATCH > 1 && rest <= per) batch(std::integral_constant<int, 1>(), i0);
+                else batch(std::integral_constant<int, RBATCH>(), i0);
             }
             fence_proxy_async_smem();  // the results, before the copy that sends them and the one that refills the stage
             __syncwarp();
@@ -592,7 +610,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                 if (e < nA) part[group * D + atA + e] = e & 1 ? accA.p[e / 2].y : accA.p[e / 2].x;
                 if (e < nB) part[group * D + atB + e] = e & 1 ? accB.p[e / 2].y : accB.p[e / 2].x;
             }
-            if (hasX) part[group * D + atX] = accX;
+            if (hasX) *reinterpret_cast<float2*>(part + group * D + atX) = accX;
             __syncthreads();
             float* row = a.partials + (static_cast<int64_t>(pass) * gridDim.x + blockIdx.x) * D;
             for (int col = tid; col < D; col += nt) {
@@ -612,7 +630,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
 // ---------------------------------------------------------------------------
 // heads a group and turn, of them at a time, stages, CTAs an SM
 #ifndef RP_T
-#define RP_T 4, 2, 2, 3
+#define RP_T 4, 1, 2, 3
 #endif
 #ifndef RP_F
 #define RP_F 4, 2, 3, 2
