@@ -27,6 +27,7 @@
 //   * kNeighbours (ROPE_INTERLEAVED): two vectors.
 //   * kHalvesAny (ROPE_HALF, any R): as kHalves, but B (and, beyond the turned part,
 //     A) lies at any even number of bytes and may be cut short by the half's end.
+//   * kHalves8 (ROPE_HALF, R a multiple of 8): the same in whole steps of 8 bytes.
 #pragma once
 
 #include <algorithm>
@@ -158,6 +159,18 @@ __device__ __forceinline__ void sts_window(uint32_t p, uint4 v, int n) {
     }
 }
 
+// Four (n > 0) or eight (n > 4) values at an address of whole 8 bytes.
+__device__ __forceinline__ uint4 lds_window8(uint32_t p, int n) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (n > 0) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
+    if (n > 4) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.z), "=r"(v.w) : "r"(p + 8) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_window8(uint32_t p, uint4 v, int n) {
+    if (n > 0) asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p), "r"(v.x), "r"(v.y) : "memory");
+    if (n > 4) asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p + 8), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // 1-D bulk copy shared -> global, in the thread's current bulk group.
 __device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes, uint64_t policy) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;"
@@ -221,7 +234,7 @@ __device__ __forceinline__ uint4 keep_if(bool k, uint4 v) {
     return make_uint4(k ? v.x : 0u, k ? v.y : 0u, k ? v.z : 0u, k ? v.w : 0u);
 }
 
-enum RopeKind : int { kHalves = 0, kNeighbours = 1, kHalvesAny = 2 };
+enum RopeKind : int { kHalves = 0, kNeighbours = 1, kHalvesAny = 2, kHalves8 = 3 };
 
 // ---------------------------------------------------------------------------
 // The kernel: 2^LG lanes a head, NR heads a group and turn, RB of them at a time.
@@ -229,7 +242,8 @@ enum RopeKind : int { kHalves = 0, kNeighbours = 1, kHalvesAny = 2 };
 // ---------------------------------------------------------------------------
 template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RBATCH, int S, int MINB>
 __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs a) {
-    constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd, ANY = KIND == kHalvesAny;
+    constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
+    constexpr bool ANY = KIND == kHalvesAny || KIND == kHalves8;  // units may be cut short
     constexpr int OPS = BWD ? 2 : 1, per = 32 >> LG, step = per * NR;
     static_assert(NR % RBATCH == 0 && !(FULL && ANY), "whole batches; cut units are not full");
     extern __shared__ __align__(128) unsigned char smem[];
@@ -293,13 +307,15 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     // priority measured 1 to 3 % slower, loads at the ordinary one 0 to 4 %).
     const uint64_t pol = policy_evict_first();
     auto load = [&](uint32_t at, bool has, int n) -> uint4 {
-        if constexpr (ANY) return lds_window(at, n);
+        if constexpr (KIND == kHalvesAny) return lds_window(at, n);
+        else if constexpr (KIND == kHalves8) return lds_window8(at, n);
         else if constexpr (FULL) return lds128(at);
         else return keep_if(has, lds128(at));
     };
     auto store = [&](uint32_t at, bool has, const Oct& o, int n) {
         const uint4 v = oct_pack<F16>(o);
-        if constexpr (ANY) sts_window(at, v, n);
+        if constexpr (KIND == kHalvesAny) sts_window(at, v, n);
+        else if constexpr (KIND == kHalves8) sts_window8(at, v, n);
         else if (has) sts128(at, v);
     };
     uint32_t phase = 0;  // of the stage that comes next
@@ -520,7 +536,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                         } else {
                             A[i] = oct_unpack<F16>(rawA[i]);
                             B[i] = oct_unpack<F16>(rawB[i]);
-                            if constexpr (ANY) {
+                            if constexpr (KIND == kHalvesAny) {  // the other half of a word at the end
                                 cut(A[i], nA);
                                 cut(B[i], nB);
                             }
@@ -628,17 +644,6 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
-// heads a group and turn, of them at a time, stages, CTAs an SM
-#ifndef RP_T
-#define RP_T 4, 1, 2, 3
-#endif
-#ifndef RP_F
-#define RP_F 4, 2, 3, 2
-#endif
-#ifndef RP_B
-#define RP_B 3, 1, 2, 2
-#endif
-
 template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
 cudaError_t rope_run_kernel(const RopeArgs& a, cudaStream_t st) {
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
@@ -667,23 +672,53 @@ cudaError_t rope_run_kernel(const RopeArgs& a, cudaStream_t st) {
     return launch_kernel(kern, static_cast<unsigned>(grid), threads, smem, st, a);
 }
 
+#ifndef RP_T
+#define RP_T 4, 1, 2, 3
+#endif
+#ifndef RP_F
+#define RP_F 4, 2, 3, 2
+#endif
+#ifndef RP_FF
+#define RP_FF 2, 1, 3, 2
+#endif
+#ifndef RP_B
+#define RP_B 3, 1, 2, 2
+#endif
+#ifndef RP_B4
+#define RP_B4 4, 1, 2, 2
+#endif
+#ifndef RP_B5
+#define RP_B5 2, 1, 2, 2
+#endif
+
 template <int MODE, int KIND, bool F16, int LG, bool FULL>
 cudaError_t rope_shape_of(const RopeArgs& a, cudaStream_t st) {
-    if constexpr (MODE == kTurn) return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_T>(a, st);
-    else if constexpr (MODE == kNormTurn) return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_F>(a, st);
-    else return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_B>(a, st);
+    if constexpr (MODE == kTurn) {
+        return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_T>(a, st);
+    } else if constexpr (MODE == kNormTurn) {
+        if constexpr (FULL && LG < 5) return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_FF>(a, st);
+        else return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_F>(a, st);
+    } else {
+        if constexpr (LG == 5) {
+            return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_B5>(a, st);
+        } else {
+            if constexpr (!FULL)
+                if (4 * a.D <= 3 * (16 << LG)) return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_B4>(a, st);
+            return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_B>(a, st);
+        }
+    }
 }
 
 template <int MODE, int KIND, bool F16, int LG>
 cudaError_t rope_full(const RopeArgs& a, cudaStream_t st) {
-    if constexpr (KIND != kHalvesAny)
+    if constexpr (KIND == kHalves || KIND == kNeighbours)
         if (a.D == 16 << LG) return rope_shape_of<MODE, KIND, F16, LG, true>(a, st);
     return rope_shape_of<MODE, KIND, F16, LG, false>(a, st);
 }
 
 template <int MODE, int KIND, bool F16>
 cudaError_t rope_lanes(const RopeArgs& a, cudaStream_t st) {
-    switch (rope_lanes_log2(a.D, a.R, KIND == kHalvesAny, MODE != kTurn)) {
+    switch (rope_lanes_log2(a.D, a.R, KIND == kHalvesAny || KIND == kHalves8, MODE != kTurn)) {
         case 2: return rope_full<MODE, KIND, F16, 2>(a, st);
         case 3: return rope_full<MODE, KIND, F16, 3>(a, st);
         case 4: return rope_full<MODE, KIND, F16, 4>(a, st);
@@ -695,6 +730,7 @@ template <int MODE, bool F16>
 cudaError_t rope_kinds(const RopeArgs& a, cudaStream_t st) {
     if (a.layout == ROPE_INTERLEAVED) return rope_lanes<MODE, kNeighbours, F16>(a, st);
     if (a.R % 16 == 0) return rope_lanes<MODE, kHalves, F16>(a, st);
+    if (a.R % 8 == 0) return rope_lanes<MODE, kHalves8, F16>(a, st);
     return rope_lanes<MODE, kHalvesAny, F16>(a, st);
 }
 
