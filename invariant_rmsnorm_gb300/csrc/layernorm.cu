@@ -107,7 +107,7 @@ int layernorm_bwd(const rmsn_act16* g, int64_t ldg, const rmsn_act16* x, int64_t
                       zero_centered_gamma ? 1 : 0, static_cast<int>(c.rows), 1.0f / static_cast<float>(D)};
     const unsigned n = static_cast<unsigned>(c.count);
     cudaError_t e = flags ? launch_ln_bwd_f16(a, n, db != nullptr, stream) : launch_ln_bwd(a, n, db != nullptr, stream);
-    if (e == cudaSuccess) e = launch_reduce_columns(a.partials, n, a.D, dw, db, stream);
+    if (e == cudaSuccess) e = launch_reduce_columns({a.partials, c.count, dw}, {a.partials + c.count * D, c.count, db}, a.D, stream);
     return cuda_status(e);
 }
 

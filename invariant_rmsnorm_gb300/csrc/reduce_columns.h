@@ -7,9 +7,13 @@
 
 namespace rmsn {
 
-// out0[j] = sum over c of partials[c][j], and out1[j] (unless null) the same over
-// the n rows of D values that follow the first n.
-cudaError_t launch_reduce_columns(const float* partials, int64_t n, int D, float* out0, float* out1,
-                                  cudaStream_t s);
+// n partial rows and the row that their sum goes to (null: nothing to do).
+struct PartialRows {
+    const float* p;
+    int64_t n;
+    float* out;
+};
+
+cudaError_t launch_reduce_columns(const PartialRows& first, const PartialRows& second, int D, cudaStream_t s);
 
 }  // namespace rmsn

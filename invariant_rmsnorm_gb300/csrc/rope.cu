@@ -11,7 +11,9 @@ namespace rmsn {
 
 namespace {
 
-int rope_run(RopeMode mode, RopeArgs& a, int flags, cudaStream_t s) {
+int rope_run(RopeMode mode, RopeArgs& a, int flags, cudaStream_t s, int* ctas_q = nullptr) {
+    int unused = 0;
+    if (ctas_q == nullptr) ctas_q = &unused;
     a.rcp_d = 1.0f / static_cast<float>(a.D);
     for (int i = 0; i < 2; ++i) {
         const bool in_place = mode == kTurn && a.out[i].p == a.in[i].p;
@@ -22,9 +24,9 @@ int rope_run(RopeMode mode, RopeArgs& a, int flags, cudaStream_t s) {
         a.dense[2][i] = whole && a.out[i].head == a.D;
     }
     switch (mode) {
-        case kTurn: return cuda_status(flags ? launch_rope_turn_f16(a, s) : launch_rope_turn(a, s));
-        case kNormTurn: return cuda_status(flags ? launch_rope_norm_f16(a, s) : launch_rope_norm(a, s));
-        default: return cuda_status(flags ? launch_rope_norm_bwd_f16(a, s) : launch_rope_norm_bwd(a, s));
+        case kTurn: return cuda_status(flags ? launch_rope_turn_f16(a, ctas_q, s) : launch_rope_turn(a, ctas_q, s));
+        case kNormTurn: return cuda_status(flags ? launch_rope_norm_f16(a, ctas_q, s) : launch_rope_norm(a, ctas_q, s));
+        default: return cuda_status(flags ? launch_rope_norm_bwd_f16(a, ctas_q, s) : launch_rope_norm_bwd(a, ctas_q, s));
     }
 }
 
@@ -201,7 +203,7 @@ int rmsnorm_rope_fwd(const rmsn_act16* q, int64_t q_token, int64_t q_head, const
 
 size_t rmsnorm_rope_bwd_workspace_bytes(int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
     if (check_sizes(T, Hq, Hk, D) != RMSN_OK || T == 0) return 0;
-    return static_cast<size_t>(rope_bwd_ctas(T, Hq, Hk, D)) * static_cast<size_t>(D) * 8u;
+    return static_cast<size_t>(rope_bwd_ctas(T, Hq, Hk, D)) * static_cast<size_t>(D) * 4u;
 }
 
 int rmsnorm_rope_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head, const rmsn_act16* gk, int64_t gk_token,
@@ -243,8 +245,11 @@ int rmsnorm_rope_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head, co
     if (ws == nullptr || ws_bytes < rmsnorm_rope_bwd_workspace_bytes(T, Hq, Hk, D)) return RMSN_EWORKSPACE;
     if (!aligned16(ws)) return RMSN_EALIGN;
     a.partials = static_cast<float*>(ws);
-    RMSN_TRY(rope_run(kNormTurnBwd, a, flags, stream));
-    return cuda_status(launch_reduce_columns(a.partials, rope_bwd_ctas(T, Hq, Hk, D), a.D, dwq, Hk > 0 ? dwk : nullptr, stream));
+    int of_q = 0;
+    RMSN_TRY(rope_run(kNormTurnBwd, a, flags, stream, &of_q));
+    const int64_t n = rope_bwd_ctas(T, Hq, Hk, D);
+    return cuda_status(launch_reduce_columns({a.partials, of_q, dwq}, {a.partials + of_q * D, n - of_q, Hk > 0 ? dwk : nullptr},
+                                             a.D, stream));
 }
 
 }  // extern "C"

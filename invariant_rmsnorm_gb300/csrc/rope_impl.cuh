@@ -19,7 +19,7 @@
 // shared memory: lanes read their values there, overwrite them with the results,
 // and one lane sends the stage back. Warps never wait for one another; dw is
 // summed in registers and joined over the CTA's groups at the end, in group order,
-// one partial row a CTA.
+// one partial row a CTA (a CTA has turns of q alone or of k alone).
 //
 // A lane's unit is two times eight values, A and B:
 //   * kHalves (ROPE_HALF, R a multiple of 16): a 16-byte vector of the first half
@@ -320,322 +320,319 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     };
     uint32_t phase = 0;  // of the stage that comes next
     int cur = 0;
-    // Forward: one pass over the turns of q and of k. Backward: q, then k, each with its own weight gradient.
-    for (int pass = 0; pass < (BWD ? 2 : 1); ++pass) {
-        const int Hq = BWD && pass ? 0 : a.H[0], Hk = BWD && !pass ? 0 : a.H[1];
-        const int nq = (Hq + step - 1) / step, nk = (Hk + step - 1) / step;
-        if (nq + nk == 0) continue;
-        Turns now(a.T, nq, nk, step, static_cast<int64_t>(blockIdx.x) * nw + warp, static_cast<int64_t>(gridDim.x) * nw);
-        Turns ahead = now;
-        int fs = cur;
-        auto fetch = [&]() {
-            if (ahead.left > 0) {
-                const int s = ahead.s, n = min(step, a.H[s] - ahead.h);
-                if (lane == 0) {
-                    const uint32_t bytes = a.row_bytes[s];
-                    unsigned char* to = smem + static_cast<size_t>(warp * S + fs) * stage_bytes;
-                    mbar_arrive_expect_tx(&full[fs], static_cast<uint32_t>(n) * OPS * bytes);
+    // Forward: every warp takes turns of q and of k. Backward: the first a.ctas_q
+    // CTAs take those of q, the others those of k, for one weight's gradient each.
+    const bool of_k = BWD && static_cast<int>(blockIdx.x) >= a.ctas_q;
+    const int Hq = of_k ? 0 : a.H[0], Hk = BWD && !of_k ? 0 : a.H[1];
+    const int cta = blockIdx.x - (of_k ? a.ctas_q : 0);
+    const int ctas = !BWD ? gridDim.x : of_k ? gridDim.x - a.ctas_q : a.ctas_q;
+    Turns now(a.T, (Hq + step - 1) / step, (Hk + step - 1) / step, step, static_cast<int64_t>(cta) * nw + warp,
+              static_cast<int64_t>(ctas) * nw);
+    Turns ahead = now;
+    int fs = 0;
+    auto fetch = [&]() {
+        if (ahead.left > 0) {
+            const int s = ahead.s, n = min(step, a.H[s] - ahead.h);
+            if (lane == 0) {
+                const uint32_t bytes = a.row_bytes[s];
+                unsigned char* to = smem + static_cast<size_t>(warp * S + fs) * stage_bytes;
+                mbar_arrive_expect_tx(&full[fs], static_cast<uint32_t>(n) * OPS * bytes);
 #pragma unroll
-                    for (int op = 0; op < OPS; ++op) {
-                        const HeadsIn& in = op ? a.x[s] : a.in[s];
-                        const uint16_t* p = in.p + ahead.t * in.token + ahead.h * in.head;
-                        if (a.dense[op][s]) {  // heads side by side come in one copy
-                            bulk_g2s(to + op * op_bytes, p, n * pitch, &full[fs], pol);
-                        } else {
-                            for (int i = 0; i < n; ++i, p += in.head) bulk_g2s(to + op * op_bytes + i * pitch, p, bytes, &full[fs], pol);
-                        }
-                    }
-                }
-                if constexpr (BWD) {
-                    const float* p = a.rstd[s] + static_cast<int64_t>(ahead.t) * a.H[s] + ahead.h;
-#pragma unroll
-                    for (int i = 0; i < step; i += 32)
-                        if (i + lane < n) cp_async4(rs + fs * step + i + lane, p + i + lane);
-                }
-                ahead.next(Hq, Hk, step);
-            }
-            if constexpr (BWD) cp_async_commit();
-            fs = fs + 1 == S ? 0 : fs + 1;
-        };
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i) fetch();
-        if (pass == 0) {  // while the first rows come
-            for (int i = tid; i < half; i += nt) F[i] = rope_turns(a.inv_freq[i]);
-            if constexpr (NORM) {
-                for (int i = tid; i < 2 * D; i += nt) {
-                    const int s = i >= D;
-                    if (a.H[s] > 0) {
-                        const float w = a.w[s][s ? i - D : i];
-                        wsm[i] = a.zc ? fadd(w, 1.0f) : w;
+                for (int op = 0; op < OPS; ++op) {
+                    const HeadsIn& in = op ? a.x[s] : a.in[s];
+                    const uint16_t* p = in.p + ahead.t * in.token + ahead.h * in.head;
+                    if (a.dense[op][s]) {  // heads side by side come in one copy
+                        bulk_g2s(to + op * op_bytes, p, n * pitch, &full[fs], pol);
+                    } else {
+                        for (int i = 0; i < n; ++i, p += in.head) bulk_g2s(to + op * op_bytes + i * pitch, p, bytes, &full[fs], pol);
                     }
                 }
             }
-            __syncthreads();
+            if constexpr (BWD) {
+                const float* p = a.rstd[s] + static_cast<int64_t>(ahead.t) * a.H[s] + ahead.h;
+#pragma unroll
+                for (int i = 0; i < step; i += 32)
+                    if (i + lane < n) cp_async4(rs + fs * step + i + lane, p + i + lane);
+            }
+            ahead.next(Hq, Hk, step);
         }
-        long long p32 = 0;  // lane i: the position of token t32 + i
-        int t32 = -32;
-        Oct accA = oct_zero(), accB = oct_zero(), wA = oct_zero(), wB = oct_zero();
-        float2 accX = make_float2(0.0f, 0.0f), wX = accX;
-        Oct c = oct_zero(), sn = oct_zero();  // cos and sin of this lane's pairs (kNeighbours: four of A, four of B)
-        int t_have = -1, s_have = -1;
-        while (now.left > 0) {
-            if (now.t != t_have) {
-                t_have = now.t;
-                if (t_have - t32 >= 32) {
-                    t32 = t_have;
-                    if (t32 + lane < a.T) p32 = position(a, t32 + lane);
-                }
-                token_angles(cs, hp, half, F, __shfl_sync(0xffffffffu, p32, t_have - t32), a.scale, BWD || a.back, lane);
-                if constexpr (KIND == kNeighbours) {
-                    const float4* q = reinterpret_cast<const float4*>(cs);
-                    const int iA = min(atA >> 3, (hp >> 2) - 1), iB = min(atB >> 3, (hp >> 2) - 1);
-                    c = oct_of(q[iA], q[iB]);
-                    sn = oct_of(q[(hp >> 2) + iA], q[(hp >> 2) + iB]);
-                } else if (turned) {
-                    const float4* q = reinterpret_cast<const float4*>(cs + atA);
-                    c = oct_of(q[0], q[1]);
-                    sn = oct_of(q[hp >> 2], q[(hp >> 2) + 1]);
-                }
-            }
-            const int s = now.s;
-            if (NORM && s != s_have) {
-                s_have = s;
-                const float* w = wsm + s * D;
-                if constexpr (!ANY) {
-                    const float4 *p = reinterpret_cast<const float4*>(w + atA), *q = reinterpret_cast<const float4*>(w + atB);
-                    wA = oct_of(p[0], p[1]);
-                    wB = oct_of(q[0], q[1]);
-                } else {
+        if constexpr (BWD) cp_async_commit();
+        fs = fs + 1 == S ? 0 : fs + 1;
+    };
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        wA.p[i] = make_float2(2 * i < nA ? w[atA + 2 * i] : 0.0f, 2 * i + 1 < nA ? w[atA + 2 * i + 1] : 0.0f);
-                        wB.p[i] = make_float2(2 * i < nB ? w[atB + 2 * i] : 0.0f, 2 * i + 1 < nB ? w[atB + 2 * i + 1] : 0.0f);
+    for (int i = 0; i < S - 1; ++i) fetch();
+    // While the first rows come:
+    for (int i = tid; i < half; i += nt) F[i] = rope_turns(a.inv_freq[i]);
+    if constexpr (NORM) {
+        for (int i = tid; i < 2 * D; i += nt) {
+            const int s = i >= D;
+            if (a.H[s] > 0) {
+                const float w = a.w[s][s ? i - D : i];
+                wsm[i] = a.zc ? fadd(w, 1.0f) : w;
+            }
+        }
+    }
+    __syncthreads();
+    long long p32 = 0;  // lane i: the position of token t32 + i
+    int t32 = -32;
+    Oct accA = oct_zero(), accB = oct_zero(), wA = oct_zero(), wB = oct_zero();
+    float2 accX = make_float2(0.0f, 0.0f), wX = accX;
+    Oct c = oct_zero(), sn = oct_zero();  // cos and sin of this lane's pairs (kNeighbours: four of A, four of B)
+    int t_have = -1, s_have = -1;
+    while (now.left > 0) {
+        if (now.t != t_have) {
+            t_have = now.t;
+            if (t_have - t32 >= 32) {
+                t32 = t_have;
+                if (t32 + lane < a.T) p32 = position(a, t32 + lane);
+            }
+            token_angles(cs, hp, half, F, __shfl_sync(0xffffffffu, p32, t_have - t32), a.scale, BWD || a.back, lane);
+            if constexpr (KIND == kNeighbours) {
+                const float4* q = reinterpret_cast<const float4*>(cs);
+                const int iA = min(atA >> 3, (hp >> 2) - 1), iB = min(atB >> 3, (hp >> 2) - 1);
+                c = oct_of(q[iA], q[iB]);
+                sn = oct_of(q[(hp >> 2) + iA], q[(hp >> 2) + iB]);
+            } else if (turned) {
+                const float4* q = reinterpret_cast<const float4*>(cs + atA);
+                c = oct_of(q[0], q[1]);
+                sn = oct_of(q[hp >> 2], q[(hp >> 2) + 1]);
+            }
+        }
+        const int s = now.s;
+        if (NORM && s != s_have) {
+            s_have = s;
+            const float* w = wsm + s * D;
+            if constexpr (!ANY) {
+                const float4 *p = reinterpret_cast<const float4*>(w + atA), *q = reinterpret_cast<const float4*>(w + atB);
+                wA = oct_of(p[0], p[1]);
+                wB = oct_of(q[0], q[1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    wA.p[i] = make_float2(2 * i < nA ? w[atA + 2 * i] : 0.0f, 2 * i + 1 < nA ? w[atA + 2 * i + 1] : 0.0f);
+                    wB.p[i] = make_float2(2 * i < nB ? w[atB + 2 * i] : 0.0f, 2 * i + 1 < nB ? w[atB + 2 * i + 1] : 0.0f);
+                }
+                if (hasX) wX = *reinterpret_cast<const float2*>(w + atX);
+            }
+        }
+        if constexpr (BWD) cp_async_wait<S - 2>();
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[cur], phase))) {
+            // Give up: wait (bounded) for the copies in flight, and leave the turns.
+            if (lane == 0) {
+                for (int i = 1, f = cur, ph = phase; i < S; ++i) {
+                    if (++f == S) {
+                        f = 0;
+                        ph ^= 1u;
                     }
-                    if (hasX) wX = *reinterpret_cast<const float2*>(w + atX);
+                    if (i < now.left) (void)mbar_wait(&full[f], ph);
+                }
+                atomicOr(&g_rope_error, kErrWaitTimeout);
+            }
+            break;
+        }
+        __syncwarp();  // BWD: the other lanes' inverse RMS
+        const uint32_t st = ring + cur * stage_bytes;
+        const int n = min(step, a.H[s] - now.h);  // heads of this turn; what is computed of others is sent nowhere
+        if constexpr (BWD) {  // a head that is not there adds zeros to the weight gradients
+            if (n < step) {
+                const int last = min(step, (n + per * RBATCH - 1) / (per * RBATCH) * (per * RBATCH));
+                for (int i = n * (D >> 3) + lane; i < last * (D >> 3); i += 32) {
+                    sts128(st + 16 * i, make_uint4(0, 0, 0, 0));
+                    sts128(st + op_bytes + 16 * i, make_uint4(0, 0, 0, 0));
+                }
+                for (int i = n + lane; i < last; i += 32) rs[cur * step + i] = 0.0f;
+                __syncwarp();
+            }
+        }
+        auto turn = [&](Oct& A, Oct& B) {
+            if constexpr (KIND == kNeighbours) {
+                const float2 c0[2] = {c.p[0], c.p[1]}, c1[2] = {c.p[2], c.p[3]}, s0[2] = {sn.p[0], sn.p[1]}, s1[2] = {sn.p[2], sn.p[3]};
+                if (tA > 0) turn_neighbours(A, c0, s0, tA);
+                if (tB > 0) turn_neighbours(B, c1, s1, tB);
+            } else if (turned) {
+                turn_halves(A, B, c, sn);
+            }
+        };
+        // A batch of RB heads a group, from the i0-th on.
+        auto batch = [&](auto count, const int i0) {
+            constexpr int RB = decltype(count)::value;
+            const uint32_t at = st + i0 * per * pitch;
+            uint4 rawA[RB], rawB[RB];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                const uint32_t p = at + i * per * pitch;
+                if (NORM || KIND == kNeighbours || turned) {
+                    rawA[i] = load(p + rowA, hasA, nA);
+                    rawB[i] = load(p + rowB, hasB, nB);
                 }
             }
-            if constexpr (BWD) cp_async_wait<S - 2>();
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[cur], phase))) {
-                // Give up: wait (bounded) for the copies in flight, and leave the turns.
-                if (lane == 0) {
-                    for (int i = 1, f = cur, ph = phase; i < S; ++i) {
-                        if (++f == S) {
-                            f = 0;
-                            ph ^= 1u;
-                        }
-                        if (i < now.left) (void)mbar_wait(&full[f], ph);
-                    }
-                    atomicOr(&g_rope_error, kErrWaitTimeout);
-                }
-                break;
-            }
-            __syncwarp();  // BWD: the other lanes' inverse RMS
-            const uint32_t st = ring + cur * stage_bytes;
-            const int n = min(step, a.H[s] - now.h);  // heads of this turn; what is computed of others is sent nowhere
-            if constexpr (BWD) {  // a head that is not there adds zeros to the weight gradients
-                if (n < step) {
-                    const int last = min(step, (n + per * RBATCH - 1) / (per * RBATCH) * (per * RBATCH));
-                    for (int i = n * (D >> 3) + lane; i < last * (D >> 3); i += 32) {
-                        sts128(st + 16 * i, make_uint4(0, 0, 0, 0));
-                        sts128(st + op_bytes + 16 * i, make_uint4(0, 0, 0, 0));
-                    }
-                    for (int i = n + lane; i < last; i += 32) rs[cur * step + i] = 0.0f;
-                    __syncwarp();
-                }
-            }
-            auto turn = [&](Oct& A, Oct& B) {
-                if constexpr (KIND == kNeighbours) {
-                    const float2 c0[2] = {c.p[0], c.p[1]}, c1[2] = {c.p[2], c.p[3]}, s0[2] = {sn.p[0], sn.p[1]}, s1[2] = {sn.p[2], sn.p[3]};
-                    if (tA > 0) turn_neighbours(A, c0, s0, tA);
-                    if (tB > 0) turn_neighbours(B, c1, s1, tB);
-                } else if (turned) {
-                    turn_halves(A, B, c, sn);
-                }
-            };
-            // A batch of RB heads a group, from the i0-th on.
-            auto batch = [&](auto count, const int i0) {
-                constexpr int RB = decltype(count)::value;
-                const uint32_t at = st + i0 * per * pitch;
-                uint4 rawA[RB], rawB[RB];
+            if constexpr (MODE == kTurn) {
+                if constexpr (ANY) __syncwarp();  // windows share words: all are read before any is written
 #pragma unroll
                 for (int i = 0; i < RB; ++i) {
                     const uint32_t p = at + i * per * pitch;
-                    if (NORM || KIND == kNeighbours || turned) {
-                        rawA[i] = load(p + rowA, hasA, nA);
-                        rawB[i] = load(p + rowB, hasB, nB);
+                    if constexpr (KIND == kNeighbours) {
+                        // What is not turned stays where it is, or keeps its bits.
+                        Oct A = oct_unpack<F16>(rawA[i]), B = oct_unpack<F16>(rawB[i]);
+                        turn(A, B);
+                        auto put = [&](uint32_t q, const Oct& o, const uint4& raw, int t) {
+                            uint4 v = oct_pack<F16>(o);
+                            if (t < 4) {
+                                if (t < 2) v.y = raw.y;
+                                if (t < 3) v.z = raw.z;
+                                v.w = raw.w;
+                            }
+                            if (t > 0) sts128(q, v);
+                        };
+                        put(p + rowA, A, rawA[i], tA);
+                        put(p + rowB, B, rawB[i], tB);
+                    } else if (turned) {
+                        Oct A = oct_unpack<F16>(rawA[i]), B = oct_unpack<F16>(rawB[i]);
+                        turn(A, B);
+                        store(p + rowA, true, A, nA);
+                        store(p + rowB, true, B, nB);
                     }
                 }
-                if constexpr (MODE == kTurn) {
-                    if constexpr (ANY) __syncwarp();  // windows share words: all are read before any is written
+            } else {
+                Oct A[RB], B[RB], xA[RB], xB[RB];
+                float sum[RB], r[RB];
+                float2 X[RB], xX[RB];
 #pragma unroll
-                    for (int i = 0; i < RB; ++i) {
-                        const uint32_t p = at + i * per * pitch;
-                        if constexpr (KIND == kNeighbours) {
-                            // What is not turned stays where it is, or keeps its bits.
-                            Oct A = oct_unpack<F16>(rawA[i]), B = oct_unpack<F16>(rawB[i]);
-                            turn(A, B);
-                            auto put = [&](uint32_t q, const Oct& o, const uint4& raw, int t) {
-                                uint4 v = oct_pack<F16>(o);
-                                if (t < 4) {
-                                    if (t < 2) v.y = raw.y;
-                                    if (t < 3) v.z = raw.z;
-                                    v.w = raw.w;
-                                }
-                                if (t > 0) sts128(q, v);
-                            };
-                            put(p + rowA, A, rawA[i], tA);
-                            put(p + rowB, B, rawB[i], tB);
-                        } else if (turned) {
-                            Oct A = oct_unpack<F16>(rawA[i]), B = oct_unpack<F16>(rawB[i]);
-                            turn(A, B);
-                            store(p + rowA, true, A, nA);
-                            store(p + rowB, true, B, nB);
+                for (int i = 0; i < RB; ++i) {
+                    const uint32_t p = at + i * per * pitch;
+                    const int row = (i0 + i) * per + head;
+                    float2 sum2 = make_float2(0.0f, 0.0f);
+                    r[i] = 0.0f;
+                    X[i] = xX[i] = make_float2(0.0f, 0.0f);
+                    if (hasX) X[i] = widen2<F16>(lds32(p + rowX));
+                    if constexpr (BWD) {
+                        A[i] = oct_unpack<F16>(rawA[i]);
+                        B[i] = oct_unpack<F16>(rawB[i]);
+                        xA[i] = oct_unpack<F16>(load(p + op_bytes + rowA, hasA, nA));
+                        xB[i] = oct_unpack<F16>(load(p + op_bytes + rowB, hasB, nB));
+                        r[i] = rs[cur * step + row];
+                        turn(A[i], B[i]);
+                        if constexpr (ANY) {  // cosines beyond the half's end
+                            cut(A[i], nA);
+                            cut(B[i], nB);
+                            cut(xA[i], nA);
+                            cut(xB[i], nB);
+                            if (hasX) {
+                                xX[i] = widen2<F16>(lds32(p + op_bytes + rowX));
+                                accX = fma2(X[i], fmul2(xX[i], both(r[i])), accX);
+                                X[i] = fmul2(X[i], wX);
+                            }
                         }
-                    }
-                } else {
-                    Oct A[RB], B[RB], xA[RB], xB[RB];
-                    float sum[RB], r[RB];
-                    float2 X[RB], xX[RB];
 #pragma unroll
-                    for (int i = 0; i < RB; ++i) {
-                        const uint32_t p = at + i * per * pitch;
-                        const int row = (i0 + i) * per + head;
-                        float2 sum2 = make_float2(0.0f, 0.0f);
-                        r[i] = 0.0f;
-                        X[i] = xX[i] = make_float2(0.0f, 0.0f);
-                        if (hasX) X[i] = widen2<F16>(lds32(p + rowX));
-                        if constexpr (BWD) {
-                            A[i] = oct_unpack<F16>(rawA[i]);
-                            B[i] = oct_unpack<F16>(rawB[i]);
-                            xA[i] = oct_unpack<F16>(load(p + op_bytes + rowA, hasA, nA));
-                            xB[i] = oct_unpack<F16>(load(p + op_bytes + rowB, hasB, nB));
-                            r[i] = rs[cur * step + row];
-                            turn(A[i], B[i]);
-                            if constexpr (ANY) {  // cosines beyond the half's end
-                                cut(A[i], nA);
-                                cut(B[i], nB);
-                                cut(xA[i], nA);
-                                cut(xB[i], nB);
-                                if (hasX) {
-                                    xX[i] = widen2<F16>(lds32(p + op_bytes + rowX));
-                                    accX = fma2(X[i], fmul2(xX[i], both(r[i])), accX);
-                                    X[i] = fmul2(X[i], wX);
-                                }
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                accA.p[e] = fma2(A[i].p[e], fmul2(xA[i].p[e], both(r[i])), accA.p[e]);
-                                accB.p[e] = fma2(B[i].p[e], fmul2(xB[i].p[e], both(r[i])), accB.p[e]);
-                                A[i].p[e] = fmul2(A[i].p[e], wA.p[e]);
-                                B[i].p[e] = fmul2(B[i].p[e], wB.p[e]);
-                                sum2 = fma2(A[i].p[e], xA[i].p[e], sum2);
-                                sum2 = fma2(B[i].p[e], xB[i].p[e], sum2);
-                            }
-                            if constexpr (ANY) sum2 = fma2(X[i], xX[i], sum2);
-                            sum[i] = fadd(sum2.x, sum2.y);
-                        } else {
-                            A[i] = oct_unpack<F16>(rawA[i]);
-                            B[i] = oct_unpack<F16>(rawB[i]);
-                            if constexpr (KIND == kHalvesAny) {  // the other half of a word at the end
-                                cut(A[i], nA);
-                                cut(B[i], nB);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                sum2 = fma2(A[i].p[e], A[i].p[e], sum2);
-                                sum2 = fma2(B[i].p[e], B[i].p[e], sum2);
-                            }
-                            if constexpr (ANY) sum2 = fma2(X[i], X[i], sum2);
-                            sum[i] = fadd(sum2.x, sum2.y);
+                        for (int e = 0; e < 4; ++e) {
+                            accA.p[e] = fma2(A[i].p[e], fmul2(xA[i].p[e], both(r[i])), accA.p[e]);
+                            accB.p[e] = fma2(B[i].p[e], fmul2(xB[i].p[e], both(r[i])), accB.p[e]);
+                            A[i].p[e] = fmul2(A[i].p[e], wA.p[e]);
+                            B[i].p[e] = fmul2(B[i].p[e], wB.p[e]);
+                            sum2 = fma2(A[i].p[e], xA[i].p[e], sum2);
+                            sum2 = fma2(B[i].p[e], xB[i].p[e], sum2);
                         }
-                    }
-                    if constexpr (ANY) __syncwarp();  // windows share words: all are read before any is written
-#pragma unroll
-                    for (int i = 0; i < RB; ++i) sum[i] = group_sum<(1 << LG)>(sum[i]);
-#pragma unroll
-                    for (int i = 0; i < RB; ++i) {
-                        const uint32_t p = at + i * per * pitch;
-                        if constexpr (BWD) {
-                            const float coef = -fmul(fmul(fmul(fmul(r[i], r[i]), r[i]), a.rcp_d), sum[i]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                A[i].p[e] = fma2(A[i].p[e], both(r[i]), fmul2(xA[i].p[e], both(coef)));
-                                B[i].p[e] = fma2(B[i].p[e], both(r[i]), fmul2(xB[i].p[e], both(coef)));
-                            }
-                            if (hasX) sts32(p + rowX, narrow2<F16>(fma2(X[i], both(r[i]), fmul2(xX[i], both(coef)))));
-                        } else {
-                            r[i] = rsqrtf(fadd(fmul(sum[i], a.rcp_d), a.eps));
-                            if (l == 0) rs[cur * step + (i0 + i) * per + head] = r[i];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                A[i].p[e] = fmul2(fmul2(A[i].p[e], both(r[i])), wA.p[e]);
-                                B[i].p[e] = fmul2(fmul2(B[i].p[e], both(r[i])), wB.p[e]);
-                            }
-                            turn(A[i], B[i]);
-                            if (hasX) sts32(p + rowX, narrow2<F16>(fmul2(fmul2(X[i], both(r[i])), wX)));
+                        if constexpr (ANY) sum2 = fma2(X[i], xX[i], sum2);
+                        sum[i] = fadd(sum2.x, sum2.y);
+                    } else {
+                        A[i] = oct_unpack<F16>(rawA[i]);
+                        B[i] = oct_unpack<F16>(rawB[i]);
+                        if constexpr (KIND == kHalvesAny) {  // the other half of a word at the end
+                            cut(A[i], nA);
+                            cut(B[i], nB);
                         }
-                        store(p + rowA, hasA, A[i], nA);
-                        store(p + rowB, hasB, B[i], nB);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            sum2 = fma2(A[i].p[e], A[i].p[e], sum2);
+                            sum2 = fma2(B[i].p[e], B[i].p[e], sum2);
+                        }
+                        if constexpr (ANY) sum2 = fma2(X[i], X[i], sum2);
+                        sum[i] = fadd(sum2.x, sum2.y);
                     }
                 }
-            };
+                if constexpr (ANY) __syncwarp();  // windows share words: all are read before any is written
 #pragma unroll
-            for (int i0 = 0; i0 < NR; i0 += RBATCH) {
-                const int rest = n - i0 * per;
-                if (rest <= 0) break;  // the same for all lanes
-                if (RBATCH > 1 && rest <= per) batch(std::integral_constant<int, 1>(), i0);
-                else batch(std::integral_constant<int, RBATCH>(), i0);
-            }
-            fence_proxy_async_smem();  // the results, before the copy that sends them and the one that refills the stage
-            __syncwarp();
-            if (lane == 0) {
-                const HeadsOut& o = a.out[s];
-                uint16_t* p = o.p + now.t * o.token + now.h * o.head;
-                if (a.dense[2][s]) {
-                    bulk_s2g(p, st, n * pitch, pol);
-                } else {
-                    const uint32_t bytes = a.row_bytes[s];
-                    for (int i = 0; i < n; ++i, p += o.head) bulk_s2g(p, st + i * pitch, bytes, pol);
+                for (int i = 0; i < RB; ++i) sum[i] = group_sum<(1 << LG)>(sum[i]);
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+                    const uint32_t p = at + i * per * pitch;
+                    if constexpr (BWD) {
+                        const float coef = -fmul(fmul(fmul(fmul(r[i], r[i]), r[i]), a.rcp_d), sum[i]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            A[i].p[e] = fma2(A[i].p[e], both(r[i]), fmul2(xA[i].p[e], both(coef)));
+                            B[i].p[e] = fma2(B[i].p[e], both(r[i]), fmul2(xB[i].p[e], both(coef)));
+                        }
+                        if (hasX) sts32(p + rowX, narrow2<F16>(fma2(X[i], both(r[i]), fmul2(xX[i], both(coef)))));
+                    } else {
+                        r[i] = rsqrtf(fadd(fmul(sum[i], a.rcp_d), a.eps));
+                        if (l == 0) rs[cur * step + (i0 + i) * per + head] = r[i];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            A[i].p[e] = fmul2(fmul2(A[i].p[e], both(r[i])), wA.p[e]);
+                            B[i].p[e] = fmul2(fmul2(B[i].p[e], both(r[i])), wB.p[e]);
+                        }
+                        turn(A[i], B[i]);
+                        if (hasX) sts32(p + rowX, narrow2<F16>(fmul2(fmul2(X[i], both(r[i])), wX)));
+                    }
+                    store(p + rowA, hasA, A[i], nA);
+                    store(p + rowB, hasB, B[i], nB);
                 }
-                bulk_commit();
-                bulk_wait_read<1>();  // the stage of the turn before is sent: it is filled next
             }
-            if constexpr (NORM && !BWD) {
-                float* p = a.rstd[s] + static_cast<int64_t>(now.t) * a.H[s] + now.h;
+        };
 #pragma unroll
-                for (int i = 0; i < step; i += 32)
-                    if (i + lane < n) p[i + lane] = rs[cur * step + i + lane];
-            }
-            if (++cur == S) {
-                cur = 0;
-                phase ^= 1u;
-            }
-            now.next(Hq, Hk, step);
-            fetch();
+        for (int i0 = 0; i0 < NR; i0 += RBATCH) {
+            const int rest = n - i0 * per;
+            if (rest <= 0) break;  // the same for all lanes
+            if (RBATCH > 1 && rest <= per) batch(std::integral_constant<int, 1>(), i0);
+            else batch(std::integral_constant<int, RBATCH>(), i0);
         }
-        if (lane == 0) bulk_wait_all();
-        if constexpr (BWD) {
-            cp_async_wait<0>();
-            // The groups' sums in group order, through the stages' memory.
-            float* part = reinterpret_cast<float*>(smem);  // [groups][D]
-            const int groups = nt >> LG, group = tid >> LG;
-            fence_proxy_async_smem();
-            __syncthreads();
+        fence_proxy_async_smem();  // the results, before the copy that sends them and the one that refills the stage
+        __syncwarp();
+        if (lane == 0) {
+            const HeadsOut& o = a.out[s];
+            uint16_t* p = o.p + now.t * o.token + now.h * o.head;
+            if (a.dense[2][s]) {
+                bulk_s2g(p, st, n * pitch, pol);
+            } else {
+                const uint32_t bytes = a.row_bytes[s];
+                for (int i = 0; i < n; ++i, p += o.head) bulk_s2g(p, st + i * pitch, bytes, pol);
+            }
+            bulk_commit();
+            bulk_wait_read<1>();  // the stage of the turn before is sent: it is filled next
+        }
+        if constexpr (NORM && !BWD) {
+            float* p = a.rstd[s] + static_cast<int64_t>(now.t) * a.H[s] + now.h;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (e < nA) part[group * D + atA + e] = e & 1 ? accA.p[e / 2].y : accA.p[e / 2].x;
-                if (e < nB) part[group * D + atB + e] = e & 1 ? accB.p[e / 2].y : accB.p[e / 2].x;
-            }
-            if (hasX) *reinterpret_cast<float2*>(part + group * D + atX) = accX;
-            __syncthreads();
-            float* row = a.partials + (static_cast<int64_t>(pass) * gridDim.x + blockIdx.x) * D;
-            for (int col = tid; col < D; col += nt) {
-                float v = part[col];
-                for (int g = 1; g < groups; ++g) v = fadd(v, part[g * D + col]);
-                row[col] = v;
-            }
-            fence_proxy_async_smem();
-            __syncthreads();  // before the next pass fills the stages
+            for (int i = 0; i < step; i += 32)
+                if (i + lane < n) p[i + lane] = rs[cur * step + i + lane];
+        }
+        if (++cur == S) {
+            cur = 0;
+            phase ^= 1u;
+        }
+        now.next(Hq, Hk, step);
+        fetch();
+    }
+    if (lane == 0) bulk_wait_all();
+    if constexpr (BWD) {
+        cp_async_wait<0>();
+        // The groups' sums in group order, through the stages' memory.
+        float* part = reinterpret_cast<float*>(smem);  // [groups][D]
+        const int groups = nt >> LG, group = tid >> LG;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e < nA) part[group * D + atA + e] = e & 1 ? accA.p[e / 2].y : accA.p[e / 2].x;
+            if (e < nB) part[group * D + atB + e] = e & 1 ? accB.p[e / 2].y : accB.p[e / 2].x;
+        }
+        if (hasX) *reinterpret_cast<float2*>(part + group * D + atX) = accX;
+        __syncthreads();
+        float* row = a.partials + static_cast<int64_t>(blockIdx.x) * D;
+        for (int col = tid; col < D; col += nt) {
+            float v = part[col];
+            for (int g = 1; g < groups; ++g) v = fadd(v, part[g * D + col]);
+            row[col] = v;
         }
     }
     pdl_release();
@@ -645,7 +642,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
 // Launchers
 // ---------------------------------------------------------------------------
 template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
-cudaError_t rope_run_kernel(const RopeArgs& a, cudaStream_t st) {
+cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
     constexpr int step = (32 >> LG) * NR;
     const auto kern = rope_kernel<MODE, KIND, F16, LG, FULL, NR, RB, S, MINB>;
@@ -669,69 +666,70 @@ cudaError_t rope_run_kernel(const RopeArgs& a, cudaStream_t st) {
         if (occ < 1) return cudaErrorInvalidConfiguration;
         grid = std::min<int64_t>((turns + threads / 32 - 1) / (threads / 32), sms * occ);
     }
-    return launch_kernel(kern, static_cast<unsigned>(grid), threads, smem, st, a);
+    RopeArgs b = a;
+    if (BWD && a.H[1] > 0) {
+        // The CTAs split by the work of a token: one for a batch of heads, four for a
+        // turn, whose chain of waits counts most (32 + 8 heads of 64: 76 % of the copy
+        // rate; by batches alone 64 %, by turns alone 73 %).
+        auto cost = [&](int64_t H) {
+            constexpr int64_t batch = (32 >> LG) * RB;
+            return H / step * (NR / RB) + (H % step + batch - 1) / batch + 4 * ((H + step - 1) / step);
+        };
+        const int64_t q = cost(a.H[0]), k = cost(a.H[1]);
+        b.ctas_q = static_cast<int>(std::min(std::max<int64_t>((grid * q + (q + k) / 2) / (q + k), 1), grid - 1));
+    } else {
+        b.ctas_q = static_cast<int>(grid);
+    }
+    *ctas_q = b.ctas_q;
+    return launch_kernel(kern, static_cast<unsigned>(grid), threads, smem, st, b);
 }
 
-#ifndef RP_T
-#define RP_T 4, 1, 2, 3
-#endif
-#ifndef RP_F
-#define RP_F 4, 2, 3, 2
-#endif
-#ifndef RP_FF
-#define RP_FF 2, 1, 3, 2
-#endif
-#ifndef RP_B
-#define RP_B 3, 1, 2, 2
-#endif
-#ifndef RP_B4
-#define RP_B4 4, 1, 2, 2
-#endif
-#ifndef RP_B5
-#define RP_B5 2, 1, 2, 2
-#endif
-
+// Heads a group and turn, of them in registers at a time, stages, CTAs an SM: the
+// fastest measured of each kind. More heads a turn cost fewer turns' waits and
+// more shared memory, which has to leave room for two CTAs an SM.
 template <int MODE, int KIND, bool F16, int LG, bool FULL>
-cudaError_t rope_shape_of(const RopeArgs& a, cudaStream_t st) {
+cudaError_t rope_shape_of(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     if constexpr (MODE == kTurn) {
-        return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_T>(a, st);
+        return rope_run_kernel<MODE, KIND, F16, LG, FULL, 4, 1, 2, 3>(a, ctas_q, st);
     } else if constexpr (MODE == kNormTurn) {
-        if constexpr (FULL && LG < 5) return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_FF>(a, st);
-        else return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_F>(a, st);
+        // 16384 x 32 + 8 x 128: 84 % of the copy rate (with 4 heads 80); 80 wide: 78 % (with 2 heads 61).
+        if constexpr (FULL && LG < 5) return rope_run_kernel<MODE, KIND, F16, LG, FULL, 2, 1, 3, 2>(a, ctas_q, st);
+        else return rope_run_kernel<MODE, KIND, F16, LG, FULL, 4, 2, 3, 2>(a, ctas_q, st);
+    } else if constexpr (LG == 5) {
+        return rope_run_kernel<MODE, KIND, F16, LG, FULL, 2, 1, 2, 2>(a, ctas_q, st);  // 3 heads: one CTA an SM, 58 % for 76
+    } else if constexpr (FULL && LG != 3) {
+        return rope_run_kernel<MODE, KIND, F16, LG, FULL, 2, 1, 3, 2>(a, ctas_q, st);
     } else {
-        if constexpr (LG == 5) {
-            return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_B5>(a, st);
-        } else {
-            if constexpr (!FULL)
-                if (4 * a.D <= 3 * (16 << LG)) return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_B4>(a, st);
-            return rope_run_kernel<MODE, KIND, F16, LG, FULL, RP_B>(a, st);
-        }
+        if constexpr (!FULL)  // narrower than its lanes could hold: four heads fit (80 wide: 70 % for 62)
+            if (4 * a.D <= 3 * (16 << LG)) return rope_run_kernel<MODE, KIND, F16, LG, FULL, 4, 1, 2, 2>(a, ctas_q, st);
+        return rope_run_kernel<MODE, KIND, F16, LG, FULL, 3, 1, 2, 2>(a, ctas_q, st);
     }
 }
 
 template <int MODE, int KIND, bool F16, int LG>
-cudaError_t rope_full(const RopeArgs& a, cudaStream_t st) {
+cudaError_t rope_full(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     if constexpr (KIND == kHalves || KIND == kNeighbours)
-        if (a.D == 16 << LG) return rope_shape_of<MODE, KIND, F16, LG, true>(a, st);
-    return rope_shape_of<MODE, KIND, F16, LG, false>(a, st);
+        if (a.D == 16 << LG) return rope_shape_of<MODE, KIND, F16, LG, true>(a, ctas_q, st);
+    return rope_shape_of<MODE, KIND, F16, LG, false>(a, ctas_q, st);
 }
 
 template <int MODE, int KIND, bool F16>
-cudaError_t rope_lanes(const RopeArgs& a, cudaStream_t st) {
+cudaError_t rope_lanes(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     switch (rope_lanes_log2(a.D, a.R, KIND == kHalvesAny || KIND == kHalves8, MODE != kTurn)) {
-        case 2: return rope_full<MODE, KIND, F16, 2>(a, st);
-        case 3: return rope_full<MODE, KIND, F16, 3>(a, st);
-        case 4: return rope_full<MODE, KIND, F16, 4>(a, st);
-        default: return rope_full<MODE, KIND, F16, 5>(a, st);
+        case 2: return rope_full<MODE, KIND, F16, 2>(a, ctas_q, st);
+        case 3: return rope_full<MODE, KIND, F16, 3>(a, ctas_q, st);
+        case 4: return rope_full<MODE, KIND, F16, 4>(a, ctas_q, st);
+        default: return rope_full<MODE, KIND, F16, 5>(a, ctas_q, st);
     }
 }
 
+// *ctas_q: the CTAs (and so the partial rows) of q in a norm backward.
 template <int MODE, bool F16>
-cudaError_t rope_kinds(const RopeArgs& a, cudaStream_t st) {
-    if (a.layout == ROPE_INTERLEAVED) return rope_lanes<MODE, kNeighbours, F16>(a, st);
-    if (a.R % 16 == 0) return rope_lanes<MODE, kHalves, F16>(a, st);
-    if (a.R % 8 == 0) return rope_lanes<MODE, kHalves8, F16>(a, st);
-    return rope_lanes<MODE, kHalvesAny, F16>(a, st);
+cudaError_t rope_kinds(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
+    if (a.layout == ROPE_INTERLEAVED) return rope_lanes<MODE, kNeighbours, F16>(a, ctas_q, st);
+    if (a.R % 16 == 0) return rope_lanes<MODE, kHalves, F16>(a, ctas_q, st);
+    if (a.R % 8 == 0) return rope_lanes<MODE, kHalves8, F16>(a, ctas_q, st);
+    return rope_lanes<MODE, kHalvesAny, F16>(a, ctas_q, st);
 }
 
 }  // namespace

@@ -25,13 +25,14 @@ struct RopeArgs {
     HeadsOut out[2];
     const float* w[2];   // norm weights
     float* rstd[2];      // written by the forward, read by the backward
-    float* partials;     // norm backward: [chunks][D] of dwq, then of dwk
+    float* partials;     // norm backward: a row of D a CTA, dwq's, then dwk's
     const double* inv_freq;
     const void* pos;     // null: the token's index
     int64_t T;
     int H[2];
     int D, R, layout, pos64, back, zc;
     float scale, eps;
+    int ctas_q;          // norm backward: CTAs whose turns are q's
     float rcp_d;         // 1/D rounded to fp32
     bool dense[3][2];    // [in | x | out]: a token's heads lie side by side and are copied whole
     uint32_t row_bytes[2];  // of a head's row to copy: all of it, or in place what is turned
@@ -56,21 +57,21 @@ inline int rope_lanes_log2(int D, int R, bool any_halves, bool norm) {
     return lg;
 }
 
-// CTAs of the norm backward, each with one partial row of dwq and of dwk: two an
-// SM of a GPU of 152, fewer where there are few heads. A function of T, Hq, Hk
+// CTAs of the norm backward, each with a partial row of dwq or of dwk: two an SM
+// of a GPU of 152, fewer where there are few heads. A function of T, Hq, Hk
 // and D alone.
 inline int64_t rope_bwd_ctas(int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
-    const int64_t values = T * std::max(Hq, Hk) * D;  // of a warp's turn: about 1024
-    return std::max<int64_t>(1, std::min<int64_t>(304, (values + 8191) / 8192));
+    const int64_t values = T * (Hq + Hk) * D;  // of a warp's turn: about 1024
+    return std::max<int64_t>(Hk > 0 ? 2 : 1, std::min<int64_t>(304, (values + 8191) / 8192));
 }
 
 // The kernels by mode and format, each in a translation unit of its own.
-cudaError_t launch_rope_turn(const RopeArgs& a, cudaStream_t s);
-cudaError_t launch_rope_norm(const RopeArgs& a, cudaStream_t s);
-cudaError_t launch_rope_norm_bwd(const RopeArgs& a, cudaStream_t s);
-cudaError_t launch_rope_turn_f16(const RopeArgs& a, cudaStream_t s);
-cudaError_t launch_rope_norm_f16(const RopeArgs& a, cudaStream_t s);
-cudaError_t launch_rope_norm_bwd_f16(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_turn(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+cudaError_t launch_rope_norm(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+cudaError_t launch_rope_norm_bwd(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+cudaError_t launch_rope_turn_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+cudaError_t launch_rope_norm_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+cudaError_t launch_rope_norm_bwd_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
 cudaError_t rope_turn_read_error(unsigned* flags, bool clear);
 cudaError_t rope_norm_read_error(unsigned* flags, bool clear);
 cudaError_t rope_norm_bwd_read_error(unsigned* flags, bool clear);

@@ -5,6 +5,6 @@
 namespace rmsn {
 
 cudaError_t rope_norm_read_error(unsigned* flags, bool clear) { return read_rope_error_word(flags, clear); }
-cudaError_t launch_rope_norm(const RopeArgs& a, cudaStream_t s) { return rope_kinds<kNormTurn, false>(a, s); }
+cudaError_t launch_rope_norm(const RopeArgs& a, int* ctas_q, cudaStream_t s) { return rope_kinds<kNormTurn, false>(a, ctas_q, s); }
 
 }  // namespace rmsn

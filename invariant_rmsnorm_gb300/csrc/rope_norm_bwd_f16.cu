@@ -5,6 +5,6 @@
 namespace rmsn {
 
 cudaError_t rope_norm_bwd_f16_read_error(unsigned* flags, bool clear) { return read_rope_error_word(flags, clear); }
-cudaError_t launch_rope_norm_bwd_f16(const RopeArgs& a, cudaStream_t s) { return rope_kinds<kNormTurnBwd, true>(a, s); }
+cudaError_t launch_rope_norm_bwd_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s) { return rope_kinds<kNormTurnBwd, true>(a, ctas_q, s); }
 
 }  // namespace rmsn
