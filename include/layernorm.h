@@ -22,8 +22,7 @@
  *
  * Batch invariance: y[t], mean[t], rstd[t] and dx[t] are bitwise independent of
  * T, of the row's position, of the other rows and of the GPU's SM count: a
- * row's reduction tree is a function of D alone (in the backward also of
- * whether db is asked for). dw and db are summed with no atomics, over row
+ * row's reduction tree is a function of D alone. dw and db are summed with no atomics, over row
  * chunks whose size depends on T and D alone and then over the chunks in a
  * fixed order: the same bits from run to run and on GPUs with different SM counts.
  */

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     }
     __syncthreads();
     long long p32 = 0;  // lane i: the position of token t32 + i
-    int t32 = -32;
+    int64_t t32 = -32;
     Oct accA = oct_zero(), accB = oct_zero(), wA = oct_zero(), wB = oct_zero();
     float2 accX = make_float2(0.0f, 0.0f), wX = accX;
     Oct c = oct_zero(), sn = oct_zero();  // cos and sin of this lane's pairs (kNeighbours: four of A, four of B)
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                 t32 = t_have;
                 if (t32 + lane < a.T) p32 = position(a, t32 + lane);
             }
-            token_angles(cs, hp, half, F, __shfl_sync(0xffffffffu, p32, t_have - t32), a.scale, BWD || a.back, lane);
+            token_angles(cs, hp, half, F, __shfl_sync(0xffffffffu, p32, static_cast<int>(t_have - t32)), a.scale, BWD || a.back, lane);
             if constexpr (KIND == kNeighbours) {
                 const float4* q = reinterpret_cast<const float4*>(cs);
                 const int iA = min(atA >> 3, (hp >> 2) - 1), iB = min(atB >> 3, (hp >> 2) - 1);

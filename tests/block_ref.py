@@ -3,7 +3,7 @@ bits, as plainly as their definitions, with bounds on the fp32 kernels' errors.
 
 u = 2^-24 is half a step of fp32, one rounding's relative error. K = 96 bounds
 the additions on one path of a row's sum: at most 64 values a thread, 5 steps of
-a warp's butterfly, at most 16 warps' totals, two CTAs' halves, and slack. Every
+a warp's butterfly, at most 16 warps' totals, and slack. Every
 bound below is a sum of |term| * (roundings on the term's way) * u; an output in
 16 bits adds half a step of its format at the larger of the two values compared.
 """
@@ -97,9 +97,10 @@ def turned(x, pos, inv_freq, scale, interleaved, back=False):
     return out, size
 
 
-# A turned value's error over scale * (|u| + |v|): the angle (pi 2^-25 for the
-# phase as a float, and |a| 2^-51 for the frequency, below 2^-28 here), cos and
-# sin (an ulp below 1), the scale, a product, a sum: under 8 u.
+# A turned value's error over scale * (|u| + |v|), in u: the angle, 1.6 (below a
+# quarter turn it is rounded twice as fp32; the phase's 2^-33 turns and the
+# frequency's |a| 2^-51 are far less here); the series of sine and cosine, 1.5; the
+# scale, 1; a product and a fused sum, 2. Together under 8.
 TURN = 8 * U
 
 

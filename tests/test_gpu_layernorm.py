@@ -156,6 +156,56 @@ def test_weight_gradients_are_the_same_from_run_to_run(T, D):
         assert torch.equal(first[1].view(torch.int16), again[1].view(torch.int16))
 
 
+@pytest.mark.parametrize("T,D", [(300, 96), (300, 520), (200, 4096), (100, 12296)])
+def test_the_bias_gradient_changes_nothing_else(T, D):
+    x, g, w, b = _inputs(T, D, 25)
+    _, _, mean, rstd = _fwd(x, w, b)
+    _, dx, dw, _ = _bwd(g, x, w, mean, rstd)
+    _, dx2, dw2, _ = _bwd(g, x, w, mean, rstd, bias=False)
+    assert torch.equal(dx.view(torch.int16), dx2.view(torch.int16)) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("T,D", [((1 << 31) // 16384 + 3, 16384), ((1 << 31) // 128 + 5, 128)])
+def test_rows_beyond_two_to_the_31_values(T, D):
+    """The last rows of a tensor of more than 2^31 values, against the same rows on their own."""
+    x = torch.zeros((T, D), dtype=BF16, device=DEV)
+    g = torch.zeros((T, D), dtype=BF16, device=DEV)
+    tx, tg, w, b = _inputs(4, D, 61)
+    x[-4:], g[-4:] = tx, tg
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    dw, db = torch.empty(D, device=DEV), torch.empty(D, device=DEV)
+    ws = torch.empty(rn.layernorm_bwd_workspace_bytes(T, D), dtype=torch.uint8, device=DEV)
+    rn.layernorm_fwd(x, w, b, y, mean, rstd, EPS)
+    rn.layernorm_bwd(g, x, w, mean, rstd, dx, dw, db, ws)
+    _, ty, tm, tr = _fwd(tx, w, b)
+    _, tdx, tdw, tdb = _bwd(tg, tx, w, tm, tr)
+    assert torch.equal(y[-4:].view(torch.int16), ty.view(torch.int16)) and torch.equal(rstd[-4:], tr)
+    assert torch.equal(dx[-4:].view(torch.int16), tdx.view(torch.int16))
+    # the rows of zeros add zeros: the sums are those of four rows in some order
+    n = (tx.double() - tm.double()[:, None]) * tr.double()[:, None]
+    ref.assert_within("dw", dw, (tg.double() * n).sum(0), 8 * ref.U * (tg.double() * n).abs().sum(0))
+    ref.assert_within("db", db, tg.double().sum(0), 8 * ref.U * tg.double().abs().sum(0))
+
+
+def test_the_binding_refuses_what_would_be_read_wrongly():
+    x, g, w, b = _inputs(8, 128, 71)
+    y, m, r = torch.empty_like(x), torch.empty(8, device=DEV), torch.empty(8, device=DEV)
+    for bad in (dict(w=w.half()), dict(w=w.cpu()), dict(w=w[:64]), dict(w=w.repeat(2)[::2]), dict(b=b.double()),
+                dict(y=y.half()), dict(y=y.cpu()), dict(mean=m[:4]), dict(rstd=r.half())):
+        a = {**dict(w=w, b=b, y=y, mean=m, rstd=r), **bad}
+        with pytest.raises(TypeError):
+            rn.layernorm_fwd(x, a["w"], a["b"], a["y"], a["mean"], a["rstd"])
+    with pytest.raises(ValueError):
+        rn.layernorm_fwd(x, w, b, y[:4], m, r)
+    with pytest.raises(ValueError):
+        rn.layernorm_fwd(x.t().contiguous().t(), w, b, y, m, r)
+    with pytest.raises(TypeError):
+        rn.layernorm_fwd(x.float(), w, b, y, m, r)
+    with pytest.raises(rn.RmsNormError, match="EALIGN"):
+        rn.layernorm_fwd(x, torch.empty(129, device=DEV)[1:], b, y, m, r)
+
+
 def test_no_rows():
     x, g, w, b = _inputs(0, 128, 1)
     _fwd(x, w, b)

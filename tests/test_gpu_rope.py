@@ -154,6 +154,87 @@ def test_nan_and_infinity_stay_in_their_pair():
         assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("Hq,Hk", [(1, 0), (1, 1), (7, 3), (40, 1), (2, 33), (128, 8)])
+@pytest.mark.parametrize("D,R,inter", [(128, 128, False), (64, 64, True), (96, 24, False), (256, 64, False), (16, 16, False)])
+def test_any_number_of_heads(Hq, Hk, D, R, inter):
+    """Turns of warps that are not full, of q, of k and of both; more tokens than a batch of positions."""
+    for T in (1, 45, 400):
+        _check_norm(T, Hq, Hk, D, R, inter, BF16, "qkv", False, seed=T)
+
+
+def test_more_than_two_to_the_31_values():
+    """The last tokens of tensors of more than 2^31 values, against the same tokens on their own."""
+    T, H, D, R = (1 << 31) // (32 * 512) + 7, 32, 512, 512
+    tq, _ = _heads(3, H, 0, D, 93)
+    tg, _ = _heads(3, H, 0, D, 94)
+    q = torch.zeros((T, H, D), dtype=BF16, device=DEV)
+    g = torch.zeros((T, H, D), dtype=BF16, device=DEV)
+    q[-3:], g[-3:] = tq, tg
+    w, _ = _weights(D, 0, 95, False)
+    f = _freq(R)
+    pos = torch.arange(T, device=DEV)
+    o, d = torch.empty_like(q), torch.empty_like(q)
+    rstd, dw = torch.empty((T, H), device=DEV), torch.empty(D, device=DEV)
+    ws = torch.empty(rn.rmsnorm_rope_bwd_workspace_bytes(T, H, 0, D), dtype=torch.uint8, device=DEV)
+    rn.rmsnorm_rope_fwd(q, None, w, None, f, o, None, rstd, None, pos, SCALE, False, EPS)
+    (_, to, tr), _ = _norm_fwd(tq, None, w, None, f, pos[-3:].clone())
+    assert torch.equal(_bits(o[-3:]), _bits(to)) and torch.equal(rstd[-3:], tr)
+    rn.rmsnorm_rope_bwd(g, None, q, None, w, None, f, rstd, None, d, None, dw, None, ws, pos, SCALE, False)
+    (_, td, tdw), _ = _norm_bwd(tg, None, tq, None, w, None, f, tr, None, pos[-3:].clone())
+    assert torch.equal(_bits(d[-3:]), _bits(td))
+    torch.testing.assert_close(dw, tdw, rtol=1e-4, atol=1e-4)  # 96 rows in another order, the others zero
+    rn.rope_fwd(q, None, f, o, None, pos, SCALE)
+    to2 = torch.empty_like(tq)
+    rn.rope_fwd(tq, None, f, to2, None, pos[-3:].clone(), SCALE)
+    assert torch.equal(_bits(o[-3:]), _bits(to2))
+
+
+def test_two_streams_at_once():
+    """Two backwards that overlap, each with a workspace of its own."""
+    T, D = 3000, 128
+    runs = []
+    for seed in (101, 102):
+        q, k = _heads(T, 8, 2, D, seed)
+        g, h = _heads(T, 8, 2, D, seed + 10)
+        wq, wk = _weights(D, 2, seed, False)
+        (_, _, r), (_, _, rk) = _norm_fwd(q, k, wq, wk, _freq(D), None)
+        runs.append((g, h, q, k, wq, wk, _freq(D), r, rk, None))
+    alone = [_norm_bwd(*a) for a in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(5):
+        got = []
+        for st, a in zip(streams, runs):
+            with torch.cuda.stream(st):
+                got.append(_norm_bwd(*a))
+        torch.cuda.synchronize()
+        for x, y in zip(alone, got):
+            for i in (0, 1):
+                assert torch.equal(_bits(x[i][1]), _bits(y[i][1])) and torch.equal(x[i][2], y[i][2])
+
+
+def test_the_binding_refuses_what_would_be_read_wrongly():
+    q, k = _heads(8, 4, 2, 64, 111)
+    f = _freq(64)
+    oq, ok = torch.empty_like(q), torch.empty_like(k)
+    p = torch.arange(8, device=DEV)
+    for a, e in (((q.float(), k, f, oq, ok, p), TypeError), ((q, k.half(), f, oq, ok, p), TypeError),
+                 ((q, k.cpu(), f, oq, ok, p), TypeError), ((q, k, f.float(), oq, ok, p), TypeError),
+                 ((q, k, f.cpu(), oq, ok, p), TypeError), ((q, k, f, oq, ok, p.float()), TypeError),
+                 ((q, k, f, oq, ok, p[:4]), TypeError), ((q, k, f, oq, None, p), TypeError),
+                 ((q, k, f, oq[:, :2], ok, p), ValueError), ((q, k[:4], f, oq, ok, p), ValueError),
+                 ((q.transpose(1, 2), None, f, oq, None, p), ValueError), ((q[0], None, f, oq, None, p), TypeError),
+                 ((q, None, f[None], oq, None, p), TypeError), ((q, k, _freq(66), oq, ok, p), rn.RmsNormError)):
+        with pytest.raises(e):
+            rn.rope_fwd(*a)
+    wq, wk = _weights(64, 2, 5, False)
+    rq, rk = torch.empty((8, 4), device=DEV), torch.empty((8, 2), device=DEV)
+    for bad in (dict(wk=None), dict(wq=wq.half()), dict(rk=rk[:, :1]), dict(rq=rq.t())):
+        a = {**dict(wq=wq, wk=wk, rq=rq, rk=rk), **bad}
+        with pytest.raises(TypeError):
+            rn.rmsnorm_rope_fwd(q, k, a["wq"], a["wk"], f, oq, ok, a["rq"], a["rk"], p)
+
+
 def test_shared_heads_and_broadcast_inputs():
     """An input of stride 0 over its heads is read once for each of them."""
     x = synth.normal16((50, 1, 64), 5, DEV)
