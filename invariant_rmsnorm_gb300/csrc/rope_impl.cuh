@@ -12,9 +12,11 @@
 // percent of its work.
 //
 // A warp takes a turn of up to NR x 32 / G heads of one token at a time, G lanes a
-// head (the smallest power of two that holds its units). The turns of a launch are
-// split among its warps in contiguous ranges, so a warp computes a token's cosines
-// once for all its heads and keeps those of its lanes' pairs in registers. Rows come
+// head (the smallest power of two that holds its units); or, where a token has few
+// heads (MANY), of up to NR heads each of 32 / G tokens, a token a group of lanes.
+// The turns of a launch are split among its warps in contiguous ranges, so a warp
+// computes a token's cosines once for all its heads (MANY: every lane those of its
+// own pairs) and keeps those of its lanes' pairs in registers. Rows come
 // and go by bulk (TMA) copies between HBM and a ring of S stages in the warp's own
 // shared memory: lanes read their values there, overwrite them with the results,
 // and one lane sends the stage back. Warps never wait for one another; dw is
@@ -239,25 +241,28 @@ enum RopeKind : int { kHalves = 0, kNeighbours = 1, kHalvesAny = 2, kHalves8 = 3
 // ---------------------------------------------------------------------------
 // The kernel: 2^LG lanes a head, NR heads a group and turn, RB of them at a time.
 // FULL: every lane has a whole unit (D = 16 x 2^LG, no unit cut short).
+// MANY: a turn is of a token a group.
 // ---------------------------------------------------------------------------
-template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RBATCH, int S, int MINB>
+template <int MODE, int KIND, bool F16, int LG, bool FULL, bool MANY, int NR, int RBATCH, int S, int MINB>
 __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs a) {
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
     constexpr bool ANY = KIND == kHalvesAny || KIND == kHalves8;  // units may be cut short
-    constexpr int OPS = BWD ? 2 : 1, per = 32 >> LG, step = per * NR;
-    static_assert(NR % RBATCH == 0 && !(FULL && ANY), "whole batches; cut units are not full");
+    constexpr int OPS = BWD ? 2 : 1, per = 32 >> LG, rows = per * NR;
+    static_assert(NR % RBATCH == 0 && RBATCH <= 2 && !(FULL && ANY), "whole batches; cut units are not full");
+    // A turn's heads: of one token, group g taking the i-th g + i per; or of per tokens, one a group.
+    constexpr int tokens = MANY ? per : 1, step = MANY ? NR : rows, spread = MANY ? 1 : per;
     extern __shared__ __align__(128) unsigned char smem[];
     const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     const int D = FULL ? 16 << LG : a.D, half = a.R >> 1, hp = (half + 7) & ~7;
     const int l = lane & ((1 << LG) - 1), head = lane >> LG;
     const uint32_t pitch = static_cast<uint32_t>(D) * 2u;
-    const uint32_t op_bytes = step * pitch, stage_bytes = OPS * op_bytes;
+    const uint32_t op_bytes = rows * pitch, stage_bytes = OPS * op_bytes;
     // Shared memory: every warp's stages; weights [q | k][D]; every warp's [cos | sin][hp];
-    // every warp's inverse RMS [S][step] (read backward, gathered forward); barriers; frequencies.
+    // every warp's inverse RMS [S][rows] (read backward, gathered forward); barriers; frequencies.
     float* wsm = reinterpret_cast<float*>(smem + static_cast<size_t>(nw) * S * stage_bytes);
     float* cs = wsm + (NORM ? 2 * D : 0) + warp * 2 * hp;
-    float* rs = wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (NORM ? warp * S * step : 0);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (NORM ? nw * S * step : 0));
+    float* rs = wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (NORM ? warp * S * rows : 0);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (NORM ? nw * S * rows : 0));
     unsigned long long* F = reinterpret_cast<unsigned long long*>(bars + nw * S);
     uint64_t* full = bars + warp * S;
     const uint32_t ring = smem_u32(smem) + warp * S * stage_bytes;
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     // kHalvesAny: two values beyond the lanes' units, if there are any for this lane.
     const int atX = ANY && NORM ? a.R + 16 * ((1 << LG) - NP) + 2 * l : D;
     const bool hasX = ANY && NORM && atX < D;
-    const uint32_t rowA = head * pitch + 2u * atA, rowB = head * pitch + 2u * atB, rowX = head * pitch + 2u * atX;
+    const uint32_t rowA = 2u * atA, rowB = 2u * atB, rowX = 2u * atX;
     // kNeighbours: pairs of A and of B that are turned (past 4: all).
     const int tA = hasA ? half - (atA >> 1) : 0, tB = hasB ? half - (atB >> 1) : 0;
 
@@ -326,33 +331,39 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     const int Hq = of_k ? 0 : a.H[0], Hk = BWD && !of_k ? 0 : a.H[1];
     const int cta = blockIdx.x - (of_k ? a.ctas_q : 0);
     const int ctas = !BWD ? gridDim.x : of_k ? gridDim.x - a.ctas_q : a.ctas_q;
-    Turns now(a.T, (Hq + step - 1) / step, (Hk + step - 1) / step, step, static_cast<int64_t>(cta) * nw + warp,
+    Turns now((a.T + tokens - 1) / tokens, (Hq + step - 1) / step, (Hk + step - 1) / step, step, static_cast<int64_t>(cta) * nw + warp,
               static_cast<int64_t>(ctas) * nw);
     Turns ahead = now;
+    // Place of row r (n heads a token) among the heads of all tokens.
+    auto in_tokens = [](int r, int n, int H) { return n == H ? r : r / n * H + r % n; };
     int fs = 0;
     auto fetch = [&]() {
         if (ahead.left > 0) {
             const int s = ahead.s, n = min(step, a.H[s] - ahead.h);
+            const int64_t t0 = static_cast<int64_t>(ahead.t) * tokens;
+            const int tk = MANY ? static_cast<int>(min(static_cast<int64_t>(tokens), a.T - t0)) : 1;
             if (lane == 0) {
                 const uint32_t bytes = a.row_bytes[s];
                 unsigned char* to = smem + static_cast<size_t>(warp * S + fs) * stage_bytes;
-                mbar_arrive_expect_tx(&full[fs], static_cast<uint32_t>(n) * OPS * bytes);
+                mbar_arrive_expect_tx(&full[fs], static_cast<uint32_t>(tk * n) * OPS * bytes);
 #pragma unroll
                 for (int op = 0; op < OPS; ++op) {
                     const HeadsIn& in = op ? a.x[s] : a.in[s];
-                    const uint16_t* p = in.p + ahead.t * in.token + ahead.h * in.head;
+                    unsigned char* q = to + op * op_bytes;
+                    const uint16_t* p = in.p + t0 * in.token + ahead.h * in.head;
                     if (a.dense[op][s]) {  // heads side by side come in one copy
-                        bulk_g2s(to + op * op_bytes, p, n * pitch, &full[fs], pol);
+                        for (int j = 0; j < tk; ++j, p += in.token, q += n * pitch) bulk_g2s(q, p, n * pitch, &full[fs], pol);
                     } else {
-                        for (int i = 0; i < n; ++i, p += in.head) bulk_g2s(to + op * op_bytes + i * pitch, p, bytes, &full[fs], pol);
+                        for (int j = 0; j < tk; ++j, p += in.token - n * in.head)
+                            for (int i = 0; i < n; ++i, p += in.head, q += pitch) bulk_g2s(q, p, bytes, &full[fs], pol);
                     }
                 }
             }
             if constexpr (BWD) {
-                const float* p = a.rstd[s] + static_cast<int64_t>(ahead.t) * a.H[s] + ahead.h;
+                const float* p = a.rstd[s] + t0 * a.H[s] + ahead.h;
 #pragma unroll
-                for (int i = 0; i < step; i += 32)
-                    if (i + lane < n) cp_async4(rs + fs * step + i + lane, p + i + lane);
+                for (int i = 0; i < rows; i += 32)
+                    if (i + lane < tk * n) cp_async4(rs + fs * rows + i + lane, p + (MANY ? in_tokens(i + lane, n, a.H[s]) : i + lane));
             }
             ahead.next(Hq, Hk, step);
         }
@@ -380,14 +391,32 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     Oct c = oct_zero(), sn = oct_zero();  // cos and sin of this lane's pairs (kNeighbours: four of A, four of B)
     int t_have = -1, s_have = -1;
     while (now.left > 0) {
+        const int64_t t0 = static_cast<int64_t>(now.t) * tokens;
         if (now.t != t_have) {
             t_have = now.t;
-            if (t_have - t32 >= 32) {
-                t32 = t_have;
+            if (t0 - t32 >= 32) {
+                t32 = t0;
                 if (t32 + lane < a.T) p32 = position(a, t32 + lane);
             }
-            token_angles(cs, hp, half, F, __shfl_sync(0xffffffffu, p32, static_cast<int>(t_have - t32)), a.scale, BWD || a.back, lane);
-            if constexpr (KIND == kNeighbours) {
+            const long long pos = __shfl_sync(0xffffffffu, p32, static_cast<int>(t0 - t32) + (MANY ? head : 0));
+            if constexpr (!MANY) token_angles(cs, hp, half, F, pos, a.scale, BWD || a.back, lane);
+            if constexpr (MANY) {  // this lane's own
+                if (KIND == kNeighbours || turned) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int pair = KIND == kNeighbours ? ((e < 4 ? atA : atB) >> 1) + (e & 3) : atA + e;
+                        float2 v = rope_cos_sin(pos, F[min(pair, half - 1)], a.scale);
+                        if (BWD || a.back) v.y = -v.y;
+                        if (e & 1) {
+                            c.p[e / 2].y = v.x;
+                            sn.p[e / 2].y = v.y;
+                        } else {
+                            c.p[e / 2].x = v.x;
+                            sn.p[e / 2].x = v.y;
+                        }
+                    }
+                }
+            } else if constexpr (KIND == kNeighbours) {
                 const float4* q = reinterpret_cast<const float4*>(cs);
                 const int iA = min(atA >> 3, (hp >> 2) - 1), iB = min(atB >> 3, (hp >> 2) - 1);
                 c = oct_of(q[iA], q[iB]);
@@ -432,15 +461,18 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         }
         __syncwarp();  // BWD: the other lanes' inverse RMS
         const uint32_t st = ring + cur * stage_bytes;
-        const int n = min(step, a.H[s] - now.h);  // heads of this turn; what is computed of others is sent nowhere
+        // Heads and tokens of this turn; what is computed of others is sent nowhere.
+        const int n = min(step, a.H[s] - now.h);
+        const int tk = MANY ? static_cast<int>(min(static_cast<int64_t>(tokens), a.T - t0)) : 1, there = tk * n;
+        const int row0 = MANY ? head * n : head;
         if constexpr (BWD) {  // a head that is not there adds zeros to the weight gradients
-            if (n < step) {
-                const int last = min(step, (n + per * RBATCH - 1) / (per * RBATCH) * (per * RBATCH));
-                for (int i = n * (D >> 3) + lane; i < last * (D >> 3); i += 32) {
+            const int last = MANY ? per * n : min(rows, (n + per * RBATCH - 1) / (per * RBATCH) * (per * RBATCH));
+            if (there < last) {
+                for (int i = there * (D >> 3) + lane; i < last * (D >> 3); i += 32) {
                     sts128(st + 16 * i, make_uint4(0, 0, 0, 0));
                     sts128(st + op_bytes + 16 * i, make_uint4(0, 0, 0, 0));
                 }
-                for (int i = n + lane; i < last; i += 32) rs[cur * step + i] = 0.0f;
+                for (int i = there + lane; i < last; i += 32) rs[cur * rows + i] = 0.0f;
                 __syncwarp();
             }
         }
@@ -456,11 +488,11 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         // A batch of RB heads a group, from the i0-th on.
         auto batch = [&](auto count, const int i0) {
             constexpr int RB = decltype(count)::value;
-            const uint32_t at = st + i0 * per * pitch;
+            const uint32_t at = st + (row0 + i0 * spread) * pitch;
             uint4 rawA[RB], rawB[RB];
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
-                const uint32_t p = at + i * per * pitch;
+                const uint32_t p = at + i * spread * pitch;
                 if (NORM || KIND == kNeighbours || turned) {
                     rawA[i] = load(p + rowA, hasA, nA);
                     rawB[i] = load(p + rowB, hasB, nB);
@@ -470,7 +502,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                 if constexpr (ANY) __syncwarp();  // windows share words: all are read before any is written
 #pragma unroll
                 for (int i = 0; i < RB; ++i) {
-                    const uint32_t p = at + i * per * pitch;
+                    const uint32_t p = at + i * spread * pitch;
                     if constexpr (KIND == kNeighbours) {
                         // What is not turned stays where it is, or keeps its bits.
                         Oct A = oct_unpack<F16>(rawA[i]), B = oct_unpack<F16>(rawB[i]);
@@ -499,8 +531,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                 float2 X[RB], xX[RB];
 #pragma unroll
                 for (int i = 0; i < RB; ++i) {
-                    const uint32_t p = at + i * per * pitch;
-                    const int row = (i0 + i) * per + head;
+                    const uint32_t p = at + i * spread * pitch;
+                    const int row = row0 + (i0 + i) * spread;
                     float2 sum2 = make_float2(0.0f, 0.0f);
                     r[i] = 0.0f;
                     X[i] = xX[i] = make_float2(0.0f, 0.0f);
@@ -510,7 +542,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                         B[i] = oct_unpack<F16>(rawB[i]);
                         xA[i] = oct_unpack<F16>(load(p + op_bytes + rowA, hasA, nA));
                         xB[i] = oct_unpack<F16>(load(p + op_bytes + rowB, hasB, nB));
-                        r[i] = rs[cur * step + row];
+                        r[i] = rs[cur * rows + row];
                         turn(A[i], B[i]);
                         if constexpr (ANY) {  // cosines beyond the half's end
                             cut(A[i], nA);
@@ -555,7 +587,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                 for (int i = 0; i < RB; ++i) sum[i] = group_sum<(1 << LG)>(sum[i]);
 #pragma unroll
                 for (int i = 0; i < RB; ++i) {
-                    const uint32_t p = at + i * per * pitch;
+                    const uint32_t p = at + i * spread * pitch;
                     if constexpr (BWD) {
                         const float coef = -fmul(fmul(fmul(fmul(r[i], r[i]), r[i]), a.rcp_d), sum[i]);
 #pragma unroll
@@ -566,7 +598,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                         if (hasX) sts32(p + rowX, narrow2<F16>(fma2(X[i], both(r[i]), fmul2(xX[i], both(coef)))));
                     } else {
                         r[i] = rsqrtf(fadd(fmul(sum[i], a.rcp_d), a.eps));
-                        if (l == 0) rs[cur * step + (i0 + i) * per + head] = r[i];
+                        if (l == 0) rs[cur * rows + row0 + (i0 + i) * spread] = r[i];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             A[i].p[e] = fmul2(fmul2(A[i].p[e], both(r[i])), wA.p[e]);
@@ -582,30 +614,32 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         };
 #pragma unroll
         for (int i0 = 0; i0 < NR; i0 += RBATCH) {
-            const int rest = n - i0 * per;
+            const int rest = n - i0 * spread;
             if (rest <= 0) break;  // the same for all lanes
-            if (RBATCH > 1 && rest <= per) batch(std::integral_constant<int, 1>(), i0);
+            if (RBATCH > 1 && rest <= spread) batch(std::integral_constant<int, 1>(), i0);
             else batch(std::integral_constant<int, RBATCH>(), i0);
         }
         fence_proxy_async_smem();  // the results, before the copy that sends them and the one that refills the stage
         __syncwarp();
         if (lane == 0) {
             const HeadsOut& o = a.out[s];
-            uint16_t* p = o.p + now.t * o.token + now.h * o.head;
+            uint16_t* p = o.p + t0 * o.token + now.h * o.head;
+            uint32_t q = st;
             if (a.dense[2][s]) {
-                bulk_s2g(p, st, n * pitch, pol);
+                for (int j = 0; j < tk; ++j, p += o.token, q += n * pitch) bulk_s2g(p, q, n * pitch, pol);
             } else {
                 const uint32_t bytes = a.row_bytes[s];
-                for (int i = 0; i < n; ++i, p += o.head) bulk_s2g(p, st + i * pitch, bytes, pol);
+                for (int j = 0; j < tk; ++j, p += o.token - n * o.head)
+                    for (int i = 0; i < n; ++i, p += o.head, q += pitch) bulk_s2g(p, q, bytes, pol);
             }
             bulk_commit();
             bulk_wait_read<1>();  // the stage of the turn before is sent: it is filled next
         }
         if constexpr (NORM && !BWD) {
-            float* p = a.rstd[s] + static_cast<int64_t>(now.t) * a.H[s] + now.h;
+            float* p = a.rstd[s] + t0 * a.H[s] + now.h;
 #pragma unroll
-            for (int i = 0; i < step; i += 32)
-                if (i + lane < n) p[i + lane] = rs[cur * step + i + lane];
+            for (int i = 0; i < rows; i += 32)
+                if (i + lane < there) p[MANY ? in_tokens(i + lane, n, a.H[s]) : i + lane] = rs[cur * rows + i + lane];
         }
         if (++cur == S) {
             cur = 0;
@@ -641,16 +675,16 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
-template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
-cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
+template <int MODE, int KIND, bool F16, int LG, bool FULL, bool MANY, int NR, int RB, int S, int MINB>
+cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
-    constexpr int step = (32 >> LG) * NR;
-    const auto kern = rope_kernel<MODE, KIND, F16, LG, FULL, NR, RB, S, MINB>;
+    constexpr int per = 32 >> LG, rows = per * NR, tokens = MANY ? per : 1, step = MANY ? NR : rows;
+    const auto kern = rope_kernel<MODE, KIND, F16, LG, FULL, MANY, NR, RB, S, MINB>;
     const int hp = (a.R / 2 + 7) & ~7;
-    const size_t warp_bytes = static_cast<size_t>(S) * (BWD ? 2 : 1) * step * a.D * 2 + hp * 8 + (NORM ? S * step * 4 : 0) + S * 8;
+    const size_t warp_bytes = static_cast<size_t>(S) * (BWD ? 2 : 1) * rows * a.D * 2 + hp * 8 + (NORM ? S * rows * 4 : 0) + S * 8;
     const size_t fixed = (NORM ? static_cast<size_t>(a.D) * 8 : 0) + static_cast<size_t>(a.R / 2) * 8;
-    const int64_t turns = a.T * ((a.H[0] + step - 1) / step + (a.H[1] + step - 1) / step);
     const int64_t sms = sm_count();
+    const int64_t turns = (a.T + tokens - 1) / tokens * ((a.H[0] + step - 1) / step + (a.H[1] + step - 1) / step);
     // Threads: few turns spread over the SMs in smaller CTAs. The backward's CTAs
     // are a function of the problem (rope_bwd_ctas).
     int threads = kRopeThreads;
@@ -668,12 +702,13 @@ cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     }
     RopeArgs b = a;
     if (BWD && a.H[1] > 0) {
-        // The CTAs split by the work of a token: one for a batch of heads, four for a
-        // turn, whose chain of waits counts most (32 + 8 heads of 64: 76 % of the copy
-        // rate; by batches alone 64 %, by turns alone 73 %).
+        // The CTAs split by the work of a token (MANY: of as many): one for a batch of
+        // heads, four for a turn, whose chain of waits counts most (32 + 8 heads of 64:
+        // 76 % of the copy rate; by batches alone 64 %, by turns alone 73 %), and where
+        // the lanes compute their angles four for those (4 + 1 heads of 128: 49 % for 41).
         auto cost = [&](int64_t H) {
-            constexpr int64_t batch = (32 >> LG) * RB;
-            return H / step * (NR / RB) + (H % step + batch - 1) / batch + 4 * ((H + step - 1) / step);
+            constexpr int64_t batch = MANY ? RB : per * RB;
+            return H / step * (NR / RB) + (H % step + batch - 1) / batch + 4 * ((H + step - 1) / step) + (MANY ? 4 : 0);
         };
         const int64_t q = cost(a.H[0]), k = cost(a.H[1]);
         b.ctas_q = static_cast<int>(std::min(std::max<int64_t>((grid * q + (q + k) / 2) / (q + k), 1), grid - 1));
@@ -682,6 +717,27 @@ cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     }
     *ctas_q = b.ctas_q;
     return launch_kernel(kern, static_cast<unsigned>(grid), threads, smem, st, b);
+}
+
+// One token a turn or one a group of lanes: the second where it leaves half the
+// turns or fewer at as many heads a group (the norm's kernels, with more to do a
+// turn: three quarters), and enough of them for every SM. 65536 x 4 + 1 x 128: rotation 48 -> 75 % of the copy
+// rate, norm and rotation 33 -> 61, its backward 32 -> 49; 14 + 2 heads: 88 both
+// ways, 55 -> 83, 46 -> 74. With as many turns (32 + 8 heads of 128) its shorter
+// copies cost: 83 -> 80, 76 -> 66, 75 -> 72, measured in one kernel for both.
+template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
+cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
+    constexpr int per = 32 >> LG;
+    if constexpr (per > 1) {
+        // Forward with the norm: then four heads a group (8 + 1 heads of 128: 75 % for two heads' 58).
+        constexpr bool wider = MODE == kNormTurn;
+        auto turns_of = [&](int step) -> int64_t { return (a.H[0] + step - 1) / step + (a.H[1] + step - 1) / step; };
+        const int64_t one = a.T * turns_of(per * NR), many = (a.T + per - 1) / per * turns_of(NR);
+        const bool fewer = MODE == kTurn ? 2 * many <= one : 4 * many <= 3 * one;
+        if (fewer && many >= sm_count() * static_cast<int64_t>(kRopeThreads / 32))
+            return rope_run_as<MODE, KIND, F16, LG, FULL, true, wider ? 4 : NR, wider ? 2 : RB, wider ? 3 : S, MINB>(a, ctas_q, st);
+    }
+    return rope_run_as<MODE, KIND, F16, LG, FULL, false, NR, RB, S, MINB>(a, ctas_q, st);
 }
 
 // Heads a group and turn, of them in registers at a time, stages, CTAs an SM: the

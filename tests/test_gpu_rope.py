@@ -314,6 +314,29 @@ def test_norm_and_rope_many_tokens(T, Hq, Hk, D, R, dtype, interleaved):
     _check_norm(T, Hq, Hk, D, R, interleaved, dtype, "qkv", dtype == F16, seed=T)
 
 
+@pytest.mark.parametrize("Hq,Hk", [(1, 0), (1, 1), (2, 1), (4, 1), (5, 0), (7, 1), (3, 2), (14, 2)])
+@pytest.mark.parametrize("D,R,inter", [(128, 128, False), (128, 128, True), (64, 64, False), (64, 20, True), (8, 8, True),
+                                       (24, 24, False), (80, 32, False), (96, 24, False), (128, 78, False),
+                                       (256, 64, False), (256, 256, True), (192, 36, False), (264, 264, False)])
+def test_few_heads_and_many_tokens(Hq, Hk, D, R, inter):
+    """Turns of several tokens, the last of which are not there; heads of their own and of a wider projection."""
+    T = 6001 + 2 * Hq
+    _check_norm(T, Hq, Hk, D, R, inter, F16 if Hq == 2 else BF16, "heads" if Hq == 3 else "own" if Hq == 4 else "qkv",
+                False, seed=Hq)
+    q, k = _heads(T, Hq, Hk, D, 3, BF16, "qkv" if Hq == 4 else "own")
+    pos, f = _pos(T, 5), _freq(R)
+    for back in (False, True):
+        bq, oq = _like(q)
+        bk, ok = _like(k)
+        (rn.rope_bwd if back else rn.rope_fwd)(q, k, f, oq, ok, pos, SCALE, inter)
+        for name, x, base, o in (("q", q, bq, oq), ("k", k, bk, ok)):
+            if x is not None:
+                want, size = ref.turned(x.double(), pos, f, SCALE, inter, back)
+                ref.assert_within(name, o, want, ref.TURN * size, BF16)
+                assert torch.equal(_bits(o[..., R:]), _bits(x[..., R:]))
+                assert bool((_beside(base, o) == 3.0).all())
+
+
 @pytest.mark.parametrize("D,R,inter", [(128, 128, False), (256, 64, False), (128, 128, True), (96, 24, False)])
 def test_norm_and_rope_rows_are_their_own(D, R, inter):
     """A token's bits do not depend on the batch, its place, the strides, the other heads or bad values beside it."""
