@@ -1,17 +1,19 @@
 // Weight-gradient pass 2 of the operators with two weights (LayerNorm's w and b,
 // the head norms of q and k).
 //
-// The chunk axis is cut into kReduceWarps ranges of ceil(n / kReduceWarps)
-// chunks; each range is added in ascending order and the ranges' totals in
-// range order: a tree fixed by n alone, no atomics. A CTA owns 8 adjacent columns,
-// a 32-byte sector of each partial row, of one of the two outputs (blockIdx.y);
-// thread (range w, column k).
-// Few columns (FEW): bound by latency, so a thread's loads are all in flight, 16
-// at a time (2.9 us at 128 columns of 304 chunks; loads in turn 3.9). Many: by
-// the loads' rate, and 16 registers of loads a thread measured slower (LayerNorm
-// backward of 8192 x 16384 131 us; with them, or with 32 columns a CTA, 142). There
-// the loads are streaming ones: such partial rows lie in L2 at high priority, and
-// an ordinary load leaves them there in the way of what comes next (145 us).
+// The chunk axis is cut into kRanges ranges of ceil(n / kRanges) chunks. Each is
+// added in ascending order, then every kParts-th range's total, then the parts: a
+// tree fixed by n alone, no atomics. A CTA owns 8 adjacent columns, a 32-byte
+// sector of each partial row, of one of the two outputs (blockIdx.y); a thread
+// adds 4 of them over one range.
+//
+// Bound by the latency of a range's loads, so the ranges are short (8192 x 1024,
+// 1216 chunks: LayerNorm backward 14.4 us, with 32 ranges and a column a thread
+// 15.8; 262144 x 128 36.5 and 37.2 us), and by the loads' rate where there are many
+// columns. Sixteen predicated loads in flight a thread measured slower at every
+// size (24.9 and 38.8 us). The loads are streaming ones: LayerNorm's partial rows
+// lie in L2 at high priority, and an ordinary load leaves them there in the way of
+// what comes next (8192 x 16384: 131 us, with ordinary loads 135).
 #include "reduce_columns.h"
 
 #include "common.cuh"
@@ -20,58 +22,58 @@
 namespace rmsn {
 
 namespace {
-constexpr int kCols = 8;
-constexpr int kUnroll = 16;  // FEW: loads in flight a thread
-}
+constexpr int kCols = 8, kQuads = kCols / 4;
+constexpr int kRanges = 128;  // of the chunk axis
+constexpr int kParts = 8;     // of the ranges, added side by side
+}  // namespace
 
-template <bool FEW>
-__global__ void __launch_bounds__(kReduceWarps * kCols)
+__global__ void __launch_bounds__(kRanges * kQuads)
 reduce_columns_kernel(const PartialRows first, const PartialRows second, int D) {
-    __shared__ float tot[kReduceWarps][kCols];
+    __shared__ float4 range[kRanges][kQuads];
+    __shared__ float part[kParts][kCols];
     pdl_wait();
     const PartialRows& a = blockIdx.y ? second : first;
-    const int k = threadIdx.x % kCols, w = threadIdx.x / kCols;
-    const int col = blockIdx.x * kCols + k;  // D is a multiple of 8
-    const int64_t per = (a.n + kReduceWarps - 1) / kReduceWarps;
-    const int64_t c0 = w * per, c1 = min(c0 + per, a.n);
-    const float* p = a.p + col;
-    float acc = 0.0f;
-    if constexpr (FEW) {
-        for (int64_t c = c0; c < c1; c += kUnroll) {  // a place without a chunk adds zero
-            float v[kUnroll];
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i) v[i] = c + i < c1 ? __ldcg(p + (c + i) * D) : 0.0f;
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i) acc = fadd(acc, v[i]);
-        }
-    } else {
-#pragma unroll 4
-        for (int64_t c = c0; c < c1; ++c) acc = fadd(acc, __ldcs(p + c * D));
+    const int q = threadIdx.x % kQuads, r = threadIdx.x / kQuads;
+    const int64_t per = (a.n + kRanges - 1) / kRanges;
+    const int64_t c0 = min(r * per, a.n), c1 = min(c0 + per, a.n);
+    const float* p = a.p + c0 * D + blockIdx.x * kCols + 4 * q;  // D is a multiple of 8
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+    for (int64_t c = c0; c < c1; ++c, p += D) {
+        const float4 u = __ldcs(reinterpret_cast<const float4*>(p));
+        v = make_float4(fadd(v.x, u.x), fadd(v.y, u.y), fadd(v.z, u.z), fadd(v.w, u.w));
     }
     pdl_release();
-    tot[w][k] = acc;
+    range[r][q] = v;
     __syncthreads();
-    if (w == 0) {
-        float s = tot[0][k];
+    const int col = threadIdx.x % kCols, s = threadIdx.x / kCols;
+    if (s < kParts) {
+        const float* t = reinterpret_cast<const float*>(range) + col;
+        float sum = t[s * kCols];
 #pragma unroll
-        for (int r = 1; r < kReduceWarps; ++r) s = fadd(s, tot[r][k]);
-        a.out[col] = s;
+        for (int i = s + kParts; i < kRanges; i += kParts) sum = fadd(sum, t[i * kCols]);
+        part[s][col] = sum;
+    }
+    __syncthreads();
+    if (s == 0) {
+        float sum = part[0][col];
+#pragma unroll
+        for (int i = 1; i < kParts; ++i) sum = fadd(sum, part[i][col]);
+        a.out[blockIdx.x * kCols + col] = sum;
     }
 }
 
 cudaError_t launch_reduce_columns(const PartialRows& first, const PartialRows& second, int D, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(D / kCols), second.out != nullptr ? 2u : 1u);
-    cfg.blockDim = dim3(kReduceWarps * kCols);
+    cfg.blockDim = dim3(kRanges * kQuads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = RMSN_PDL;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const bool few = static_cast<int>(cfg.gridDim.x * cfg.gridDim.y) <= 2 * sm_count();
-    const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, reduce_columns_kernel<true>, first, second, D)
-                              : cudaLaunchKernelEx(&cfg, reduce_columns_kernel<false>, first, second, D);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, reduce_columns_kernel, first, second, D);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
