@@ -721,7 +721,7 @@ cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
 
 // One token a turn or one a group of lanes: the second where it leaves half the
 // turns or fewer at as many heads a group (the norm's kernels, with more to do a
-// turn: three quarters), and enough of them for every SM. 65536 x 4 + 1 x 128: rotation 48 -> 75 % of the copy
+// turn: three quarters), and still kRopeManyFrom turns. 65536 x 4 + 1 x 128: rotation 48 -> 75 % of the copy
 // rate, norm and rotation 33 -> 61, its backward 32 -> 49; 14 + 2 heads: 88 both
 // ways, 55 -> 83, 46 -> 74. With as many turns (32 + 8 heads of 128) its shorter
 // copies cost: 83 -> 80, 76 -> 66, 75 -> 72, measured in one kernel for both.
@@ -734,7 +734,7 @@ cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
         auto turns_of = [&](int step) -> int64_t { return (a.H[0] + step - 1) / step + (a.H[1] + step - 1) / step; };
         const int64_t one = a.T * turns_of(per * NR), many = (a.T + per - 1) / per * turns_of(NR);
         const bool fewer = MODE == kTurn ? 2 * many <= one : 4 * many <= 3 * one;
-        if (fewer && many >= sm_count() * static_cast<int64_t>(kRopeThreads / 32))
+        if (fewer && many >= kRopeManyFrom)
             return rope_run_as<MODE, KIND, F16, LG, FULL, true, wider ? 4 : NR, wider ? 2 : RB, wider ? 3 : S, MINB>(a, ctas_q, st);
     }
     return rope_run_as<MODE, KIND, F16, LG, FULL, false, NR, RB, S, MINB>(a, ctas_q, st);

@@ -39,6 +39,9 @@ struct RopeArgs {
 };
 
 constexpr int kRopeThreads = 256;
+// Turns of several tokens from one for every warp of a CTA an SM on, of a GPU of
+// 152: the order of the weight gradients' sums is the same on every GPU.
+constexpr int64_t kRopeManyFrom = 152 * (kRopeThreads / 32);
 
 // log2 of the lanes a head: the smallest power of two that holds its units of two
 // times eight values. Where R is no multiple of 16 the halves' last unit is cut
