@@ -113,10 +113,6 @@ __device__ __forceinline__ Oct oct_dx(const Oct& gw, const Oct& c, float r, floa
 // ---------------------------------------------------------------------------
 constexpr int kLnRowThreads = 256;
 
-// Every lane keeps its own ring of S turns in flight: it copies its vectors to
-// its own slots of shared memory (cp.async, past L1) and reads them back itself,
-// so a wait for its own copies is all the synchronisation there is, and data in
-// flight costs no registers. Slot layout [turn][vector][thread]: conflict-free.
 // w_eff and b of a row in shared memory as [w low | w high | b low | b high][NV]
 // float4 (the halves of a vector's eight): conflict-free reads.
 __device__ __forceinline__ void stage_weights(float4* wb, const float* w, const float* b, int zc, int NV) {
@@ -136,6 +132,10 @@ __device__ __forceinline__ Oct staged_bias(const float4* wb, bool bias, int NV, 
     return bias ? oct_of(wb[2 * NV + v], wb[3 * NV + v]) : oct_zero();
 }
 
+// Every lane keeps its own ring of S turns in flight: it copies its vectors to
+// its own slots of shared memory (cp.async, past L1) and reads them back itself,
+// so a wait for its own copies is all the synchronisation there is, and data in
+// flight costs no registers. Slot layout [turn][vector][thread]: conflict-free.
 // Weights in registers at one vector a lane, else in shared memory, read once
 // for the NR rows of a turn.
 template <bool F16, int G, int V, int NR, int S, int MINB>
@@ -722,8 +722,8 @@ cudaError_t wide_bwd(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
 }
 
 // Shapes by width, each the fastest measured (ln_shape has their CTAs an SM). Of
-// the copy rate, both passes, 65536 to 8192 rows: D = 768 85 % (a CTA a row: 80),
-// 1024 87, 2048 92, 4096 95, 5000 90, 8192 93, 16384 89. D = 128: 79 % of 30 us.
+// the copy rate, both passes, 65536 to 8192 rows: D = 768 87 % (a CTA a row: 80),
+// 1024 88, 2048 91, 4096 96, 5000 91, 8192 96, 16384 92. D = 128: 82 % of 30 us.
 template <bool F16, bool BIAS>
 cudaError_t ln_bwd_dispatch(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
     const int NV = a.D / 8;

@@ -1,6 +1,6 @@
 // Rotary positions and the head norm fused with them: kernels and launchers,
-// included by the translation units that instantiate them (rope.cu: bf16
-// activations; rope_f16.cu: fp16).
+// included by the translation units that instantiate them (rope_turn, rope_norm and
+// rope_norm_bwd: bf16 activations; with _f16: fp16).
 //
 // Mathematics, per pair (u, v) of a head and its angle a:
 //   turn:            (u c - v s, v c + u s), c = scale cos a, s = scale sin a
@@ -721,10 +721,11 @@ cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
 
 // One token a turn or one a group of lanes: the second where it leaves half the
 // turns or fewer at as many heads a group (the norm's kernels, with more to do a
-// turn: three quarters), and still kRopeManyFrom turns. 65536 x 4 + 1 x 128: rotation 48 -> 75 % of the copy
-// rate, norm and rotation 33 -> 61, its backward 32 -> 49; 14 + 2 heads: 88 both
-// ways, 55 -> 83, 46 -> 74. With as many turns (32 + 8 heads of 128) its shorter
-// copies cost: 83 -> 80, 76 -> 66, 75 -> 72, measured in one kernel for both.
+// turn: three quarters), and still kRopeManyFrom turns. 65536 x 4 + 1 x 128:
+// rotation 48 -> 75 % of the copy rate, norm and rotation 33 -> 61, its backward
+// 32 -> 50; 14 + 2 heads: 88 both ways, 55 -> 81, 46 -> 75. With as many turns
+// (32 + 8 heads of 128) its shorter copies cost: 83 -> 80, 76 -> 66, 75 -> 72,
+// measured in one kernel for both.
 template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
 cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     constexpr int per = 32 >> LG;

@@ -45,9 +45,4 @@ __device__ __forceinline__ float2 rope_cos_sin(long long p, unsigned long long F
     return make_float2(fmul(cq, scale), fmul(sq, scale));
 }
 
-// (u, v) turned by the angle of cs = scale (cos, sin); backward: by minus it.
-__device__ __forceinline__ float2 rope_turn(float u, float v, float2 cs) {
-    return make_float2(fsub(fmul(u, cs.x), fmul(v, cs.y)), fadd(fmul(v, cs.x), fmul(u, cs.y)));
-}
-
 }  // namespace rmsn
