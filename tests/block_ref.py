@@ -73,7 +73,7 @@ def ln_bwd(g, x, w, mean, rstd):
 
 def rows_chain(T):
     """Additions on one path of a weight gradient's sum over T rows: at most a
-    chunk of 256 rows, 32 ranges of chunks, the chunks of one range, slack."""
+    chunk of 256 rows, 16 and 8 of the ranges' totals, the chunks of one range, slack."""
     return min(T, 256) + 32 + T // 2048 + 8
 
 
