@@ -336,28 +336,31 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     Turns ahead = now;
     // Place of row r (n heads a token) among the heads of all tokens.
     auto in_tokens = [](int r, int n, int H) { return n == H ? r : r / n * H + r % n; };
+    // The copies of a turn, one a lane: a token's heads where they lie side by side, else a head.
+    auto pieces = [&](bool dense, int64_t token, int64_t head_stride, int64_t t0, int h, int n, int tk, uint32_t bytes, auto&& copy) {
+        if (dense) {
+            if (lane < tk) copy((t0 + lane) * token + h * head_stride, lane * n * pitch, n * pitch);
+        } else if (lane < tk * n) {
+            const int j = MANY ? lane / n : 0;
+            copy((t0 + j) * token + (h + lane - j * n) * head_stride, lane * pitch, bytes);
+        }
+    };
     int fs = 0;
     auto fetch = [&]() {
         if (ahead.left > 0) {
             const int s = ahead.s, n = min(step, a.H[s] - ahead.h);
             const int64_t t0 = static_cast<int64_t>(ahead.t) * tokens;
             const int tk = MANY ? static_cast<int>(min(static_cast<int64_t>(tokens), a.T - t0)) : 1;
-            if (lane == 0) {
-                const uint32_t bytes = a.row_bytes[s];
-                unsigned char* to = smem + static_cast<size_t>(warp * S + fs) * stage_bytes;
-                mbar_arrive_expect_tx(&full[fs], static_cast<uint32_t>(tk * n) * OPS * bytes);
+            const uint32_t bytes = a.row_bytes[s];
+            if (lane == 0) mbar_arrive_expect_tx(&full[fs], static_cast<uint32_t>(tk * n) * OPS * bytes);
+            __syncwarp();  // and every lane's copies out of the stage have read it
+            unsigned char* to = smem + static_cast<size_t>(warp * S + fs) * stage_bytes;
 #pragma unroll
-                for (int op = 0; op < OPS; ++op) {
-                    const HeadsIn& in = op ? a.x[s] : a.in[s];
-                    unsigned char* q = to + op * op_bytes;
-                    const uint16_t* p = in.p + t0 * in.token + ahead.h * in.head;
-                    if (a.dense[op][s]) {  // heads side by side come in one copy
-                        for (int j = 0; j < tk; ++j, p += in.token, q += n * pitch) bulk_g2s(q, p, n * pitch, &full[fs], pol);
-                    } else {
-                        for (int j = 0; j < tk; ++j, p += in.token - n * in.head)
-                            for (int i = 0; i < n; ++i, p += in.head, q += pitch) bulk_g2s(q, p, bytes, &full[fs], pol);
-                    }
-                }
+            for (int op = 0; op < OPS; ++op) {
+                const HeadsIn& in = op ? a.x[s] : a.in[s];
+                pieces(a.dense[op][s], in.token, in.head, t0, ahead.h, n, tk, bytes, [&](int64_t from, uint32_t at, uint32_t size) {
+                    bulk_g2s(to + op * op_bytes + at, in.p + from, size, &full[fs], pol);
+                });
             }
             if constexpr (BWD) {
                 const float* p = a.rstd[s] + t0 * a.H[s] + ahead.h;
@@ -621,20 +624,11 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         }
         fence_proxy_async_smem();  // the results, before the copy that sends them and the one that refills the stage
         __syncwarp();
-        if (lane == 0) {
-            const HeadsOut& o = a.out[s];
-            uint16_t* p = o.p + t0 * o.token + now.h * o.head;
-            uint32_t q = st;
-            if (a.dense[2][s]) {
-                for (int j = 0; j < tk; ++j, p += o.token, q += n * pitch) bulk_s2g(p, q, n * pitch, pol);
-            } else {
-                const uint32_t bytes = a.row_bytes[s];
-                for (int j = 0; j < tk; ++j, p += o.token - n * o.head)
-                    for (int i = 0; i < n; ++i, p += o.head, q += pitch) bulk_s2g(p, q, bytes, pol);
-            }
-            bulk_commit();
-            bulk_wait_read<1>();  // the stage of the turn before is sent: it is filled next
-        }
+        const HeadsOut& o = a.out[s];
+        pieces(a.dense[2][s], o.token, o.head, t0, now.h, n, tk, a.row_bytes[s],
+               [&](int64_t to, uint32_t at, uint32_t size) { bulk_s2g(o.p + to, st + at, size, pol); });
+        bulk_commit();
+        bulk_wait_read<1>();  // the stage of the turn before is sent: it is filled next
         if constexpr (NORM && !BWD) {
             float* p = a.rstd[s] + t0 * a.H[s] + now.h;
 #pragma unroll
@@ -648,7 +642,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         now.next(Hq, Hk, step);
         fetch();
     }
-    if (lane == 0) bulk_wait_all();
+    bulk_wait_all();
     if constexpr (BWD) {
         cp_async_wait<0>();
         // The groups' sums in group order, through the stages' memory.
