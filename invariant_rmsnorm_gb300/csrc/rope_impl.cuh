@@ -698,11 +698,12 @@ cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     if (BWD && a.H[1] > 0) {
         // The CTAs split by the work of a token (MANY: of as many): one for a batch of
         // heads, four for a turn, whose chain of waits counts most (32 + 8 heads of 64:
-        // 76 % of the copy rate; by batches alone 64 %, by turns alone 73 %), and where
-        // the lanes compute their angles four for those (4 + 1 heads of 128: 49 % for 41).
+        // 76 % of the copy rate; by batches alone 64 %, by turns alone 73 %). MANY: two
+        // a turn and two for the angles that each lane computes (4 + 1 heads of 128:
+        // 58 %; by four and four 57, 14 + 2 heads 81 and 80).
         auto cost = [&](int64_t H) {
             constexpr int64_t batch = MANY ? RB : per * RB;
-            return H / step * (NR / RB) + (H % step + batch - 1) / batch + 4 * ((H + step - 1) / step) + (MANY ? 4 : 0);
+            return H / step * (NR / RB) + (H % step + batch - 1) / batch + (MANY ? 2 : 4) * ((H + step - 1) / step) + (MANY ? 2 : 0);
         };
         const int64_t q = cost(a.H[0]), k = cost(a.H[1]);
         b.ctas_q = static_cast<int>(std::min(std::max<int64_t>((grid * q + (q + k) / 2) / (q + k), 1), grid - 1));
