@@ -717,8 +717,8 @@ cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
 // One token a turn or one a group of lanes: the second where it leaves half the
 // turns or fewer at as many heads a group (the norm's kernels, with more to do a
 // turn: three quarters), and still kRopeManyFrom turns. 65536 x 4 + 1 x 128:
-// rotation 48 -> 75 % of the copy rate, norm and rotation 33 -> 61, its backward
-// 32 -> 50; 14 + 2 heads: 88 both ways, 55 -> 81, 46 -> 75. With as many turns
+// rotation 48 -> 79 % of the copy rate, norm and rotation 33 -> 68, its backward
+// 32 -> 58; 14 + 2 heads: 88 both ways, 55 -> 79, 46 -> 81. With as many turns
 // (32 + 8 heads of 128) its shorter copies cost: 83 -> 80, 76 -> 66, 75 -> 72,
 // measured in one kernel for both.
 template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
