@@ -4,7 +4,9 @@
 Argument marshalling only: every function here takes torch tensors that the
 caller allocated on a CUDA device, checks dtypes/shapes/devices, and passes raw
 pointers, row strides and sizes to the ``extern "C"`` entry point of the same
-name in ``_build/librmsnorm_gb300.so``. All arithmetic runs in the library's
+name in ``_build/librmsnorm_gb300.so`` (LayerNorm and the rotary calls: through
+``norm_call`` of ``include/slots.h``, one packed array in place of a conversion
+an argument). All arithmetic runs in the library's
 sm_103a kernels. If the library has not been built, ``load()`` raises; there is
 no other implementation to fall back to.
 
@@ -18,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -39,7 +42,7 @@ __all__ = [
     "DEVICE_ERR_WAIT_TIMEOUT", "rmsnorm_bwd_workspace_bytes_max",
     "rmsnorm_rope_fwd", "rmsnorm_rope_bwd", "rmsnorm_rope_bwd_workspace_bytes",
     "layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_bytes", "layernorm_bwd_workspace_bytes_max",
-    "rope_fwd", "rope_bwd", "rope_frequencies", "LAYERNORM_SYMBOLS", "ROPE_SYMBOLS", "ROPE_SCALINGS",
+    "rope_fwd", "rope_bwd", "rope_frequencies", "LAYERNORM_SYMBOLS", "ROPE_SYMBOLS", "SLOTS_SYMBOLS", "ROPE_SCALINGS",
 ]
 
 EXPORTED_SYMBOLS = (
@@ -60,6 +63,8 @@ EXPORTED_SYMBOLS = (
 LAYERNORM_SYMBOLS = ("layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_bytes",
                      "layernorm_bwd_workspace_bytes_max")
 ROPE_SYMBOLS = ("rope_frequencies", "rope_fwd", "rope_bwd")
+# of include/slots.h
+SLOTS_SYMBOLS = ("norm_call",)
 
 # RMSN_DEVICE_ERR_WAIT_TIMEOUT of include/rmsnorm.h: the flag a wait that ran out of time raises
 DEVICE_ERR_WAIT_TIMEOUT = 1
@@ -129,6 +134,16 @@ _SIGS["rmsnorm_rope_fwd"] = (_INT, _HEADS * 2 + [_P, _P, _P, _P, _INT] + _HEADS 
 _SIGS["rmsnorm_rope_bwd_workspace_bytes"] = (_SZ, [_I64] * 4)
 _SIGS["rmsnorm_rope_bwd"] = (_INT, _HEADS * 4 + [_P, _P, _P, _P, _INT, _P, _P] + _HEADS * 2 + [_P, _P, _P, _SZ] +
                              [_I64] * 5 + [_F, _INT, _INT, _INT, _P])
+
+# The entry points that are called with their arguments in an array (include/slots.h):
+# enum norm_entry, the array's packing and its length.
+_SIGS["norm_call"] = (_INT, [_INT, ctypes.c_char_p, _I64])
+_SLOTS = {}
+for _entry, _name in enumerate(("layernorm_fwd", "layernorm_bwd", "rope_fwd", "rope_bwd", "rmsnorm_rope_fwd",
+                                "rmsnorm_rope_bwd")):
+    _args = _SIGS[_name][1]
+    _SLOTS[_name] = (_entry, struct.Struct("=" + "".join("d" if a is _F else "q" for a in _args)).pack, len(_args))
+del _entry, _name, _args
 
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
@@ -563,7 +578,7 @@ def _heads(t, name: str, shape, dtype, index: int):
     """Pointer, token stride and head stride of [T, heads, D] (None: of no heads)."""
     if t is None:
         if shape[1] == 0:
-            return None, 0, 0
+            return 0, 0, 0
         raise TypeError(f"{name}: expected a tensor of shape {shape}")
     if t.dtype is dtype and t.get_device() == index and t.shape == shape:
         token, head, one = t.stride()
@@ -593,7 +608,7 @@ def _bytes_of(ws, index: int):
 def _positions(t, T: int, index: int):
     """Pointer and enum rope_pos_dtype (None: 0, 1, 2, ...)."""
     if t is None:
-        return None, 1
+        return 0, 1
     if t.dtype is torch.int64:
         return _vec(t, "positions", (T,), index, torch.int64), 1
     if t.dtype is torch.int32:
@@ -614,13 +629,15 @@ def _handle(stream, index: int) -> int:
 
 
 def _call(name: str, index: int, stream, *args):
-    """The entry point ``name`` on ``stream``, with the tensors' device current."""
-    fn = getattr(_lib or load(), name)
+    """The entry point ``name`` on ``stream``, with the tensors' device current (a null pointer is 0)."""
+    entry, pack, n = _SLOTS[name]
+    slots = pack(*args, _handle(stream, index))
+    fn = (_lib or load()).norm_call
     if _device_now() == index:
-        st = fn(*args, _handle(stream, index))
+        st = fn(entry, slots, n)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, _handle(stream, index))
+            st = fn(entry, slots, n)
     if st != 0:
         raise RmsNormError(name, st)
 
@@ -633,7 +650,7 @@ def layernorm_fwd(x, w, b, y, mean, rstd, eps: float = 1e-5, zero_centered_gamma
     T, D = shape
     xp, ldx = _rows(x, "x", shape, dt, i)
     yp, ldy = _rows(y, "y", shape, dt, i)
-    _call("layernorm_fwd", i, stream, xp, ldx, _vec(w, "w", (D,), i), None if b is None else _vec(b, "b", (D,), i), yp, ldy,
+    _call("layernorm_fwd", i, stream, xp, ldx, _vec(w, "w", (D,), i), 0 if b is None else _vec(b, "b", (D,), i), yp, ldy,
           _vec(mean, "mean", (T,), i), _vec(rstd, "rstd", (T,), i), T, D, eps, 1 if zero_centered_gamma else 0, code)
 
 
@@ -657,7 +674,7 @@ def layernorm_bwd(g, x, w, mean, rstd, dx, dw, db, ws, zero_centered_gamma: bool
     dp, ldd = _rows(dx, "dx", shape, dt, i)
     wp, wb = _bytes_of(ws, i)
     _call("layernorm_bwd", i, stream, gp, ldg, xp, ldx, _vec(w, "w", (D,), i), _vec(mean, "mean", (T,), i),
-          _vec(rstd, "rstd", (T,), i), dp, ldd, _vec(dw, "dw", (D,), i), None if db is None else _vec(db, "db", (D,), i), wp,
+          _vec(rstd, "rstd", (T,), i), dp, ldd, _vec(dw, "dw", (D,), i), 0 if db is None else _vec(db, "db", (D,), i), wp,
           wb, T, D, 1 if zero_centered_gamma else 0, code)
 
 
@@ -722,9 +739,9 @@ def rmsnorm_rope_fwd(q, k, wq, wk, inv_freq, q_out, k_out, rstd_q, rstd_k, posit
     T, Hq, D = sq
     Hk = sk[1]
     _call("rmsnorm_rope_fwd", i, stream, *_heads(q, "q", sq, dt, i), *_heads(k, "k", sk, dt, i), _vec(wq, "wq", (D,), i),
-          _vec(wk, "wk", (D,), i) if Hk else None, _vec(inv_freq, "inv_freq", (n,), i, _F64), *_positions(positions, T, i),
+          _vec(wk, "wk", (D,), i) if Hk else 0, _vec(inv_freq, "inv_freq", (n,), i, _F64), *_positions(positions, T, i),
           *_heads(q_out, "q_out", sq, dt, i), *_heads(k_out, "k_out", sk, dt, i), _vec(rstd_q, "rstd_q", (T, Hq), i),
-          _vec(rstd_k, "rstd_k", (T, Hk), i) if Hk else None, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0, eps,
+          _vec(rstd_k, "rstd_k", (T, Hk), i) if Hk else 0, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0, eps,
           1 if zero_centered_gamma else 0, code)
 
 
@@ -744,10 +761,10 @@ def rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, inv_freq, rstd_q, rstd_k, dq, dk, dwq
     wp, wb = _bytes_of(ws, i)
     _call("rmsnorm_rope_bwd", i, stream, *_heads(gq, "gq", sq, dt, i), *_heads(gk, "gk", sk, dt, i),
           *_heads(q, "q", sq, dt, i), *_heads(k, "k", sk, dt, i), _vec(wq, "wq", (D,), i),
-          _vec(wk, "wk", (D,), i) if Hk else None, _vec(inv_freq, "inv_freq", (n,), i, _F64), *_positions(positions, T, i),
-          _vec(rstd_q, "rstd_q", (T, Hq), i), _vec(rstd_k, "rstd_k", (T, Hk), i) if Hk else None,
+          _vec(wk, "wk", (D,), i) if Hk else 0, _vec(inv_freq, "inv_freq", (n,), i, _F64), *_positions(positions, T, i),
+          _vec(rstd_q, "rstd_q", (T, Hq), i), _vec(rstd_k, "rstd_k", (T, Hk), i) if Hk else 0,
           *_heads(dq, "dq", sq, dt, i), *_heads(dk, "dk", sk, dt, i), _vec(dwq, "dwq", (D,), i),
-          _vec(dwk, "dwk", (D,), i) if Hk else None, wp, wb, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0,
+          _vec(dwk, "dwk", (D,), i) if Hk else 0, wp, wb, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0,
           1 if zero_centered_gamma else 0, code)
 
 

@@ -52,9 +52,9 @@ def test_prototypes_match_the_headers(lib, header, names):
 
 
 def test_a_c_program_links_every_entry_point(lib, tmp_path):
-    names = [*rn.LAYERNORM_SYMBOLS, *rn.ROPE_SYMBOLS]
+    names = [*rn.LAYERNORM_SYMBOLS, *rn.ROPE_SYMBOLS, *rn.SLOTS_SYMBOLS]
     src, exe = tmp_path / "c.c", tmp_path / "c"
-    src.write_text('#include <stdio.h>\n#include "layernorm.h"\n#include "rope.h"\ntypedef void (*fn)(void);\n'
+    src.write_text('#include <stdio.h>\n#include "layernorm.h"\n#include "rope.h"\n#include "slots.h"\ntypedef void (*fn)(void);\n'
                    "static const fn all[] = {" + ", ".join(f"(fn){n}" for n in names) + "};\n"
                    "int main(void) {\n  double f[4];\n"
                    "  const int st = rope_frequencies(8, 10000.0, ROPE_SCALING_NONE, 1.0, 0, 0, 0, f);\n"
@@ -152,6 +152,52 @@ def _norm_bwd(lib, w=A, wk=A, r=A, rk=A, x=A, xs=(256, 64), xk=A, dw=A, dwk=A, w
     (dict(dw=0, T=0), EINVAL), (dict(ws=0), EWORKSPACE), (dict(size=16), EWORKSPACE), (dict(ws=A + 8), EALIGN)])
 def test_norm_rope_bwd_refuses(lib, bad, status):
     assert _norm_bwd(lib, **bad) == status
+
+
+class _Slots:
+    """The library through ``norm_call``."""
+
+    def __init__(self, lib):
+        self.lib = lib
+
+    def __getattr__(self, name):
+        entry, pack, n = rn._SLOTS[name]
+        return lambda *args: self.lib.norm_call(entry, pack(*(0 if a is None else a for a in args)), n)
+
+
+@pytest.mark.parametrize("bad,status", ROPE_BAD + [(dict(w=0), EINVAL), (dict(wk=A + 4), EALIGN), (dict(r=0), EINVAL),
+                                                   (dict(dtype=7), EINVAL), (dict(T=0), 0)])
+def test_arguments_in_an_array_are_the_same_arguments(lib, bad, status):
+    """Every refusal depends on the argument at its own place, so the array's order is the prototype's."""
+    by_array = _Slots(lib)
+    if not {"w", "wk", "r"} & set(bad):
+        for fn in ("rope_fwd", "rope_bwd"):
+            assert _rope(by_array, fn, **bad) == _rope(lib, fn, **bad) == status
+    assert _norm_fwd(by_array, **bad) == _norm_fwd(lib, **bad) == status
+    if bad != dict(T=0):
+        assert _norm_bwd(by_array, **bad) == _norm_bwd(lib, **bad) == status
+    ln = {k: v for k, v in bad.items() if k in ("w", "r", "dtype", "T")}
+    if ln == bad:
+        assert _ln_fwd(by_array, **bad) == _ln_fwd(lib, **bad) == status
+        if bad != dict(T=0):
+            assert _ln_bwd(by_array, **bad) == _ln_bwd(lib, **bad) == status
+
+
+@pytest.mark.parametrize("bad,status", [(dict(eps=-1.0), EINVAL), (dict(eps=1e300), EINVAL), (dict(eps=math.nan), EINVAL)])
+def test_floats_in_an_array(lib, bad, status):
+    assert _ln_fwd(_Slots(lib), **bad) == _norm_fwd(_Slots(lib), **bad) == status
+
+
+def test_arrays_that_are_not_the_entry_points(lib):
+    for name, (entry, pack, n) in rn._SLOTS.items():
+        assert n == len(rn._SIGS[name][1])
+        good = pack(*[0] * n)
+        assert lib.norm_call(entry, good, n - 1) == lib.norm_call(entry, good, n + 1) == EINVAL
+        assert lib.norm_call(entry, None, n) == EINVAL
+    assert lib.norm_call(len(rn._SLOTS), good, n) == lib.norm_call(-1, good, n) == EINVAL
+    assert _rope(_Slots(lib), layout=1 << 32) == EINVAL and _rope(_Slots(lib), dtype=(1 << 32) + 1) == EINVAL
+    enum = re.findall(r"NORM_(\w+)\s*=\s*(\d+)", open(os.path.join(ROOT, "include", "slots.h")).read())
+    assert {n.lower(): int(v) for n, v in enum} == {n: e for n, (e, _, _) in rn._SLOTS.items()}
 
 
 def test_workspace_queries(lib):

@@ -206,6 +206,32 @@ def test_the_binding_refuses_what_would_be_read_wrongly():
         rn.layernorm_fwd(x, torch.empty(129, device=DEV)[1:], b, y, m, r)
 
 
+def test_the_entry_points_called_with_their_own_arguments():
+    """The C entry points, which the binding calls with an array, argument by argument: the same bits."""
+    lib, st = rn.load(), torch.cuda.current_stream().cuda_stream
+    T, D = 21, 200
+    x, g = (synth.normal16((T, D), i, DEV) for i in (131, 132))
+    w, b = synth.gamma_f32(D, 133, DEV), synth.gamma_f32(D, 134, DEV, mean=0.0)
+    out = []
+    for direct in (False, True):
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        m, r = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+        dw, db = torch.empty(D, device=DEV), torch.empty(D, device=DEV)
+        ws = torch.empty(rn.layernorm_bwd_workspace_bytes(T, D), dtype=torch.uint8, device=DEV)
+        if direct:
+            assert lib.layernorm_fwd(x.data_ptr(), D, w.data_ptr(), b.data_ptr(), y.data_ptr(), D, m.data_ptr(),
+                                     r.data_ptr(), T, D, 1e-5, 1, 0, st) == 0
+            assert lib.layernorm_bwd(g.data_ptr(), D, x.data_ptr(), D, w.data_ptr(), m.data_ptr(), r.data_ptr(),
+                                     dx.data_ptr(), D, dw.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel(), T, D, 1, 0,
+                                     st) == 0
+        else:
+            rn.layernorm_fwd(x, w, b, y, m, r, 1e-5, True)
+            rn.layernorm_bwd(g, x, w, m, r, dx, dw, db, ws, True)
+        out.append((y, dx, m, r, dw, db))
+    for a, c in zip(*out):
+        assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+
+
 def test_no_rows():
     x, g, w, b = _inputs(0, 128, 1)
     _fwd(x, w, b)

@@ -412,6 +412,42 @@ def test_norm_and_rope_weight_gradients_repeat():
         assert torch.equal(first[0][2], again[0][2]) and torch.equal(first[1][2], again[1][2])
 
 
+def test_the_entry_points_called_with_their_own_arguments():
+    """The C entry points, which the binding calls with an array, argument by argument: the same bits."""
+    lib, st = rn.load(), torch.cuda.current_stream().cuda_stream
+    T, Hq, Hk, D = 37, 4, 2, 64
+    q, k = _heads(T, Hq, Hk, D, 121, F16, "qkv")
+    g, h = _heads(T, Hq, Hk, D, 122, F16)
+    wq, wk = _weights(D, Hk, 123, True)
+    f, pos = _freq(32), _pos(T, 124)
+    W = (Hq + 2 * Hk) * D
+
+    def p(t):
+        return t.data_ptr()
+
+    (_, o, r), (_, ok, rk) = _norm_fwd(q, k, wq, wk, f, pos, True, True)
+    (_, d, dw), (_, dk, dwk) = _norm_bwd(g, h, q, k, wq, wk, f, r, rk, pos, True, True)
+    o2, ok2, d2, dk2 = (torch.empty((T, n, D), dtype=F16, device=DEV) for n in (Hq, Hk, Hq, Hk))
+    r2, rk2 = torch.empty_like(r), torch.empty_like(rk)
+    dw2, dwk2 = torch.empty_like(dw), torch.empty_like(dwk)
+    own = ((Hq * D, D), (Hk * D, D))
+    assert lib.rmsnorm_rope_fwd(p(q), W, D, p(k), W, D, p(wq), p(wk), p(f), p(pos), 1, p(o2), *own[0], p(ok2), *own[1],
+                                p(r2), p(rk2), T, Hq, Hk, D, 32, SCALE, 1, EPS, 1, 1, st) == 0
+    ws = torch.empty(rn.rmsnorm_rope_bwd_workspace_bytes(T, Hq, Hk, D), dtype=torch.uint8, device=DEV)
+    assert lib.rmsnorm_rope_bwd(p(g), *own[0], p(h), *own[1], p(q), W, D, p(k), W, D, p(wq), p(wk), p(f), p(pos), 1,
+                                p(r2), p(rk2), p(d2), *own[0], p(dk2), *own[1], p(dw2), p(dwk2), p(ws), ws.numel(), T,
+                                Hq, Hk, D, 32, SCALE, 1, 1, 1, st) == 0
+    for a, b in ((o, o2), (ok, ok2), (d, d2), (dk, dk2)):
+        assert torch.equal(_bits(a), _bits(b))
+    for a, b in ((r, r2), (rk, rk2), (dw, dw2), (dwk, dwk2)):
+        assert torch.equal(a, b)
+    for fn in ("rope_fwd", "rope_bwd"):
+        getattr(rn, fn)(q, k, f, o2, ok2, pos, SCALE, True)
+        assert getattr(lib, fn)(p(q), W, D, p(k), W, D, p(f), p(pos), 1, p(d2), *own[0], p(dk2), *own[1], T, Hq, Hk, D, 32,
+                                SCALE, 1, 1, st) == 0
+        assert torch.equal(_bits(o2), _bits(d2)) and torch.equal(_bits(ok2), _bits(dk2))
+
+
 def test_no_tokens():
     q, k = _heads(0, 4, 2, 64, 1)
     f = _freq(64)
