@@ -27,8 +27,10 @@
 //   * kHalves (ROPE_HALF, R a multiple of 16): a 16-byte vector of the first half
 //     and the vector of its partners R/2 values on; beyond the turned part two vectors.
 //   * kNeighbours (ROPE_INTERLEAVED): two vectors.
-//   * kHalvesAny (ROPE_HALF, any R): as kHalves, but B (and, beyond the turned part,
-//     A) lies at any even number of bytes and may be cut short by the half's end.
+//   * kHalvesAny (ROPE_HALF, any R): as kHalves, but the turned B lies at any even
+//     number of bytes, and both may be cut short by the half's end. Beyond the turned
+//     part the vectors are counted from the row's end; what is left between, two
+//     values a lane.
 //   * kHalves8 (ROPE_HALF, R a multiple of 8): the same in whole steps of 8 bytes.
 #pragma once
 
@@ -125,8 +127,8 @@ __device__ __forceinline__ uint32_t narrow2(float2 v) {
     return w;
 }
 
-// Sixteen bytes at any even address, through the words that hold them (n <= 8
-// values are wanted; no word without one of them is read).
+// Eight values at any even address, through the words that hold them (the first n
+// are wanted; no word without one of them is read).
 __device__ __forceinline__ uint4 lds_window(uint32_t p, int n) {
     const bool odd = p & 2u;
     const uint32_t q = p & ~3u;
@@ -161,7 +163,23 @@ __device__ __forceinline__ void sts_window(uint32_t p, uint4 v, int n) {
     }
 }
 
-// Four (n > 0) or eight (n > 4) values at an address of whole 8 bytes.
+// The first n (even) of eight values at an address of whole words, zeros beyond.
+__device__ __forceinline__ uint4 lds_words(uint32_t p, int n) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (n > 0) v.x = lds32(p);
+    if (n > 2) v.y = lds32(p + 4);
+    if (n > 4) v.z = lds32(p + 8);
+    if (n > 6) v.w = lds32(p + 12);
+    return v;
+}
+__device__ __forceinline__ void sts_words(uint32_t p, uint4 v, int n) {
+    if (n > 0) sts32(p, v.x);
+    if (n > 2) sts32(p + 4, v.y);
+    if (n > 4) sts32(p + 8, v.z);
+    if (n > 6) sts32(p + 12, v.w);
+}
+
+// Four (n > 0) or eight (n > 4) values at an address of whole 8 bytes, zeros beyond.
 __device__ __forceinline__ uint4 lds_window8(uint32_t p, int n) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (n > 0) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
@@ -222,18 +240,17 @@ __device__ __forceinline__ void turn_neighbours(Oct& A, const float2 (&c)[2], co
             if (i >= n) A.p[i] = was.p[i];
     }
 }
-// Values from place n on become zero.
-__device__ __forceinline__ void cut(Oct& A, int n) {
-    if (n < 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (2 * i >= n) A.p[i].x = 0.0f;
-            if (2 * i + 1 >= n) A.p[i].y = 0.0f;
-        }
-    }
-}
 __device__ __forceinline__ uint4 keep_if(bool k, uint4 v) {
     return make_uint4(k ? v.x : 0u, k ? v.y : 0u, k ? v.z : 0u, k ? v.w : 0u);
+}
+
+// The first n of eight 16-bit values, zeros beyond.
+__device__ __forceinline__ uint4 first_of(uint4 v, int n) {
+    if (n < 8) {
+        auto word = [n](uint32_t w, int i) { return 2 * i + 1 < n ? w : 2 * i < n ? w & 0xffffu : 0u; };
+        v = make_uint4(word(v.x, 0), word(v.y, 1), word(v.z, 2), word(v.w, 3));
+    }
+    return v;
 }
 
 enum RopeKind : int { kHalves = 0, kNeighbours = 1, kHalvesAny = 2, kHalves8 = 3 };
@@ -271,6 +288,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     // their eight values there are.
     const int NC = D >> 3;
     const int NP = KIND == kNeighbours ? 0 : ANY ? (half + 7) >> 3 : half >> 3;  // units of the halves
+    const int NV = ANY ? min((D - a.R) >> 3, 2 * ((1 << LG) - NP)) : 0;  // ANY: vectors at the row's end, not turned
     const bool turned = l < NP;
     int atA, atB, nA = 8, nB = 8;
     if (turned) {
@@ -278,10 +296,11 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         atB = half + 8 * l;
         if constexpr (ANY) nA = nB = min(8, half - 8 * l);
     } else if constexpr (ANY) {
-        atA = a.R + 16 * (l - NP);
-        atB = atA + 8;
-        nA = max(0, min(8, D - atA));
-        nB = max(0, min(8, D - atB));
+        const int c = l - NP, rest = (NV + 1) >> 1;
+        atA = D - 8 * (NV - c);
+        atB = D - 8 * (NV - rest - c);
+        nA = c < rest ? 8 : 0;
+        nB = c + rest < NV ? 8 : 0;
     } else {
         const int rest = (NC - 2 * NP + 1) >> 1, c = l + NP;  // 2 NP + (l - NP)
         atA = 8 * c;
@@ -296,9 +315,9 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
         if (nB == 0) atB = 0;
     }
     const bool hasA = FULL || nA > 0, hasB = FULL || nB > 0;
-    // kHalvesAny: two values beyond the lanes' units, if there are any for this lane.
-    const int atX = ANY && NORM ? a.R + 16 * ((1 << LG) - NP) + 2 * l : D;
-    const bool hasX = ANY && NORM && atX < D;
+    // ANY: two values between the halves and those vectors, if there are any for this lane.
+    const int atX = a.R + 2 * l;
+    const bool hasX = ANY && NORM && atX < D - 8 * NV;
     const uint32_t rowA = 2u * atA, rowB = 2u * atB, rowX = 2u * atX;
     // kNeighbours: pairs of A and of B that are turned (past 4: all).
     const int tA = hasA ? half - (atA >> 1) : 0, tB = hasB ? half - (atB >> 1) : 0;
@@ -311,17 +330,40 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     // Rows come and go once: out of L2 first, both ways (stores at the default
     // priority measured 1 to 3 % slower, loads at the ordinary one 0 to 4 %).
     const uint64_t pol = policy_evict_first();
-    auto load = [&](uint32_t at, bool has, int n) -> uint4 {
-        if constexpr (KIND == kHalvesAny) return lds_window(at, n);
-        else if constexpr (KIND == kHalves8) return lds_window8(at, n);
-        else if constexpr (FULL) return lds128(at);
-        else return keep_if(has, lds128(at));
+    const bool words = (half & 1) == 0;  // kHalvesAny: B lies at whole words
+    auto loadA = [&](uint32_t at) -> uint4 {
+        if constexpr (KIND == kHalves8) return lds_window8(at, nA);
+        const uint4 v = lds128(at);
+        if constexpr (ANY) return NORM ? first_of(v, nA) : v;
+        else return FULL ? v : keep_if(hasA, v);
     };
-    auto store = [&](uint32_t at, bool has, const Oct& o, int n) {
+    auto loadB = [&](uint32_t at) -> uint4 {
+        if constexpr (KIND == kHalvesAny) {
+            if (words) return lds_words(at, nB);
+            const uint4 v = lds_window(at, nB);
+            return NORM ? first_of(v, nB) : v;
+        } else if constexpr (KIND == kHalves8) {
+            return lds_window8(at, nB);
+        } else {
+            return FULL ? lds128(at) : keep_if(hasB, lds128(at));
+        }
+    };
+    auto storeA = [&](uint32_t at, const Oct& o) {
         const uint4 v = oct_pack<F16>(o);
-        if constexpr (KIND == kHalvesAny) sts_window(at, v, n);
-        else if constexpr (KIND == kHalves8) sts_window8(at, v, n);
-        else if (has) sts128(at, v);
+        if constexpr (KIND == kHalves8) sts_window8(at, v, nA);
+        else if (FULL || nA == 8) sts128(at, v);
+        else if constexpr (KIND == kHalvesAny) sts_window(at, v, nA);
+    };
+    auto storeB = [&](uint32_t at, const Oct& o) {
+        const uint4 v = oct_pack<F16>(o);
+        if constexpr (KIND == kHalves8) {
+            sts_window8(at, v, nB);
+        } else if constexpr (KIND == kHalvesAny) {
+            if (words) sts_words(at, v, nB);
+            else sts_window(at, v, nB);
+        } else if (FULL || nB == 8) {
+            sts128(at, v);
+        }
     };
     uint32_t phase = 0;  // of the stage that comes next
     int cur = 0;
@@ -376,6 +418,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) fetch();
     // While the first rows come:
+    for (int i = half + lane; i < hp; i += 32) cs[i] = cs[hp + i] = 0.0f;  // zeros are turned there
     for (int i = tid; i < half; i += nt) F[i] = rope_turns(a.inv_freq[i]);
     if constexpr (NORM) {
         for (int i = tid; i < 2 * D; i += nt) {
@@ -497,8 +540,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
             for (int i = 0; i < RB; ++i) {
                 const uint32_t p = at + i * spread * pitch;
                 if (NORM || KIND == kNeighbours || turned) {
-                    rawA[i] = load(p + rowA, hasA, nA);
-                    rawB[i] = load(p + rowB, hasB, nB);
+                    rawA[i] = loadA(p + rowA);
+                    rawB[i] = loadB(p + rowB);
                 }
             }
             if constexpr (MODE == kTurn) {
@@ -524,8 +567,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                     } else if (turned) {
                         Oct A = oct_unpack<F16>(rawA[i]), B = oct_unpack<F16>(rawB[i]);
                         turn(A, B);
-                        store(p + rowA, true, A, nA);
-                        store(p + rowB, true, B, nB);
+                        storeA(p + rowA, A);
+                        storeB(p + rowB, B);
                     }
                 }
             } else {
@@ -543,20 +586,14 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                     if constexpr (BWD) {
                         A[i] = oct_unpack<F16>(rawA[i]);
                         B[i] = oct_unpack<F16>(rawB[i]);
-                        xA[i] = oct_unpack<F16>(load(p + op_bytes + rowA, hasA, nA));
-                        xB[i] = oct_unpack<F16>(load(p + op_bytes + rowB, hasB, nB));
+                        xA[i] = oct_unpack<F16>(loadA(p + op_bytes + rowA));
+                        xB[i] = oct_unpack<F16>(loadB(p + op_bytes + rowB));
                         r[i] = rs[cur * rows + row];
                         turn(A[i], B[i]);
-                        if constexpr (ANY) {  // cosines beyond the half's end
-                            cut(A[i], nA);
-                            cut(B[i], nB);
-                            cut(xA[i], nA);
-                            cut(xB[i], nB);
-                            if (hasX) {
-                                xX[i] = widen2<F16>(lds32(p + op_bytes + rowX));
-                                accX = fma2(X[i], fmul2(xX[i], both(r[i])), accX);
-                                X[i] = fmul2(X[i], wX);
-                            }
+                        if (hasX) {
+                            xX[i] = widen2<F16>(lds32(p + op_bytes + rowX));
+                            accX = fma2(X[i], fmul2(xX[i], both(r[i])), accX);
+                            X[i] = fmul2(X[i], wX);
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -572,10 +609,6 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                     } else {
                         A[i] = oct_unpack<F16>(rawA[i]);
                         B[i] = oct_unpack<F16>(rawB[i]);
-                        if constexpr (KIND == kHalvesAny) {  // the other half of a word at the end
-                            cut(A[i], nA);
-                            cut(B[i], nB);
-                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             sum2 = fma2(A[i].p[e], A[i].p[e], sum2);
@@ -610,8 +643,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                         turn(A[i], B[i]);
                         if (hasX) sts32(p + rowX, narrow2<F16>(fmul2(fmul2(X[i], both(r[i])), wX)));
                     }
-                    store(p + rowA, hasA, A[i], nA);
-                    store(p + rowB, hasB, B[i], nB);
+                    storeA(p + rowA, A[i]);
+                    storeB(p + rowB, B[i]);
                 }
             }
         };

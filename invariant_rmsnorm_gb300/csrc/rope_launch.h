@@ -45,17 +45,17 @@ constexpr int64_t kRopeManyFrom = 152 * (kRopeThreads / 32);
 
 // log2 of the lanes a head: the smallest power of two that holds its units of two
 // times eight values. Where R is no multiple of 16 the halves' last unit is cut
-// short, and the rest of a head that is normalised has units of its own, one more
-// than a head's 16th at most: what is beyond the last lane's unit, at most 14
-// values, is taken two a lane, or needs twice the lanes. A function of D, R and the
-// layout alone, so a row's reduction tree is too.
+// short, and the rest of a head that is normalised has units of its own, of whole
+// vectors counted from the row's end: what they leave is taken two values a lane,
+// or needs twice the lanes. A function of D, R and the layout alone, so a row's
+// reduction tree is too.
 inline int rope_lanes_log2(int D, int R, bool any_halves, bool norm) {
     const int units = (D / 8 + 1) / 2;
     int lg = 2;
     while ((1 << lg) < units) ++lg;
     if (any_halves && norm) {
-        const int beyond = D - R - 16 * ((1 << lg) - (R / 2 + 7) / 8);
-        if (beyond > 2 << lg) ++lg;
+        const int vectors = std::min((D - R) / 8, 2 * ((1 << lg) - (R / 2 + 7) / 8));
+        if (D - R - 8 * vectors > 2 << lg) ++lg;
     }
     return lg;
 }
