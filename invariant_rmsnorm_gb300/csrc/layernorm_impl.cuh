@@ -14,11 +14,12 @@
 //     the group; no barrier.
 //   * Teams (forward, wider rows): 1 to 8 warps a row, up to 8 vectors a thread in
 //     registers. A row's two sums meet at its team's own barrier.
-//   * CTA rows (backward, wider rows): a CTA a row from a ring of bulk (TMA) copies;
-//     thread t owns the 16-byte vectors t, t + NT, ... and their columns' weight
-//     gradients; warps' sums are added in warp order after one barrier, which also
-//     tells thread 0 that the stage is read, so it refills it: there is no producer
-//     warp, and 512 threads keep 128 registers each (a 17th warp would cut them to 96).
+//   * CTA rows (backward, wider rows): a CTA, or a team of its warps, a row from a
+//     ring of bulk (TMA) copies; thread t owns the 16-byte vectors t, t + NT, ... and
+//     their columns' weight gradients; warps' sums are added in warp order after one
+//     barrier, which also tells thread 0 that the stage is read, so it refills it:
+//     there is no producer warp, and 512 threads keep 128 registers each (a 17th warp
+//     would cut them to 96).
 // Either way a row's tree depends on D alone. The arithmetic is issued in pairs
 // (f32x2): at one operation a value the group kernels spent 19 issue slots a value
 // and stood at 64 % of the copy rate at D = 128. Weight gradients are summed by the
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kLnRowThreads, MINB) ln_rows_bwd_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
-// A CTA a row
+// A CTA, or a team of its warps, a row
 // ---------------------------------------------------------------------------
 
 // K values a lane (1, 2 or 4) summed over the warp: lane l ends with the total
@@ -496,23 +497,43 @@ __global__ void __launch_bounds__(THREADS, MINB) ln_team_fwd_kernel(const LnFwdA
     pdl_release();
 }
 
+// The teams' predicate, true for all of a team's threads if it is for each.
+template <bool TEAMS>
+__device__ __forceinline__ bool team_and(bool ok, int bar, int threads) {
+    if constexpr (!TEAMS) return __syncthreads_and(ok ? 1 : 0);
+    int all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 q, %1, 0;\n\tbarrier.cta.red.and.pred p, %2, %3, q;\n\tselp.s32 %0, 1, 0, p;\n\t}"
+        : "=r"(all) : "r"(ok ? 1 : 0), "r"(bar), "r"(threads) : "memory");
+    return all != 0;
+}
+
 // Backward: one CTA a chunk of rows. Stage: [g | x][D] 16-bit. Between the two
 // halves of a row its c and g w stay in registers; SW (the widest rows, whose
 // weight gradients take 48 or 64 registers): the packed g and x stay instead, and
-// the weights lie in shared memory.
-template <bool F16, int VPT, int MAXT, int MINB, bool BIAS, bool SW>
-__global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs a, const int S) {
+// the weights lie in shared memory. TEAMS: several teams of nt threads a CTA, each
+// with a ring and a barrier of its own, take every so many-th row; their weight
+// gradients are added in team order at the end, so that narrow rows leave a partial
+// row a CTA and not one a few warps.
+template <bool F16, int VPT, int MAXT, int THREADS, int MINB, bool BIAS, bool SW, bool TEAMS>
+__global__ void __launch_bounds__(THREADS, MINB) ln_wide_bwd_kernel(const LnBwdArgs a, const int S, const int team_threads) {
     constexpr int NW = warp_places(MAXT);
     extern __shared__ __align__(128) unsigned char smem[];
-    const int NV = a.D >> 3, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nt = TEAMS ? team_threads : blockDim.x, teams = TEAMS ? blockDim.x / nt : 1;
+    const int team = TEAMS ? threadIdx.x / nt : 0, tid = threadIdx.x - team * nt;
+    const int NV = a.D >> 3, lane = tid & 31, warp = tid >> 5;
     const uint32_t row_bytes = static_cast<uint32_t>(a.D) * 2u;
     const uint32_t stage_bytes = 2 * row_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * stage_bytes);
-    float* red = reinterpret_cast<float*>(full + ((S + 1) & ~1));      // [2][2][NW]
-    float4* wb = reinterpret_cast<float4*>(red + 4 * NW);              // SW: the weights
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(teams) * S * stage_bytes);
+    uint64_t* full = bars + team * S;
+    float* reds = reinterpret_cast<float*>(bars + ((teams * S + 1) & ~1));  // [teams][2][2][NW]
+    float* red = reds + team * 4 * NW;
+    unsigned char* ring = smem + static_cast<size_t>(team) * S * stage_bytes;
+    float4* wb = reinterpret_cast<float4*>(reds + teams * 4 * NW);     // SW: the weights
     float2* stat = reinterpret_cast<float2*>(wb + (SW ? 2 * NV : 0));  // [chunk]: mean, rstd
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
-    const int n_my = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.T - row0));
+    const int n_rows = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.T - row0));
+    const int n_my = TEAMS ? (n_rows - team + teams - 1) / teams : n_rows;  // rows team, team + teams, ... of the chunk
     if (tid == 0) {
         for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
         fence_mbar_init();
@@ -524,14 +545,15 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
     const uint64_t pol = policy_evict_first();
     auto issue = [&](int i) {
         const int s = i % S;
-        unsigned char* dst = smem + static_cast<size_t>(s) * stage_bytes;
+        unsigned char* dst = ring + static_cast<size_t>(s) * stage_bytes;
+        const int64_t row = row0 + i * teams + team;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
-        bulk_g2s(dst, a.g + (row0 + i) * a.ldg, row_bytes, &full[s], pol);
-        bulk_g2s(dst + row_bytes, a.x + (row0 + i) * a.ldx, row_bytes, &full[s], pol);
+        bulk_g2s(dst, a.g + row * a.ldg, row_bytes, &full[s], pol);
+        bulk_g2s(dst + row_bytes, a.x + row * a.ldx, row_bytes, &full[s], pol);
     };
     if (tid == 0)
         for (int i = 0; i < min(S, n_my); ++i) issue(i);
-    for (int i = tid; i < n_my; i += nt) stat[i] = make_float2(__ldg(a.mean + row0 + i), __ldg(a.rstd + row0 + i));
+    for (int i = threadIdx.x; i < n_rows; i += blockDim.x) stat[i] = make_float2(__ldg(a.mean + row0 + i), __ldg(a.rstd + row0 + i));
     Oct w[VPT], aw[VPT], ab[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -545,8 +567,8 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
     uint32_t ph = 0;
     for (int i = 0; i < n_my; ++i) {
         const bool ok = mbar_wait(&full[s], ph);
-        const unsigned char* st = smem + static_cast<size_t>(s) * stage_bytes;
-        const float2 mr = stat[i];
+        const unsigned char* st = ring + static_cast<size_t>(s) * stage_bytes;
+        const float2 mr = stat[i * teams + team];
         Oct g[VPT], c[VPT];  // g w and x - mu
         uint4 gv[VPT], xv[VPT];
         float2 p1 = make_float2(0.0f, 0.0f), p2 = p1;
@@ -567,9 +589,9 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
             const float t = warp_sums<2>(sum, lane);
             if ((lane & 15) == 0) rb[(lane >> 4) * NW + warp] = t;
         }
-        if (!__syncthreads_and(ok ? 1 : 0)) {
+        if (!team_and<TEAMS>(ok, team + 1, nt)) {
             if (tid == 0) ln_abort(full, S, i, min(i + S, n_my) - 1);
-            return;
+            break;
         }
         if (tid == 0 && i + S < n_my) {  // every thread has the stage in registers
             fence_proxy_async_smem();
@@ -581,7 +603,7 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
         }
         const float rc1 = fmul(mr.y, fmul(warps_total<NW>(rb), a.rcp_d));
         const float m = -fmul(fmul(mr.y, mr.y), fmul(fmul(warps_total<NW>(rb + NW), mr.y), a.rcp_d));
-        uint16_t* dx = a.dx + (row0 + i) * a.lddx;
+        uint16_t* dx = a.dx + (row0 + i * teams + team) * a.lddx;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = j * nt + tid;
@@ -604,6 +626,34 @@ __global__ void __launch_bounds__(MAXT, MINB) ln_wide_bwd_kernel(const LnBwdArgs
     const uint64_t keep = policy_evict_last();
     float* pw = a.partials + static_cast<int64_t>(blockIdx.x) * a.D;
     float* pb = pw + static_cast<int64_t>(gridDim.x) * a.D;
+    if constexpr (TEAMS) {  // the teams' sums in team order, dw, then db through the rings' memory
+        float* comb = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int part = 0; part < (BIAS ? 2 : 1); ++part) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = j * nt + tid;
+                if (v < NV) {
+                    float4* o = reinterpret_cast<float4*>(comb + team * a.D + 8 * v);
+                    const Oct& t = part ? ab[j] : aw[j];
+                    o[0] = make_float4(t.p[0].x, t.p[0].y, t.p[1].x, t.p[1].y);
+                    o[1] = make_float4(t.p[2].x, t.p[2].y, t.p[3].x, t.p[3].y);
+                }
+            }
+            __syncthreads();
+            for (int q = threadIdx.x; q < a.D / 4; q += blockDim.x) {
+                float4 t = reinterpret_cast<const float4*>(comb)[q];
+                for (int m = 1; m < teams; ++m) {
+                    const float4 u = reinterpret_cast<const float4*>(comb + m * a.D)[q];
+                    t = make_float4(fadd(t.x, u.x), fadd(t.y, u.y), fadd(t.z, u.z), fadd(t.w, u.w));
+                }
+                st_global_f4_hint((part ? pb : pw) + 4 * q, t.x, t.y, t.z, t.w, keep);
+            }
+        }
+        pdl_release();
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int v = j * nt + tid;
@@ -699,31 +749,36 @@ cudaError_t rows_bwd(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
     return launch_kernel(kern, grid, kLnRowThreads, smem, st, a);
 }
 
-// The ring's stages: as many as bring the copies in flight on an SM (all its
-// CTAs') to 88 KB. More measured slower as well as fewer (32768 x 4096, two CTAs
-// with three stages of 16 KB each 95 % of the copy rate, with four 87 %, with two
-// 89 %; 16384 x 8192, one CTA: three of 32 KB 93 %, four 92 %, two 82 %).
+// The ring's stages: as many as bring the copies in flight on an SM (of all its
+// CTAs and teams) to 88 KB. More measured slower as well as fewer (32768 x 4096,
+// two rows at a time with three stages of 16 KB each 95 % of the copy rate, with
+// four 87 %, with two 89 %; 16384 x 8192, one CTA: three of 32 KB 93 %, four 92 %, two 82 %).
 constexpr size_t kLnBwdInFlight = 88 * 1024;
 
-template <bool F16, int VPT, int MAXT, int MINB, bool BIAS, bool SW>
+template <bool F16, int VPT, int MAXT, int THREADS, int MINB, bool BIAS, bool SW>
 cudaError_t wide_bwd(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
+    constexpr bool TEAMS = THREADS > MAXT;
     const int NV = a.D / 8;
+    const LnShape shape = ln_shape(a.D);
+    const int teams = TEAMS ? static_cast<int>(shape.step) : 1;
     const int threads = ((NV + VPT - 1) / VPT + 31) / 32 * 32;
     const size_t stage = static_cast<size_t>(4) * a.D;
-    const size_t fixed = 4 * warp_places(MAXT) * 4 + 8 * static_cast<size_t>(a.chunk) + 16 + (SW ? static_cast<size_t>(a.D) * 4 : 0);
-    const size_t all = stage * ln_shape(a.D).per_sm;
+    const size_t fixed = teams * 4 * warp_places(MAXT) * 4 + 8 * static_cast<size_t>(a.chunk) + 16 + (SW ? static_cast<size_t>(a.D) * 4 : 0);
+    const size_t all = stage * shape.per_sm * teams;
     const int S = std::max(2, static_cast<int>((kLnBwdInFlight + all - 1) / all));
-    const size_t smem = S * (stage + 8) + fixed;
-    if (smem > kLnMaxSmem) return cudaErrorInvalidConfiguration;
-    const auto kern = ln_wide_bwd_kernel<F16, VPT, MAXT, MINB, BIAS, SW>;
+    const size_t smem = teams * S * (stage + 8) + fixed;
+    if (smem > kLnMaxSmem || threads > MAXT || teams * threads > THREADS) return cudaErrorInvalidConfiguration;
+    const auto kern = ln_wide_bwd_kernel<F16, VPT, MAXT, THREADS, MINB, BIAS, SW, TEAMS>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_kernel(kern, grid, threads, smem, st, a, S);
+    return launch_kernel(kern, grid, teams * threads, smem, st, a, S, threads);
 }
 
 // Shapes by width, each the fastest measured (ln_shape has their CTAs an SM). Of
 // the copy rate, both passes, 65536 to 8192 rows: D = 768 87 % (a CTA a row: 80),
-// 1024 88, 2048 91, 4096 96, 5000 91, 8192 96, 16384 92. D = 128: 82 % of 30 us.
+// 1024 91, 2048 97, 4096 97, 5000 91, 8192 96, 16384 92. D = 128: 82 % of 30 us.
+// Up to 4096 several teams a CTA leave 152 partial rows: a CTA a row, as many warps
+// an SM and 304 to 1216 partial rows, 88, 92 and 96 %.
 template <bool F16, bool BIAS>
 cudaError_t ln_bwd_dispatch(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
     const int NV = a.D / 8;
@@ -739,13 +794,12 @@ cudaError_t ln_bwd_dispatch(const LnBwdArgs& a, unsigned grid, cudaStream_t st) 
     if (NV <= 64) return rows_bwd<F16, 32, 2, 1, 3, 2, false, BIAS>(a, grid, st);
     if (NV <= 96) return rows_bwd<F16, 32, 3, 1, 3, 2, true, BIAS>(a, grid, st);
     if (NV < kLnCtaRowFrom) return rows_bwd<F16, 32, 4, 1, 3, 2, true, BIAS>(a, grid, st);
-    if (NV <= 256) return wide_bwd<F16, 2, 128, 4, BIAS, false>(a, grid, st);
-    if (NV <= 512) return wide_bwd<F16, 2, 256, 2, BIAS, false>(a, grid, st);
-    if (NV <= 640) return wide_bwd<F16, 2, 320, 2, BIAS, false>(a, grid, st);
-    if (NV <= 768) return wide_bwd<F16, 2, 384, 1, BIAS, false>(a, grid, st);
-    if (NV <= 1024) return wide_bwd<F16, 2, 512, 1, BIAS, false>(a, grid, st);
-    if (NV <= 1536) return wide_bwd<F16, 3, 512, 1, BIAS, true>(a, grid, st);
-    return wide_bwd<F16, 4, 512, 1, BIAS, true>(a, grid, st);
+    if (NV <= kLnTeamsTo) return wide_bwd<F16, 2, 256, 512, 1, BIAS, false>(a, grid, st);
+    if (NV <= 640) return wide_bwd<F16, 2, 320, 320, 2, BIAS, false>(a, grid, st);
+    if (NV <= 768) return wide_bwd<F16, 2, 384, 384, 1, BIAS, false>(a, grid, st);
+    if (NV <= 1024) return wide_bwd<F16, 2, 512, 512, 1, BIAS, false>(a, grid, st);
+    if (NV <= 1536) return wide_bwd<F16, 3, 512, 512, 1, BIAS, true>(a, grid, st);
+    return wide_bwd<F16, 4, 512, 512, 1, BIAS, true>(a, grid, st);
 }
 
 }  // namespace

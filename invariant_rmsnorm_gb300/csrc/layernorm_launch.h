@@ -36,6 +36,8 @@ struct LnBwdArgs {
 // The backward's launch shape, by D alone: it decides the weight gradients' chunks.
 constexpr int64_t kLnCtaRowFrom = 128;  // 16-byte vectors a row from which a CTA takes a row (D >= 1024)
 
+constexpr int64_t kLnTeamsTo = 512;      // and up to which a CTA of several teams takes a row a team (D <= 4096)
+
 struct LnShape {
     int64_t per_sm;  // CTAs an SM
     int64_t step;    // rows that a CTA takes at a time
@@ -55,9 +57,10 @@ inline LnShape ln_shape(int64_t D) {
         if (NV > 8 && lanes(3) < G) G = lanes(3);
         return {2, 256 / std::min<int64_t>(G, 32)};
     }
-    // A CTA of two vectors a thread: 16 warps an SM, 20 at 10 warps a row.
+    // Two vectors a thread. One CTA of 16 warps an SM, in teams of a row's warps; a row
+    // of more warps is a CTA's alone, two an SM at 10 warps, else one.
     const int64_t warps = ((NV + 1) / 2 + 31) / 32;
-    if (NV <= 512) return {16 / warps, 1};
+    if (NV <= kLnTeamsTo) return {1, 16 / warps};
     return {NV <= 640 ? 20 / warps : 1, 1};
 }
 
