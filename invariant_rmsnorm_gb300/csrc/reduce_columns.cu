@@ -7,9 +7,9 @@
 // sector of each partial row, of one of the two outputs (blockIdx.y); a thread
 // adds 4 of them over one range.
 //
-// Bound by the latency of a range's loads, so the ranges are short (8192 x 1024,
-// 1216 chunks: LayerNorm backward 14.4 us, with 32 ranges and a column a thread
-// 15.8; 262144 x 128 36.5 and 37.2 us), and by the loads' rate where there are many
+// Bound by the latency of a range's loads, so the ranges are short (LayerNorm
+// backward of 8192 x 1024 in 1216 chunks: 14.4 us, with 32 ranges and a column a
+// thread 15.8; of 262144 x 128 in 304: 36.5 and 37.2 us), and by the loads' rate where there are many
 // columns. Sixteen predicated loads in flight a thread measured slower at every
 // size (24.9 and 38.8 us). The loads are streaming ones: LayerNorm's partial rows
 // lie in L2 at high priority, and an ordinary load leaves them there in the way of
