@@ -9,11 +9,12 @@
 //
 // Bound by the latency of a range's loads, so the ranges are short (LayerNorm
 // backward of 8192 x 1024 in 1216 chunks: 14.4 us, with 32 ranges and a column a
-// thread 15.8; of 262144 x 128 in 304: 36.5 and 37.2 us), and by the loads' rate where there are many
-// columns. Sixteen predicated loads in flight a thread measured slower at every
-// size (24.9 and 38.8 us). The loads are streaming ones: LayerNorm's partial rows
-// lie in L2 at high priority, and an ordinary load leaves them there in the way of
-// what comes next (8192 x 16384: 131 us, with ordinary loads 135).
+// thread 15.8; of 262144 x 128 in 304: 36.5 and 37.2 us), and by the loads' rate
+// where there are many columns. Sixteen predicated loads in flight a thread
+// measured slower at both (24.9 and 38.8 us). The loads are streaming ones:
+// LayerNorm's partial rows lie in L2 at high priority, and an ordinary load leaves
+// them there in the way of what comes next (8192 x 16384: 131 us, with ordinary
+// loads 135).
 #include "reduce_columns.h"
 
 #include "common.cuh"
