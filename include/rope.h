@@ -49,7 +49,8 @@ enum rope_scaling {
                                     turns over `length` positions rise from `low` to `high`          */
     ROPE_SCALING_RAMP_INDEX = 4  /* the same, k falling from 1 to 0 linearly in the pair's index, from
                                     the pair that turns `high` times over `length` positions (rounded
-                                    down) to the one that turns `low` times (rounded up)             */
+                                    down) to the one that turns `low` times (rounded up), whether
+                                    or not the head has these pairs                                  */
 };
 
 /* HOST function: the R/2 frequencies (radians a position) of a scaling, in fp64.

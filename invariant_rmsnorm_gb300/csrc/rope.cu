@@ -134,11 +134,12 @@ int rope_frequencies(int64_t R, double theta, int scaling, double factor, double
     auto index_of = [&](double turns) {
         return static_cast<double>(R) * std::log(length / (kTwoPi * turns)) / (2.0 * std::log(theta));
     };
-    const double last = static_cast<double>(n - 1);
+    // The ramp's ends, wherever they lie: a head that ends within the ramp, or
+    // begins there, has that part of it.
     double from = 0.0, to = 0.0;
     if (scaling == ROPE_SCALING_RAMP_INDEX) {
-        from = std::min(std::max(std::floor(index_of(high)), 0.0), last);
-        to = std::min(std::max(std::ceil(index_of(low)), 0.0), last);
+        from = std::floor(index_of(high));
+        to = std::ceil(index_of(low));
     }
     for (int64_t i = 0; i < n; ++i) {
         const double f = std::pow(theta, -2.0 * static_cast<double>(i) / static_cast<double>(R));

@@ -247,6 +247,25 @@ def test_frequencies(lib, R):
     assert len(i) == len(plain)
 
 
+@pytest.mark.parametrize("R,theta,length", [(64, 1e4, 65536.0), (64, 1e4, 4096.0), (128, 1e4, 131072.0), (128, 1e6, 32768.0),
+                                            (32, 500.0, 1e7), (64, 1e4, 100.0), (8, 1e4, 3.0), (2, 1e4, 4096.0)])
+@pytest.mark.parametrize("low,high", [(1.0, 32.0), (0.25, 4.0)])
+def test_ramp_by_index_has_the_slope_of_its_definition(lib, R, theta, length, low, high):
+    """From the pair that turns `high` times over `length` positions to the one that turns `low` times, whether or not
+    the head has these pairs."""
+    def index(turns):  # theta^(-2 i / R) length / 2 pi = turns
+        return R * (math.log(length) - math.log(2 * math.pi * turns)) / (2 * math.log(theta))
+
+    first, last = math.floor(index(high)), math.ceil(index(low))
+    want = []
+    for i in range(R // 2):
+        k = min(1.0, max(0.0, (last - i) / (last - first)))
+        want.append(math.exp(-math.log(theta) * 2 * i / R) * (k + (1 - k) / 16.0))
+    got = rn.rope_frequencies(R, theta, "ramp_index", factor=16.0, low=low, high=high, length=length)
+    # pow and exp(log) differ by a few of their arguments' roundings: |log f| 2^-53 and less
+    torch.testing.assert_close(got, torch.tensor(want, dtype=torch.float64), rtol=1e-13, atol=0)
+
+
 @pytest.mark.parametrize("kw", [dict(R=0), dict(R=3), dict(R=514), dict(theta=1.0), dict(theta=math.inf), dict(factor=0.5),
                                 dict(factor=math.nan), dict(R=2, scaling="base", factor=2.0),
                                 dict(scaling="ramp_turns", length=0.0), dict(scaling="ramp_turns", length=10.0, low=5.0, high=5.0),
