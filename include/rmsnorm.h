@@ -357,6 +357,8 @@ size_t rmsnorm_rope_bwd_workspace_bytes(int64_t T, int64_t Hq, int64_t Hk, int64
 /* Backward: the gradients gq, gk of q_out, k_out are turned back (by -a, same
  * scale), then go through rmsnorm_bwd's formula at q and k (the forward's
  * INPUTS: a forward in place has overwritten them) with the saved rstd.
+ * (The formula's r^3 is taken as r^2 and r apart, so heads of any size whose
+ * sum of squares fits fp32 keep their digits.)
  * dwq_j and dwk_j are summed over tokens and heads in fp32, with no atomics, in
  * an order that depends on T, Hq, Hk, D, R and the layout alone. dq, dk may be
  * gq, gk themselves (same strides). T == 0 sets dwq and dwk to zero. */

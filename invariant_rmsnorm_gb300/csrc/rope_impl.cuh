@@ -6,7 +6,7 @@
 //   turn:            (u c - v s, v c + u s), c = scale cos a, s = scale sin a
 //   norm + turn:     r = rsqrt(sum x^2 / D + eps), the turn of (x r) w
 //   its backward:    g' = turn of g by -a; gw = g' w;
-//                    dx = r gw - x (r^3 / D) sum(gw x);  dw = sum g' (x r)
+//                    dx = r gw - x r^2 (r sum(gw x) / D);  dw = sum g' (x r)
 // The kernels are bound by HBM: 4 D bytes a head forward, 6 D backward; the
 // angles (rope_math.cuh) are computed once a token by the warp that has it, a few
 // percent of its work.
@@ -625,7 +625,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
                 for (int i = 0; i < RB; ++i) {
                     const uint32_t p = at + i * spread * pitch;
                     if constexpr (BWD) {
-                        const float coef = -fmul(fmul(fmul(fmul(r[i], r[i]), r[i]), a.rcp_d), sum[i]);
+                        // r with the sum, r^2 apart: r^3 leaves fp32's range long before the result does.
+                        const float coef = -fmul(fmul(r[i], r[i]), fmul(fmul(sum[i], r[i]), a.rcp_d));
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             A[i].p[e] = fma2(A[i].p[e], both(r[i]), fmul2(xA[i].p[e], both(coef)));

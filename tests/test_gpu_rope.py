@@ -551,3 +551,29 @@ def test_infinity_beside_the_turned_part():
         rest = o.isfinite().all(2)
         rest[1, 0] = True
         assert bool(rest.all())
+
+
+@pytest.mark.parametrize("size,eps", [(5e17, EPS), (1e16, EPS), (1e14, EPS), (1e-14, 0.0), (1e-18, 0.0)])
+@pytest.mark.parametrize("T,Hq,Hk,D,R,inter", [(67, 4, 2, 128, 128, False), (67, 4, 2, 256, 64, True), (67, 3, 0, 96, 20, False),
+                                               (6001, 4, 1, 64, 64, False)])
+def test_norm_and_rope_at_any_magnitude(size, eps, T, Hq, Hk, D, R, inter):
+    """Heads whose squares still fit fp32: the inverse RMS to its third power would not."""
+    q, k = _heads(T, Hq, Hk, D, 141)
+    q, k = q * size, None if k is None else k * size
+    g, h = _heads(T, Hq, Hk, D, 142)
+    wq, wk = _weights(D, Hk, 143, False)
+    pos, f = _pos(T, 144), _freq(R)
+    rq, rk = torch.empty((T, Hq), device=DEV), torch.empty((T, Hk), device=DEV) if Hk else None
+    oq, ok = torch.empty_like(q), None if k is None else torch.empty_like(k)
+    rn.rmsnorm_rope_fwd(q, k, wq, wk, f, oq, ok, rq, rk, pos, SCALE, inter, eps)
+    (_, dq, dwq), (_, dk, dwk) = _norm_bwd(g, h, q, k, wq, wk, f, rq, rk, pos, inter)
+    eps32 = float(torch.tensor(eps, dtype=torch.float32))
+    for name, gg, x, w, o, r, d, dw in (("q", g, q, wq, oq, rq, dq, dwq), ("k", h, k, wk, ok, rk, dk, dwk)):
+        if x is None:
+            continue
+        (want, rstd), (e, er) = ref.norm_turn_fwd(x.double(), w.double(), eps32, pos, f, SCALE, inter)
+        ref.assert_within(f"rstd {name}", r, rstd, er)
+        ref.assert_within(name, o, want, e, BF16)
+        (want, rdw), (e, ew) = ref.norm_turn_bwd(gg.double(), x.double(), w.double(), r.double(), pos, f, SCALE, inter)
+        ref.assert_within(f"d{name}", d, want, e, BF16)
+        ref.assert_within(f"dw{name}", dw, rdw, ew)
