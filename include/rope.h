@@ -13,9 +13,10 @@
  *
  * Angles: inv_freq_i / 2 pi is taken in fp64 to a 64-bit fraction of a turn, and
  * pos * that fraction modulo one turn is an exact 64-bit integer product. The
- * angle's error is about |a| 2^-52, whatever the position: there is no table of
+ * angle's error is about |a| 2^-52 + |pos| 2^-62 rad from the frequency, whatever
+ * the position, and 2^-52 rad from the product's lowest bits: there is no table of
  * cosines and no longest context. Every 64-bit position is allowed, negative
- * ones too. cos and sin are fp32 (error about 2^-23).
+ * ones too. cos and sin are fp32, each right to about 2^-22 of itself beside that.
  *
  * q is [T][Hq][D] and k [T][Hk][D], 16-bit values given by two strides in
  * ELEMENTS, from token to token and from head to head (multiples of 8; an

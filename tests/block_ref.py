@@ -98,7 +98,7 @@ def turned(x, pos, inv_freq, scale, interleaved, back=False):
 
 
 # A turned value's error over scale * (|u| + |v|), in u: the angle, 1.6 (below a
-# quarter turn it is rounded twice as fp32; the phase's 2^-33 turns and the
+# quarter turn it is rounded twice as fp32; the phase's 2^-55 turns and the
 # frequency's |a| 2^-51 are far less here); the series of sine and cosine, 1.5; the
 # scale, 1; a product and a fused sum, 2. Together under 8.
 TURN = 8 * U

@@ -577,3 +577,26 @@ def test_norm_and_rope_at_any_magnitude(size, eps, T, Hq, Hk, D, R, inter):
         (want, rdw), (e, ew) = ref.norm_turn_bwd(gg.double(), x.double(), w.double(), r.double(), pos, f, SCALE, inter)
         ref.assert_within(f"d{name}", d, want, e, BF16)
         ref.assert_within(f"dw{name}", dw, rdw, ew)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T", [16, 6001])
+@pytest.mark.parametrize("dtype,scale", [(BF16, 1.0), (F16, 2.0 ** 14)])
+def test_small_angles_keep_their_digits(T, interleaved, dtype, scale):
+    """Pairs (1, 0) at slow frequencies: the sine is right relative to itself, not to the pair. TURN bounds the
+    arithmetic; the frequency's rounding is |a| 2^-51 and |p| 2^-62 of an angle, and 2^-55 turns of the phase are kept."""
+    turn = 6.283185307179586476925
+    n = 37
+    f = turn * 1.37 * 2.0 ** -torch.arange(4, 4 + n, device=DEV, dtype=torch.float64)
+    pos = torch.tensor([1, -1, 2, 3, -3, 7, 100, -1000, 4095, 0, 65537, 1 << 20, -(1 << 20) - 1, 5, 6, 12345],
+                       device=DEV).repeat(T // 16 + 1)[:T]
+    x = torch.zeros((T, 1, 80), dtype=dtype, device=DEV)
+    first, second = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved else (slice(0, n), slice(n, 2 * n))
+    x[..., first] = 1.0
+    a = pos.double()[:, None] * f
+    err = a.abs() * 2.0 ** -51 + pos.double().abs()[:, None] * 2.0 ** -62 + turn * 2.0 ** -55
+    for back in (False, True):
+        o = torch.empty_like(x)
+        (rn.rope_bwd if back else rn.rope_fwd)(x, None, f, o, None, pos, scale, interleaved)
+        for name, got, want in (("cos", o[:, 0, first], a.cos()), ("sin", o[:, 0, second], -a.sin() if back else a.sin())):
+            ref.assert_within(name, got, scale * want, scale * (ref.TURN * want.abs() + err), dtype)
