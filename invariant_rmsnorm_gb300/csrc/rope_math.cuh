@@ -12,9 +12,12 @@
 
 namespace rmsn {
 
+// A negative frequency is the complement of its size's fraction: the fraction of
+// the frequency itself, 1 less a small number, would be rounded at 2^-54 turns.
 __device__ __forceinline__ unsigned long long rope_turns(double inv_freq) {
-    const double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-    return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+    const double t = fabs(inv_freq) * 0.15915494309189533577;  // 1 / (2 pi)
+    const unsigned long long F = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+    return inv_freq < 0.0 ? 0ull - F : F;
 }
 
 // scale (cos, sin) of position p at the frequency F. Of the phase (64 bits of a

@@ -600,3 +600,18 @@ def test_small_angles_keep_their_digits(T, interleaved, dtype, scale):
         (rn.rope_bwd if back else rn.rope_fwd)(x, None, f, o, None, pos, scale, interleaved)
         for name, got, want in (("cos", o[:, 0, first], a.cos()), ("sin", o[:, 0, second], -a.sin() if back else a.sin())):
             ref.assert_within(name, got, scale * want, scale * (ref.TURN * want.abs() + err), dtype)
+
+
+def test_negative_frequencies_at_far_positions():
+    """They keep as many digits as positive ones: the angle's error is |a| 2^-51 and |p| 2^-62."""
+    turn = 6.283185307179586476925
+    f = -turn * torch.tensor([1.1, 1.3, 1.5, 1.7], dtype=torch.float64, device=DEV) * 2.0 ** -30
+    pos = torch.tensor([1 << 44, (1 << 44) + 12345, -(1 << 43) - 1, 1 << 40, 10 ** 12 + 7, 1 << 31], device=DEV)
+    x = torch.zeros((6, 1, 8), dtype=F16, device=DEV)
+    x[..., 0:4] = 1.0
+    o = torch.empty_like(x)
+    rn.rope_fwd(x, None, f, o, None, pos)
+    a = pos.double()[:, None] * f
+    err = ref.TURN + a.abs() * 2.0 ** -51 + pos.double().abs()[:, None] * 2.0 ** -62
+    ref.assert_within("cos", o[:, 0, 0:4], a.cos(), err, F16)
+    ref.assert_within("sin", o[:, 0, 4:8], a.sin(), err, F16)
