@@ -647,6 +647,8 @@ def layernorm_fwd(x, w, b, y, mean, rstd, eps: float = 1e-5, zero_centered_gamma
     The activation format (bf16 or fp16) is ``x``'s."""
     i, code = _index_and_code(x, "x")
     dt, shape = x.dtype, x.shape
+    if len(shape) != 2:
+        raise TypeError(f"x: expected a 2-D tensor [T, D], got {tuple(shape)}")
     T, D = shape
     xp, ldx = _rows(x, "x", shape, dt, i)
     yp, ldy = _rows(y, "y", shape, dt, i)
@@ -668,6 +670,8 @@ def layernorm_bwd(g, x, w, mean, rstd, dx, dw, db, ws, zero_centered_gamma: bool
     ``layernorm_bwd_workspace_bytes(T, D)`` bytes."""
     i, code = _index_and_code(x, "x")
     dt, shape = x.dtype, x.shape
+    if len(shape) != 2:
+        raise TypeError(f"x: expected a 2-D tensor [T, D], got {tuple(shape)}")
     T, D = shape
     gp, ldg = _rows(g, "g", shape, dt, i)
     xp, ldx = _rows(x, "x", shape, dt, i)

@@ -294,3 +294,15 @@ def test_on_a_stream_of_its_own():
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(y0.view(torch.int16), y1.view(torch.int16))
     assert rn.rmsnorm_device_error() == 0
+
+
+def test_shapes_are_named_in_refusals():
+    x, g, w, b = _inputs(8, 128, 71)
+    m, r, dw = torch.empty(8, device=DEV), torch.empty(8, device=DEV), torch.empty(128, device=DEV)
+    for t in (x.view(2, 4, 128), x[0]):
+        with pytest.raises(TypeError, match="x: expected a 2-D"):
+            rn.layernorm_fwd(t, w, b, torch.empty_like(t), m, r)
+        with pytest.raises(TypeError, match="x: expected a 2-D"):
+            rn.layernorm_bwd(t, t, w, m, r, torch.empty_like(t), dw, None, torch.empty(8192, dtype=torch.uint8, device=DEV))
+    with pytest.raises(TypeError, match="y: expected a 2-D"):
+        rn.layernorm_fwd(x, w, b, x.view(2, 4, 128), m, r)
