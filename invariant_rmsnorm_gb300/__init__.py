@@ -567,7 +567,7 @@ def _rows(t, name: str, shape, dtype, index: int):
     if t.dtype is dtype and t.get_device() == index and t.shape == shape:
         ld, one = t.stride()
         if one == 1 or shape[1] <= 1:
-            return t.data_ptr(), ld if shape[0] > 1 else max(ld, shape[1])
+            return t.data_ptr(), ld if shape[0] > 1 else shape[1]  # a stride that is never taken may be anything
         raise ValueError(f"{name}: columns must be contiguous")
     if t.dtype is not dtype or t.get_device() != index or t.dim() != 2:
         raise TypeError(f"{name}: expected a 2-D {dtype} tensor on cuda:{index}, got {t.dtype} {t.device} {tuple(t.shape)}")

@@ -306,3 +306,22 @@ def test_shapes_are_named_in_refusals():
             rn.layernorm_bwd(t, t, w, m, r, torch.empty_like(t), dw, None, torch.empty(8192, dtype=torch.uint8, device=DEV))
     with pytest.raises(TypeError, match="y: expected a 2-D"):
         rn.layernorm_fwd(x, w, b, x.view(2, 4, 128), m, r)
+
+
+def test_the_stride_of_a_single_row_is_never_taken():
+    _, _, w, b = _inputs(8, 128, 71)
+    m, r, dw = torch.empty(8, device=DEV), torch.empty(8, device=DEV), torch.empty(128, device=DEV)
+    wide = synth.normal16((1, 132), 5, DEV)  # rows 132 apart: of one row, a stride that is never taken
+    x1, y0, y1 = wide[:, :128], torch.empty((1, 128), dtype=BF16, device=DEV), torch.empty_like(wide)[:, :128]
+    rn.layernorm_fwd(x1.contiguous(), w, b, y0, m[:1], r[:1])
+    m1, r1 = torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+    rn.layernorm_fwd(x1, w, b, y1, m1, r1)
+    assert torch.equal(y0, y1) and torch.equal(m1, m[:1]) and torch.equal(r1, r[:1])
+    ws = torch.empty(rn.layernorm_bwd_workspace_bytes(1, 128), dtype=torch.uint8, device=DEV)
+    d0, d1 = torch.empty_like(y0), torch.empty_like(wide)[:, :128]
+    rn.layernorm_bwd(x1.contiguous(), x1.contiguous(), w, m1, r1, d0, dw, None, ws)
+    rn.layernorm_bwd(x1, x1, w, m1, r1, d1, dw, None, ws)
+    assert torch.equal(d0, d1)
+    with pytest.raises(rn.RmsNormError, match="EALIGN"):
+        two = synth.normal16((2, 132), 5, DEV)[:, :128]
+        rn.layernorm_fwd(two, w, b, torch.empty((2, 128), dtype=BF16, device=DEV), m[:2], r[:2])
