@@ -7,7 +7,8 @@
  *   n_tj  = (x_tj - mu_t) * r_t
  *   y_tj  = round( n_tj * w_eff_j + b_j )               w_eff = w, or (fp32) w + 1 (zero-centred gamma)
  * The variance is the second pass over the row's deviations from its mean, not
- * a difference of two sums, so a mean far from zero costs no digits.
+ * a difference of two sums, so a mean far from zero costs no digits. A row whose
+ * sum of squared deviations passes fp32's range (3.4e38) has rstd 0 and y = b.
  * Backward, per row (g = dL/dy, the saved mu and r):
  *   c1    = (sum_j g_j w_eff_j) / D,   c2 = (sum_j g_j w_eff_j n_j) / D
  *   dx_j  = round( r * (g_j w_eff_j - c1 - n_j * c2) )

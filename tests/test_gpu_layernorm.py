@@ -325,3 +325,69 @@ def test_the_stride_of_a_single_row_is_never_taken():
     with pytest.raises(rn.RmsNormError, match="EALIGN"):
         two = synth.normal16((2, 132), 5, DEV)[:, :128]
         rn.layernorm_fwd(two, w, b, torch.empty((2, 128), dtype=BF16, device=DEV), m[:2], r[:2])
+
+
+@pytest.mark.parametrize("T,D", [(20011, 1024), (9001, 1536), (20000, 2048), (6007, 3080), (30001, 520), (20000, 776),
+                                 (6001, 4104), (3001, 6152)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_rings_and_rows_go_round(T, D, dtype):
+    """More rows a team than its ring has stages, or than one trip of the forward's loop, and an uneven last chunk."""
+    _check(T, D, seed=T + D, dtype=dtype, zc=dtype == F16, bias=T % 2 == 1)
+
+
+@pytest.mark.parametrize("D", [24, 1000, 1016, 5000, 16376])
+@pytest.mark.parametrize("value", [2.0, -1.171875, 3.0078125, 1.3e30])
+def test_constant_rows_at_widths_that_are_no_power_of_two(D, value):
+    """The mean is the sum's correctly rounded quotient by D, where 1 / D is not exact: n = 0 and y = b."""
+    x = torch.full((5, D), value, dtype=BF16, device=DEV)
+    w, b = synth.gamma_f32(D, 1, DEV), synth.gamma_f32(D, 2, DEV, mean=0.0)
+    _, y, mean, rstd = _fwd(x, w, b)
+    assert bool((mean == x[:, 0].float()).all())
+    assert torch.equal(y, b.to(BF16).expand(5, D))
+
+
+@pytest.mark.parametrize("size,eps", [(1e17, 1e-5), (1e14, 1e-5), (1e-14, 0.0), (1e-18, 0.0)])
+@pytest.mark.parametrize("T,D", [(67, 128), (67, 1000), (67, 2048), (67, 5000), (67, 16384)])
+def test_any_magnitude(size, eps, T, D):
+    """Rows whose sum of squares still fits fp32; one that does not (16384 values of 1.5e17: 3.7e38) has rstd 0."""
+    x, g, w, b = _inputs(T, D, 161)
+    x = x * size
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd, dw, db = (torch.empty(n, device=DEV) for n in (T, T, D, D))
+    ws = torch.empty(rn.layernorm_bwd_workspace_bytes(T, D), dtype=torch.uint8, device=DEV)
+    rn.layernorm_fwd(x, w, b, y, mean, rstd, eps)
+    if D * (1.5 * size) ** 2 > 3.5e38:
+        assert bool((rstd == 0).all()) and torch.equal(y, b.to(BF16).expand(T, D))
+        return
+    rn.layernorm_bwd(g, x, w, mean, rstd, dx, dw, db, ws)
+    (ry, rm, rr), (ey, em, er) = ref.ln_fwd(x.double(), w.double(), b.double(), float(torch.tensor(eps, dtype=torch.float32)))
+    ref.assert_within("mean", mean, rm, em)
+    ref.assert_within("rstd", rstd, rr, er)
+    ref.assert_within("y", y, ry, ey, BF16)
+    (rdx, rdw, rdb), (edx, edw, edb) = ref.ln_bwd(g.double(), x.double(), w.double(), mean.double(), rstd.double())
+    ref.assert_within("dx", dx, rdx, edx, BF16)
+    ref.assert_within("dw", dw, rdw, edw)
+    ref.assert_within("db", db, rdb, edb)
+
+
+def test_weight_gradients_of_one_sign_and_many_rows():
+    """Sums of terms of one sign along the longest chains that the chunks allow: 256 rows a lane, 256 groups of a CTA,
+    3 partial rows a range, 16 ranges and 8 parts."""
+    T, D = 304 * 256 * 256, 8
+    x = synth.normal16((T, D), 171, DEV)
+    g = synth.normal16((T, D), 172, DEV).abs_().add_(0.5)
+    w = torch.ones(D, device=DEV)
+    _, _, mean, rstd = _fwd(x, w, None)
+    # the sign of n = (x - mean) rstd on g: every product is positive
+    g = torch.where(x.float() < mean[:, None], -g, g)
+    _, _, dw, db = _bwd(g, x, w, mean, rstd)
+    want, size, sums = (torch.zeros(D, dtype=torch.float64, device=DEV) for _ in range(3))
+    for i in range(0, T, 1 << 18):
+        gg = g[i:i + (1 << 18)].double()
+        n = (x[i:i + (1 << 18)].double() - mean[i:i + (1 << 18), None].double()) * rstd[i:i + (1 << 18), None].double()
+        want += (gg * n).sum(0)
+        sums += gg.sum(0)
+        size += gg.abs().sum(0)
+    chain = 256 + 256 + 3 + 16 + 8
+    ref.assert_within("dw", dw, want, (chain + 4) * ref.U * want.abs())
+    ref.assert_within("db", db, sums, chain * ref.U * size)
