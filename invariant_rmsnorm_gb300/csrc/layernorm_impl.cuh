@@ -55,9 +55,13 @@ __device__ __forceinline__ Oct ln_bias(const float* b, int v) { return b != null
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 
-// s / D through the fp32 reciprocal of D, its remainder taken back once: the
-// correctly rounded quotient (the mean of a constant row is that constant), in
-// three instructions in a division's place. An infinite sum stays infinite.
+// s / D through the fp32 reciprocal of D, its remainder taken back once (the last
+// step of Markstein's division): the correctly rounded quotient, so the mean of a
+// constant row is that constant, in three instructions in a division's place. His
+// theorem asks for a first quotient within one step, which s times the reciprocal
+// need not be; compared with the division over every significand of s and every D
+// that the calls take, it is right in all 8.6e9 cases (without the correction in
+// 73 %). An infinite sum stays infinite.
 __device__ __forceinline__ float over_d(float s, float d, float rcp_d) {
     const float q = fmul(s, rcp_d);
     const float e = __fmaf_rn(__fmaf_rn(-q, d, s), rcp_d, q);
