@@ -615,3 +615,24 @@ def test_negative_frequencies_at_far_positions():
     err = ref.TURN + a.abs() * 2.0 ** -51 + pos.double().abs()[:, None] * 2.0 ** -62
     ref.assert_within("cos", o[:, 0, 0:4], a.cos(), err, F16)
     ref.assert_within("sin", o[:, 0, 4:8], a.sin(), err, F16)
+
+
+def test_weight_gradients_of_one_sign_and_many_rows():
+    """Sums of products of one sign, longer a lane than any other test's: 38 million rows of 8 values are
+    T H / (304 CTAs x 8 warps x 8 groups) = 2000 additions a lane, then 64 groups, 3 partial rows a range, 16 ranges
+    and 8 parts."""
+    T, H, D = 2432000, 16, 8
+    q = synth.normal16((T, H, D), 151, DEV).abs_().add_(0.5)
+    g = synth.normal16((T, H, D), 152, DEV).abs_().add_(0.5)
+    w = torch.ones(D, device=DEV)
+    pos, f = torch.zeros(T, dtype=torch.int64, device=DEV), _freq(2)
+    (_, _, r), _ = _norm_fwd(q, None, w, None, f, pos)
+    (_, _, dw), _ = _norm_bwd(g, None, q, None, w, None, f, r, None, pos)
+    want = torch.zeros(D, dtype=torch.float64, device=DEV)
+    for i in range(0, T, 76000):
+        n = g[i:i + 76000].double() * q[i:i + 76000].double() * r[i:i + 76000].double()[..., None]
+        n[..., :2] *= SCALE
+        want += n.sum((0, 1))
+    chain = -(-T * H // (304 * 8 * 8)) + 1 + 64 + 3 + 16 + 8
+    # of a term: the turn (by no angle, scaled), x r, and the fused product
+    ref.assert_within("dw", dw, want, (chain * ref.U + ref.TURN + 2 * ref.U) * want)
