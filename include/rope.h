@@ -22,9 +22,10 @@
  * ELEMENTS, from token to token and from head to head (multiples of 8; an
  * input's may be zero, outputs must not overlap themselves). D is a multiple of
  * 8 with 8 <= D <= 512. Hk == 0 (k and k_out NULL) turns q alone. q_out may be q
- * and k_out may be k, with the same strides: the call then works in place and
- * touches the rotated part alone. Any other overlap of outputs with inputs is
- * not allowed. inv_freq: fp64 [R/2], finite. positions: [T] of enum
+ * and k_out may be k, with the same strides: the call then works in place, and
+ * reads and writes the 16-byte vectors that hold the rotated part alone (up to 7
+ * values beyond R are written again with their own bits). Any other overlap of
+ * outputs with inputs is not allowed. inv_freq: fp64 [R/2], finite. positions: [T] of enum
  * rope_pos_dtype, or NULL for 0, 1, 2, ... Pointers are DEVICE pointers, 16-byte
  * aligned (positions: aligned to its type). scale is finite. T == 0 returns
  * RMSN_OK and launches nothing. Otherwise as rmsnorm.h.
