@@ -707,9 +707,9 @@ cudaError_t team_fwd(const LnFwdArgs& a, cudaStream_t st) {
 // lanes, vectors a lane, rows a turn, turns in flight, CTAs an SM
 // Shapes by width, each the fastest measured: as many vectors a lane as its
 // registers hold (fewer lanes a row: fewer shuffles, more loads in flight a lane),
-// in steps that leave few lanes idle. Of the rates at 256 MB a tensor: D = 128
-// 89 % of the copy rate (with 16 lanes of one vector 76 %), 2048 95 %, 4096 93 %,
-// 5000 93 %, 8192 91 %, 16384 91 %. Rows of 8 vectors a lane on one or two warps
+// in steps that leave few lanes idle. Of the copy rate at 256 MB a tensor: D = 128
+// 85 % (at 64 MB 90 %, with 16 lanes of one vector 76 %), 2048 95 %, 4096 93 %,
+// 5000 92 %, 8192 91 %, 16384 91 %. Rows of 8 vectors a lane on one or two warps
 // do without PRE (2048: 95 against 89 %): 16 warps of 4 KB are in flight as it is.
 template <bool F16>
 cudaError_t ln_fwd_dispatch(const LnFwdArgs& a, cudaStream_t st) {
@@ -780,7 +780,9 @@ cudaError_t wide_bwd(const LnBwdArgs& a, unsigned grid, cudaStream_t st) {
 
 // Shapes by width, each the fastest measured (ln_shape has their CTAs an SM). Of
 // the copy rate, both passes, 65536 to 8192 rows: D = 768 87 % (a CTA a row: 80),
-// 1024 91, 2048 97, 4096 97, 5000 91, 8192 96, 16384 92. D = 128: 82 % of 30 us.
+// 1024 91, 2048 97, 4096 97, 5000 91, 8192 96, 16384 92; 2^20 rows of 128 or 2^21
+// of 64 96, 262144 of them 82 and 71. (4104 to 5120 without a bias spill 8 bytes at
+// the 96 registers that two CTAs leave them.)
 // Up to 4096 several teams a CTA leave 152 partial rows: a CTA a row, as many warps
 // an SM and 304 to 1216 partial rows, 88, 92 and 96 %.
 template <bool F16, bool BIAS>

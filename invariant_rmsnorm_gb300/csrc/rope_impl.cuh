@@ -734,7 +734,7 @@ cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
         // heads, four for a turn, whose chain of waits counts most (32 + 8 heads of 64:
         // 76 % of the copy rate; by batches alone 64 %, by turns alone 73 %). MANY: two
         // a turn and two for the angles that each lane computes (4 + 1 heads of 128:
-        // 58 %; by four and four 57, 14 + 2 heads 81 and 80).
+        // 57 %; by four and four a point less, 14 + 2 heads 81 and 80).
         auto cost = [&](int64_t H) {
             constexpr int64_t batch = MANY ? RB : per * RB;
             return H / step * (NR / RB) + (H % step + batch - 1) / batch + (MANY ? 2 : 4) * ((H + step - 1) / step) + (MANY ? 2 : 0);
@@ -751,8 +751,8 @@ cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
 // One token a turn or one a group of lanes: the second where it leaves half the
 // turns or fewer at as many heads a group (the norm's kernels, with more to do a
 // turn: three quarters), and still kRopeManyFrom turns. 65536 x 4 + 1 x 128:
-// rotation 48 -> 79 % of the copy rate, norm and rotation 33 -> 68, its backward
-// 32 -> 58; 14 + 2 heads: 88 both ways, 55 -> 79, 46 -> 81. With as many turns
+// rotation 48 -> 79 % of the copy rate, norm and rotation 33 -> 67, its backward
+// 32 -> 57; 14 + 2 heads: 88 both ways, 55 -> 79, 46 -> 81. With as many turns
 // (32 + 8 heads of 128) its shorter copies cost: 83 -> 80, 76 -> 66, 75 -> 72,
 // measured in one kernel for both.
 template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
@@ -772,7 +772,11 @@ cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
 
 // Heads a group and turn, of them in registers at a time, stages, CTAs an SM: the
 // fastest measured of each kind. More heads a turn cost fewer turns' waits and
-// more shared memory, which has to leave room for two CTAs an SM.
+// more shared memory, which has to leave room for two CTAs an SM. Some kernels
+// spill: most backward ones of several tokens whose heads leave lanes idle or are
+// cut (4 to 56 bytes at 128 registers), two forward ones with the norm (4 bytes),
+// and of the rotation those of neighbours in fp16 and of several tokens (4 to 20
+// bytes at 80 registers, three CTAs an SM).
 template <int MODE, int KIND, bool F16, int LG, bool FULL>
 cudaError_t rope_shape_of(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     if constexpr (MODE == kTurn) {
