@@ -72,8 +72,10 @@ def ln_bwd(g, x, w, mean, rstd):
 
 
 def rows_chain(T):
-    """Additions on one path of a weight gradient's sum over T rows: at most a
-    chunk of 256 rows, 16 and 8 of the ranges' totals, the chunks of one range, slack."""
+    """Additions on one path of a weight gradient's sum over T rows, at the sizes that
+    are checked with it: a lane's rows and its CTA's groups (together at most 256
+    there), 16 and 8 of the ranges' totals, the chunks of one range, slack. The tests
+    of longer sums, of 256 rows and more a lane, count their chains themselves."""
     return min(T, 256) + 32 + T // 2048 + 8
 
 
