@@ -132,7 +132,7 @@ int rope_frequencies(int64_t R, double theta, int scaling, double factor, double
     const int64_t n = R / 2;
     // The (fractional) index of the pair that turns `turns` times over `length`.
     auto index_of = [&](double turns) {
-        return static_cast<double>(R) * std::log(length / (kTwoPi * turns)) / (2.0 * std::log(theta));
+        return static_cast<double>(R) * (std::log(length) - std::log(kTwoPi) - std::log(turns)) / (2.0 * std::log(theta));
     };
     // The ramp's ends, wherever they lie: a head that ends within the ramp, or
     // begins there, has that part of it.

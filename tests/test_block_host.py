@@ -248,8 +248,8 @@ def test_frequencies(lib, R):
 
 
 @pytest.mark.parametrize("R,theta,length", [(64, 1e4, 65536.0), (64, 1e4, 4096.0), (128, 1e4, 131072.0), (128, 1e6, 32768.0),
-                                            (32, 500.0, 1e7), (64, 1e4, 100.0), (8, 1e4, 3.0), (2, 1e4, 4096.0)])
-@pytest.mark.parametrize("low,high", [(1.0, 32.0), (0.25, 4.0)])
+                                            (32, 500.0, 1e7), (64, 1e4, 100.0), (8, 1e4, 3.0), (2, 1e4, 4096.0), (64, 1e4, 1e-30)])
+@pytest.mark.parametrize("low,high", [(1.0, 32.0), (0.25, 4.0), (1.0, 1e300)])
 def test_ramp_by_index_has_the_slope_of_its_definition(lib, R, theta, length, low, high):
     """From the pair that turns `high` times over `length` positions to the one that turns `low` times, whether or not
     the head has these pairs."""
