@@ -1,6 +1,6 @@
 /*
- * slots.h — LayerNorm, rotary positions and the head norm with their arguments
- * in an array, for callers whose foreign-function interface converts every
+ * slots.h — LayerNorm, rotary positions, the head norm and the projections with
+ * their arguments in an array, for callers whose foreign-function interface converts every
  * argument by itself (a call of 20 to 40 arguments through such an interface
  * costs more than the launch of its kernel).
  */
@@ -8,6 +8,7 @@
 #define SLOTS_GB300_H_
 
 #include "layernorm.h"
+#include "linear.h"
 #include "rmsnorm.h"
 #include "rope.h"
 
@@ -29,7 +30,11 @@ enum norm_entry {
     NORM_ROPE_FWD = 2,
     NORM_ROPE_BWD = 3,
     NORM_RMSNORM_ROPE_FWD = 4,
-    NORM_RMSNORM_ROPE_BWD = 5
+    NORM_RMSNORM_ROPE_BWD = 5,
+    NORM_LINEAR_FWD = 6,
+    NORM_LINEAR_BWD = 7,
+    NORM_LINEAR_GATED_FWD = 8,
+    NORM_LINEAR_GATED_BWD = 9
 };
 
 /* Calls the entry point with the n arguments args[0 .. n-1] in its prototype's

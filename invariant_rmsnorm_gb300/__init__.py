@@ -1,12 +1,12 @@
 """Python binding of the GB300 batch-invariant RMSNorm library (C ABI in
-``include/rmsnorm.h``, ``layernorm.h`` and ``rope.h``).
+``include/rmsnorm.h``, ``layernorm.h``, ``rope.h`` and ``linear.h``).
 
 Argument marshalling only: every function here takes torch tensors that the
 caller allocated on a CUDA device, checks dtypes/shapes/devices, and passes raw
 pointers, row strides and sizes to the ``extern "C"`` entry point of the same
-name in ``_build/librmsnorm_gb300.so`` (LayerNorm and the rotary calls: through
-``norm_call`` of ``include/slots.h``, one packed array in place of a conversion
-an argument). All arithmetic runs in the library's
+name in ``_build/librmsnorm_gb300.so`` (LayerNorm, the rotary calls and the
+projections: through ``norm_call`` of ``include/slots.h``, one packed array in
+place of a conversion an argument). All arithmetic runs in the library's
 sm_103a kernels. If the library has not been built, ``load()`` raises; there is
 no other implementation to fall back to.
 
@@ -43,6 +43,8 @@ __all__ = [
     "rmsnorm_rope_fwd", "rmsnorm_rope_bwd", "rmsnorm_rope_bwd_workspace_bytes",
     "layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_bytes", "layernorm_bwd_workspace_bytes_max",
     "rope_fwd", "rope_bwd", "rope_frequencies", "LAYERNORM_SYMBOLS", "ROPE_SYMBOLS", "SLOTS_SYMBOLS", "ROPE_SCALINGS",
+    "linear_fwd", "linear_bwd", "linear_bwd_workspace_bytes", "linear_gated_fwd", "linear_gated_bwd",
+    "linear_gated_bwd_workspace_bytes", "LINEAR_SYMBOLS", "LINEAR_ACTS",
 ]
 
 EXPORTED_SYMBOLS = (
@@ -63,6 +65,9 @@ EXPORTED_SYMBOLS = (
 LAYERNORM_SYMBOLS = ("layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_bytes",
                      "layernorm_bwd_workspace_bytes_max")
 ROPE_SYMBOLS = ("rope_frequencies", "rope_fwd", "rope_bwd")
+# of include/linear.h
+LINEAR_SYMBOLS = ("linear_fwd", "linear_bwd", "linear_bwd_workspace_bytes", "linear_gated_fwd", "linear_gated_bwd",
+                  "linear_gated_bwd_workspace_bytes")
 # of include/slots.h
 SLOTS_SYMBOLS = ("norm_call",)
 
@@ -75,6 +80,9 @@ GATE_CODES = {"silu": 0, "sigmoid": 1}
 
 # enum rope_scaling of include/rope.h
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp_turns": 3, "ramp_index": 4}
+
+# enum linear_act of include/linear.h
+LINEAR_ACTS = {"none": 0, "silu": 1, "sigmoid": 2, "gelu": 3, "gelu_tanh": 4, "relu": 5}
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -135,12 +143,22 @@ _SIGS["rmsnorm_rope_bwd_workspace_bytes"] = (_SZ, [_I64] * 4)
 _SIGS["rmsnorm_rope_bwd"] = (_INT, _HEADS * 4 + [_P, _P, _P, _P, _INT, _P, _P] + _HEADS * 2 + [_P, _P, _P, _SZ] +
                              [_I64] * 5 + [_F, _INT, _INT, _INT, _P])
 
+# A matrix is its pointer and row stride.
+_MAT = [_P, _I64]
+_SIGS["linear_fwd"] = (_INT, _MAT * 2 + [_P] + _MAT * 3 + [_I64] * 3 + [_INT, _INT, _P])
+_SIGS["linear_bwd_workspace_bytes"] = (_SZ, [_I64] * 3 + [_INT])
+_SIGS["linear_bwd"] = (_INT, _MAT * 6 + [_P, _P, _SZ] + [_I64] * 3 + [_INT, _INT, _P])
+_SIGS["linear_gated_fwd"] = (_INT, _MAT * 6 + [_I64] * 3 + [_INT, _INT, _P])
+_SIGS["linear_gated_bwd_workspace_bytes"] = (_SZ, [_I64] * 3)
+_SIGS["linear_gated_bwd"] = (_INT, _MAT * 9 + [_P, _SZ] + [_I64] * 3 + [_INT, _INT, _P])
+
 # The entry points that are called with their arguments in an array (include/slots.h):
 # enum norm_entry, the array's packing and its length.
 _SIGS["norm_call"] = (_INT, [_INT, ctypes.c_char_p, _I64])
 _SLOTS = {}
 for _entry, _name in enumerate(("layernorm_fwd", "layernorm_bwd", "rope_fwd", "rope_bwd", "rmsnorm_rope_fwd",
-                                "rmsnorm_rope_bwd")):
+                                "rmsnorm_rope_bwd", "linear_fwd", "linear_bwd", "linear_gated_fwd",
+                                "linear_gated_bwd")):
     _args = _SIGS[_name][1]
     _SLOTS[_name] = (_entry, struct.Struct("=" + "".join("d" if a is _F else "q" for a in _args)).pack, len(_args))
 del _entry, _name, _args
@@ -770,6 +788,103 @@ def rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, inv_freq, rstd_q, rstd_k, dq, dk, dwq
           *_heads(dq, "dq", sq, dt, i), *_heads(dk, "dk", sk, dt, i), _vec(dwq, "dwq", (D,), i),
           _vec(dwk, "dwk", (D,), i) if Hk else 0, wp, wb, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0,
           1 if zero_centered_gamma else 0, code)
+
+
+# --------------------------------------------------------------------------
+# projections
+# --------------------------------------------------------------------------
+def _linear_act(act: str) -> int:
+    code = LINEAR_ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {sorted(LINEAR_ACTS)}, got {act!r}")
+    return code
+
+
+def _x_w(x, w, xn: str = "x", wn: str = "w"):
+    """T, K and N of x [T, K] and w [N, K]."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise TypeError(f"{xn}, {wn}: expected 2-D tensors [T, K] and [N, K], got {tuple(x.shape)} and {tuple(w.shape)}")
+    return x.shape[0], x.shape[1], w.shape[0]
+
+
+def linear_fwd(x, w, b, res, y, z=None, act: str = "none", stream=None):
+    """``y = act(x @ w.T + b) + res`` of ``x`` [T, K] and ``w`` [N, K], one rounding. ``b`` (fp32 [N]) and ``res`` [T, N]
+    may be None; ``y`` may be ``res``. ``z`` [T, N], unless None, keeps the pre-activation for the backward."""
+    i, code = _index_and_code(x, "x")
+    dt = x.dtype
+    T, K, N = _x_w(x, w)
+    out = (T, N)
+    xp, ldx = _rows(x, "x", (T, K), dt, i)
+    wp, ldw = _rows(w, "w", (N, K), dt, i)
+    rp, ldr = (0, N) if res is None else _rows(res, "res", out, dt, i)
+    yp, ldy = _rows(y, "y", out, dt, i)
+    zp, ldz = (0, N) if z is None else _rows(z, "z", out, dt, i)
+    _call("linear_fwd", i, stream, xp, ldx, wp, ldw, 0 if b is None else _vec(b, "b", (N,), i), rp, ldr, yp, ldy, zp, ldz, T, N,
+          K, _linear_act(act), code)
+
+
+def linear_bwd_workspace_bytes(T: int, N: int, K: int, act: str = "none") -> int:
+    return int(load().linear_bwd_workspace_bytes(int(T), int(N), int(K), _linear_act(act)))
+
+
+def linear_bwd(g, x, w, z, dx, dw, db, ws, act: str = "none", stream=None):
+    """Gradients of linear_fwd from that of ``y``: ``dx`` [T, K], ``dw`` [N, K] and ``db`` (fp32 [N]), each of which may be
+    None. ``z`` is the forward's (None without an activation); the gradient of ``res`` is ``g``. ``ws`` is a workspace of
+    ``linear_bwd_workspace_bytes(T, N, K, act)`` bytes."""
+    i, code = _index_and_code(x, "x")
+    dt = x.dtype
+    T, K, N = _x_w(x, w)
+    a = _linear_act(act)
+    if a and z is None:
+        raise TypeError("z: expected the forward's pre-activation")
+    gp, ldg = _rows(g, "g", (T, N), dt, i)
+    xp, ldx = _rows(x, "x", (T, K), dt, i)
+    wp, ldw = _rows(w, "w", (N, K), dt, i)
+    zp, ldz = _rows(z, "z", (T, N), dt, i) if a else (0, N)
+    dxp, lddx = (0, K) if dx is None else _rows(dx, "dx", (T, K), dt, i)
+    dwp, lddw = (0, K) if dw is None else _rows(dw, "dw", (N, K), dt, i)
+    sp, sb = _bytes_of(ws, i)
+    _call("linear_bwd", i, stream, gp, ldg, xp, ldx, wp, ldw, zp, ldz, dxp, lddx, dwp, lddw,
+          0 if db is None else _vec(db, "db", (N,), i), sp, sb, T, N, K, a, code)
+
+
+def linear_gated_fwd(x, wg, wu, h, gate=None, up=None, act: str = "silu", stream=None):
+    """``h = act(x @ wg.T) * (x @ wu.T)`` [T, N] of ``x`` [T, K], ``wg`` and ``wu`` [N, K], one rounding. ``gate`` and
+    ``up`` [T, N], unless both are None, keep the two projections for the backward."""
+    i, code = _index_and_code(x, "x")
+    dt = x.dtype
+    T, K, N = _x_w(x, wg, wn="wg")
+    if (gate is None) != (up is None):
+        raise TypeError("gate, up: expected both or neither")
+    xp, ldx = _rows(x, "x", (T, K), dt, i)
+    gp, ldwg = _rows(wg, "wg", (N, K), dt, i)
+    up_, ldwu = _rows(wu, "wu", (N, K), dt, i)
+    hp, ldh = _rows(h, "h", (T, N), dt, i)
+    ap, lda = (0, N) if gate is None else _rows(gate, "gate", (T, N), dt, i)
+    bp, ldb = (0, N) if up is None else _rows(up, "up", (T, N), dt, i)
+    _call("linear_gated_fwd", i, stream, xp, ldx, gp, ldwg, up_, ldwu, hp, ldh, ap, lda, bp, ldb, T, N, K, _linear_act(act), code)
+
+
+def linear_gated_bwd_workspace_bytes(T: int, N: int, K: int) -> int:
+    return int(load().linear_gated_bwd_workspace_bytes(int(T), int(N), int(K)))
+
+
+def linear_gated_bwd(g, x, wg, wu, gate, up, dx, dwg, dwu, ws, act: str = "silu", stream=None):
+    """Gradients of linear_gated_fwd from that of ``h``: ``dx`` [T, K] (or None), ``dwg`` and ``dwu`` [N, K] (or both None).
+    ``gate`` and ``up`` are the forward's. ``ws`` is a workspace of ``linear_gated_bwd_workspace_bytes(T, N, K)`` bytes."""
+    i, code = _index_and_code(x, "x")
+    dt = x.dtype
+    T, K, N = _x_w(x, wg, wn="wg")
+    if (dwg is None) != (dwu is None):
+        raise TypeError("dwg, dwu: expected both or neither")
+    tn, nk = (T, N), (N, K)
+    dxp, lddx = (0, K) if dx is None else _rows(dx, "dx", (T, K), dt, i)
+    dgp, lddg = (0, K) if dwg is None else _rows(dwg, "dwg", nk, dt, i)
+    dup, lddu = (0, K) if dwu is None else _rows(dwu, "dwu", nk, dt, i)
+    sp, sb = _bytes_of(ws, i)
+    _call("linear_gated_bwd", i, stream, *_rows(g, "g", tn, dt, i), *_rows(x, "x", (T, K), dt, i), *_rows(wg, "wg", nk, dt, i),
+          *_rows(wu, "wu", nk, dt, i), *_rows(gate, "gate", tn, dt, i), *_rows(up, "up", tn, dt, i), dxp, lddx, dgp, lddg, dup,
+          lddu, sp, sb, T, N, K, _linear_act(act), code)
 
 
 def rmsnorm_dgamma_reduce(ws, T: int, D: int, dgamma, stream=None):

@@ -149,5 +149,11 @@ cudaError_t narrow_f16_read_error(unsigned* flags, bool clear);
 cudaError_t encode_rows_2d(CUtensorMap* map, const void* base, int64_t T, int D, int64_t ld_elems,
                            int box_rows, bool f16);
 cudaError_t encode_vec_1d(CUtensorMap* map, const float* base, int64_t T, int box);
+// A 16-bit matrix [rows][cols] in boxes of [box_rows][64], whose rows of 128 bytes are swizzled in shared memory;
+// what lies beyond the matrix is filled with zeros.
+cudaError_t encode_blocks_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld_elems, int box_rows);
+// The same with a third dimension: blocks of 64 columns (cols a multiple of 64), `deep` of them a box; or, if `deep`
+// is 0, a single one of all columns.
+cudaError_t encode_blocks_3d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld_elems, int box_rows, int deep);
 
 }  // namespace rmsn

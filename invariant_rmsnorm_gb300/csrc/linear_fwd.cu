@@ -1,0 +1,11 @@
+// Projections and gated blocks forward, bf16 values: the instantiations of linear_impl.cuh.
+#include "linear_impl.cuh"
+
+namespace rmsn {
+
+cudaError_t linear_fwd_read_error(unsigned* flags, bool clear) { return read_linear_error_word(flags, clear); }
+cudaError_t launch_linear_fwd(ProductKind kind, const Product& p, cudaStream_t s) {
+    return kind == kGatedFwd ? product_shape<kGatedFwd, false>(p, s) : product_shape<kForward, false>(p, s);
+}
+
+}  // namespace rmsn

@@ -1,0 +1,594 @@
+// Matrix products of the projections on the fifth-generation tensor cores: kernel
+// and launcher, included by the translation units that instantiate them (linear_fwd,
+// linear_grad: bf16; with _f16: fp16).
+//
+// Mathematics: C = A B^T, its epilogue by kind (linear_launch.h). Every value of C is
+// one chain of tensor-core sums over the reduced axis in ascending order, 16 at a
+// time, whatever the tile's size, so a row's bits do not depend on M.
+//
+// A tile of C belongs to a CTA (CTAS = 1: 128 rows, `bn` columns) or to a pair of CTAs
+// (CTAS = 2: 256 x 256; each CTA holds 128 rows of A and half of the columns of B,
+// and one instruction multiplies both halves). A warp copies blocks of 64
+// reduced values of A and B by tensor copies into a ring of stages in shared memory, a
+// thread issues their products, which accumulate in tensor memory, and eight warps
+// take finished accumulators through the epilogue while the next tile's products run into
+// the other half of tensor memory. CTAs are persistent and walk the tiles.
+//
+// Operands whose rows run along the reduced axis (A, B of the forward, A of kGradX) are
+// stages of rows of 128 bytes, the others (B of kGradX, A and B of kGradW) of blocks of 64
+// columns: [64 reduced values][128 bytes]. Both are 128-byte swizzled, and zeros are
+// filled in beyond the matrix, in both operands alike.
+//
+// Bounded by the tensor cores where M is large, by the reads of B where it is small.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "activation.cuh"
+#include "kernels.h"
+#include "linear_launch.h"
+
+namespace rmsn {
+namespace {
+
+constexpr int kBlockK = 64;            // reduced values a block: one swizzled row of 128 bytes
+constexpr int kMostDeep = 4;           // blocks a stage
+constexpr int kProductThreads = 384;   // warp 0 copies, 1 multiplies, 2 holds tensor memory, 4 .. 11 epilogue
+constexpr int kEpilogueWarps = 8;
+constexpr int kMaxStages = 32;
+constexpr uint32_t kStageBytes = 227 * 1024 - 2048;  // of shared memory for the stages
+
+struct ProductArgs {
+    CUtensorMap a[2], b[2];
+    MatOut out[2], z[2];
+    MatIn res;
+    const float* bias;
+    float* partials;
+    int64_t M;
+    int N;
+    int act;
+    int tiles_m, tiles_n;     // of one output
+    int tiles;                // with the outputs and splits
+    int blocks;               // blocks of the reduced axis
+    int segments;             // products that are added (kGradX: 1 or 2)
+    int splits;
+    int bn;                   // columns of the accumulators of a tile
+    int a_rows;               // rows of A in a stage
+    int m;                    // rows of the products: 64 or 128 a CTA
+    int stages;
+    int deep;                 // blocks of 64 reduced values a stage
+    int copy_deep;            // blocks a copy (of one matrix): all of a stage's, or one
+    bool whole;               // no block is cut short
+    uint32_t a_block, b_block, a_bytes, stage_bytes;
+    uint32_t idesc;
+    int tmem_cols;
+};
+
+// Device error word of the including translation unit.
+__device__ unsigned int g_linear_error;
+
+cudaError_t read_linear_error_word(unsigned* flags, bool clear) {
+    unsigned v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_linear_error, sizeof(v));
+    if (e != cudaSuccess) return e;
+    *flags |= v;
+    if (clear && v) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(g_linear_error, &zero, sizeof(zero));
+    }
+    return e;
+}
+
+// ---------------------------------------------------------------------------
+// Tensor memory and tensor cores
+// ---------------------------------------------------------------------------
+template <int CTAS>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+    if constexpr (CTAS == 2) asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    else asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void tmem_relinquish() {
+    if constexpr (CTAS == 2) asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    else asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
+    if constexpr (CTAS == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+}
+
+// D += A B^T over 16 reduced values (D = A B^T if !add), issued by one thread.
+template <int CTAS>
+__device__ __forceinline__ void mma16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    if constexpr (CTAS == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1 : 0) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1 : 0) : "memory");
+}
+
+// Arrive on `bar` (in both CTAs of a pair) once the thread's earlier products are done.
+template <int CTAS>
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    if constexpr (CTAS == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// 16 adjacent columns of this lane's row of the accumulators.
+__device__ __forceinline__ void tmem_ld16(uint32_t tmem, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(tmem));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory descriptor: 128-byte swizzle, groups of 8 rows 1024 bytes apart,
+// blocks of 64 columns (operands along their columns) `block` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t at, uint32_t block) {
+    return static_cast<uint64_t>((at >> 4) & 0x3fffu) | static_cast<uint64_t>(block >> 4) << 16 |
+           static_cast<uint64_t>(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+// A tensor copy into this CTA; a pair's copies count on the first CTA's barrier (`bar`: its
+// shared::cluster address).
+template <int CTAS>
+__device__ __forceinline__ void tile_g2s(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    if constexpr (CTAS == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+
+// The same of several blocks of 64 columns at once: [blocks][rows][64], for single CTAs.
+__device__ __forceinline__ void tile3_g2s(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// True in one lane of a converged warp. (The loops around tensor instructions are
+// run by the whole warp, so that their operands stay in uniform registers.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+template <int CTAS>
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
+    return mbar_wait_scoped<CTAS == 2>(bar, parity, kWaitTimeoutNs);
+}
+
+// ---------------------------------------------------------------------------
+// Tiles
+// ---------------------------------------------------------------------------
+struct Tile { int m, n, which, split; };
+
+// Output and split outermost; then bands of 8 rows of tiles, whose operands stay in
+// L2 while the band's columns are walked.
+__device__ __forceinline__ Tile tile_of(const ProductArgs& g, int t) {
+    Tile o;
+    const int each = g.tiles_m * g.tiles_n, s = t / each;
+    t -= s * each;
+    o.which = s / g.splits;
+    o.split = s - o.which * g.splits;
+    const int band = 8 * g.tiles_n, first = t / band * 8, rows = min(8, g.tiles_m - first);
+    t -= first / 8 * band;
+    o.n = t / rows;
+    o.m = first + t - o.n * rows;
+    return o;
+}
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+template <int KIND, int CTAS, bool F16>
+__global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ ProductArgs g) {
+    constexpr bool A_COLS = KIND == kGradW, B_COLS = KIND == kGradX || KIND == kGradW;  // rows across the reduced axis
+    constexpr int ROWS = 128 * CTAS;  // of a tile
+    constexpr bool DEEP = CTAS == 1 && !B_COLS;  // several blocks a stage
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t tmem_slot;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = CTAS == 2 ? cluster_ctarank() : 0u;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int first_tile = CTAS == 2 ? cluster_id_x() : blockIdx.x, tile_step = CTAS == 2 ? cluster_count_x() : gridDim.x;
+
+    if (warp == 2) {
+        tmem_alloc<CTAS>(smem_u32(&tmem_slot), g.tmem_cols);
+        tmem_relinquish<CTAS>();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < g.stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], kEpilogueWarps * CTAS);
+        }
+        mbar_init(&drained, 1);
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane < 4) prefetch_tensormap(lane < 2 ? &g.a[lane] : &g.b[lane - 2]);
+    tmem_fence_before();
+    __syncthreads();
+    if constexpr (CTAS == 2) cluster_sync_all();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait();
+
+    if (warp == 0) {
+        {
+            int s = 0;
+            uint32_t phase = 0;
+            int64_t sent = 0;
+            bool ok = true;
+            const uint32_t all_bytes = g.stage_bytes * CTAS;
+            const bool one = elect_one();
+            const int deep = DEEP ? g.deep : 1;
+            for (int t = first_tile; ok && t < g.tiles; t += tile_step) {
+                const Tile c = tile_of(g, t);
+                const int k0 = static_cast<int>(static_cast<int64_t>(g.blocks) * c.split / g.splits);
+                const int k1 = static_cast<int>(static_cast<int64_t>(g.blocks) * (c.split + 1) / g.splits);
+                const int row = c.m * ROWS + rank * 128;
+                for (int seg = 0; ok && seg < g.segments; ++seg) {
+                    const CUtensorMap* ma = &g.a[KIND == kGradW ? c.which : seg];
+                    for (int k = k0; k < k1; k += deep) {
+                        if (!wait_on<CTAS>(&empty[s], phase ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        if (one) {
+                            if (rank == 0) mbar_arrive_expect_tx(&full[s], all_bytes);
+                            const uint32_t bar = CTAS == 2 ? cluster_map(&full[s], 0) : smem_u32(&full[s]);
+                            const uint32_t at = ring + s * g.stage_bytes, bt = at + g.a_bytes;
+                            const int kk = k * kBlockK;
+                            // Columns of the accumulators: kGatedFwd has half of them of gate, half of up.
+                            const int half = g.bn >> 1;
+                            if constexpr (A_COLS) {
+                                tile_g2s<CTAS>(at, ma, row, kk, bar);
+                                tile_g2s<CTAS>(at + 8192, ma, row + 64, kk, bar);
+                            } else if constexpr (CTAS == 2 || B_COLS) {
+                                tile_g2s<CTAS>(at, ma, kk, row, bar);
+                            }
+                            if constexpr (B_COLS) {
+                                const int mine = g.bn / CTAS, col = c.n * g.bn + rank * mine;
+                                for (int i = 0; i < mine; i += 64) tile_g2s<CTAS>(bt + i * 128, &g.b[seg], col + i, kk, bar);
+                            } else if constexpr (CTAS == 2) {
+                                if constexpr (KIND == kGatedFwd) tile_g2s<CTAS>(bt, &g.b[rank], kk, c.n * half, bar);
+                                else tile_g2s<CTAS>(bt, &g.b[0], kk, c.n * g.bn + rank * half, bar);
+                            } else {
+                                // Whole blocks lie along a third axis; if the last is cut short, columns are counted on.
+                                auto copy = [&](uint32_t to, const CUtensorMap* map, int r, int j) {
+                                    tile3_g2s(to, map, g.whole ? 0 : kk + j * kBlockK, r, g.whole ? k + j : 0, bar);
+                                };
+                                for (int j = 0; j < deep; j += g.copy_deep) copy(at + j * g.a_block, ma, row, j);
+                                if constexpr (KIND == kGatedFwd) {
+                                    for (int j = 0; j < deep; ++j) {
+                                        copy(bt + j * g.b_block, &g.b[0], c.n * half, j);
+                                        copy(bt + j * g.b_block + half * 128, &g.b[1], c.n * half, j);
+                                    }
+                                } else {
+                                    for (int j = 0; j < deep; j += g.copy_deep) copy(bt + j * g.b_block, &g.b[0], c.n * g.bn, j);
+                                }
+                            }
+                        }
+                        ++sent;
+                        if (++s == g.stages) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+            // Every stage is free again: no arrival on this CTA's barriers is left.
+            for (int i = 0; ok && i < g.stages; ++i) {
+                ok = wait_on<CTAS>(&empty[s], phase ^ 1u);
+                if (++s == g.stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) {
+                // Give up: wait (bounded) for the copies in flight. A pair's count on its first
+                // CTA, so the second waits a millisecond, a thousand times what a copy takes.
+                if (one) atomicOr(&g_linear_error, kErrWaitTimeout);
+                if (rank == 0) {
+                    for (int64_t i = sent > g.stages ? sent - g.stages : 0; i < sent; ++i)
+                        (void)wait_on<CTAS>(&full[i % g.stages], static_cast<uint32_t>(i / g.stages) & 1u);
+                }
+                const unsigned long long t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000000ull) {}
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const bool one = elect_one();
+            const int deep = DEEP ? g.deep : 1;
+            int s = 0, n = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = first_tile; ok && t < g.tiles; t += tile_step, ++n) {
+                const int split = t / (g.tiles_m * g.tiles_n) % g.splits;
+                const int k0 = static_cast<int>(static_cast<int64_t>(g.blocks) * split / g.splits);
+                const int k1 = static_cast<int>(static_cast<int64_t>(g.blocks) * (split + 1) / g.splits);
+                const int blocks = (k1 - k0) * g.segments, buf = n & 1;
+                if (!wait_on<CTAS>(&acc_empty[buf], ((n >> 1) & 1) ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                const uint32_t d = tmem + buf * g.bn;
+                for (int k = 0; k < blocks; k += deep) {
+                    if (!wait_on<CTAS>(&full[s], phase)) {
+                        ok = false;
+                        break;
+                    }
+                    tmem_fence_after();
+                    const uint32_t at = ring + s * g.stage_bytes, bt = at + g.a_bytes;
+                    const uint64_t da = smem_desc(at, A_COLS ? 8192u : 16u), db = smem_desc(bt, B_COLS ? 8192u : 16u);
+                    // 16 reduced values: 32 bytes of a row, or two groups of 8 rows.
+                    constexpr uint32_t step_a = (A_COLS ? 2048 : 32) >> 4, step_b = (B_COLS ? 2048 : 32) >> 4;
+                    if (one) {
+#pragma unroll
+                        for (int j = 0; j < (DEEP ? kMostDeep : 1); ++j) {
+                            if (DEEP && j >= min(deep, blocks - k)) break;
+#pragma unroll
+                            for (int i = 0; i < kBlockK / 16; ++i)
+                                mma16<CTAS>(d, da + j * (g.a_block >> 4) + i * step_a, db + j * (g.b_block >> 4) + i * step_b, g.idesc,
+                                            k > 0 || i > 0 || j > 0);
+                        }
+                        mma_commit<CTAS>(&empty[s]);
+                    }
+                    __syncwarp();
+                    if (++s == g.stages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok && one) mma_commit<CTAS>(&acc_full[buf]);
+                __syncwarp();
+            }
+            if (!ok) {  // wait (bounded) for the products in flight
+                if (one) {
+                    atomicOr(&g_linear_error, kErrWaitTimeout);
+                    mma_commit<CTAS>(&drained);
+                }
+                (void)wait_on<CTAS>(&drained, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int quad = warp & 3, part = (warp - 4) >> 2;  // a warp reads the lanes of its quarter
+        int n = 0;
+        for (int t = first_tile; t < g.tiles; t += tile_step, ++n) {
+            const Tile c = tile_of(g, t);
+            const int buf = n & 1;
+            if (!__all_sync(0xffffffffu, wait_on<CTAS>(&acc_full[buf], (n >> 1) & 1))) {
+                if (lane == 0) atomicOr(&g_linear_error, kErrWaitTimeout);
+                break;
+            }
+            tmem_fence_after();
+            // Products of 64 rows leave 16 of them in each quarter's first lanes.
+            const int lanes = CTAS == 1 && !A_COLS && g.m == 64 ? 16 : 32;
+            const int64_t row0 = static_cast<int64_t>(c.m) * ROWS + rank * 128 + quad * lanes, row = row0 + lane;
+            const bool there = lane < lanes && row < g.M;
+            const uint32_t acc = tmem + buf * g.bn + (static_cast<uint32_t>(quad * 32) << 16);
+            constexpr bool GATED = KIND == kGatedFwd;
+            const int width = GATED ? g.bn >> 1 : g.bn;
+            if (row0 < g.M) {
+                for (int j = part * 16; j < width; j += 32) {
+                    const int col = c.n * width + j;
+                    if (col >= g.N) break;
+                    float v[16], u[16];
+                    tmem_ld16(acc + j, v);
+                    if constexpr (GATED) tmem_ld16(acc + width + j, u);
+                    tmem_wait_ld();
+                    const int groups = min(2, (g.N - col) >> 3);
+                    if constexpr (KIND == kForward) {
+                        if (g.bias != nullptr) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (i < 2 * groups) {
+                                    const float4 b = __ldg(reinterpret_cast<const float4*>(g.bias + col) + i);
+                                    v[4 * i] = fadd(v[4 * i], b.x);
+                                    v[4 * i + 1] = fadd(v[4 * i + 1], b.y);
+                                    v[4 * i + 2] = fadd(v[4 * i + 2], b.z);
+                                    v[4 * i + 3] = fadd(v[4 * i + 3], b.w);
+                                }
+                            }
+                        }
+                    }
+                    auto put = [&](const MatOut& o, const float (&x)[16]) {
+                        uint4* p = reinterpret_cast<uint4*>(o.p + row * o.ld + col);
+                        if (there) {
+                            p[0] = pack_act<F16>(reinterpret_cast<const float(&)[8]>(x[0]));
+                            if (groups > 1) p[1] = pack_act<F16>(reinterpret_cast<const float(&)[8]>(x[8]));
+                        }
+                    };
+                    if constexpr (KIND == kForward || GATED) {
+                        if (g.z[0].p != nullptr) put(g.z[0], v);
+                        if (GATED && g.z[1].p != nullptr) put(g.z[1], u);
+                        with_act(g.act, [&](auto act) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = act_value<decltype(act)::value>(v[i]);
+                        });
+                        if constexpr (GATED) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = fmul(v[i], u[i]);
+                        }
+                        if constexpr (KIND == kForward) {
+                            if (g.res.p != nullptr && there) {
+                                const uint4* p = reinterpret_cast<const uint4*>(g.res.p + row * g.res.ld + col);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    if (h < groups) {
+                                        float r[8];
+                                        unpack_act<F16>(p[h], r);
+#pragma unroll
+                                        for (int i = 0; i < 8; ++i) v[8 * h + i] = fadd(v[8 * h + i], r[i]);
+                                    }
+                                }
+                            }
+                        }
+                        put(g.out[0], v);
+                    } else if (KIND == kGradW && g.splits > 1) {
+                        if (there) {
+                            float4* p = reinterpret_cast<float4*>(
+                                g.partials + ((static_cast<int64_t>(c.which) * g.splits + c.split) * g.M + row) * g.N + col);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (i < 2 * groups) p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        }
+                    } else {
+                        put(g.out[KIND == kGradW ? c.which : 0], v);
+                    }
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CTAS == 2) cluster_arrive(cluster_map(&acc_empty[buf], 0));
+                else mbar_arrive(&acc_empty[buf]);
+            }
+        }
+    }
+    pdl_release();
+    tmem_fence_before();
+    __syncthreads();
+    if constexpr (CTAS == 2) cluster_sync_all();
+    tmem_fence_after();
+    if (warp == 2) tmem_free<CTAS>(tmem, g.tmem_cols);
+}
+
+// ---------------------------------------------------------------------------
+// Launcher
+// ---------------------------------------------------------------------------
+template <int KIND, int CTAS, bool F16>
+cudaError_t product_run(const Product& p, int bn, cudaStream_t st) {
+    constexpr bool A_COLS = KIND == kGradW, B_COLS = KIND == kGradX || KIND == kGradW;
+    ProductArgs g{};
+    const int width = KIND == kGatedFwd ? bn / 2 : bn;  // columns of C a tile
+    const int64_t rows = 128 * CTAS, pairs = KIND == kGradW && p.a[1].p != nullptr ? 2 : 1;
+    g.M = p.M;
+    g.N = static_cast<int>(p.N);
+    g.act = p.act;
+    g.splits = p.splits;
+    g.segments = KIND == kGradX && p.a[1].p != nullptr ? 2 : 1;
+    const int64_t tiles_m = (p.M + rows - 1) / rows, tiles_n = (p.N + width - 1) / width;
+    const int64_t tiles = tiles_m * tiles_n * pairs * p.splits, blocks = (p.K + kBlockK - 1) / kBlockK;
+    if (tiles >= (int64_t(1) << 30)) return cudaErrorInvalidValue;
+    g.tiles_m = static_cast<int>(tiles_m);
+    g.tiles_n = static_cast<int>(tiles_n);
+    g.tiles = static_cast<int>(tiles);
+    g.blocks = static_cast<int>(blocks);
+    g.bn = bn;
+    // Few rows: only those are copied. The products read 64 or 128 rows from the block's start
+    // all the same, into what lies behind them in the ring; a row of C depends on its own
+    // row of A alone, and the others are not stored. (Products of 64 rows read half of that.)
+    const bool few = CTAS == 1 && !A_COLS;
+    g.m = few && p.M <= 64 ? 64 : 128;
+    g.a_rows = few && p.M <= 120 ? static_cast<int>((p.M + 7) / 8 * 8) : 128;
+    g.a_block = static_cast<uint32_t>(g.a_rows) * 128u;
+    g.b_block = static_cast<uint32_t>(B_COLS ? (bn / CTAS + 63) / 64 * 64 : bn / CTAS) * 128u;
+    // Blocks a stage: each stage costs the multiplying thread a wait, a fence and a commit, some
+    // 280 cycles beside 25 to 40 a product; four stages at least.
+    g.whole = p.K % kBlockK == 0;
+    g.deep = few && !B_COLS ? std::max(1, std::min<int>(kMostDeep, static_cast<int>(kStageBytes / 4 / (g.a_block + g.b_block)))) : 1;
+    g.copy_deep = g.whole ? g.deep : 1;
+    g.a_bytes = g.a_block * g.deep;
+    g.stage_bytes = (g.a_block + g.b_block) * g.deep;
+    // What the rows of the last stage's last block reach past the ring.
+    const uint32_t reach = (g.deep - 1) * g.a_block + static_cast<uint32_t>(g.m) * 128u;
+    const uint32_t behind = std::max(reach, g.stage_bytes) - g.stage_bytes;
+    g.stages = std::min<int>(kMaxStages, static_cast<int>((kStageBytes - behind) / g.stage_bytes));
+    const size_t smem = static_cast<size_t>(g.stages) * g.stage_bytes + behind + 1024;
+    g.tmem_cols = 32;
+    while (g.tmem_cols < 2 * bn) g.tmem_cols *= 2;
+    // fp32 sums; both operands' format; which of them lie along their columns; N / 8; M / 16.
+    g.idesc = 1u << 4 | (F16 ? 0u : 1u) << 7 | (F16 ? 0u : 1u) << 10 | (A_COLS ? 1u : 0u) << 15 | (B_COLS ? 1u : 0u) << 16 |
+              static_cast<uint32_t>(bn >> 3) << 17 | static_cast<uint32_t>(g.m * CTAS >> 4) << 24;
+    for (int i = 0; i < 2; ++i) {
+        g.out[i] = p.out[i];
+        g.z[i] = p.z[i];
+        const MatIn &a = p.a[i].p != nullptr ? p.a[i] : p.a[0], &b = p.b[i].p != nullptr ? p.b[i] : p.b[0];
+        // Operands along their columns, a pair's and those of kGradX: in two dimensions; the others in three.
+        auto rows_map = [&](CUtensorMap* map, const MatIn& o, int64_t n, int box, int deep) {
+            if (CTAS == 2 || B_COLS) return encode_blocks_2d(map, o.p, n, p.K, o.ld, box);
+            return encode_blocks_3d(map, o.p, n, p.K, o.ld, box, g.whole ? deep : 0);
+        };
+        cudaError_t e = cudaSuccess;
+        if (i == 1 && p.a[1].p == nullptr) g.a[1] = g.a[0];
+        else e = A_COLS ? encode_blocks_2d(&g.a[i], a.p, p.K, p.M, a.ld, kBlockK) : rows_map(&g.a[i], a, p.M, g.a_rows, g.deep);
+        if (e != cudaSuccess) return e;
+        if (i == 1 && p.b[1].p == nullptr) g.b[1] = g.b[0];
+        else if (B_COLS) e = encode_blocks_2d(&g.b[i], b.p, p.K, p.N, b.ld, kBlockK);
+        else if (KIND == kGatedFwd) e = rows_map(&g.b[i], b, p.N, bn / 2, 1);
+        else e = rows_map(&g.b[i], b, p.N, bn / CTAS, g.deep);
+        if (e != cudaSuccess) return e;
+    }
+    g.res = p.res;
+    g.bias = p.bias;
+    g.partials = p.partials;
+    const auto kern = product_kernel<KIND, CTAS, F16>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    int64_t grid;
+    if (CTAS == 2) {
+        const int64_t n = pair_clusters(reinterpret_cast<const void*>(kern), kProductThreads, static_cast<int>(smem));
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        grid = 2 * std::min(tiles, n);
+    } else {
+        grid = std::min<int64_t>(tiles, sm_count());
+    }
+    return launch_kernel_clustered(kern, static_cast<unsigned>(CTAS), static_cast<unsigned>(grid), kProductThreads, smem, st, g);
+}
+
+// The tile. Pairs of CTAs (256 x 256) where they have tiles enough for half the GPU;
+// else single ones, 128 rows by as many columns as give every SM about one
+// tile of the narrowest count (a multiple of 16, or of 64 where B lies along its columns).
+template <int KIND, bool F16>
+cudaError_t product_shape(const Product& p, cudaStream_t st) {
+    constexpr int64_t kSms = 152;
+    const int64_t cols = KIND == kGatedFwd ? 2 * p.N : p.N, outs = KIND == kGradW && p.a[1].p != nullptr ? 2 : 1;
+    const int64_t big = (p.M + 255) / 256 * ((cols + 255) / 256) * outs * p.splits;
+    if (big >= kSms / 4 && p.M > 128) return product_run<KIND, 2, F16>(p, 256, st);
+    constexpr int unit = KIND == kGradX || KIND == kGradW ? 64 : 32;
+    const int64_t rows = (p.M + 127) / 128 * outs * p.splits;
+    const int64_t per_row = std::max<int64_t>(1, kSms / rows);          // column tiles for one wave
+    int64_t bn = (cols + per_row - 1) / per_row;                        // one wave
+    for (int waves = 2; bn > 256; ++waves) bn = (cols + waves * per_row - 1) / (waves * per_row);
+    bn = std::min<int64_t>(256, (bn + unit - 1) / unit * unit);
+    return product_run<KIND, 1, F16>(p, static_cast<int>(bn), st);
+}
+
+}  // namespace
+}  // namespace rmsn

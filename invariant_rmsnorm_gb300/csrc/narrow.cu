@@ -1,8 +1,9 @@
 // Narrow-row kernels (D <= 256) with bf16 activations: the instantiations of
 // narrow_impl.cuh for every bf16 mode and their launch entry points, plus the
-// host-side tensor-map encoding shared with narrow_f16.cu.
+// host-side tensor-map encoding shared with the other kernels.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "narrow_impl.cuh"
@@ -43,6 +44,30 @@ cudaError_t encode_rows_2d(CUtensorMap* map, const void* base, int64_t T, int D,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+namespace {
+cudaError_t encode_blocks(CUtensorMap* map, const void* base, cuuint32_t rank, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                          const cuuint32_t (&box)[3]) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return cudaErrorNotSupported;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+}  // namespace
+
+cudaError_t encode_blocks_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld_elems, int box_rows) {
+    return encode_blocks(map, base, 2, {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), 1},
+                         {static_cast<cuuint64_t>(ld_elems) * 2u, 0}, {64u, static_cast<cuuint32_t>(box_rows), 1u});
+}
+
+cudaError_t encode_blocks_3d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld_elems, int box_rows, int deep) {
+    const cuuint64_t across = deep > 0 ? 64u : static_cast<cuuint64_t>(cols), blocks = deep > 0 ? static_cast<cuuint64_t>(cols / 64) : 1u;
+    return encode_blocks(map, base, 3, {across, static_cast<cuuint64_t>(rows), blocks}, {static_cast<cuuint64_t>(ld_elems) * 2u, 128u},
+                         {64u, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(std::max(deep, 1))});
 }
 
 cudaError_t encode_vec_1d(CUtensorMap* map, const float* base, int64_t T, int box) {
