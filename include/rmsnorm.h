@@ -375,6 +375,33 @@ int rmsnorm_rope_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head,
                      int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale, int layout,
                      int zero_centered_gamma, int dtype, rmsn_stream stream);
 
+/* The same with positions of several axes (rope.h: axis, axes, positions [axes][T] by two
+ * strides). The workspace is rmsnorm_rope_bwd's. */
+int rmsnorm_rope_axes_fwd(const rmsn_act16* q, int64_t q_token, int64_t q_head,
+                          const rmsn_act16* k, int64_t k_token, int64_t k_head,
+                          const float* wq, const float* wk,
+                          const double* inv_freq, const uint8_t* axis, int64_t axes,
+                          const void* positions, int64_t pos_axis, int64_t pos_token, int pos_dtype,
+                          rmsn_act16* q_out, int64_t qo_token, int64_t qo_head,
+                          rmsn_act16* k_out, int64_t ko_token, int64_t ko_head,
+                          float* rstd_q, float* rstd_k,
+                          int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale, int layout,
+                          float eps, int zero_centered_gamma, int dtype, rmsn_stream stream);
+
+int rmsnorm_rope_axes_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head,
+                          const rmsn_act16* gk, int64_t gk_token, int64_t gk_head,
+                          const rmsn_act16* q, int64_t q_token, int64_t q_head,
+                          const rmsn_act16* k, int64_t k_token, int64_t k_head,
+                          const float* wq, const float* wk,
+                          const double* inv_freq, const uint8_t* axis, int64_t axes,
+                          const void* positions, int64_t pos_axis, int64_t pos_token, int pos_dtype,
+                          const float* rstd_q, const float* rstd_k,
+                          rmsn_act16* dq, int64_t dq_token, int64_t dq_head,
+                          rmsn_act16* dk, int64_t dk_token, int64_t dk_head,
+                          float* dwq, float* dwk, void* ws, size_t ws_bytes,
+                          int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale, int layout,
+                          int zero_centered_gamma, int dtype, rmsn_stream stream);
+
 /* Weight-gradient pass 2 on its own: sums the per-chunk partials that a backward
  * call with a NULL dgamma/dw left in ws (same T, D and workspace), in the fixed
  * order, into dgamma [D]. ws must be unchanged since that call. */

@@ -78,6 +78,41 @@ int rope_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head,
              int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale, int layout,
              int dtype, rmsn_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Positions of several axes (time, height and width of a picture's or a video's
+ * tokens): pair i of token t is turned by the angle
+ *   a = pos[axis_i][t] * inv_freq_i
+ * and everything else is as above. axis: [R/2], the axis of every pair (one that
+ * is `axes` or more counts as the last). positions: [axes][T] of enum
+ * rope_pos_dtype by two strides in elements, from axis to axis and from token to token, each
+ * zero or more; not NULL. 1 <= axes <= 256. The gradients turn by -a.
+ * (The head norm fused with these, rmsnorm_rope_axes_fwd / _bwd, is in rmsnorm.h.)
+ * ------------------------------------------------------------------------ */
+
+/* HOST function: the axis of each of the sections' n = sum(sections) <= 256 pairs, sections[a] >= 1 of
+ * them of axis a: side by side, or (cycled) dealt in turn, pair i to axis i mod axes while that
+ * axis lacks some, the rest to axis 0. RMSN_EINVAL for anything else, and for sections that cannot be
+ * dealt so (an axis would need a pair beyond the last); nothing is written then. */
+int rope_axes_map(const int64_t* sections, int64_t axes, int cycled, uint8_t* axis);
+
+int rope_axes_fwd(const rmsn_act16* q, int64_t q_token, int64_t q_head,
+                  const rmsn_act16* k, int64_t k_token, int64_t k_head,
+                  const double* inv_freq, const uint8_t* axis, int64_t axes,
+                  const void* positions, int64_t pos_axis, int64_t pos_token, int pos_dtype,
+                  rmsn_act16* q_out, int64_t qo_token, int64_t qo_head,
+                  rmsn_act16* k_out, int64_t ko_token, int64_t ko_head,
+                  int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale, int layout,
+                  int dtype, rmsn_stream stream);
+
+int rope_axes_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head,
+                  const rmsn_act16* gk, int64_t gk_token, int64_t gk_head,
+                  const double* inv_freq, const uint8_t* axis, int64_t axes,
+                  const void* positions, int64_t pos_axis, int64_t pos_token, int pos_dtype,
+                  rmsn_act16* dq, int64_t dq_token, int64_t dq_head,
+                  rmsn_act16* dk, int64_t dk_token, int64_t dk_head,
+                  int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale, int layout,
+                  int dtype, rmsn_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,11 @@ enum norm_entry {
     NORM_LINEAR_FWD = 6,
     NORM_LINEAR_BWD = 7,
     NORM_LINEAR_GATED_FWD = 8,
-    NORM_LINEAR_GATED_BWD = 9
+    NORM_LINEAR_GATED_BWD = 9,
+    NORM_ROPE_AXES_FWD = 10,
+    NORM_ROPE_AXES_BWD = 11,
+    NORM_RMSNORM_ROPE_AXES_FWD = 12,
+    NORM_RMSNORM_ROPE_AXES_BWD = 13
 };
 
 /* Calls the entry point with the n arguments args[0 .. n-1] in its prototype's

@@ -45,6 +45,7 @@ __all__ = [
     "rope_fwd", "rope_bwd", "rope_frequencies", "LAYERNORM_SYMBOLS", "ROPE_SYMBOLS", "SLOTS_SYMBOLS", "ROPE_SCALINGS",
     "linear_fwd", "linear_bwd", "linear_bwd_workspace_bytes", "linear_gated_fwd", "linear_gated_bwd",
     "linear_gated_bwd_workspace_bytes", "LINEAR_SYMBOLS", "LINEAR_ACTS",
+    "rope_axes_map", "rope_axes_fwd", "rope_axes_bwd", "rmsnorm_rope_axes_fwd", "rmsnorm_rope_axes_bwd",
 ]
 
 EXPORTED_SYMBOLS = (
@@ -59,12 +60,13 @@ EXPORTED_SYMBOLS = (
     "rmsnorm_residual_step_host_work_bytes", "rmsnorm_residual_step_host", "rmsnorm_selftest_wait_timeout",
     "rmsnorm_bwd_workspace_bytes_max",
     "rmsnorm_rope_fwd", "rmsnorm_rope_bwd", "rmsnorm_rope_bwd_workspace_bytes",
+    "rmsnorm_rope_axes_fwd", "rmsnorm_rope_axes_bwd",
 )
 
 # the entry points of include/layernorm.h and include/rope.h
 LAYERNORM_SYMBOLS = ("layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_bytes",
                      "layernorm_bwd_workspace_bytes_max")
-ROPE_SYMBOLS = ("rope_frequencies", "rope_fwd", "rope_bwd")
+ROPE_SYMBOLS = ("rope_frequencies", "rope_fwd", "rope_bwd", "rope_axes_map", "rope_axes_fwd", "rope_axes_bwd")
 # of include/linear.h
 LINEAR_SYMBOLS = ("linear_fwd", "linear_bwd", "linear_bwd_workspace_bytes", "linear_gated_fwd", "linear_gated_bwd",
                   "linear_gated_bwd_workspace_bytes")
@@ -143,6 +145,15 @@ _SIGS["rmsnorm_rope_bwd_workspace_bytes"] = (_SZ, [_I64] * 4)
 _SIGS["rmsnorm_rope_bwd"] = (_INT, _HEADS * 4 + [_P, _P, _P, _P, _INT, _P, _P] + _HEADS * 2 + [_P, _P, _P, _SZ] +
                              [_I64] * 5 + [_F, _INT, _INT, _INT, _P])
 
+# Positions of several axes: the pairs' axes, their number, the positions with two strides and their type.
+_AXES = [_P, _I64, _P, _I64, _I64, _INT]
+_SIGS["rope_axes_map"] = (_INT, [_P, _I64, _INT, _P])
+_SIGS["rope_axes_fwd"] = _SIGS["rope_axes_bwd"] = (_INT, _HEADS * 2 + [_P] + _AXES + _HEADS * 2 + [_I64] * 5 + [_F, _INT, _INT, _P])
+_SIGS["rmsnorm_rope_axes_fwd"] = (_INT, _HEADS * 2 + [_P, _P, _P] + _AXES + _HEADS * 2 + [_P, _P] + [_I64] * 5 +
+                                  [_F, _INT, _F, _INT, _INT, _P])
+_SIGS["rmsnorm_rope_axes_bwd"] = (_INT, _HEADS * 4 + [_P, _P, _P] + _AXES + [_P, _P] + _HEADS * 2 + [_P, _P, _P, _SZ] +
+                                  [_I64] * 5 + [_F, _INT, _INT, _INT, _P])
+
 # A matrix is its pointer and row stride.
 _MAT = [_P, _I64]
 _SIGS["linear_fwd"] = (_INT, _MAT * 2 + [_P] + _MAT * 3 + [_I64] * 3 + [_INT, _INT, _P])
@@ -158,7 +169,8 @@ _SIGS["norm_call"] = (_INT, [_INT, ctypes.c_char_p, _I64])
 _SLOTS = {}
 for _entry, _name in enumerate(("layernorm_fwd", "layernorm_bwd", "rope_fwd", "rope_bwd", "rmsnorm_rope_fwd",
                                 "rmsnorm_rope_bwd", "linear_fwd", "linear_bwd", "linear_gated_fwd",
-                                "linear_gated_bwd")):
+                                "linear_gated_bwd", "rope_axes_fwd", "rope_axes_bwd", "rmsnorm_rope_axes_fwd",
+                                "rmsnorm_rope_axes_bwd")):
     _args = _SIGS[_name][1]
     _SLOTS[_name] = (_entry, struct.Struct("=" + "".join("d" if a is _F else "q" for a in _args)).pack, len(_args))
 del _entry, _name, _args
@@ -784,6 +796,92 @@ def rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, inv_freq, rstd_q, rstd_k, dq, dk, dwq
     _call("rmsnorm_rope_bwd", i, stream, *_heads(gq, "gq", sq, dt, i), *_heads(gk, "gk", sk, dt, i),
           *_heads(q, "q", sq, dt, i), *_heads(k, "k", sk, dt, i), _vec(wq, "wq", (D,), i),
           _vec(wk, "wk", (D,), i) if Hk else 0, _vec(inv_freq, "inv_freq", (n,), i, _F64), *_positions(positions, T, i),
+          _vec(rstd_q, "rstd_q", (T, Hq), i), _vec(rstd_k, "rstd_k", (T, Hk), i) if Hk else 0,
+          *_heads(dq, "dq", sq, dt, i), *_heads(dk, "dk", sk, dt, i), _vec(dwq, "dwq", (D,), i),
+          _vec(dwk, "dwk", (D,), i) if Hk else 0, wp, wb, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0,
+          1 if zero_centered_gamma else 0, code)
+
+
+# --------------------------------------------------------------------------
+# rotary positions of several axes
+# --------------------------------------------------------------------------
+def rope_axes_map(sections, cycled: bool = False) -> torch.Tensor:
+    """The axis of every pair as a uint8 CPU tensor: ``sections[a]`` pairs of axis a, side by side or (``cycled``) dealt
+    in turn, pair i to axis i mod axes while that axis lacks some, the rest to axis 0."""
+    s = torch.tensor([int(v) for v in sections], dtype=torch.int64)
+    out = torch.empty(max(int(s.clamp(0, 256).sum()), 0), dtype=torch.uint8)
+    _check("rope_axes_map", load().rope_axes_map(_ptr(s), s.numel(), 1 if cycled else 0, _ptr(out)))
+    return out
+
+
+def _axes(axis, positions, n: int, T: int, index: int):
+    """The arguments of positions [axes, T] (any strides) and of the pairs' axes [n]."""
+    ap = _vec(axis, "axis", (n,), index, torch.uint8)
+    if positions.dim() != 2 or positions.shape[1] != T:
+        raise ValueError(f"positions: expected shape (axes, {T}), got {tuple(positions.shape)}")
+    if positions.get_device() != index:
+        raise TypeError(f"positions: expected a tensor on cuda:{index}, got {positions.device}")
+    if positions.dtype is torch.int64:
+        code = 1
+    elif positions.dtype is torch.int32:
+        code = 0
+    else:
+        raise TypeError(f"positions: expected int32 or int64, got {positions.dtype}")
+    sa, st = positions.stride()
+    A = positions.shape[0]
+    # a stride that is never taken may be anything
+    return ap, A, positions.data_ptr(), sa if A > 1 else 0, st if T > 1 else 0, code
+
+
+def _rope_axes(name, q, k, inv_freq, axis, q_out, k_out, positions, scale, interleaved, stream):
+    i, code = _index_and_code(q, "q")
+    dt = q.dtype
+    sq, sk, n = _q_k(q, k, inv_freq)
+    T, Hq, D = sq
+    _call(name, i, stream, *_heads(q, "q", sq, dt, i), *_heads(k, "k", sk, dt, i), _vec(inv_freq, "inv_freq", (n,), i, _F64),
+          *_axes(axis, positions, n, T, i), *_heads(q_out, "q_out", sq, dt, i), *_heads(k_out, "k_out", sk, dt, i), T, Hq, sk[1],
+          D, 2 * n, scale, 1 if interleaved else 0, code)
+
+
+def rope_axes_fwd(q, k, inv_freq, axis, q_out, k_out, positions, scale: float = 1.0, interleaved: bool = False, stream=None):
+    """``rope_fwd`` with positions of several axes: pair i is turned by ``positions[axis[i], t] * inv_freq[i]``.
+    ``positions`` is an int32 or int64 tensor [axes, T] of any strides, ``axis`` a uint8 tensor of the pairs' axes (one that
+    ``positions`` does not have counts as its last)."""
+    _rope_axes("rope_axes_fwd", q, k, inv_freq, axis, q_out, k_out, positions, scale, interleaved, stream)
+
+
+def rope_axes_bwd(gq, gk, inv_freq, axis, dq, dk, positions, scale: float = 1.0, interleaved: bool = False, stream=None):
+    """Gradients of rope_axes_fwd's inputs from those of its outputs (``dq`` may be ``gq``, ``dk`` may be ``gk``)."""
+    _rope_axes("rope_axes_bwd", gq, gk, inv_freq, axis, dq, dk, positions, scale, interleaved, stream)
+
+
+def rmsnorm_rope_axes_fwd(q, k, wq, wk, inv_freq, axis, q_out, k_out, rstd_q, rstd_k, positions, scale: float = 1.0,
+                          interleaved: bool = False, eps: float = 1e-6, zero_centered_gamma: bool = False, stream=None):
+    """``rmsnorm_rope_fwd`` with positions of several axes (``rope_axes_fwd``)."""
+    i, code = _index_and_code(q, "q")
+    dt = q.dtype
+    sq, sk, n = _q_k(q, k, inv_freq)
+    T, Hq, D = sq
+    Hk = sk[1]
+    _call("rmsnorm_rope_axes_fwd", i, stream, *_heads(q, "q", sq, dt, i), *_heads(k, "k", sk, dt, i), _vec(wq, "wq", (D,), i),
+          _vec(wk, "wk", (D,), i) if Hk else 0, _vec(inv_freq, "inv_freq", (n,), i, _F64), *_axes(axis, positions, n, T, i),
+          *_heads(q_out, "q_out", sq, dt, i), *_heads(k_out, "k_out", sk, dt, i), _vec(rstd_q, "rstd_q", (T, Hq), i),
+          _vec(rstd_k, "rstd_k", (T, Hk), i) if Hk else 0, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0, eps,
+          1 if zero_centered_gamma else 0, code)
+
+
+def rmsnorm_rope_axes_bwd(gq, gk, q, k, wq, wk, inv_freq, axis, rstd_q, rstd_k, dq, dk, dwq, dwk, ws, positions,
+                          scale: float = 1.0, interleaved: bool = False, zero_centered_gamma: bool = False, stream=None):
+    """Gradients of rmsnorm_rope_axes_fwd, as ``rmsnorm_rope_bwd``'s, with its workspace."""
+    i, code = _index_and_code(q, "q")
+    dt = q.dtype
+    sq, sk, n = _q_k(q, k, inv_freq)
+    T, Hq, D = sq
+    Hk = sk[1]
+    wp, wb = _bytes_of(ws, i)
+    _call("rmsnorm_rope_axes_bwd", i, stream, *_heads(gq, "gq", sq, dt, i), *_heads(gk, "gk", sk, dt, i),
+          *_heads(q, "q", sq, dt, i), *_heads(k, "k", sk, dt, i), _vec(wq, "wq", (D,), i),
+          _vec(wk, "wk", (D,), i) if Hk else 0, _vec(inv_freq, "inv_freq", (n,), i, _F64), *_axes(axis, positions, n, T, i),
           _vec(rstd_q, "rstd_q", (T, Hq), i), _vec(rstd_k, "rstd_k", (T, Hk), i) if Hk else 0,
           *_heads(dq, "dq", sq, dt, i), *_heads(dk, "dk", sk, dt, i), _vec(dwq, "dwq", (D,), i),
           _vec(dwk, "dwk", (D,), i) if Hk else 0, wp, wb, T, Hq, Hk, D, 2 * n, scale, 1 if interleaved else 0,

@@ -1,0 +1,12 @@
+// Head norm and rotary positions of several axes, turns of several tokens, bf16 activations: the
+// instantiations of rope_impl.cuh.
+#include "rope_impl.cuh"
+
+namespace rmsn {
+
+cudaError_t rope_axes_norm_read_error(unsigned* flags, bool clear) { return read_rope_error_word(flags, clear); }
+cudaError_t launch_rope_axes_norm(const RopeArgs& a, int* ctas_q, cudaStream_t s) {
+    return rope_kinds<kNormTurn, false, true>(a, ctas_q, s);
+}
+
+}  // namespace rmsn

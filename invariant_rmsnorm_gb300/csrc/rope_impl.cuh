@@ -50,6 +50,12 @@ __device__ __forceinline__ long long position(const RopeArgs& a, int64_t t) {
     return a.pos64 ? static_cast<const long long*>(a.pos)[t] : static_cast<const int*>(a.pos)[t];
 }
 
+// With several axes, the position of token t along one of them.
+__device__ __forceinline__ long long axis_position(const RopeArgs& a, int axis, int64_t t) {
+    const int64_t i = axis * a.pos_axis + t * a.pos_token;
+    return a.pos64 ? __ldg(static_cast<const long long*>(a.pos) + i) : __ldg(static_cast<const int*>(a.pos) + i);
+}
+
 // Device error word of the including translation unit.
 __device__ unsigned int g_rope_error;
 
@@ -215,6 +221,20 @@ __device__ __forceinline__ void token_angles(float* cs, int hp, int half, const 
     __syncwarp();
 }
 
+// The same with several axes, `axis` that of every pair. A pair's position is read
+// by the lane that has the pair, out of L1 for all but one token of 16: no register of the
+// kernels' other users is taken, and a token's 32 + 8 heads hide the read.
+__device__ __forceinline__ void token_axis_angles(float* cs, int hp, int half, const unsigned long long* F, const uint8_t* axis,
+                                                  const RopeArgs& a, int64_t t, bool back, int lane) {
+    __syncwarp();
+    for (int i = lane; i < half; i += 32) {
+        const float2 c = rope_cos_sin(axis_position(a, axis[i], t), F[i], a.scale);
+        cs[i] = c.x;
+        cs[hp + i] = back ? -c.y : c.y;
+    }
+    __syncwarp();
+}
+
 // (A, B) turned, pair by pair: halves.
 __device__ __forceinline__ void turn_halves(Oct& A, Oct& B, const Oct& c, const Oct& s) {
 #pragma unroll
@@ -254,14 +274,18 @@ __device__ __forceinline__ uint4 first_of(uint4 v, int n) {
 }
 
 enum RopeKind : int { kHalves = 0, kNeighbours = 1, kHalvesAny = 2, kHalves8 = 3 };
+enum RopeTokens : int { kOne = 0, kMany = 1, kManyAxes = 2 };
 
 // ---------------------------------------------------------------------------
 // The kernel: 2^LG lanes a head, NR heads a group and turn, RB of them at a time.
 // FULL: every lane has a whole unit (D = 16 x 2^LG, no unit cut short).
-// MANY: a turn is of a token a group.
+// TOKENS: kOne: a turn is of one token; kMany: of a token a group; kManyAxes: the
+// same, with positions of several axes (in kOne kernels a branch, which costs those
+// no register; in kMany ones it would spill 12 to 52 bytes).
 // ---------------------------------------------------------------------------
-template <int MODE, int KIND, bool F16, int LG, bool FULL, bool MANY, int NR, int RBATCH, int S, int MINB>
+template <int MODE, int KIND, bool F16, int LG, bool FULL, int TOKENS, int NR, int RBATCH, int S, int MINB>
 __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs a) {
+    constexpr bool MANY = TOKENS != kOne, AXES = TOKENS == kManyAxes;
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
     constexpr bool ANY = KIND == kHalvesAny || KIND == kHalves8;  // units may be cut short
     constexpr int OPS = BWD ? 2 : 1, per = 32 >> LG, rows = per * NR;
@@ -275,12 +299,14 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     const uint32_t pitch = static_cast<uint32_t>(D) * 2u;
     const uint32_t op_bytes = rows * pitch, stage_bytes = OPS * op_bytes;
     // Shared memory: every warp's stages; weights [q | k][D]; every warp's [cos | sin][hp];
-    // every warp's inverse RMS [S][rows] (read backward, gathered forward); barriers; frequencies.
+    // every warp's inverse RMS [S][rows] (read backward, gathered forward); barriers; frequencies;
+    // with several axes, each pair's.
     float* wsm = reinterpret_cast<float*>(smem + static_cast<size_t>(nw) * S * stage_bytes);
     float* cs = wsm + (NORM ? 2 * D : 0) + warp * 2 * hp;
     float* rs = wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (NORM ? warp * S * rows : 0);
     uint64_t* bars = reinterpret_cast<uint64_t*>(wsm + (NORM ? 2 * D : 0) + nw * 2 * hp + (NORM ? nw * S * rows : 0));
     unsigned long long* F = reinterpret_cast<unsigned long long*>(bars + nw * S);
+    uint8_t* axis = reinterpret_cast<uint8_t*>(F + half);
     uint64_t* full = bars + warp * S;
     const uint32_t ring = smem_u32(smem) + warp * S * stage_bytes;
 
@@ -420,6 +446,8 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     // While the first rows come:
     for (int i = half + lane; i < hp; i += 32) cs[i] = cs[hp + i] = 0.0f;  // zeros are turned there
     for (int i = tid; i < half; i += nt) F[i] = rope_turns(a.inv_freq[i]);
+    if ((AXES || !MANY) && a.axis != nullptr)
+        for (int i = tid; i < half; i += nt) axis[i] = static_cast<uint8_t>(min(static_cast<int>(a.axis[i]), a.axes - 1));
     if constexpr (NORM) {
         for (int i = tid; i < 2 * D; i += nt) {
             const int s = i >= D;
@@ -442,16 +470,20 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
             t_have = now.t;
             if (t0 - t32 >= 32) {
                 t32 = t0;
-                if (t32 + lane < a.T) p32 = position(a, t32 + lane);
+                if (!AXES && (MANY || a.axis == nullptr) && t32 + lane < a.T) p32 = position(a, t32 + lane);
             }
             const long long pos = __shfl_sync(0xffffffffu, p32, static_cast<int>(t0 - t32) + (MANY ? head : 0));
-            if constexpr (!MANY) token_angles(cs, hp, half, F, pos, a.scale, BWD || a.back, lane);
+            if constexpr (!MANY) {
+                if (a.axis == nullptr) token_angles(cs, hp, half, F, pos, a.scale, BWD || a.back, lane);
+                else token_axis_angles(cs, hp, half, F, axis, a, t0, BWD || a.back, lane);
+            }
             if constexpr (MANY) {  // this lane's own
                 if (KIND == kNeighbours || turned) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int pair = KIND == kNeighbours ? ((e < 4 ? atA : atB) >> 1) + (e & 3) : atA + e;
-                        float2 v = rope_cos_sin(pos, F[min(pair, half - 1)], a.scale);
+                        const int i = min(pair, half - 1);
+                        float2 v = rope_cos_sin(AXES ? axis_position(a, axis[i], min(t0 + head, a.T - 1)) : pos, F[i], a.scale);
                         if (BWD || a.back) v.y = -v.y;
                         if (e & 1) {
                             c.p[e / 2].y = v.x;
@@ -703,14 +735,15 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
-template <int MODE, int KIND, bool F16, int LG, bool FULL, bool MANY, int NR, int RB, int S, int MINB>
+template <int MODE, int KIND, bool F16, int LG, bool FULL, int TOKENS, int NR, int RB, int S, int MINB>
 cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
+    constexpr bool MANY = TOKENS != kOne;
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
     constexpr int per = 32 >> LG, rows = per * NR, tokens = MANY ? per : 1, step = MANY ? NR : rows;
-    const auto kern = rope_kernel<MODE, KIND, F16, LG, FULL, MANY, NR, RB, S, MINB>;
+    const auto kern = rope_kernel<MODE, KIND, F16, LG, FULL, TOKENS, NR, RB, S, MINB>;
     const int hp = (a.R / 2 + 7) & ~7;
     const size_t warp_bytes = static_cast<size_t>(S) * (BWD ? 2 : 1) * rows * a.D * 2 + hp * 8 + (NORM ? S * rows * 4 : 0) + S * 8;
-    const size_t fixed = (NORM ? static_cast<size_t>(a.D) * 8 : 0) + static_cast<size_t>(a.R / 2) * 8;
+    const size_t fixed = (NORM ? static_cast<size_t>(a.D) * 8 : 0) + static_cast<size_t>(a.R / 2) * (a.axis != nullptr ? 9 : 8);
     const int64_t sms = sm_count();
     const int64_t turns = (a.T + tokens - 1) / tokens * ((a.H[0] + step - 1) / step + (a.H[1] + step - 1) / step);
     // Threads: few turns spread over the SMs in smaller CTAs. The backward's CTAs
@@ -755,19 +788,31 @@ cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
 // 32 -> 57; 14 + 2 heads: 88 both ways, 55 -> 79, 46 -> 81. With as many turns
 // (32 + 8 heads of 128) its shorter copies cost: 83 -> 80, 76 -> 66, 75 -> 72,
 // measured in one kernel for both.
-template <int MODE, int KIND, bool F16, int LG, bool FULL, int NR, int RB, int S, int MINB>
+//
+// Turns of several tokens with positions of several axes are a launch of another
+// translation unit (`Axes`: instantiating them alone), which comes here by the same rules.
+template <int MODE, int KIND, bool F16, int LG, bool FULL, bool Axes, int NR, int RB, int S, int MINB>
 cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     constexpr int per = 32 >> LG;
+    // Forward with the norm: then four heads a group (8 + 1 heads of 128: 75 % for two heads' 58).
+    constexpr bool wider = MODE == kNormTurn;
+    if constexpr (Axes) {
+        if constexpr (per > 1)
+            return rope_run_as<MODE, KIND, F16, LG, FULL, kManyAxes, wider ? 4 : NR, wider ? 2 : RB, wider ? 3 : S, MINB>(a, ctas_q, st);
+        else
+            return cudaErrorInvalidValue;  // never chosen: one token fills the warp
+    } else {
     if constexpr (per > 1) {
-        // Forward with the norm: then four heads a group (8 + 1 heads of 128: 75 % for two heads' 58).
-        constexpr bool wider = MODE == kNormTurn;
         auto turns_of = [&](int step) -> int64_t { return (a.H[0] + step - 1) / step + (a.H[1] + step - 1) / step; };
         const int64_t one = a.T * turns_of(per * NR), many = (a.T + per - 1) / per * turns_of(NR);
         const bool fewer = MODE == kTurn ? 2 * many <= one : 4 * many <= 3 * one;
-        if (fewer && many >= kRopeManyFrom)
-            return rope_run_as<MODE, KIND, F16, LG, FULL, true, wider ? 4 : NR, wider ? 2 : RB, wider ? 3 : S, MINB>(a, ctas_q, st);
+        if (fewer && many >= kRopeManyFrom) {
+            if (a.axis != nullptr) return launch_rope_axes(MODE, F16, a, ctas_q, st);
+            return rope_run_as<MODE, KIND, F16, LG, FULL, kMany, wider ? 4 : NR, wider ? 2 : RB, wider ? 3 : S, MINB>(a, ctas_q, st);
+        }
     }
-    return rope_run_as<MODE, KIND, F16, LG, FULL, false, NR, RB, S, MINB>(a, ctas_q, st);
+    return rope_run_as<MODE, KIND, F16, LG, FULL, kOne, NR, RB, S, MINB>(a, ctas_q, st);
+    }
 }
 
 // Heads a group and turn, of them in registers at a time, stages, CTAs an SM: the
@@ -777,49 +822,49 @@ cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
 // cut (4 to 56 bytes at 128 registers), two forward ones with the norm (4 bytes),
 // and of the rotation those of neighbours in fp16 and of several tokens (4 to 20
 // bytes at 80 registers, three CTAs an SM).
-template <int MODE, int KIND, bool F16, int LG, bool FULL>
+template <int MODE, int KIND, bool F16, int LG, bool FULL, bool Axes>
 cudaError_t rope_shape_of(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     if constexpr (MODE == kTurn) {
-        return rope_run_kernel<MODE, KIND, F16, LG, FULL, 4, 1, 2, 3>(a, ctas_q, st);
+        return rope_run_kernel<MODE, KIND, F16, LG, FULL, Axes, 4, 1, 2, 3>(a, ctas_q, st);
     } else if constexpr (MODE == kNormTurn) {
         // 16384 x 32 + 8 x 128: 84 % of the copy rate (with 4 heads 80); 80 wide: 78 % (with 2 heads 61).
-        if constexpr (FULL && LG < 5) return rope_run_kernel<MODE, KIND, F16, LG, FULL, 2, 1, 3, 2>(a, ctas_q, st);
-        else return rope_run_kernel<MODE, KIND, F16, LG, FULL, 4, 2, 3, 2>(a, ctas_q, st);
+        if constexpr (FULL && LG < 5) return rope_run_kernel<MODE, KIND, F16, LG, FULL, Axes, 2, 1, 3, 2>(a, ctas_q, st);
+        else return rope_run_kernel<MODE, KIND, F16, LG, FULL, Axes, 4, 2, 3, 2>(a, ctas_q, st);
     } else if constexpr (LG == 5) {
-        return rope_run_kernel<MODE, KIND, F16, LG, FULL, 2, 1, 2, 2>(a, ctas_q, st);  // 3 heads: one CTA an SM, 58 % for 76
+        return rope_run_kernel<MODE, KIND, F16, LG, FULL, Axes, 2, 1, 2, 2>(a, ctas_q, st);  // 3 heads: one CTA an SM, 58 % for 76
     } else if constexpr (FULL && LG != 3) {
-        return rope_run_kernel<MODE, KIND, F16, LG, FULL, 2, 1, 3, 2>(a, ctas_q, st);
+        return rope_run_kernel<MODE, KIND, F16, LG, FULL, Axes, 2, 1, 3, 2>(a, ctas_q, st);
     } else {
         if constexpr (!FULL)  // narrower than its lanes could hold: four heads fit (80 wide: 70 % for 62)
-            if (4 * a.D <= 3 * (16 << LG)) return rope_run_kernel<MODE, KIND, F16, LG, FULL, 4, 1, 2, 2>(a, ctas_q, st);
-        return rope_run_kernel<MODE, KIND, F16, LG, FULL, 3, 1, 2, 2>(a, ctas_q, st);
+            if (4 * a.D <= 3 * (16 << LG)) return rope_run_kernel<MODE, KIND, F16, LG, FULL, Axes, 4, 1, 2, 2>(a, ctas_q, st);
+        return rope_run_kernel<MODE, KIND, F16, LG, FULL, Axes, 3, 1, 2, 2>(a, ctas_q, st);
     }
 }
 
-template <int MODE, int KIND, bool F16, int LG>
+template <int MODE, int KIND, bool F16, int LG, bool Axes>
 cudaError_t rope_full(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     if constexpr (KIND == kHalves || KIND == kNeighbours)
-        if (a.D == 16 << LG) return rope_shape_of<MODE, KIND, F16, LG, true>(a, ctas_q, st);
-    return rope_shape_of<MODE, KIND, F16, LG, false>(a, ctas_q, st);
+        if (a.D == 16 << LG) return rope_shape_of<MODE, KIND, F16, LG, true, Axes>(a, ctas_q, st);
+    return rope_shape_of<MODE, KIND, F16, LG, false, Axes>(a, ctas_q, st);
 }
 
-template <int MODE, int KIND, bool F16>
+template <int MODE, int KIND, bool F16, bool Axes>
 cudaError_t rope_lanes(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     switch (rope_lanes_log2(a.D, a.R, KIND == kHalvesAny || KIND == kHalves8, MODE != kTurn)) {
-        case 2: return rope_full<MODE, KIND, F16, 2>(a, ctas_q, st);
-        case 3: return rope_full<MODE, KIND, F16, 3>(a, ctas_q, st);
-        case 4: return rope_full<MODE, KIND, F16, 4>(a, ctas_q, st);
-        default: return rope_full<MODE, KIND, F16, 5>(a, ctas_q, st);
+        case 2: return rope_full<MODE, KIND, F16, 2, Axes>(a, ctas_q, st);
+        case 3: return rope_full<MODE, KIND, F16, 3, Axes>(a, ctas_q, st);
+        case 4: return rope_full<MODE, KIND, F16, 4, Axes>(a, ctas_q, st);
+        default: return rope_full<MODE, KIND, F16, 5, Axes>(a, ctas_q, st);
     }
 }
 
 // *ctas_q: the CTAs (and so the partial rows) of q in a norm backward.
-template <int MODE, bool F16>
+template <int MODE, bool F16, bool Axes = false>
 cudaError_t rope_kinds(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
-    if (a.layout == ROPE_INTERLEAVED) return rope_lanes<MODE, kNeighbours, F16>(a, ctas_q, st);
-    if (a.R % 16 == 0) return rope_lanes<MODE, kHalves, F16>(a, ctas_q, st);
-    if (a.R % 8 == 0) return rope_lanes<MODE, kHalves8, F16>(a, ctas_q, st);
-    return rope_lanes<MODE, kHalvesAny, F16>(a, ctas_q, st);
+    if (a.layout == ROPE_INTERLEAVED) return rope_lanes<MODE, kNeighbours, F16, Axes>(a, ctas_q, st);
+    if (a.R % 16 == 0) return rope_lanes<MODE, kHalves, F16, Axes>(a, ctas_q, st);
+    if (a.R % 8 == 0) return rope_lanes<MODE, kHalves8, F16, Axes>(a, ctas_q, st);
+    return rope_lanes<MODE, kHalvesAny, F16, Axes>(a, ctas_q, st);
 }
 
 }  // namespace

@@ -28,6 +28,9 @@ struct RopeArgs {
     float* partials;     // norm backward: a row of D a CTA, dwq's, then dwk's
     const double* inv_freq;
     const void* pos;     // null: the token's index
+    const uint8_t* axis; // several axes: that of every pair (null: one position a token)
+    int axes;
+    int64_t pos_axis, pos_token;  // strides of pos [axes][T], several axes alone
     int64_t T;
     int H[2];
     int D, R, layout, pos64, back, zc;
@@ -75,6 +78,26 @@ cudaError_t launch_rope_norm_bwd(const RopeArgs& a, int* ctas_q, cudaStream_t s)
 cudaError_t launch_rope_turn_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
 cudaError_t launch_rope_norm_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
 cudaError_t launch_rope_norm_bwd_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+// Turns of several tokens with positions of several axes, chosen by the launchers above.
+cudaError_t launch_rope_axes_turn(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+cudaError_t launch_rope_axes_norm(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+cudaError_t launch_rope_axes_norm_bwd(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+cudaError_t launch_rope_axes_turn_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+cudaError_t launch_rope_axes_norm_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+cudaError_t launch_rope_axes_norm_bwd_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
+inline cudaError_t launch_rope_axes(int mode, bool f16, const RopeArgs& a, int* ctas_q, cudaStream_t s) {
+    switch (mode) {
+        case kTurn: return f16 ? launch_rope_axes_turn_f16(a, ctas_q, s) : launch_rope_axes_turn(a, ctas_q, s);
+        case kNormTurn: return f16 ? launch_rope_axes_norm_f16(a, ctas_q, s) : launch_rope_axes_norm(a, ctas_q, s);
+        default: return f16 ? launch_rope_axes_norm_bwd_f16(a, ctas_q, s) : launch_rope_axes_norm_bwd(a, ctas_q, s);
+    }
+}
+cudaError_t rope_axes_turn_read_error(unsigned* flags, bool clear);
+cudaError_t rope_axes_norm_read_error(unsigned* flags, bool clear);
+cudaError_t rope_axes_norm_bwd_read_error(unsigned* flags, bool clear);
+cudaError_t rope_axes_turn_f16_read_error(unsigned* flags, bool clear);
+cudaError_t rope_axes_norm_f16_read_error(unsigned* flags, bool clear);
+cudaError_t rope_axes_norm_bwd_f16_read_error(unsigned* flags, bool clear);
 cudaError_t rope_turn_read_error(unsigned* flags, bool clear);
 cudaError_t rope_norm_read_error(unsigned* flags, bool clear);
 cudaError_t rope_norm_bwd_read_error(unsigned* flags, bool clear);

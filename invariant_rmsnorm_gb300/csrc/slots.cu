@@ -46,6 +46,10 @@ extern "C" int norm_call(int entry, const union norm_slot* args, int64_t n) {
         case NORM_LINEAR_BWD: return call(linear_bwd, args, n);
         case NORM_LINEAR_GATED_FWD: return call(linear_gated_fwd, args, n);
         case NORM_LINEAR_GATED_BWD: return call(linear_gated_bwd, args, n);
+        case NORM_ROPE_AXES_FWD: return call(rope_axes_fwd, args, n);
+        case NORM_ROPE_AXES_BWD: return call(rope_axes_bwd, args, n);
+        case NORM_RMSNORM_ROPE_AXES_FWD: return call(rmsnorm_rope_axes_fwd, args, n);
+        case NORM_RMSNORM_ROPE_AXES_BWD: return call(rmsnorm_rope_axes_bwd, args, n);
         default: return RMSN_EINVAL;
     }
 }
