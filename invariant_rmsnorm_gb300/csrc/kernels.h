@@ -155,5 +155,7 @@ cudaError_t encode_blocks_2d(CUtensorMap* map, const void* base, int64_t rows, i
 // The same with a third dimension: blocks of 64 columns (cols a multiple of 64), `deep` of them a box; or, if `deep`
 // is 0, a single one of all columns.
 cudaError_t encode_blocks_3d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld_elems, int box_rows, int deep);
+// An output of 16-bit values in pieces of [32][32], whose rows of 64 bytes are swizzled in shared memory.
+cudaError_t encode_pieces_2d(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld_elems);
 
 }  // namespace rmsn

@@ -25,49 +25,69 @@ constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements: a tensor map's st
 // ---------------------------------------------------------------------------
 constexpr int kSlopeThreads = 256, kSlopeRows = 8, kSlopeCols = 256;
 
-// Ranges of rows: four CTAs an SM of a GPU of 152 over all columns, of 64 rows at least. A
+// Ranges of rows: twelve CTAs an SM of a GPU of 152 over all columns, of 32 rows at least. A
 // function of T and N alone, so the order of db's sums is too.
 int64_t slope_ranges(int64_t T, int64_t N) {
     const int64_t across = (N + kSlopeCols - 1) / kSlopeCols;
-    return std::max<int64_t>(1, std::min<int64_t>((608 + across - 1) / across, (T + 63) / 64));
+    return std::max<int64_t>(1, std::min<int64_t>((1824 + across - 1) / across, (T + 31) / 32));
 }
 
 template <int ACT, bool GATED, bool F16>
 __device__ __forceinline__ void slope_rows(const Slopes& a, int64_t t0, int64_t t1, int col, float (&sum)[8]) {
-    for (int64_t t = t0; t < t1; t += kSlopeRows) {
-        float g[8], z[8];
-        unpack_act<F16>(__ldcs(reinterpret_cast<const uint4*>(a.g.p + t * a.g.ld + col)), g);
-        if constexpr (GATED) {
-            float u[8], dup[8];
-            unpack_act<F16>(__ldcs(reinterpret_cast<const uint4*>(a.z.p + t * a.z.ld + col)), z);
-            unpack_act<F16>(__ldcs(reinterpret_cast<const uint4*>(a.up.p + t * a.up.ld + col)), u);
+    constexpr int BATCH = GATED || ACT != LINEAR_ACT_NONE ? 2 : 4;  // rows whose loads are in flight at once
+    constexpr bool HAS_Z = GATED || ACT != LINEAR_ACT_NONE;
+    const auto load = [](const MatIn& m, int64_t t, int c) { return __ldcs(reinterpret_cast<const uint4*>(m.p + t * m.ld + c)); };
+    for (int64_t t = t0; t < t1; t += BATCH * kSlopeRows) {
+        uint4 gv[BATCH], zv[BATCH], uv[BATCH];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 v = act_slope<ACT>(z[i]);
-                dup[i] = fmul(g[i], v.x);
-                g[i] = fmul(fmul(g[i], v.y), u[i]);
+        for (int b = 0; b < BATCH; ++b) {
+            const int64_t r = t + b * kSlopeRows;
+            if (r < t1) {
+                gv[b] = load(a.g, r, col);
+                if constexpr (HAS_Z) zv[b] = load(a.z, r, col);
+                if constexpr (GATED) uv[b] = load(a.up, r, col);
             }
-            *reinterpret_cast<uint4*>(a.out[1].p + t * a.out[1].ld + col) = pack_act<F16>(dup);
-        } else if constexpr (ACT != LINEAR_ACT_NONE) {
-            unpack_act<F16>(__ldcs(reinterpret_cast<const uint4*>(a.z.p + t * a.z.ld + col)), z);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = fmul(g[i], act_slope<ACT>(z[i]).y);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = fadd(sum[i], g[i]);
-        if (a.out[0].p != nullptr) *reinterpret_cast<uint4*>(a.out[0].p + t * a.out[0].ld + col) = pack_act<F16>(g);
+        for (int b = 0; b < BATCH; ++b) {
+            const int64_t r = t + b * kSlopeRows;
+            if (r < t1) {
+                float g[8], z[8];
+                unpack_act<F16>(gv[b], g);
+                if constexpr (HAS_Z) unpack_act<F16>(zv[b], z);
+                if constexpr (GATED) {
+                    float u[8], dup[8];
+                    unpack_act<F16>(uv[b], u);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 v = act_slope<ACT>(z[i]);
+                        dup[i] = fmul(g[i], v.x);
+                        g[i] = fmul(fmul(g[i], v.y), u[i]);
+                    }
+                    *reinterpret_cast<uint4*>(a.out[1].p + r * a.out[1].ld + col) = pack_act<F16>(dup);
+                } else if constexpr (HAS_Z) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[i] = fmul(g[i], act_slope<ACT>(z[i]).y);
+                }
+                if constexpr (!GATED) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[i] = fadd(sum[i], g[i]);
+                }
+                if (a.out[0].p != nullptr) *reinterpret_cast<uint4*>(a.out[0].p + r * a.out[0].ld + col) = pack_act<F16>(g);
+            }
+        }
     }
 }
 
-template <bool GATED, bool F16>
-__global__ void __launch_bounds__(kSlopeThreads) slopes_kernel(const Slopes a) {
+template <int ACT, bool GATED, bool F16>
+__global__ void __launch_bounds__(kSlopeThreads, GATED ? 3 : 4) slopes_kernel(const Slopes a) {
     __shared__ float part[kSlopeRows][kSlopeCols];
     pdl_wait();
     const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
     const int col = blockIdx.x * kSlopeCols + 8 * lane;
     const int64_t t0 = a.T * blockIdx.y / a.ranges, t1 = a.T * (blockIdx.y + 1) / a.ranges;
     float sum[8] = {};
-    if (col < a.N) with_act(a.act, [&](auto act) { slope_rows<decltype(act)::value, GATED, F16>(a, t0 + r, t1, col, sum); });
+    if (col < a.N) slope_rows<ACT, GATED, F16>(a, t0 + r, t1, col, sum);
     pdl_release();
     if (a.partials == nullptr) return;
 #pragma unroll
@@ -80,6 +100,12 @@ __global__ void __launch_bounds__(kSlopeThreads) slopes_kernel(const Slopes a) {
         for (int i = 1; i < kSlopeRows; ++i) v = fadd(v, part[i][threadIdx.x]);
         a.partials[blockIdx.y * a.N + c] = v;
     }
+}
+
+template <int ACT>
+auto slopes_of(bool gated, bool f16) -> void (*)(Slopes) {
+    if (gated) return f16 ? slopes_kernel<ACT, true, true> : slopes_kernel<ACT, true, false>;
+    return f16 ? slopes_kernel<ACT, false, true> : slopes_kernel<ACT, false, false>;
 }
 
 // ---------------------------------------------------------------------------
@@ -177,9 +203,15 @@ cudaError_t launch_linear_slopes(const Slopes& a, bool f16, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = RMSN_PDL;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const bool gated = a.up.p != nullptr;
-    const auto kern = gated ? (f16 ? slopes_kernel<true, true> : slopes_kernel<true, false>)
-                            : (f16 ? slopes_kernel<false, true> : slopes_kernel<false, false>);
+    void (*kern)(Slopes) = nullptr;
+    switch (a.act) {
+        case LINEAR_ACT_SILU: kern = slopes_of<LINEAR_ACT_SILU>(a.up.p != nullptr, f16); break;
+        case LINEAR_ACT_SIGMOID: kern = slopes_of<LINEAR_ACT_SIGMOID>(a.up.p != nullptr, f16); break;
+        case LINEAR_ACT_GELU: kern = slopes_of<LINEAR_ACT_GELU>(a.up.p != nullptr, f16); break;
+        case LINEAR_ACT_GELU_TANH: kern = slopes_of<LINEAR_ACT_GELU_TANH>(a.up.p != nullptr, f16); break;
+        case LINEAR_ACT_RELU: kern = slopes_of<LINEAR_ACT_RELU>(a.up.p != nullptr, f16); break;
+        default: kern = slopes_of<LINEAR_ACT_NONE>(a.up.p != nullptr, f16); break;
+    }
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -33,14 +33,17 @@ namespace rmsn {
 namespace {
 
 constexpr int kBlockK = 64;            // reduced values a block: one swizzled row of 128 bytes
-constexpr int kMostDeep = 4;           // blocks a stage
-constexpr int kProductThreads = 384;   // warp 0 copies, 1 multiplies, 2 holds tensor memory, 4 .. 11 epilogue
+constexpr int kMostDeep = 8;           // blocks a stage
+constexpr int kProductThreads = 384;   // warps 0, 2 and 3 copy, 1 multiplies, 2 holds tensor memory, 4 .. 11 epilogue
+constexpr int kCopyWarps = 3;          // 0, 2 and 3
 constexpr int kEpilogueWarps = 8;
 constexpr int kMaxStages = 32;
 constexpr uint32_t kStageBytes = 227 * 1024 - 2048;  // of shared memory for the stages
+constexpr uint32_t kTileBytes = 32 * 64;             // pairs of CTAs: a warp's piece of the output on its way
 
 struct ProductArgs {
     CUtensorMap a[2], b[2];
+    CUtensorMap out_map[2], z_map[2];  // pairs of CTAs: boxes of 32 rows of 32 values
     MatOut out[2], z[2];
     MatIn res;
     const float* bias;
@@ -63,6 +66,7 @@ struct ProductArgs {
     uint32_t a_block, b_block, a_bytes, stage_bytes;
     uint32_t idesc;
     int tmem_cols;
+    uint32_t staging;         // offset of the epilogue's staging from the ring's start
 };
 
 // Device error word of the including translation unit.
@@ -146,37 +150,45 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t at, uint32_t block) {
            static_cast<uint64_t>(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
+// A warp's 32 rows of 32 values from shared memory to the output; beyond the matrix nothing is written.
+__device__ __forceinline__ void tile_s2g(const CUtensorMap* map, int c0, int c1, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(map), "r"(c0), "r"(c1), "r"(src) : "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // A tensor copy into this CTA; a pair's copies count on the first CTA's barrier (`bar`: its
 // shared::cluster address).
 template <int CTAS>
 __device__ __forceinline__ void tile_g2s(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
     if constexpr (CTAS == 2)
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+                        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
             ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
     else
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
             ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
 }
 
 // The same of several blocks of 64 columns at once: [blocks][rows][64], for single CTAs.
 __device__ __forceinline__ void tile3_g2s(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
-
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // True in one lane of a converged warp. (The loops around tensor instructions are
 // run by the whole warp, so that their operands stay in uniform registers.)
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-    return p != 0;
+    return p;
 }
 
 template <int CTAS>
@@ -189,18 +201,34 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
 // ---------------------------------------------------------------------------
 struct Tile { int m, n, which, split; };
 
+// The blocks of the reduced axis that a split has.
+__device__ __forceinline__ int2 blocks_of(const ProductArgs& g, int split) {
+    if (g.splits == 1) return make_int2(0, g.blocks);
+    const unsigned b = g.blocks, s = g.splits;  // at most 2^25 blocks and 76 splits
+    return make_int2(static_cast<int>(b * split / s), static_cast<int>(b * (split + 1) / s));
+}
+
 // Output and split outermost; then bands of 8 rows of tiles, whose operands stay in
 // L2 while the band's columns are walked.
 __device__ __forceinline__ Tile tile_of(const ProductArgs& g, int t) {
-    Tile o;
-    const int each = g.tiles_m * g.tiles_n, s = t / each;
-    t -= s * each;
-    o.which = s / g.splits;
-    o.split = s - o.which * g.splits;
-    const int band = 8 * g.tiles_n, first = t / band * 8, rows = min(8, g.tiles_m - first);
-    t -= first / 8 * band;
-    o.n = t / rows;
-    o.m = first + t - o.n * rows;
+    Tile o{0, 0, 0, 0};
+    const unsigned each = g.tiles_m * g.tiles_n;
+    unsigned u = t;
+    if (u >= each) {
+        const unsigned s = u / each;
+        u -= s * each;
+        o.which = s / g.splits;
+        o.split = s - o.which * g.splits;
+    }
+    unsigned first = 0, rows = g.tiles_m;
+    if (rows > 8) {
+        const unsigned band = 8 * g.tiles_n, b = u / band;
+        u -= b * band;
+        first = 8 * b;
+        rows = min(8u, rows - first);
+    }
+    o.n = rows == 1 ? u : u / rows;
+    o.m = first + u - o.n * rows;
     return o;
 }
 
@@ -211,100 +239,111 @@ template <int KIND, int CTAS, bool F16>
 __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ ProductArgs g) {
     constexpr bool A_COLS = KIND == kGradW, B_COLS = KIND == kGradX || KIND == kGradW;  // rows across the reduced axis
     constexpr int ROWS = 128 * CTAS;  // of a tile
-    constexpr bool DEEP = CTAS == 1 && !B_COLS;  // several blocks a stage
+    constexpr bool DEEP = CTAS == 1;  // several blocks a stage
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // From lane 0, so that what depends on it is known to be the same for the whole warp.
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t rank = CTAS == 2 ? cluster_ctarank() : 0u;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int first_tile = CTAS == 2 ? cluster_id_x() : blockIdx.x, tile_step = CTAS == 2 ? cluster_count_x() : gridDim.x;
 
-    if (warp == 2) {
+    if (warp == 0) {
+        if (lane < g.stages) {
+            mbar_init(&full[lane], 1);
+            mbar_init(&empty[lane], 1);
+        }
+        if (lane < 2) {
+            mbar_init(&acc_full[lane], 1);
+            mbar_init(&acc_empty[lane], kEpilogueWarps * CTAS);
+        }
+        if (lane == 0) mbar_init(&drained, 1);
+        fence_mbar_init();
+        if (lane < 4) prefetch_tensormap(lane < 2 ? &g.a[lane] : &g.b[lane - 2]);
+        __syncwarp();
+    } else if (warp == 2) {
         tmem_alloc<CTAS>(smem_u32(&tmem_slot), g.tmem_cols);
         tmem_relinquish<CTAS>();
     }
-    if (tid == 0) {
-        for (int i = 0; i < g.stages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], kEpilogueWarps * CTAS);
-        }
-        mbar_init(&drained, 1);
-        fence_mbar_init();
-    }
-    if (warp == 0 && lane < 4) prefetch_tensormap(lane < 2 ? &g.a[lane] : &g.b[lane - 2]);
     tmem_fence_before();
-    __syncthreads();
-    if constexpr (CTAS == 2) cluster_sync_all();
+    if constexpr (CTAS == 2) {
+        __syncthreads();
+        cluster_sync_all();
+    } else if (warp == 0) {
+        // The first copies need no tensor memory: this warp does not wait for it.
+        asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kProductThreads) : "memory");
+    } else {
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(kProductThreads) : "memory");
+    }
     tmem_fence_after();
-    const uint32_t tmem = tmem_slot;
     pdl_wait();
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2 || warp == 3) {
         {
+            // The stages in turn: a copy costs its warp 150 to 200 cycles, as much as a small tile's products of a block.
+            const int mine_of = warp == 0 ? 0 : warp - 1;
+            int turn = 0;
             int s = 0;
             uint32_t phase = 0;
             int64_t sent = 0;
             bool ok = true;
             const uint32_t all_bytes = g.stage_bytes * CTAS;
-            const bool one = elect_one();
+            const uint32_t one = elect_one();
             const int deep = DEEP ? g.deep : 1;
             for (int t = first_tile; ok && t < g.tiles; t += tile_step) {
                 const Tile c = tile_of(g, t);
-                const int k0 = static_cast<int>(static_cast<int64_t>(g.blocks) * c.split / g.splits);
-                const int k1 = static_cast<int>(static_cast<int64_t>(g.blocks) * (c.split + 1) / g.splits);
+                const int2 range = blocks_of(g, c.split);
+                const int k0 = range.x, k1 = range.y;
                 const int row = c.m * ROWS + rank * 128;
                 for (int seg = 0; ok && seg < g.segments; ++seg) {
                     const CUtensorMap* ma = &g.a[KIND == kGradW ? c.which : seg];
                     for (int k = k0; k < k1; k += deep) {
-                        if (!wait_on<CTAS>(&empty[s], phase ^ 1u)) {
-                            ok = false;
-                            break;
-                        }
-                        if (one) {
-                            if (rank == 0) mbar_arrive_expect_tx(&full[s], all_bytes);
-                            const uint32_t bar = CTAS == 2 ? cluster_map(&full[s], 0) : smem_u32(&full[s]);
-                            const uint32_t at = ring + s * g.stage_bytes, bt = at + g.a_bytes;
-                            const int kk = k * kBlockK;
-                            // Columns of the accumulators: kGatedFwd has half of them of gate, half of up.
-                            const int half = g.bn >> 1;
-                            if constexpr (A_COLS) {
-                                tile_g2s<CTAS>(at, ma, row, kk, bar);
-                                tile_g2s<CTAS>(at + 8192, ma, row + 64, kk, bar);
-                            } else if constexpr (CTAS == 2 || B_COLS) {
-                                tile_g2s<CTAS>(at, ma, kk, row, bar);
-                            }
-                            if constexpr (B_COLS) {
-                                const int mine = g.bn / CTAS, col = c.n * g.bn + rank * mine;
-                                for (int i = 0; i < mine; i += 64) tile_g2s<CTAS>(bt + i * 128, &g.b[seg], col + i, kk, bar);
-                            } else if constexpr (CTAS == 2) {
-                                if constexpr (KIND == kGatedFwd) tile_g2s<CTAS>(bt, &g.b[rank], kk, c.n * half, bar);
-                                else tile_g2s<CTAS>(bt, &g.b[0], kk, c.n * g.bn + rank * half, bar);
-                            } else {
-                                // Whole blocks lie along a third axis; if the last is cut short, columns are counted on.
-                                auto copy = [&](uint32_t to, const CUtensorMap* map, int r, int j) {
-                                    tile3_g2s(to, map, g.whole ? 0 : kk + j * kBlockK, r, g.whole ? k + j : 0, bar);
-                                };
-                                for (int j = 0; j < deep; j += g.copy_deep) copy(at + j * g.a_block, ma, row, j);
-                                if constexpr (KIND == kGatedFwd) {
-                                    for (int j = 0; j < deep; ++j) {
-                                        copy(bt + j * g.b_block, &g.b[0], c.n * half, j);
-                                        copy(bt + j * g.b_block + half * 128, &g.b[1], c.n * half, j);
-                                    }
-                                } else {
-                                    for (int j = 0; j < deep; j += g.copy_deep) copy(bt + j * g.b_block, &g.b[0], c.n * g.bn, j);
-                                }
-                            }
-                        }
-                        ++sent;
+                        const int now = s;
+                        const uint32_t was = phase;
+                        const bool skip = turn != mine_of;
+                        turn = turn + 1 == kCopyWarps ? 0 : turn + 1;
                         if (++s == g.stages) {
                             s = 0;
                             phase ^= 1u;
                         }
+                        ++sent;
+                        if (skip) continue;
+                        if (!wait_on<CTAS>(&empty[now], was ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        if (one) {
+                            if (rank == 0) mbar_arrive_expect_tx(&full[now], all_bytes);
+                            const uint32_t bar = CTAS == 2 ? cluster_map(&full[now], 0) : smem_u32(&full[now]);
+                            const uint32_t at = ring + now * g.stage_bytes, bt = at + g.a_bytes;
+                            // Columns of the accumulators: kGatedFwd has half of them of gate, half of up.
+                            const int half = g.bn >> 1, mine = g.bn / CTAS, col = c.n * g.bn + rank * mine;
+                            // One block (single CTAs: or, along a third axis, all of a stage's) of rows.
+                            auto rows_of = [&](uint32_t to, const CUtensorMap* map, int r, int j) {
+                                if constexpr (CTAS == 2) tile_g2s<CTAS>(to, map, k * kBlockK, r, bar);
+                                else tile3_g2s(to, map, g.whole ? 0 : (k + j) * kBlockK, r, g.whole ? k + j : 0, bar);
+                            };
+                            auto cols_of = [&](uint32_t to, const CUtensorMap* map, int first, int n, int j) {
+                                for (int i = 0; i < n; i += 64) tile_g2s<CTAS>(to + i * 128, map, first + i, (k + j) * kBlockK, bar);
+                            };
+                            if constexpr (A_COLS) {
+                                for (int j = 0; j < deep; ++j) cols_of(at + j * g.a_block, ma, row, 128, j);
+                            } else {
+                                for (int j = 0; j < deep; j += g.copy_deep) rows_of(at + j * g.a_block, ma, row, j);
+                            }
+                            if constexpr (B_COLS) {
+                                for (int j = 0; j < deep; ++j) cols_of(bt + j * g.b_block, &g.b[seg], col, mine, j);
+                            } else if constexpr (KIND == kGatedFwd) {
+                                for (int j = 0; j < deep; ++j) {
+                                    rows_of(bt + j * g.b_block, &g.b[CTAS == 2 ? rank : 0], c.n * half, j);
+                                    if constexpr (CTAS == 1) rows_of(bt + j * g.b_block + half * 128, &g.b[1], c.n * half, j);
+                                }
+                            } else {
+                                for (int j = 0; j < deep; j += g.copy_deep) rows_of(bt + j * g.b_block, &g.b[0], col, j);
+                            }
+                        }
+                        __syncwarp();
                     }
                 }
             }
@@ -331,47 +370,48 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
-            const bool one = elect_one();
+            const uint32_t one = elect_one();
             const int deep = DEEP ? g.deep : 1;
             int s = 0, n = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int t = first_tile; ok && t < g.tiles; t += tile_step, ++n) {
-                const int split = t / (g.tiles_m * g.tiles_n) % g.splits;
-                const int k0 = static_cast<int>(static_cast<int64_t>(g.blocks) * split / g.splits);
-                const int k1 = static_cast<int>(static_cast<int64_t>(g.blocks) * (split + 1) / g.splits);
-                const int blocks = (k1 - k0) * g.segments, buf = n & 1;
+                const int2 range = blocks_of(g, g.splits == 1 ? 0 : t / (g.tiles_m * g.tiles_n) % g.splits);
+                const int blocks = range.y - range.x, buf = n & 1;
                 if (!wait_on<CTAS>(&acc_empty[buf], ((n >> 1) & 1) ^ 1u)) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
-                const uint32_t d = tmem + buf * g.bn;
-                for (int k = 0; k < blocks; k += deep) {
-                    if (!wait_on<CTAS>(&full[s], phase)) {
-                        ok = false;
-                        break;
-                    }
-                    tmem_fence_after();
-                    const uint32_t at = ring + s * g.stage_bytes, bt = at + g.a_bytes;
-                    const uint64_t da = smem_desc(at, A_COLS ? 8192u : 16u), db = smem_desc(bt, B_COLS ? 8192u : 16u);
-                    // 16 reduced values: 32 bytes of a row, or two groups of 8 rows.
-                    constexpr uint32_t step_a = (A_COLS ? 2048 : 32) >> 4, step_b = (B_COLS ? 2048 : 32) >> 4;
-                    if (one) {
-#pragma unroll
-                        for (int j = 0; j < (DEEP ? kMostDeep : 1); ++j) {
-                            if (DEEP && j >= min(deep, blocks - k)) break;
-#pragma unroll
-                            for (int i = 0; i < kBlockK / 16; ++i)
-                                mma16<CTAS>(d, da + j * (g.a_block >> 4) + i * step_a, db + j * (g.b_block >> 4) + i * step_b, g.idesc,
-                                            k > 0 || i > 0 || j > 0);
+                const uint32_t d = tmem_slot + buf * g.bn;
+                for (int seg = 0; ok && seg < g.segments; ++seg) {
+                    for (int k = 0; k < blocks; k += deep) {
+                        if (!wait_on<CTAS>(&full[s], phase)) {
+                            ok = false;
+                            break;
                         }
-                        mma_commit<CTAS>(&empty[s]);
-                    }
-                    __syncwarp();
-                    if (++s == g.stages) {
-                        s = 0;
-                        phase ^= 1u;
+                        tmem_fence_after();
+                        const uint32_t at = ring + s * g.stage_bytes, bt = at + g.a_bytes;
+                        const uint64_t da = smem_desc(at, A_COLS ? 8192u : 16u), db = smem_desc(bt, B_COLS ? 8192u : 16u);
+                        uint64_t* const used = &empty[s];
+                        if (++s == g.stages) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
+                        // 16 reduced values: 32 bytes of a row, or two groups of 8 rows.
+                        constexpr uint32_t step_a = (A_COLS ? 2048 : 32) >> 4, step_b = (B_COLS ? 2048 : 32) >> 4;
+                        if (one) {
+#pragma unroll
+                            for (int j = 0; j < (DEEP ? kMostDeep : 1); ++j) {
+                                if (DEEP && j >= min(deep, blocks - k)) break;
+#pragma unroll
+                                for (int i = 0; i < kBlockK / 16; ++i)
+                                    mma16<CTAS>(d, da + j * (g.a_block >> 4) + i * step_a, db + j * (g.b_block >> 4) + i * step_b, g.idesc,
+                                                seg > 0 || k > 0 || i > 0 || j > 0);
+                            }
+                            mma_commit<CTAS>(used);
+                        }
+                        __syncwarp();
                     }
                 }
                 if (ok && one) mma_commit<CTAS>(&acc_full[buf]);
@@ -388,6 +428,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
         __syncwarp();
     } else if (warp >= 4) {
         const int quad = warp & 3, part = (warp - 4) >> 2;  // a warp reads the lanes of its quarter
+        const uint32_t staged = ring + g.staging + (warp - 4) * 2 * kTileBytes;
+        uint32_t piece = 0;
         int n = 0;
         for (int t = first_tile; t < g.tiles; t += tile_step, ++n) {
             const Tile c = tile_of(g, t);
@@ -401,22 +443,29 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             const int lanes = CTAS == 1 && !A_COLS && g.m == 64 ? 16 : 32;
             const int64_t row0 = static_cast<int64_t>(c.m) * ROWS + rank * 128 + quad * lanes, row = row0 + lane;
             const bool there = lane < lanes && row < g.M;
-            const uint32_t acc = tmem + buf * g.bn + (static_cast<uint32_t>(quad * 32) << 16);
+            const uint32_t acc = tmem_slot + buf * g.bn + (static_cast<uint32_t>(quad * 32) << 16);
             constexpr bool GATED = KIND == kGatedFwd;
             const int width = GATED ? g.bn >> 1 : g.bn;
             if (row0 < g.M) {
-                for (int j = part * 16; j < width; j += 32) {
+                // W columns at a time. Single CTAs write them from the registers, 16 bytes a lane. A pair's, whose
+                // output is a large part of the traffic, go through shared memory (rows of 64 bytes, swizzled) and leave
+                // by tensor copies, in whole sectors: 8192 x 4096 x 16384 with z kept 591 us from registers.
+                constexpr int W = CTAS == 2 ? 32 : 16;
+                for (int j = part * W; j < width; j += 2 * W) {
                     const int col = c.n * width + j;
                     if (col >= g.N) break;
-                    float v[16], u[16];
-                    tmem_ld16(acc + j, v);
-                    if constexpr (GATED) tmem_ld16(acc + width + j, u);
+                    float v[W], u[GATED ? W : 1];
+#pragma unroll
+                    for (int i = 0; i < W; i += 16) {
+                        tmem_ld16(acc + j + i, reinterpret_cast<float(&)[16]>(v[i]));
+                        if constexpr (GATED) tmem_ld16(acc + width + j + i, reinterpret_cast<float(&)[16]>(u[i]));
+                    }
                     tmem_wait_ld();
-                    const int groups = min(2, (g.N - col) >> 3);
+                    const int groups = min(W / 8, (g.N - col) >> 3);
                     if constexpr (KIND == kForward) {
                         if (g.bias != nullptr) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < W / 4; ++i) {
                                 if (i < 2 * groups) {
                                     const float4 b = __ldg(reinterpret_cast<const float4*>(g.bias + col) + i);
                                     v[4 * i] = fadd(v[4 * i], b.x);
@@ -427,29 +476,47 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                             }
                         }
                     }
-                    auto put = [&](const MatOut& o, const float (&x)[16]) {
-                        uint4* p = reinterpret_cast<uint4*>(o.p + row * o.ld + col);
-                        if (there) {
-                            p[0] = pack_act<F16>(reinterpret_cast<const float(&)[8]>(x[0]));
-                            if (groups > 1) p[1] = pack_act<F16>(reinterpret_cast<const float(&)[8]>(x[8]));
+                    auto put = [&](const MatOut& o, const CUtensorMap* map, const float* x) {
+                        if constexpr (CTAS == 2) {
+                            // The two pieces in turn: the one before the last has been read.
+                            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                            __syncwarp();
+                            const uint32_t to = staged + piece * kTileBytes;
+                            piece ^= 1u;
+#pragma unroll
+                            for (int i = 0; i < W / 8; ++i)
+                                st_shared_v4(to + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), pack_act<F16>(reinterpret_cast<const float(&)[8]>(x[8 * i])));
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tile_s2g(map, col, static_cast<int>(row0), to);
+                                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                            }
+                        } else if (there) {
+                            uint4* p = reinterpret_cast<uint4*>(o.p + row * o.ld + col);
+#pragma unroll
+                            for (int i = 0; i < W / 8; ++i)
+                                if (i < groups) p[i] = pack_act<F16>(reinterpret_cast<const float(&)[8]>(x[8 * i]));
                         }
                     };
                     if constexpr (KIND == kForward || GATED) {
-                        if (g.z[0].p != nullptr) put(g.z[0], v);
-                        if (GATED && g.z[1].p != nullptr) put(g.z[1], u);
+                        if (g.z[0].p != nullptr) put(g.z[0], &g.z_map[0], v);
+                        if constexpr (GATED) {
+                            if (g.z[1].p != nullptr) put(g.z[1], &g.z_map[1], u);
+                        }
                         with_act(g.act, [&](auto act) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] = act_value<decltype(act)::value>(v[i]);
+                            for (int i = 0; i < W; ++i) v[i] = act_value<decltype(act)::value>(v[i]);
                         });
                         if constexpr (GATED) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] = fmul(v[i], u[i]);
+                            for (int i = 0; i < W; ++i) v[i] = fmul(v[i], u[i]);
                         }
                         if constexpr (KIND == kForward) {
                             if (g.res.p != nullptr && there) {
                                 const uint4* p = reinterpret_cast<const uint4*>(g.res.p + row * g.res.ld + col);
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
+                                for (int h = 0; h < W / 8; ++h) {
                                     if (h < groups) {
                                         float r[8];
                                         unpack_act<F16>(p[h], r);
@@ -459,17 +526,18 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                                 }
                             }
                         }
-                        put(g.out[0], v);
+                        put(g.out[0], &g.out_map[0], v);
                     } else if (KIND == kGradW && g.splits > 1) {
                         if (there) {
                             float4* p = reinterpret_cast<float4*>(
                                 g.partials + ((static_cast<int64_t>(c.which) * g.splits + c.split) * g.M + row) * g.N + col);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
+                            for (int i = 0; i < W / 4; ++i)
                                 if (i < 2 * groups) p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                         }
                     } else {
-                        put(g.out[KIND == kGradW ? c.which : 0], v);
+                        const int which = KIND == kGradW ? c.which : 0;
+                        put(g.out[which], &g.out_map[which], v);
                     }
                 }
             }
@@ -480,13 +548,15 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                 else mbar_arrive(&acc_empty[buf]);
             }
         }
+        if (CTAS == 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     pdl_release();
     tmem_fence_before();
     __syncthreads();
     if constexpr (CTAS == 2) cluster_sync_all();
     tmem_fence_after();
-    if (warp == 2) tmem_free<CTAS>(tmem, g.tmem_cols);
+    if (warp == 2) tmem_free<CTAS>(tmem_slot, g.tmem_cols);
 }
 
 // ---------------------------------------------------------------------------
@@ -522,15 +592,17 @@ cudaError_t product_run(const Product& p, int bn, cudaStream_t st) {
     // Blocks a stage: each stage costs the multiplying thread a wait, a fence and a commit, some
     // 280 cycles beside 25 to 40 a product; four stages at least.
     g.whole = p.K % kBlockK == 0;
-    g.deep = few && !B_COLS ? std::max(1, std::min<int>(kMostDeep, static_cast<int>(kStageBytes / 4 / (g.a_block + g.b_block)))) : 1;
+    g.deep = CTAS == 1 ? std::max(1, std::min<int>(kMostDeep, static_cast<int>(kStageBytes / 4 / (g.a_block + g.b_block)))) : 1;
     g.copy_deep = g.whole ? g.deep : 1;
     g.a_bytes = g.a_block * g.deep;
     g.stage_bytes = (g.a_block + g.b_block) * g.deep;
     // What the rows of the last stage's last block reach past the ring.
     const uint32_t reach = (g.deep - 1) * g.a_block + static_cast<uint32_t>(g.m) * 128u;
     const uint32_t behind = std::max(reach, g.stage_bytes) - g.stage_bytes;
-    g.stages = std::min<int>(kMaxStages, static_cast<int>((kStageBytes - behind) / g.stage_bytes));
-    const size_t smem = static_cast<size_t>(g.stages) * g.stage_bytes + behind + 1024;
+    const uint32_t staging = CTAS == 2 ? kEpilogueWarps * 2 * kTileBytes : 0;
+    g.stages = std::min<int>(kMaxStages, static_cast<int>((kStageBytes - behind - staging) / g.stage_bytes));
+    g.staging = static_cast<uint32_t>(g.stages) * g.stage_bytes;
+    const size_t smem = static_cast<size_t>(g.staging) + behind + staging + 1024;
     g.tmem_cols = 32;
     while (g.tmem_cols < 2 * bn) g.tmem_cols *= 2;
     // fp32 sums; both operands' format; which of them lie along their columns; N / 8; M / 16.
@@ -540,9 +612,9 @@ cudaError_t product_run(const Product& p, int bn, cudaStream_t st) {
         g.out[i] = p.out[i];
         g.z[i] = p.z[i];
         const MatIn &a = p.a[i].p != nullptr ? p.a[i] : p.a[0], &b = p.b[i].p != nullptr ? p.b[i] : p.b[0];
-        // Operands along their columns, a pair's and those of kGradX: in two dimensions; the others in three.
+        // Operands along their columns and a pair's: in two dimensions; the others in three.
         auto rows_map = [&](CUtensorMap* map, const MatIn& o, int64_t n, int box, int deep) {
-            if (CTAS == 2 || B_COLS) return encode_blocks_2d(map, o.p, n, p.K, o.ld, box);
+            if (CTAS == 2) return encode_blocks_2d(map, o.p, n, p.K, o.ld, box);
             return encode_blocks_3d(map, o.p, n, p.K, o.ld, box, g.whole ? deep : 0);
         };
         cudaError_t e = cudaSuccess;
@@ -554,6 +626,11 @@ cudaError_t product_run(const Product& p, int bn, cudaStream_t st) {
         else if (KIND == kGatedFwd) e = rows_map(&g.b[i], b, p.N, bn / 2, 1);
         else e = rows_map(&g.b[i], b, p.N, bn / CTAS, g.deep);
         if (e != cudaSuccess) return e;
+        if (CTAS == 2) {
+            if (p.out[i].p != nullptr && p.splits == 1) e = encode_pieces_2d(&g.out_map[i], p.out[i].p, p.M, p.N, p.out[i].ld);
+            if (e == cudaSuccess && p.z[i].p != nullptr) e = encode_pieces_2d(&g.z_map[i], p.z[i].p, p.M, p.N, p.z[i].ld);
+            if (e != cudaSuccess) return e;
+        }
     }
     g.res = p.res;
     g.bias = p.bias;
@@ -581,7 +658,7 @@ cudaError_t product_shape(const Product& p, cudaStream_t st) {
     const int64_t cols = KIND == kGatedFwd ? 2 * p.N : p.N, outs = KIND == kGradW && p.a[1].p != nullptr ? 2 : 1;
     const int64_t big = (p.M + 255) / 256 * ((cols + 255) / 256) * outs * p.splits;
     if (big >= kSms / 4 && p.M > 128) return product_run<KIND, 2, F16>(p, 256, st);
-    constexpr int unit = KIND == kGradX || KIND == kGradW ? 64 : 32;
+    constexpr int unit = KIND == kGradX || KIND == kGradW ? 64 : KIND == kGatedFwd ? 32 : 16;
     const int64_t rows = (p.M + 127) / 128 * outs * p.splits;
     const int64_t per_row = std::max<int64_t>(1, kSms / rows);          // column tiles for one wave
     int64_t bn = (cols + per_row - 1) / per_row;                        // one wave

@@ -48,12 +48,12 @@ cudaError_t encode_rows_2d(CUtensorMap* map, const void* base, int64_t T, int D,
 
 namespace {
 cudaError_t encode_blocks(CUtensorMap* map, const void* base, cuuint32_t rank, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
-                          const cuuint32_t (&box)[3]) {
+                          const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     auto fn = encode_fn();
     if (fn == nullptr) return cudaErrorNotSupported;
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -62,6 +62,11 @@ cudaError_t encode_blocks(CUtensorMap* map, const void* base, cuuint32_t rank, c
 cudaError_t encode_blocks_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld_elems, int box_rows) {
     return encode_blocks(map, base, 2, {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), 1},
                          {static_cast<cuuint64_t>(ld_elems) * 2u, 0}, {64u, static_cast<cuuint32_t>(box_rows), 1u});
+}
+
+cudaError_t encode_pieces_2d(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld_elems) {
+    return encode_blocks(map, base, 2, {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), 1},
+                         {static_cast<cuuint64_t>(ld_elems) * 2u, 0}, {32u, 32u, 1u}, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 cudaError_t encode_blocks_3d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld_elems, int box_rows, int deep) {
