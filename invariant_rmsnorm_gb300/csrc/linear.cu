@@ -156,12 +156,22 @@ int check_in_place(const void* res, int64_t ldr, const void* y, int64_t ldy, int
 constexpr size_t kAlign = 256;
 size_t padded(size_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 
-// Ranges of rows that a weight gradient is split into, where its tiles of 256 x 256 leave
-// most pairs of SMs (76 on a GPU of 152) without one: as many as fill them, of 512 rows at
-// least. A function of the sizes alone.
+// Ranges of rows that a weight gradient is split into, where its tiles leave SMs without one:
+// the power of two, of 512 rows at least a range, with the fewest cycles by the tiles' model, in which the join
+// costs a launch (5000) and the partial sums' way to L2 and back (3000 bytes a cycle). A function of the sizes alone.
 int weight_splits(int64_t T, int64_t N, int64_t K, int outputs) {
-    const int64_t tiles = (N + 255) / 256 * ((K + 255) / 256) * outputs;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(76 / tiles, T / 512)));
+    const int64_t blocks = (T + 63) / 64;
+    int best = 1;
+    int64_t least = linear_tiling(kGradW, N, K, blocks, outputs).cycles;
+    for (int s = 2; s <= 64 && T / s >= 512; s *= 2) {
+        const int64_t cycles = linear_tiling(kGradW, N, K, (blocks + s - 1) / s, static_cast<int64_t>(outputs) * s).cycles +
+                               5000 + 8 * s * outputs * N * K / 3000;
+        if (cycles < least) {
+            least = cycles;
+            best = s;
+        }
+    }
+    return best;
 }
 
 size_t split_bytes(int64_t T, int64_t N, int64_t K, int outputs) {

@@ -33,13 +33,23 @@ namespace rmsn {
 namespace {
 
 constexpr int kBlockK = 64;            // reduced values a block: one swizzled row of 128 bytes
-constexpr int kMostDeep = 8;           // blocks a stage
 constexpr int kProductThreads = 384;   // warps 0, 2 and 3 copy, 1 multiplies, 2 holds tensor memory, 4 .. 11 epilogue
 constexpr int kCopyWarps = 3;          // 0, 2 and 3
 constexpr int kEpilogueWarps = 8;
 constexpr int kMaxStages = 32;
-constexpr uint32_t kStageBytes = 227 * 1024 - 2048;  // of shared memory for the stages
 constexpr uint32_t kTileBytes = 32 * 64;             // pairs of CTAs: a warp's piece of the output on its way
+
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery): a division costs 150 cycles, and a tile's
+// first copy waits for three of them.
+struct Divisor {
+    uint32_t mul, shift;
+    __device__ __forceinline__ uint32_t of(uint32_t n) const { return (__umulhi(mul, n) + n) >> shift; }
+};
+inline Divisor divisor(uint32_t d) {
+    uint32_t s = 0;
+    while ((uint64_t(1) << s) < d) ++s;
+    return {static_cast<uint32_t>((uint64_t(1) << 32) * ((uint64_t(1) << s) - d) / d + 1), s};
+}
 
 struct ProductArgs {
     CUtensorMap a[2], b[2];
@@ -53,6 +63,7 @@ struct ProductArgs {
     int act;
     int tiles_m, tiles_n;     // of one output
     int tiles;                // with the outputs and splits
+    Divisor per_output, per_split, per_band, per_last;  // tiles of an output and split, splits, tiles of 8 rows, rows of the last band
     int blocks;               // blocks of the reduced axis
     int segments;             // products that are added (kGradX: 1 or 2)
     int splits;
@@ -179,8 +190,10 @@ __device__ __forceinline__ void tile3_g2s(uint32_t dst, const CUtensorMap* map, 
                 "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
+// Arrive on a barrier of the pair's first CTA. Relaxed: it orders no memory but tensor memory, whose reads are
+// complete and fenced; a release at cluster scope waits for the output's copies (8192 x 256 x 4096: 30.4 us for 18.7).
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // True in one lane of a converged warp. (The loops around tensor instructions are
@@ -204,31 +217,27 @@ struct Tile { int m, n, which, split; };
 // The blocks of the reduced axis that a split has.
 __device__ __forceinline__ int2 blocks_of(const ProductArgs& g, int split) {
     if (g.splits == 1) return make_int2(0, g.blocks);
-    const unsigned b = g.blocks, s = g.splits;  // at most 2^25 blocks and 76 splits
-    return make_int2(static_cast<int>(b * split / s), static_cast<int>(b * (split + 1) / s));
+    const uint32_t b = g.blocks;  // at most 2^25 blocks and 64 splits: the product fits 32 bits
+    return make_int2(static_cast<int>(g.per_split.of(b * split)), static_cast<int>(g.per_split.of(b * (split + 1))));
 }
 
 // Output and split outermost; then bands of 8 rows of tiles, whose operands stay in
 // L2 while the band's columns are walked.
 __device__ __forceinline__ Tile tile_of(const ProductArgs& g, int t) {
     Tile o{0, 0, 0, 0};
-    const unsigned each = g.tiles_m * g.tiles_n;
-    unsigned u = t;
+    const uint32_t each = g.tiles_m * g.tiles_n;
+    uint32_t u = t;
     if (u >= each) {
-        const unsigned s = u / each;
+        const uint32_t s = g.per_output.of(u);
         u -= s * each;
-        o.which = s / g.splits;
+        o.which = g.per_split.of(s);
         o.split = s - o.which * g.splits;
     }
-    unsigned first = 0, rows = g.tiles_m;
-    if (rows > 8) {
-        const unsigned band = 8 * g.tiles_n, b = u / band;
-        u -= b * band;
-        first = 8 * b;
-        rows = min(8u, rows - first);
-    }
-    o.n = rows == 1 ? u : u / rows;
-    o.m = first + u - o.n * rows;
+    const uint32_t b = g.tiles_m > 8 ? g.per_band.of(u) : 0u;
+    u -= b * 8 * g.tiles_n;
+    const uint32_t rows = min(8u, g.tiles_m - 8 * b);
+    o.n = rows == 8 ? u >> 3 : g.per_last.of(u);
+    o.m = 8 * b + u - o.n * rows;
     return o;
 }
 
@@ -239,7 +248,6 @@ template <int KIND, int CTAS, bool F16>
 __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ ProductArgs g) {
     constexpr bool A_COLS = KIND == kGradW, B_COLS = KIND == kGradX || KIND == kGradW;  // rows across the reduced axis
     constexpr int ROWS = 128 * CTAS;  // of a tile
-    constexpr bool DEEP = CTAS == 1;  // several blocks a stage
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
@@ -290,7 +298,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             bool ok = true;
             const uint32_t all_bytes = g.stage_bytes * CTAS;
             const uint32_t one = elect_one();
-            const int deep = DEEP ? g.deep : 1;
+            const int deep = g.deep;
             for (int t = first_tile; ok && t < g.tiles; t += tile_step) {
                 const Tile c = tile_of(g, t);
                 const int2 range = blocks_of(g, c.split);
@@ -321,7 +329,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                             const int half = g.bn >> 1, mine = g.bn / CTAS, col = c.n * g.bn + rank * mine;
                             // One block (single CTAs: or, along a third axis, all of a stage's) of rows.
                             auto rows_of = [&](uint32_t to, const CUtensorMap* map, int r, int j) {
-                                if constexpr (CTAS == 2) tile_g2s<CTAS>(to, map, k * kBlockK, r, bar);
+                                if constexpr (CTAS == 2) tile_g2s<CTAS>(to, map, (k + j) * kBlockK, r, bar);
                                 else tile3_g2s(to, map, g.whole ? 0 : (k + j) * kBlockK, r, g.whole ? k + j : 0, bar);
                             };
                             auto cols_of = [&](uint32_t to, const CUtensorMap* map, int first, int n, int j) {
@@ -371,12 +379,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
     } else if (warp == 1) {
         if (rank == 0) {
             const uint32_t one = elect_one();
-            const int deep = DEEP ? g.deep : 1;
+            const int deep = g.deep;
             int s = 0, n = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int t = first_tile; ok && t < g.tiles; t += tile_step, ++n) {
-                const int2 range = blocks_of(g, g.splits == 1 ? 0 : t / (g.tiles_m * g.tiles_n) % g.splits);
+                const int2 range = blocks_of(g, g.splits == 1 ? 0 : tile_of(g, t).split);
                 const int blocks = range.y - range.x, buf = n & 1;
                 if (!wait_on<CTAS>(&acc_empty[buf], ((n >> 1) & 1) ^ 1u)) {
                     ok = false;
@@ -402,8 +410,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                         constexpr uint32_t step_a = (A_COLS ? 2048 : 32) >> 4, step_b = (B_COLS ? 2048 : 32) >> 4;
                         if (one) {
 #pragma unroll
-                            for (int j = 0; j < (DEEP ? kMostDeep : 1); ++j) {
-                                if (DEEP && j >= min(deep, blocks - k)) break;
+                            for (int j = 0; j < (CTAS == 2 ? kMostDeepPair : kMostDeep); ++j) {
+                                if (j >= min(deep, blocks - k)) break;
 #pragma unroll
                                 for (int i = 0; i < kBlockK / 16; ++i)
                                     mma16<CTAS>(d, da + j * (g.a_block >> 4) + i * step_a, db + j * (g.b_block >> 4) + i * step_b, g.idesc,
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             __syncwarp();
             if (lane == 0) {
                 if constexpr (CTAS == 2) cluster_arrive(cluster_map(&acc_empty[buf], 0));
-                else mbar_arrive(&acc_empty[buf]);
+                else asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&acc_empty[buf])) : "memory");
             }
         }
         if (CTAS == 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -580,6 +588,10 @@ cudaError_t product_run(const Product& p, int bn, cudaStream_t st) {
     g.tiles_n = static_cast<int>(tiles_n);
     g.tiles = static_cast<int>(tiles);
     g.blocks = static_cast<int>(blocks);
+    g.per_output = divisor(static_cast<uint32_t>(tiles_m * tiles_n));
+    g.per_split = divisor(static_cast<uint32_t>(p.splits));
+    g.per_band = divisor(static_cast<uint32_t>(8 * tiles_n));
+    g.per_last = divisor(static_cast<uint32_t>(tiles_m % 8 ? tiles_m % 8 : 8));
     g.bn = bn;
     // Few rows: only those are copied. The products read 64 or 128 rows from the block's start
     // all the same, into what lies behind them in the ring; a row of C depends on its own
@@ -592,8 +604,8 @@ cudaError_t product_run(const Product& p, int bn, cudaStream_t st) {
     // Blocks a stage: each stage costs the multiplying thread a wait, a fence and a commit, some
     // 280 cycles beside 25 to 40 a product; four stages at least.
     g.whole = p.K % kBlockK == 0;
-    g.deep = CTAS == 1 ? std::max(1, std::min<int>(kMostDeep, static_cast<int>(kStageBytes / 4 / (g.a_block + g.b_block)))) : 1;
-    g.copy_deep = g.whole ? g.deep : 1;
+    g.deep = std::max(1, std::min<int>(CTAS == 2 ? kMostDeepPair : kMostDeep, static_cast<int>(kStageBytes / 4 / (g.a_block + g.b_block))));
+    g.copy_deep = CTAS == 1 && g.whole ? g.deep : 1;
     g.a_bytes = g.a_block * g.deep;
     g.stage_bytes = (g.a_block + g.b_block) * g.deep;
     // What the rows of the last stage's last block reach past the ring.
@@ -649,22 +661,11 @@ cudaError_t product_run(const Product& p, int bn, cudaStream_t st) {
     return launch_kernel_clustered(kern, static_cast<unsigned>(CTAS), static_cast<unsigned>(grid), kProductThreads, smem, st, g);
 }
 
-// The tile. Pairs of CTAs (256 x 256) where they have tiles enough for half the GPU;
-// else single ones, 128 rows by as many columns as give every SM about one
-// tile of the narrowest count (a multiple of 16, or of 64 where B lies along its columns).
 template <int KIND, bool F16>
 cudaError_t product_shape(const Product& p, cudaStream_t st) {
-    constexpr int64_t kSms = 152;
-    const int64_t cols = KIND == kGatedFwd ? 2 * p.N : p.N, outs = KIND == kGradW && p.a[1].p != nullptr ? 2 : 1;
-    const int64_t big = (p.M + 255) / 256 * ((cols + 255) / 256) * outs * p.splits;
-    if (big >= kSms / 4 && p.M > 128) return product_run<KIND, 2, F16>(p, 256, st);
-    constexpr int unit = KIND == kGradX || KIND == kGradW ? 64 : KIND == kGatedFwd ? 32 : 16;
-    const int64_t rows = (p.M + 127) / 128 * outs * p.splits;
-    const int64_t per_row = std::max<int64_t>(1, kSms / rows);          // column tiles for one wave
-    int64_t bn = (cols + per_row - 1) / per_row;                        // one wave
-    for (int waves = 2; bn > 256; ++waves) bn = (cols + waves * per_row - 1) / (waves * per_row);
-    bn = std::min<int64_t>(256, (bn + unit - 1) / unit * unit);
-    return product_run<KIND, 1, F16>(p, static_cast<int>(bn), st);
+    const int64_t outputs = KIND == kGradW && p.a[1].p != nullptr ? 2 : 1, blocks = (p.K + kBlockK - 1) / kBlockK;
+    const Tiling t = linear_tiling(static_cast<ProductKind>(KIND), p.M, p.N, (blocks + p.splits - 1) / p.splits, outputs * p.splits);
+    return t.ctas == 2 ? product_run<KIND, 2, F16>(p, t.bn, st) : product_run<KIND, 1, F16>(p, t.bn, st);
 }
 
 }  // namespace

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "linear.h"
 
 namespace rmsn {
@@ -36,6 +38,42 @@ struct Product {
     int splits;
     int act;
 };
+
+// A product's tile: CTAs (two: a pair, 256 rows; one: 128 rows), columns of accumulators, and the model's cycles.
+struct Tiling { int ctas, bn; int64_t cycles; };
+
+constexpr int kMostDeep = 8, kMostDeepPair = 2;      // blocks of 64 reduced values a stage
+constexpr uint32_t kStageBytes = 227 * 1024 - 2048;  // of shared memory for the stages
+
+// The tile by a model of a GPU of 152 SMs, in cycles. Tiles go round it in waves, of 76 pairs or
+// 152 single CTAs. A block of a tile takes a pair of 256 x 256 512 (its products) and of 256 x 128 340
+// (390 with both operands along their columns); a single CTA its products, 2 a column, or 100 and 310 a stage of the issuing
+// thread; a tile at least its epilogue, 12 a column. Single CTAs have as many columns as give every SM one
+// tile or, past 256, two and more (a multiple of 16; of 32 with two matrices' columns, of 64 where B lies along them).
+// 512 x 4096 x 4096: pairs of 256 x 128 14.4 us, single CTAs of 128 columns 18.1; 1024 x 4096 x 4096: 21.0 and,
+// with 256 x 256, 23.0; 64 x 4096 x 6144: CTAs of 48 columns 12.3, of 64 13.1.
+inline Tiling linear_tiling(ProductKind kind, int64_t M, int64_t N, int64_t blocks, int64_t outputs) {
+    constexpr int64_t kSms = 152;
+    const int64_t unit = kind == kGradX || kind == kGradW ? 64 : kind == kGatedFwd ? 32 : 16;
+    const int64_t cols = kind == kGatedFwd ? 2 * N : N;
+    auto cycles = [&](int64_t tiles, int64_t at_once, int64_t block, int64_t bn) {
+        return (tiles + at_once - 1) / at_once * std::max(blocks * block, 12 * bn) + 12 * bn;
+    };
+    const int64_t rows = (M + 127) / 128 * outputs, per_row = std::max<int64_t>(1, kSms / rows);
+    int64_t bn = (cols + per_row - 1) / per_row;
+    for (int64_t waves = 2; bn > 256; ++waves) bn = (cols + waves * per_row - 1) / (waves * per_row);
+    bn = std::min<int64_t>(256, (bn + unit - 1) / unit * unit);
+    const int64_t deep = std::max<int64_t>(1, std::min<int64_t>(kMostDeep, kStageBytes / 4 / (16384 + bn * 128)));
+    Tiling best{1, static_cast<int>(bn), cycles(rows * ((cols + bn - 1) / bn), kSms, std::max<int64_t>(2 * bn, 100 + 310 / deep), bn)};
+    if (M > 128) {
+        const int64_t pair_rows = (M + 255) / 256 * outputs;
+        const Tiling narrow{2, 128, cycles(pair_rows * ((cols + 127) / 128), kSms / 2, kind == kGradW ? 390 : 340, 128)};
+        const Tiling wide{2, 256, cycles(pair_rows * ((cols + 255) / 256), kSms / 2, 512, 256)};
+        if (narrow.cycles <= best.cycles) best = narrow;
+        if (wide.cycles <= best.cycles) best = wide;
+    }
+    return best;
+}
 
 cudaError_t launch_linear_fwd(ProductKind kind, const Product& p, cudaStream_t s);
 cudaError_t launch_linear_fwd_f16(ProductKind kind, const Product& p, cudaStream_t s);
