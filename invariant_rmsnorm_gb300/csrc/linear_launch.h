@@ -46,12 +46,13 @@ constexpr int kMostDeep = 8, kMostDeepPair = 2;      // blocks of 64 reduced val
 constexpr uint32_t kStageBytes = 227 * 1024 - 2048;  // of shared memory for the stages
 
 // The tile by a model of a GPU of 152 SMs, in cycles. Tiles go round it in waves, of 76 pairs or
-// 152 single CTAs. A block of a tile takes a pair of 256 x 256 512 (its products) and of 256 x 128 340
-// (390 with both operands along their columns); a single CTA its products, 2 a column, or 100 and 310 a stage of the issuing
-// thread; a tile at least its epilogue, 12 a column. Single CTAs have as many columns as give every SM one
-// tile or, past 256, two and more (a multiple of 16; of 32 with two matrices' columns, of 64 where B lies along them).
-// 512 x 4096 x 4096: pairs of 256 x 128 14.4 us, single CTAs of 128 columns 18.1; 1024 x 4096 x 4096: 21.0 and,
-// with 256 x 256, 23.0; 64 x 4096 x 6144: CTAs of 48 columns 12.3, of 64 13.1.
+// 152 single CTAs. A block of a tile takes a pair of 256 x 256 512 (its products) and of 256 x 128 270
+// (290 with both operands along their columns) in a single wave, 340 (390) in more: its operands are three quarters
+// of the larger tile's for half the products (8192 x 4096 x 16384: 796 us for 666); a single CTA its products, 2 a column, or its operands at 80
+// bytes a cycle, or 140 and 310 a stage of the issuing thread; a tile at least its epilogue, 12 a column; a launch of pairs 900 more. Single CTAs have as many columns
+// as give every SM one tile or, past 256, two and more (a multiple of 16; of 32 with two matrices' columns, of 64
+// where B lies along them). 512 x 4096 x 4096: pairs of 256 x 128 13.6 us, single CTAs of 128 columns 18.1;
+// 1024 x 4096 x 4096: 20.8 and, with 256 x 256, 23.0; 64 x 4096 x 6144: CTAs of 48 columns 12.3, of 64 13.1.
 inline Tiling linear_tiling(ProductKind kind, int64_t M, int64_t N, int64_t blocks, int64_t outputs) {
     constexpr int64_t kSms = 152;
     const int64_t unit = kind == kGradX || kind == kGradW ? 64 : kind == kGatedFwd ? 32 : 16;
@@ -64,11 +65,13 @@ inline Tiling linear_tiling(ProductKind kind, int64_t M, int64_t N, int64_t bloc
     for (int64_t waves = 2; bn > 256; ++waves) bn = (cols + waves * per_row - 1) / (waves * per_row);
     bn = std::min<int64_t>(256, (bn + unit - 1) / unit * unit);
     const int64_t deep = std::max<int64_t>(1, std::min<int64_t>(kMostDeep, kStageBytes / 4 / (16384 + bn * 128)));
-    Tiling best{1, static_cast<int>(bn), cycles(rows * ((cols + bn - 1) / bn), kSms, std::max<int64_t>(2 * bn, 100 + 310 / deep), bn)};
+    Tiling best{1, static_cast<int>(bn), cycles(rows * ((cols + bn - 1) / bn), kSms, std::max<int64_t>({2 * bn, (16384 + bn * 128) / 80, 140 + 310 / deep}), bn)};
     if (M > 128) {
         const int64_t pair_rows = (M + 255) / 256 * outputs;
-        const Tiling narrow{2, 128, cycles(pair_rows * ((cols + 127) / 128), kSms / 2, kind == kGradW ? 390 : 340, 128)};
-        const Tiling wide{2, 256, cycles(pair_rows * ((cols + 255) / 256), kSms / 2, 512, 256)};
+        const int64_t narrow_tiles = pair_rows * ((cols + 127) / 128);
+        const int64_t narrow_block = narrow_tiles <= kSms / 2 ? (kind == kGradW ? 290 : 270) : (kind == kGradW ? 390 : 340);
+        const Tiling narrow{2, 128, cycles(narrow_tiles, kSms / 2, narrow_block, 128) + 900};
+        const Tiling wide{2, 256, cycles(pair_rows * ((cols + 255) / 256), kSms / 2, 512, 256) + 900};
         if (narrow.cycles <= best.cycles) best = narrow;
         if (wide.cycles <= best.cycles) best = wide;
     }
