@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
     pdl_wait();
 
     if (warp == 0 || warp == 2 || warp == 3) {
-        {
+        {  // copies
             // The stages in turn: a copy costs its warp 150 to 200 cycles, as much as a small tile's products of a block.
             const int mine_of = warp == 0 ? 0 : warp - 1;
             int turn = 0;
@@ -327,13 +327,15 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                             const uint32_t at = ring + now * g.stage_bytes, bt = at + g.a_bytes;
                             // Columns of the accumulators: kGatedFwd has half of them of gate, half of up.
                             const int half = g.bn >> 1, mine = g.bn / CTAS, col = c.n * g.bn + rank * mine;
-                            // One block (single CTAs: or, along a third axis, all of a stage's) of rows.
+                            // One block (single CTAs: or, along a third axis, all of a stage's) of rows. Blocks past the
+                            // last are zeros, or another split's, and not multiplied.
+                            auto at_block = [&](int j) { return static_cast<int>(static_cast<uint32_t>(k + j) * kBlockK); };
                             auto rows_of = [&](uint32_t to, const CUtensorMap* map, int r, int j) {
-                                if constexpr (CTAS == 2) tile_g2s<CTAS>(to, map, (k + j) * kBlockK, r, bar);
-                                else tile3_g2s(to, map, g.whole ? 0 : (k + j) * kBlockK, r, g.whole ? k + j : 0, bar);
+                                if constexpr (CTAS == 2) tile_g2s<CTAS>(to, map, at_block(j), r, bar);
+                                else tile3_g2s(to, map, g.whole ? 0 : at_block(j), r, g.whole ? k + j : 0, bar);
                             };
                             auto cols_of = [&](uint32_t to, const CUtensorMap* map, int first, int n, int j) {
-                                for (int i = 0; i < n; i += 64) tile_g2s<CTAS>(to + i * 128, map, first + i, (k + j) * kBlockK, bar);
+                                for (int i = 0; i < n; i += 64) tile_g2s<CTAS>(to + i * 128, map, first + i, at_block(j), bar);
                             };
                             if constexpr (A_COLS) {
                                 for (int j = 0; j < deep; ++j) cols_of(at + j * g.a_block, ma, row, 128, j);

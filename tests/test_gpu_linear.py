@@ -126,6 +126,15 @@ def test_pairs_of_ctas_and_split_weight_gradients(T, K, N):
     test_gated_bwd(T, K, N, F16, "silu", 8)
 
 
+@pytest.mark.parametrize("T,K,N", [(4864, 1000, 1024), (4864, 1024, 1000), (600, 1024, 4864), (4864, 1024, 520), (4860, 200, 512)])
+def test_the_largest_tiles(T, K, N):
+    """Sizes whose outputs are whole waves of 256 x 256 tiles: forward, input gradient, weight gradient, and gated."""
+    test_linear_fwd(T, K, N, F16, "silu", True, True, True, 8)
+    test_linear_bwd(T, K, N, F16, "none", True, 8)
+    test_gated_fwd(T, K, N, BF16, "gelu", True, 8)
+    test_gated_bwd(T, K, N, BF16, "silu", 8)
+
+
 # --------------------------------------------------------------------------
 # activations over their whole range
 # --------------------------------------------------------------------------
@@ -194,7 +203,7 @@ def test_rows_do_not_depend_on_the_batch(K, N, dtype):
         return y, z, h, p, q, dx, dh
 
     whole = step(slice(0, T))
-    for n in (1, 5, 16, 17, 63, 64, 65, 100, 120, 121, 128, 129, 200, 300, 500, 1000, 2000, 3000):
+    for n in (1, 5, 16, 17, 63, 64, 65, 100, 120, 121, 128, 129, 200, 257, 300, 500, 800, 1000, 1300, 2000, 2560, 3000, 3900):
         for first in (0, 1234 if n < 2000 else 7, T - n):
             for a, b_ in zip(step(slice(first, first + n)), whole):
                 assert torch.equal(_bits(a), _bits(b_[first:first + n])), (n, first)
