@@ -6,9 +6,9 @@
 // one chain of tensor-core sums over the reduced axis in ascending order, 16 at a
 // time, whatever the tile's size, so a row's bits do not depend on M.
 //
-// A tile of C belongs to a CTA (CTAS = 1: 128 rows, `bn` columns) or to a pair of CTAs
-// (CTAS = 2: 256 x 256; each CTA holds 128 rows of A and half of the columns of B,
-// and one instruction multiplies both halves). A warp copies blocks of 64
+// A tile of C belongs to a CTA (CTAS = 1: 64 or 128 rows, `bn` columns) or to a pair of CTAs
+// (CTAS = 2: 256 rows, 128 or 256 columns; each CTA holds 128 rows of A and half of the columns of B,
+// and one instruction multiplies both halves); linear_tiling chooses. Three warps copy blocks of 64
 // reduced values of A and B by tensor copies into a ring of stages in shared memory, a
 // thread issues their products, which accumulate in tensor memory, and eight warps
 // take finished accumulators through the epilogue while the next tile's products run into
@@ -19,7 +19,13 @@
 // columns: [64 reduced values][128 bytes]. Both are 128-byte swizzled, and zeros are
 // filled in beyond the matrix, in both operands alike.
 //
-// Bounded by the tensor cores where M is large, by the reads of B where it is small.
+// What bounds it. Many rows: the tensor cores, busy 94 to 96 % of a kernel's time (8192 x 4096 x
+// 8192: 280 us, 1960 TFLOP/s; back to back for seconds the board's power holds 8192 x 4096 x 16384 at 636 us
+// forward, 670 and 666 the gradients, where the library's product takes 622, 655 and 656). Few rows: the issuing
+// thread. A product of 16 reduced values reads (rows + columns) x 32 bytes of shared memory, 24 cycles at 64 x 32, 48 at
+// 128 x 64; a stage costs the thread 240 more for its wait, descriptors and reconvergence and 75 to 166 for its
+// commit. One token of 4096 x 4096: 9.4 us in a graph (5 the reads at the copy rate), 4.3 of them products.
+// Between: the operands' way from L2, about 80 bytes a cycle and SM.
 #pragma once
 
 #include <algorithm>
@@ -34,7 +40,7 @@ namespace {
 
 constexpr int kBlockK = 64;            // reduced values a block: one swizzled row of 128 bytes
 constexpr int kProductThreads = 384;   // warps 0, 2 and 3 copy, 1 multiplies, 2 holds tensor memory, 4 .. 11 epilogue
-constexpr int kCopyWarps = 3;          // 0, 2 and 3
+constexpr int kCopyWarps = 3;          // of a single one's 512 x 4096 x 4096 input gradient 24.9 us, 18.6 of two or three
 constexpr int kEpilogueWarps = 8;
 constexpr int kMaxStages = 32;
 constexpr uint32_t kTileBytes = 32 * 64;             // pairs of CTAs: a warp's piece of the output on its way
@@ -247,7 +253,6 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs& g, int t) {
 template <int KIND, int CTAS, bool F16>
 __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ ProductArgs g) {
     constexpr bool A_COLS = KIND == kGradW, B_COLS = KIND == kGradX || KIND == kGradW;  // rows across the reduced axis
-    constexpr int ROWS = 128 * CTAS;  // of a tile
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                 const Tile c = tile_of(g, t);
                 const int2 range = blocks_of(g, c.split);
                 const int k0 = range.x, k1 = range.y;
-                const int row = c.m * ROWS + rank * 128;
+                const int row = c.m * CTAS * g.m + rank * 128;
                 for (int seg = 0; ok && seg < g.segments; ++seg) {
                     const CUtensorMap* ma = &g.a[KIND == kGradW ? c.which : seg];
                     for (int k = k0; k < k1; k += deep) {
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             tmem_fence_after();
             // Products of 64 rows leave 16 of them in each quarter's first lanes.
             const int lanes = CTAS == 1 && !A_COLS && g.m == 64 ? 16 : 32;
-            const int64_t row0 = static_cast<int64_t>(c.m) * ROWS + rank * 128 + quad * lanes, row = row0 + lane;
+            const int64_t row0 = static_cast<int64_t>(c.m) * CTAS * g.m + rank * 128 + quad * lanes, row = row0 + lane;
             const bool there = lane < lanes && row < g.M;
             const uint32_t acc = tmem_slot + buf * g.bn + (static_cast<uint32_t>(quad * 32) << 16);
             constexpr bool GATED = KIND == kGatedFwd;
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             if (row0 < g.M) {
                 // W columns at a time. Single CTAs write them from the registers, 16 bytes a lane. A pair's, whose
                 // output is a large part of the traffic, go through shared memory (rows of 64 bytes, swizzled) and leave
-                // by tensor copies, in whole sectors: 8192 x 4096 x 16384 with z kept 591 us from registers.
+                // by tensor copies, in whole sectors: 8192 x 4096 x 16384 with z kept 591 us from registers, 566 so.
                 constexpr int W = CTAS == 2 ? 32 : 16;
                 for (int j = part * W; j < width; j += 2 * W) {
                     const int col = c.n * width + j;
@@ -573,11 +578,13 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
 // Launcher
 // ---------------------------------------------------------------------------
 template <int KIND, int CTAS, bool F16>
-cudaError_t product_run(const Product& p, int bn, cudaStream_t st) {
+cudaError_t product_run(const Product& p, const Tiling& tile, cudaStream_t st) {
     constexpr bool A_COLS = KIND == kGradW, B_COLS = KIND == kGradX || KIND == kGradW;
     ProductArgs g{};
+    const int bn = tile.bn;
     const int width = KIND == kGatedFwd ? bn / 2 : bn;  // columns of C a tile
-    const int64_t rows = 128 * CTAS, pairs = KIND == kGradW && p.a[1].p != nullptr ? 2 : 1;
+    g.m = tile.rows;
+    const int64_t rows = static_cast<int64_t>(g.m) * CTAS, pairs = KIND == kGradW && p.a[1].p != nullptr ? 2 : 1;
     g.M = p.M;
     g.N = static_cast<int>(p.N);
     g.act = p.act;
@@ -599,12 +606,11 @@ cudaError_t product_run(const Product& p, int bn, cudaStream_t st) {
     // all the same, into what lies behind them in the ring; a row of C depends on its own
     // row of A alone, and the others are not stored. (Products of 64 rows read half of that.)
     const bool few = CTAS == 1 && !A_COLS;
-    g.m = few && p.M <= 64 ? 64 : 128;
-    g.a_rows = few && p.M <= 120 ? static_cast<int>((p.M + 7) / 8 * 8) : 128;
+    g.a_rows = few && p.M < g.m ? static_cast<int>((p.M + 7) / 8 * 8) : g.m;
     g.a_block = static_cast<uint32_t>(g.a_rows) * 128u;
     g.b_block = static_cast<uint32_t>(B_COLS ? (bn / CTAS + 63) / 64 * 64 : bn / CTAS) * 128u;
-    // Blocks a stage: each stage costs the multiplying thread a wait, a fence and a commit, some
-    // 280 cycles beside 25 to 40 a product; four stages at least.
+    // Blocks a stage: as many as leave four stages (1 x 4096 x 4096 by 1, 2, 4 and 8 blocks: 18.9, 14.4, 10.5
+    // and 9.4 us).
     g.whole = p.K % kBlockK == 0;
     g.deep = std::max(1, std::min<int>(CTAS == 2 ? kMostDeepPair : kMostDeep, static_cast<int>(kStageBytes / 4 / (g.a_block + g.b_block))));
     g.copy_deep = CTAS == 1 && g.whole ? g.deep : 1;
@@ -615,6 +621,9 @@ cudaError_t product_run(const Product& p, int bn, cudaStream_t st) {
     const uint32_t behind = std::max(reach, g.stage_bytes) - g.stage_bytes;
     const uint32_t staging = CTAS == 2 ? kEpilogueWarps * 2 * kTileBytes : 0;
     g.stages = std::min<int>(kMaxStages, static_cast<int>((kStageBytes - behind - staging) / g.stage_bytes));
+    // A copying warp passes over the others' stages without waiting for them: with fewer stages than such warps
+    // it would come to one that is two uses behind, and take its barrier's older phase for the newer.
+    if (g.stages < kCopyWarps) return cudaErrorInvalidConfiguration;
     g.staging = static_cast<uint32_t>(g.stages) * g.stage_bytes;
     const size_t smem = static_cast<size_t>(g.staging) + behind + staging + 1024;
     g.tmem_cols = 32;
@@ -667,7 +676,7 @@ template <int KIND, bool F16>
 cudaError_t product_shape(const Product& p, cudaStream_t st) {
     const int64_t outputs = KIND == kGradW && p.a[1].p != nullptr ? 2 : 1, blocks = (p.K + kBlockK - 1) / kBlockK;
     const Tiling t = linear_tiling(static_cast<ProductKind>(KIND), p.M, p.N, (blocks + p.splits - 1) / p.splits, outputs * p.splits);
-    return t.ctas == 2 ? product_run<KIND, 2, F16>(p, t.bn, st) : product_run<KIND, 1, F16>(p, t.bn, st);
+    return t.ctas == 2 ? product_run<KIND, 2, F16>(p, t, st) : product_run<KIND, 1, F16>(p, t, st);
 }
 
 }  // namespace

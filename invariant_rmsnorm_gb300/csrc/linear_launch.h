@@ -39,8 +39,8 @@ struct Product {
     int act;
 };
 
-// A product's tile: CTAs (two: a pair, 256 rows; one: 128 rows), columns of accumulators, and the model's cycles.
-struct Tiling { int ctas, bn; int64_t cycles; };
+// A product's tile: CTAs (two: a pair, 256 rows), rows a CTA, columns of accumulators, and the model's cycles.
+struct Tiling { int ctas, rows, bn; int64_t cycles; };
 
 constexpr int kMostDeep = 8, kMostDeepPair = 2;      // blocks of 64 reduced values a stage
 constexpr uint32_t kStageBytes = 227 * 1024 - 2048;  // of shared memory for the stages
@@ -48,11 +48,14 @@ constexpr uint32_t kStageBytes = 227 * 1024 - 2048;  // of shared memory for the
 // The tile by a model of a GPU of 152 SMs, in cycles. Tiles go round it in waves, of 76 pairs or
 // 152 single CTAs. A block of a tile takes a pair of 256 x 256 512 (its products) and of 256 x 128 270
 // (290 with both operands along their columns) in a single wave, 340 (390) in more: its operands are three quarters
-// of the larger tile's for half the products (8192 x 4096 x 16384: 796 us for 666); a single CTA its products, 2 a column, or its operands at 80
-// bytes a cycle, or 140 and 310 a stage of the issuing thread; a tile at least its epilogue, 12 a column; a launch of pairs 900 more. Single CTAs have as many columns
-// as give every SM one tile or, past 256, two and more (a multiple of 16; of 32 with two matrices' columns, of 64
-// where B lies along them). 512 x 4096 x 4096: pairs of 256 x 128 13.6 us, single CTAs of 128 columns 18.1;
-// 1024 x 4096 x 4096: 20.8 and, with 256 x 256, 23.0; 64 x 4096 x 6144: CTAs of 48 columns 12.3, of 64 13.1.
+// of the larger tile's for half the products (8192 x 4096 x 16384: 796 us for 666); a single CTA its products, 2 a
+// column, or their operands from shared memory, 1 a row and column, or from L2 at 80 bytes a cycle, or 140 and 310
+// a stage of the issuing thread; a tile at least its epilogue, 12 a column; a launch of pairs 900 more. Single CTAs
+// have as many columns as give every SM one tile or, past 256, two and more (a multiple of 16; of 32 with two
+// matrices' columns, of 64 where B lies along them), and 64 rows up to 64 in all, 64 or 128 beyond.
+// 512 x 4096 x 4096: pairs of 256 x 128 13.6 us, single CTAs of 128 columns 18.1; 1024 x 4096 x 4096: 20.8 and,
+// with 256 x 256, 23.0; 64 x 4096 x 6144: CTAs of 48 columns 12.3, of 64 13.1; 128 x 4096 x 4096: 64 x 64 10.6,
+// 128 x 32 12.5; 128 x 4096 x 14336: 128 x 96 22.8, 64 x 192 23.7.
 inline Tiling linear_tiling(ProductKind kind, int64_t M, int64_t N, int64_t blocks, int64_t outputs) {
     constexpr int64_t kSms = 152;
     const int64_t unit = kind == kGradX || kind == kGradW ? 64 : kind == kGatedFwd ? 32 : 16;
@@ -60,20 +63,30 @@ inline Tiling linear_tiling(ProductKind kind, int64_t M, int64_t N, int64_t bloc
     auto cycles = [&](int64_t tiles, int64_t at_once, int64_t block, int64_t bn) {
         return (tiles + at_once - 1) / at_once * std::max(blocks * block, 12 * bn) + 12 * bn;
     };
-    const int64_t rows = (M + 127) / 128 * outputs, per_row = std::max<int64_t>(1, kSms / rows);
-    int64_t bn = (cols + per_row - 1) / per_row;
-    for (int64_t waves = 2; bn > 256; ++waves) bn = (cols + waves * per_row - 1) / (waves * per_row);
-    bn = std::min<int64_t>(256, (bn + unit - 1) / unit * unit);
-    const int64_t deep = std::max<int64_t>(1, std::min<int64_t>(kMostDeep, kStageBytes / 4 / (16384 + bn * 128)));
-    Tiling best{1, static_cast<int>(bn), cycles(rows * ((cols + bn - 1) / bn), kSms, std::max<int64_t>({2 * bn, (16384 + bn * 128) / 80, 140 + 310 / deep}), bn)};
+    auto single = [&](int64_t high) {
+        const int64_t rows = (M + high - 1) / high * outputs, per_row = std::max<int64_t>(1, kSms / rows);
+        int64_t bn = (cols + per_row - 1) / per_row;
+        for (int64_t waves = 2; bn > 256; ++waves) bn = (cols + waves * per_row - 1) / (waves * per_row);
+        bn = std::min<int64_t>(256, (bn + unit - 1) / unit * unit);
+        const int64_t copied = kind == kGradW ? 128 : std::min(high, (M + 7) / 8 * 8), bytes = (copied + bn) * 128;
+        const int64_t deep = std::max<int64_t>(1, std::min<int64_t>(kMostDeep, kStageBytes / 4 / bytes));
+        const int64_t block = std::max<int64_t>({2 * bn, high + bn, bytes / 80, 140 + 310 / deep});
+        return Tiling{1, static_cast<int>(high), static_cast<int>(bn), cycles(rows * ((cols + bn - 1) / bn), kSms, block, bn)};
+    };
+    if (kind != kGradW && M <= 64) return single(64);
+    Tiling best = single(128);
     if (M > 128) {
         const int64_t pair_rows = (M + 255) / 256 * outputs;
         const int64_t narrow_tiles = pair_rows * ((cols + 127) / 128);
         const int64_t narrow_block = narrow_tiles <= kSms / 2 ? (kind == kGradW ? 290 : 270) : (kind == kGradW ? 390 : 340);
-        const Tiling narrow{2, 128, cycles(narrow_tiles, kSms / 2, narrow_block, 128) + 900};
-        const Tiling wide{2, 256, cycles(pair_rows * ((cols + 255) / 256), kSms / 2, 512, 256) + 900};
+        const Tiling narrow{2, 128, 128, cycles(narrow_tiles, kSms / 2, narrow_block, 128) + 900};
+        const Tiling wide{2, 128, 256, cycles(pair_rows * ((cols + 255) / 256), kSms / 2, 512, 256) + 900};
         if (narrow.cycles <= best.cycles) best = narrow;
         if (wide.cycles <= best.cycles) best = wide;
+    }
+    if (kind != kGradW) {
+        const Tiling low = single(64);
+        if (low.cycles < best.cycles) best = low;
     }
     return best;
 }
