@@ -34,7 +34,11 @@
  * independent of T, of the row's position and of the other rows: every value is
  * one chain of sums over the reduced axis in ascending order, at every tile size.
  * The weights' gradients are summed with no atomics, over ranges of rows that
- * depend on T, N and K alone: the same bits from run to run.
+ * depend on T, N and K alone: the same bits from run to run. (Every kernel's tiles are
+ * chosen by the sizes alone, whatever the GPU's SM count.)
+ *
+ * Calls that may run at the same time (on two streams, in two graphs) need
+ * workspaces of their own.
  */
 #ifndef LINEAR_GB300_H_
 #define LINEAR_GB300_H_

@@ -303,6 +303,32 @@ def test_more_than_two_to_the_31_values():
     assert torch.equal(_bits(dx[-200:]), _bits(dfew)) and bool(db.isfinite().all())
 
 
+@pytest.mark.parametrize("T,K,N", [(3, 8, 1 << 20), (3, 1 << 20, 8), (300, 1 << 17, 24), (1 << 20, 8, 8)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_the_longest_sides(T, K, N, dtype):
+    """Values of -1, 0 and 1, whose sums are exact in fp32: the results are the rounded integers themselves."""
+    def ints(r, c, seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        return torch.randint(-1, 2, (r, c), generator=g, device=DEV).to(dtype)
+
+    def same(got, want):
+        assert torch.equal(got, want.to(dtype))
+
+    x, w, v, g = ints(T, K, 1), ints(N, K, 2), ints(N, K, 3), ints(T, N, 4)
+    y, h = torch.empty_like(g), torch.empty_like(g)
+    rn.linear_fwd(x, w, None, g, y)
+    rn.linear_gated_fwd(x, w, v, h, None, None, "relu")
+    z, u = x.double() @ w.double().t(), x.double() @ v.double().t()
+    same(y, z + g.double())
+    ok = (z.clamp_min(0) * u).abs() < 2.0 ** 24  # exact there
+    assert torch.equal(h[ok], (z.clamp_min(0) * u).to(dtype)[ok])
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(N, device=DEV)
+    rn.linear_bwd(g, x, w, None, dx, dw, db, _ws(rn.linear_bwd_workspace_bytes(T, N, K)))
+    same(dx, g.double() @ w.double())
+    same(dw, g.double().t() @ x.double())
+    assert torch.equal(db, g.double().sum(0).float())
+
+
 def test_long_sums_of_one_sign():
     T, N = 200000, 72
     g = torch.full((T, N), 1.0, dtype=BF16, device=DEV)
