@@ -65,9 +65,8 @@ inline Tiling linear_tiling(ProductKind kind, int64_t M, int64_t N, int64_t bloc
     };
     auto single = [&](int64_t high) {
         const int64_t rows = (M + high - 1) / high * outputs, per_row = std::max<int64_t>(1, kSms / rows);
-        int64_t bn = (cols + per_row - 1) / per_row;
-        for (int64_t waves = 2; bn > 256; ++waves) bn = (cols + waves * per_row - 1) / (waves * per_row);
-        bn = std::min<int64_t>(256, (bn + unit - 1) / unit * unit);
+        const int64_t across = per_row * ((cols + 256 * per_row - 1) / (256 * per_row));  // column tiles, of 256 at most
+        const int64_t bn = std::min<int64_t>(256, ((cols + across - 1) / across + unit - 1) / unit * unit);
         const int64_t copied = kind == kGradW ? 128 : std::min(high, (M + 7) / 8 * 8), bytes = (copied + bn) * 128;
         const int64_t deep = std::max<int64_t>(1, std::min<int64_t>(kMostDeep, kStageBytes / 4 / bytes));
         const int64_t block = std::max<int64_t>({2 * bn, high + bn, bytes / 80, 140 + 310 / deep});

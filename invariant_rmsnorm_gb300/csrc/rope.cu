@@ -23,10 +23,17 @@ int rope_run(RopeMode mode, RopeArgs& a, int flags, cudaStream_t s, int* ctas_q 
         a.dense[1][i] = whole && a.x[i].head == a.D;
         a.dense[2][i] = whole && a.out[i].head == a.D;
     }
+    const bool axes = a.axis != nullptr;
     switch (mode) {
-        case kTurn: return cuda_status(flags ? launch_rope_turn_f16(a, ctas_q, s) : launch_rope_turn(a, ctas_q, s));
-        case kNormTurn: return cuda_status(flags ? launch_rope_norm_f16(a, ctas_q, s) : launch_rope_norm(a, ctas_q, s));
-        default: return cuda_status(flags ? launch_rope_norm_bwd_f16(a, ctas_q, s) : launch_rope_norm_bwd(a, ctas_q, s));
+        case kTurn:
+            if (axes) return cuda_status(flags ? launch_rope_axes_turn_f16(a, ctas_q, s) : launch_rope_axes_turn(a, ctas_q, s));
+            return cuda_status(flags ? launch_rope_turn_f16(a, ctas_q, s) : launch_rope_turn(a, ctas_q, s));
+        case kNormTurn:
+            if (axes) return cuda_status(flags ? launch_rope_axes_norm_f16(a, ctas_q, s) : launch_rope_axes_norm(a, ctas_q, s));
+            return cuda_status(flags ? launch_rope_norm_f16(a, ctas_q, s) : launch_rope_norm(a, ctas_q, s));
+        default:
+            if (axes) return cuda_status(flags ? launch_rope_axes_norm_bwd_f16(a, ctas_q, s) : launch_rope_axes_norm_bwd(a, ctas_q, s));
+            return cuda_status(flags ? launch_rope_norm_bwd_f16(a, ctas_q, s) : launch_rope_norm_bwd(a, ctas_q, s));
     }
 }
 

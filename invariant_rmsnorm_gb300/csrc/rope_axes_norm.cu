@@ -1,4 +1,4 @@
-// Head norm and rotary positions of several axes, turns of several tokens, bf16 activations: the
+// Head norm and rotary positions of several axes, bf16 activations: the
 // instantiations of rope_impl.cuh.
 #include "rope_impl.cuh"
 

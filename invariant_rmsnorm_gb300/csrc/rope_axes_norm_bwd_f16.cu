@@ -1,4 +1,4 @@
-// Backward of head norm and rotary positions of several axes, turns of several tokens, fp16 activations: the
+// Backward of head norm and rotary positions of several axes, fp16 activations: the
 // instantiations of rope_impl.cuh.
 #include "rope_impl.cuh"
 

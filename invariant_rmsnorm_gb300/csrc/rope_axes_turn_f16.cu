@@ -1,4 +1,4 @@
-// Rotary positions of several axes, turns of several tokens, fp16 activations: the
+// Rotary positions of several axes, fp16 activations: the
 // instantiations of rope_impl.cuh.
 #include "rope_impl.cuh"
 

@@ -222,8 +222,8 @@ __device__ __forceinline__ void token_angles(float* cs, int hp, int half, const 
 }
 
 // The same with several axes, `axis` that of every pair. A pair's position is read
-// by the lane that has the pair, out of L1 for all but one token of 16: no register of the
-// kernels' other users is taken, and a token's 32 + 8 heads hide the read.
+// by the lane that has the pair, out of L1 for all but one token of 16 (fetching it there ahead measured no
+// faster).
 __device__ __forceinline__ void token_axis_angles(float* cs, int hp, int half, const unsigned long long* F, const uint8_t* axis,
                                                   const RopeArgs& a, int64_t t, bool back, int lane) {
     __syncwarp();
@@ -274,18 +274,18 @@ __device__ __forceinline__ uint4 first_of(uint4 v, int n) {
 }
 
 enum RopeKind : int { kHalves = 0, kNeighbours = 1, kHalvesAny = 2, kHalves8 = 3 };
-enum RopeTokens : int { kOne = 0, kMany = 1, kManyAxes = 2 };
+enum RopeTokens : int { kOne = 0, kMany = 1, kOneAxes = 2, kManyAxes = 3 };
 
 // ---------------------------------------------------------------------------
 // The kernel: 2^LG lanes a head, NR heads a group and turn, RB of them at a time.
 // FULL: every lane has a whole unit (D = 16 x 2^LG, no unit cut short).
-// TOKENS: kOne: a turn is of one token; kMany: of a token a group; kManyAxes: the
-// same, with positions of several axes (in kOne kernels a branch, which costs those
-// no register; in kMany ones it would spill 12 to 52 bytes).
+// TOKENS: kOne: a turn is of one token; kMany: of a token a group; kOneAxes, kManyAxes:
+// the same with positions of several axes (kernels of their own: a branch would spill 12 to
+// 52 bytes more in kMany and cost kOne up to 1.5 %).
 // ---------------------------------------------------------------------------
 template <int MODE, int KIND, bool F16, int LG, bool FULL, int TOKENS, int NR, int RBATCH, int S, int MINB>
 __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs a) {
-    constexpr bool MANY = TOKENS != kOne, AXES = TOKENS == kManyAxes;
+    constexpr bool MANY = TOKENS == kMany || TOKENS == kManyAxes, AXES = TOKENS == kOneAxes || TOKENS == kManyAxes;
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
     constexpr bool ANY = KIND == kHalvesAny || KIND == kHalves8;  // units may be cut short
     constexpr int OPS = BWD ? 2 : 1, per = 32 >> LG, rows = per * NR;
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
     // While the first rows come:
     for (int i = half + lane; i < hp; i += 32) cs[i] = cs[hp + i] = 0.0f;  // zeros are turned there
     for (int i = tid; i < half; i += nt) F[i] = rope_turns(a.inv_freq[i]);
-    if ((AXES || !MANY) && a.axis != nullptr)
+    if constexpr (AXES)
         for (int i = tid; i < half; i += nt) axis[i] = static_cast<uint8_t>(min(static_cast<int>(a.axis[i]), a.axes - 1));
     if constexpr (NORM) {
         for (int i = tid; i < 2 * D; i += nt) {
@@ -470,13 +470,11 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
             t_have = now.t;
             if (t0 - t32 >= 32) {
                 t32 = t0;
-                if (!AXES && (MANY || a.axis == nullptr) && t32 + lane < a.T) p32 = position(a, t32 + lane);
+                if (!AXES && t32 + lane < a.T) p32 = position(a, t32 + lane);
             }
             const long long pos = __shfl_sync(0xffffffffu, p32, static_cast<int>(t0 - t32) + (MANY ? head : 0));
-            if constexpr (!MANY) {
-                if (a.axis == nullptr) token_angles(cs, hp, half, F, pos, a.scale, BWD || a.back, lane);
-                else token_axis_angles(cs, hp, half, F, axis, a, t0, BWD || a.back, lane);
-            }
+            if constexpr (!MANY && !AXES) token_angles(cs, hp, half, F, pos, a.scale, BWD || a.back, lane);
+            if constexpr (!MANY && AXES) token_axis_angles(cs, hp, half, F, axis, a, t0, BWD || a.back, lane);
             if constexpr (MANY) {  // this lane's own
                 if (KIND == kNeighbours || turned) {
 #pragma unroll
@@ -737,13 +735,13 @@ __global__ void __launch_bounds__(kRopeThreads, MINB) rope_kernel(const RopeArgs
 // ---------------------------------------------------------------------------
 template <int MODE, int KIND, bool F16, int LG, bool FULL, int TOKENS, int NR, int RB, int S, int MINB>
 cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
-    constexpr bool MANY = TOKENS != kOne;
+    constexpr bool MANY = TOKENS == kMany || TOKENS == kManyAxes, AXES = TOKENS == kOneAxes || TOKENS == kManyAxes;
     constexpr bool NORM = MODE != kTurn, BWD = MODE == kNormTurnBwd;
     constexpr int per = 32 >> LG, rows = per * NR, tokens = MANY ? per : 1, step = MANY ? NR : rows;
     const auto kern = rope_kernel<MODE, KIND, F16, LG, FULL, TOKENS, NR, RB, S, MINB>;
     const int hp = (a.R / 2 + 7) & ~7;
     const size_t warp_bytes = static_cast<size_t>(S) * (BWD ? 2 : 1) * rows * a.D * 2 + hp * 8 + (NORM ? S * rows * 4 : 0) + S * 8;
-    const size_t fixed = (NORM ? static_cast<size_t>(a.D) * 8 : 0) + static_cast<size_t>(a.R / 2) * (a.axis != nullptr ? 9 : 8);
+    const size_t fixed = (NORM ? static_cast<size_t>(a.D) * 8 : 0) + static_cast<size_t>(a.R / 2) * (AXES ? 9 : 8);
     const int64_t sms = sm_count();
     const int64_t turns = (a.T + tokens - 1) / tokens * ((a.H[0] + step - 1) / step + (a.H[1] + step - 1) / step);
     // Threads: few turns spread over the SMs in smaller CTAs. The backward's CTAs
@@ -788,31 +786,19 @@ cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
 // 32 -> 57; 14 + 2 heads: 88 both ways, 55 -> 79, 46 -> 81. With as many turns
 // (32 + 8 heads of 128) its shorter copies cost: 83 -> 80, 76 -> 66, 75 -> 72,
 // measured in one kernel for both.
-//
-// Turns of several tokens with positions of several axes are a launch of another
-// translation unit (`Axes`: instantiating them alone), which comes here by the same rules.
 template <int MODE, int KIND, bool F16, int LG, bool FULL, bool Axes, int NR, int RB, int S, int MINB>
 cudaError_t rope_run_kernel(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
     constexpr int per = 32 >> LG;
-    // Forward with the norm: then four heads a group (8 + 1 heads of 128: 75 % for two heads' 58).
-    constexpr bool wider = MODE == kNormTurn;
-    if constexpr (Axes) {
-        if constexpr (per > 1)
-            return rope_run_as<MODE, KIND, F16, LG, FULL, kManyAxes, wider ? 4 : NR, wider ? 2 : RB, wider ? 3 : S, MINB>(a, ctas_q, st);
-        else
-            return cudaErrorInvalidValue;  // never chosen: one token fills the warp
-    } else {
     if constexpr (per > 1) {
+        // Forward with the norm: then four heads a group (8 + 1 heads of 128: 75 % for two heads' 58).
+        constexpr bool wider = MODE == kNormTurn;
         auto turns_of = [&](int step) -> int64_t { return (a.H[0] + step - 1) / step + (a.H[1] + step - 1) / step; };
         const int64_t one = a.T * turns_of(per * NR), many = (a.T + per - 1) / per * turns_of(NR);
         const bool fewer = MODE == kTurn ? 2 * many <= one : 4 * many <= 3 * one;
-        if (fewer && many >= kRopeManyFrom) {
-            if (a.axis != nullptr) return launch_rope_axes(MODE, F16, a, ctas_q, st);
-            return rope_run_as<MODE, KIND, F16, LG, FULL, kMany, wider ? 4 : NR, wider ? 2 : RB, wider ? 3 : S, MINB>(a, ctas_q, st);
-        }
+        if (fewer && many >= kRopeManyFrom)
+            return rope_run_as<MODE, KIND, F16, LG, FULL, Axes ? kManyAxes : kMany, wider ? 4 : NR, wider ? 2 : RB, wider ? 3 : S, MINB>(a, ctas_q, st);
     }
-    return rope_run_as<MODE, KIND, F16, LG, FULL, kOne, NR, RB, S, MINB>(a, ctas_q, st);
-    }
+    return rope_run_as<MODE, KIND, F16, LG, FULL, Axes ? kOneAxes : kOne, NR, RB, S, MINB>(a, ctas_q, st);
 }
 
 // Heads a group and turn, of them in registers at a time, stages, CTAs an SM: the

@@ -78,20 +78,13 @@ cudaError_t launch_rope_norm_bwd(const RopeArgs& a, int* ctas_q, cudaStream_t s)
 cudaError_t launch_rope_turn_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
 cudaError_t launch_rope_norm_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
 cudaError_t launch_rope_norm_bwd_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
-// Turns of several tokens with positions of several axes, chosen by the launchers above.
+// The same with positions of several axes.
 cudaError_t launch_rope_axes_turn(const RopeArgs& a, int* ctas_q, cudaStream_t s);
 cudaError_t launch_rope_axes_norm(const RopeArgs& a, int* ctas_q, cudaStream_t s);
 cudaError_t launch_rope_axes_norm_bwd(const RopeArgs& a, int* ctas_q, cudaStream_t s);
 cudaError_t launch_rope_axes_turn_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
 cudaError_t launch_rope_axes_norm_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
 cudaError_t launch_rope_axes_norm_bwd_f16(const RopeArgs& a, int* ctas_q, cudaStream_t s);
-inline cudaError_t launch_rope_axes(int mode, bool f16, const RopeArgs& a, int* ctas_q, cudaStream_t s) {
-    switch (mode) {
-        case kTurn: return f16 ? launch_rope_axes_turn_f16(a, ctas_q, s) : launch_rope_axes_turn(a, ctas_q, s);
-        case kNormTurn: return f16 ? launch_rope_axes_norm_f16(a, ctas_q, s) : launch_rope_axes_norm(a, ctas_q, s);
-        default: return f16 ? launch_rope_axes_norm_bwd_f16(a, ctas_q, s) : launch_rope_axes_norm_bwd(a, ctas_q, s);
-    }
-}
 cudaError_t rope_axes_turn_read_error(unsigned* flags, bool clear);
 cudaError_t rope_axes_norm_read_error(unsigned* flags, bool clear);
 cudaError_t rope_axes_norm_bwd_read_error(unsigned* flags, bool clear);
