@@ -287,6 +287,30 @@ def test_views_of_wider_matrices():
     assert torch.equal(_bits(row), _bits(a[5:6]))
 
 
+@pytest.mark.parametrize("T", [1, 100, 2600])
+def test_outputs_as_parts_of_wider_matrices(T):
+    """gate and up side by side in one buffer, dwg and dwu one above the other, each between columns that stay as they were."""
+    K, N = 264, 1032
+    x, g, wg, wu = _mat(T, K, 1), _mat(T, N, 2), _mat(N, K, 3, std=0.1), _mat(N, K, 4, std=0.1)
+    h, gate, up = (torch.empty((T, N), dtype=BF16, device=DEV) for _ in range(3))
+    rn.linear_gated_fwd(x, wg, wu, h, gate, up)
+    both = torch.full((T, 2 * N + 24), 3.0, dtype=BF16, device=DEV)
+    wide = torch.full((T, N + 16), 3.0, dtype=BF16, device=DEV)
+    rn.linear_gated_fwd(x, wg, wu, wide[:, 8:N + 8], both[:, 8:N + 8], both[:, N + 16:2 * N + 16])
+    for a, b in ((h, wide[:, 8:N + 8]), (gate, both[:, 8:N + 8]), (up, both[:, N + 16:2 * N + 16])):
+        assert torch.equal(_bits(a), _bits(b))
+    gaps = torch.cat((wide[:, :8], wide[:, -8:], both[:, :8], both[:, N + 8:N + 16], both[:, -8:]), 1)
+    assert bool((gaps == 3.0).all())
+    ws = _ws(rn.linear_gated_bwd_workspace_bytes(T, N, K))
+    dx, dwg, dwu = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+    rn.linear_gated_bwd(g, x, wg, wu, gate, up, dx, dwg, dwu, ws)
+    stack, dwide = torch.full((2 * N, K + 8), 3.0, dtype=BF16, device=DEV), torch.full((T, K + 8), 3.0, dtype=BF16, device=DEV)
+    rn.linear_gated_bwd(g, x, wg, wu, both[:, 8:N + 8], both[:, N + 16:2 * N + 16], dwide[:, 8:], stack[:N, :K], stack[N:, :K], ws)
+    for a, b in ((dx, dwide[:, 8:]), (dwg, stack[:N, :K]), (dwu, stack[N:, :K])):
+        assert torch.equal(_bits(a), _bits(b))
+    assert bool((stack[:, K:] == 3.0).all()) and bool((dwide[:, :8] == 3.0).all())
+
+
 def test_more_than_two_to_the_31_values():
     T, K, N = (1 << 31) // 16384 + 300, 64, 16384
     x, w = _mat(T, K, 1), _mat(N, K, 2)
