@@ -164,9 +164,9 @@ size_t padded(size_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 int weight_splits(int64_t T, int64_t N, int64_t K, int outputs) {
     const int64_t blocks = (T + 63) / 64;
     int best = 1;
-    int64_t least = linear_tiling(kGradW, N, K, blocks, outputs).cycles;
+    int64_t least = linear_tiling(kGradW, N, K, blocks, outputs, true).cycles;
     for (int s = 2; s <= 64 && T / s >= 512; s *= 2) {
-        const int64_t cycles = linear_tiling(kGradW, N, K, (blocks + s - 1) / s, static_cast<int64_t>(outputs) * s).cycles +
+        const int64_t cycles = linear_tiling(kGradW, N, K, (blocks + s - 1) / s, static_cast<int64_t>(outputs) * s, true).cycles +
                                5000 + 8 * s * outputs * N * K / 3000;
         if (cycles < least) {
             least = cycles;

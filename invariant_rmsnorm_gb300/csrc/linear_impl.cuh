@@ -675,7 +675,9 @@ cudaError_t product_run(const Product& p, const Tiling& tile, cudaStream_t st) {
 template <int KIND, bool F16>
 cudaError_t product_shape(const Product& p, cudaStream_t st) {
     const int64_t outputs = KIND == kGradW && p.a[1].p != nullptr ? 2 : 1, blocks = (p.K + kBlockK - 1) / kBlockK;
-    const Tiling t = linear_tiling(static_cast<ProductKind>(KIND), p.M, p.N, (blocks + p.splits - 1) / p.splits, outputs * p.splits);
+    bool lines = true;  // every row of the operands starts on a line of 128 bytes
+    for (const MatIn& m : {p.a[0], p.a[1], p.b[0], p.b[1]}) lines = lines && m.ld % 64 == 0 && reinterpret_cast<uintptr_t>(m.p) % 128 == 0;
+    const Tiling t = linear_tiling(static_cast<ProductKind>(KIND), p.M, p.N, (blocks + p.splits - 1) / p.splits, outputs * p.splits, lines);
     return t.ctas == 2 ? product_run<KIND, 2, F16>(p, t, st) : product_run<KIND, 1, F16>(p, t, st);
 }
 

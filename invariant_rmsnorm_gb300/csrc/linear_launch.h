@@ -53,11 +53,14 @@ constexpr uint32_t kStageBytes = 227 * 1024 - 2048;  // of shared memory for the
 // a stage of the issuing thread; a tile at least its epilogue, 12 a column; a launch of pairs 900 more. Single CTAs
 // have as many columns as give every SM one tile or, past 256, two and more (a multiple of 16; of 32 with two
 // matrices' columns, of 64 where B lies along them), and 64 rows up to 64 in all, 64 or 128 beyond.
+// Where rows of the operands do not start on lines (`lines` false) their way is 45 bytes a cycle and SM: 2048 x 4104 x 4096
+// 697 cycles a block of 256 x 256 and 521 of 256 x 128.
 // 512 x 4096 x 4096: pairs of 256 x 128 13.6 us, single CTAs of 128 columns 18.1; 1024 x 4096 x 4096: 20.8 and,
 // with 256 x 256, 23.0; 64 x 4096 x 6144: CTAs of 48 columns 12.3, of 64 13.1; 128 x 4096 x 4096: 64 x 64 10.6,
 // 128 x 32 12.5; 128 x 4096 x 14336: 128 x 96 22.8, 64 x 192 23.7.
-inline Tiling linear_tiling(ProductKind kind, int64_t M, int64_t N, int64_t blocks, int64_t outputs) {
+inline Tiling linear_tiling(ProductKind kind, int64_t M, int64_t N, int64_t blocks, int64_t outputs, bool lines) {
     constexpr int64_t kSms = 152;
+    const int64_t rate = lines ? 80 : 45;
     const int64_t unit = kind == kGradX || kind == kGradW ? 64 : kind == kGatedFwd ? 32 : 16;
     const int64_t cols = kind == kGatedFwd ? 2 * N : N;
     auto cycles = [&](int64_t tiles, int64_t at_once, int64_t block, int64_t bn) {
@@ -69,7 +72,7 @@ inline Tiling linear_tiling(ProductKind kind, int64_t M, int64_t N, int64_t bloc
         const int64_t bn = std::min<int64_t>(256, ((cols + across - 1) / across + unit - 1) / unit * unit);
         const int64_t copied = kind == kGradW ? 128 : std::min(high, (M + 7) / 8 * 8), bytes = (copied + bn) * 128;
         const int64_t deep = std::max<int64_t>(1, std::min<int64_t>(kMostDeep, kStageBytes / 4 / bytes));
-        const int64_t block = std::max<int64_t>({2 * bn, high + bn, bytes / 80, 140 + 310 / deep});
+        const int64_t block = std::max<int64_t>({2 * bn, high + bn, bytes / rate, 140 + 310 / deep});
         return Tiling{1, static_cast<int>(high), static_cast<int>(bn), cycles(rows * ((cols + bn - 1) / bn), kSms, block, bn)};
     };
     if (kind != kGradW && M <= 64) return single(64);
@@ -78,8 +81,8 @@ inline Tiling linear_tiling(ProductKind kind, int64_t M, int64_t N, int64_t bloc
         const int64_t pair_rows = (M + 255) / 256 * outputs;
         const int64_t narrow_tiles = pair_rows * ((cols + 127) / 128);
         const int64_t narrow_block = narrow_tiles <= kSms / 2 ? (kind == kGradW ? 290 : 270) : (kind == kGradW ? 390 : 340);
-        const Tiling narrow{2, 128, 128, cycles(narrow_tiles, kSms / 2, narrow_block, 128) + 900};
-        const Tiling wide{2, 128, 256, cycles(pair_rows * ((cols + 255) / 256), kSms / 2, 512, 256) + 900};
+        const Tiling narrow{2, 128, 128, cycles(narrow_tiles, kSms / 2, lines ? narrow_block : 540, 128) + 900};
+        const Tiling wide{2, 128, 256, cycles(pair_rows * ((cols + 255) / 256), kSms / 2, lines ? 512 : 700, 256) + 900};
         if (narrow.cycles <= best.cycles) best = narrow;
         if (wide.cycles <= best.cycles) best = wide;
     }

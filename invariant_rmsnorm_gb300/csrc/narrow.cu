@@ -46,6 +46,8 @@ cudaError_t encode_rows_2d(CUtensorMap* map, const void* base, int64_t T, int D,
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Fetched into L2 by 128 bytes: by 256, rows that do not start on lines cost 10 % more (433 x 11832 x 11392: 169 us for
+// 152), the others the same.
 namespace {
 cudaError_t encode_blocks(CUtensorMap* map, const void* base, cuuint32_t rank, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
                           const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
@@ -53,7 +55,7 @@ cudaError_t encode_blocks(CUtensorMap* map, const void* base, cuuint32_t rank, c
     if (fn == nullptr) return cudaErrorNotSupported;
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
