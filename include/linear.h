@@ -20,6 +20,8 @@
  * dup are rounded to the activation format before their products (they are these
  * products' operands; an fp16 one that passes 65504 becomes infinite), but db sums
  * the unrounded fp32 values. Without an activation dz is g and nothing is rounded.
+ * An fp16 z, gate or up that passed 65504 was saved as infinite: the backward takes act' at its limit there,
+ * and a zero factor beside it gives zero (NaN stays NaN).
  *
  * Layouts, ownership, streams and errors are those of rmsnorm.h: 16-bit
  * activations and weights [rows][ld] with a row stride of a multiple of 8
