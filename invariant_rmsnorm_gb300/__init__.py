@@ -43,8 +43,8 @@ __all__ = [
     "rmsnorm_rope_fwd", "rmsnorm_rope_bwd", "rmsnorm_rope_bwd_workspace_bytes",
     "layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_bytes", "layernorm_bwd_workspace_bytes_max",
     "rope_fwd", "rope_bwd", "rope_frequencies", "LAYERNORM_SYMBOLS", "ROPE_SYMBOLS", "SLOTS_SYMBOLS", "ROPE_SCALINGS",
-    "linear_fwd", "linear_bwd", "linear_bwd_workspace_bytes", "linear_gated_fwd", "linear_gated_bwd",
-    "linear_gated_bwd_workspace_bytes", "LINEAR_SYMBOLS", "LINEAR_ACTS",
+    "linear_fwd", "linear_bwd", "linear_bwd_workspace_bytes", "linear_bwd_workspace_bytes_max", "linear_gated_fwd",
+    "linear_gated_bwd", "linear_gated_bwd_workspace_bytes", "linear_gated_bwd_workspace_bytes_max", "LINEAR_SYMBOLS", "LINEAR_ACTS",
     "rope_axes_map", "rope_axes_fwd", "rope_axes_bwd", "rmsnorm_rope_axes_fwd", "rmsnorm_rope_axes_bwd",
 ]
 
@@ -68,8 +68,8 @@ LAYERNORM_SYMBOLS = ("layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_
                      "layernorm_bwd_workspace_bytes_max")
 ROPE_SYMBOLS = ("rope_frequencies", "rope_fwd", "rope_bwd", "rope_axes_map", "rope_axes_fwd", "rope_axes_bwd")
 # of include/linear.h
-LINEAR_SYMBOLS = ("linear_fwd", "linear_bwd", "linear_bwd_workspace_bytes", "linear_gated_fwd", "linear_gated_bwd",
-                  "linear_gated_bwd_workspace_bytes")
+LINEAR_SYMBOLS = ("linear_fwd", "linear_bwd", "linear_bwd_workspace_bytes", "linear_bwd_workspace_bytes_max", "linear_gated_fwd",
+                  "linear_gated_bwd", "linear_gated_bwd_workspace_bytes", "linear_gated_bwd_workspace_bytes_max")
 # of include/slots.h
 SLOTS_SYMBOLS = ("norm_call",)
 
@@ -157,10 +157,10 @@ _SIGS["rmsnorm_rope_axes_bwd"] = (_INT, _HEADS * 4 + [_P, _P, _P] + _AXES + [_P,
 # A matrix is its pointer and row stride.
 _MAT = [_P, _I64]
 _SIGS["linear_fwd"] = (_INT, _MAT * 2 + [_P] + _MAT * 3 + [_I64] * 3 + [_INT, _INT, _P])
-_SIGS["linear_bwd_workspace_bytes"] = (_SZ, [_I64] * 3 + [_INT])
+_SIGS["linear_bwd_workspace_bytes"] = _SIGS["linear_bwd_workspace_bytes_max"] = (_SZ, [_I64] * 3 + [_INT])
 _SIGS["linear_bwd"] = (_INT, _MAT * 6 + [_P, _P, _SZ] + [_I64] * 3 + [_INT, _INT, _P])
 _SIGS["linear_gated_fwd"] = (_INT, _MAT * 6 + [_I64] * 3 + [_INT, _INT, _P])
-_SIGS["linear_gated_bwd_workspace_bytes"] = (_SZ, [_I64] * 3)
+_SIGS["linear_gated_bwd_workspace_bytes"] = _SIGS["linear_gated_bwd_workspace_bytes_max"] = (_SZ, [_I64] * 3)
 _SIGS["linear_gated_bwd"] = (_INT, _MAT * 9 + [_P, _SZ] + [_I64] * 3 + [_INT, _INT, _P])
 
 # The entry points that are called with their arguments in an array (include/slots.h):
@@ -925,6 +925,11 @@ def linear_bwd_workspace_bytes(T: int, N: int, K: int, act: str = "none") -> int
     return int(load().linear_bwd_workspace_bytes(int(T), int(N), int(K), _linear_act(act)))
 
 
+def linear_bwd_workspace_bytes_max(T_max: int, N: int, K: int, act: str = "none") -> int:
+    """Bytes of one workspace that serves every T up to T_max (the per-T size is not monotone in T)."""
+    return int(load().linear_bwd_workspace_bytes_max(int(T_max), int(N), int(K), _linear_act(act)))
+
+
 def linear_bwd(g, x, w, z, dx, dw, db, ws, act: str = "none", stream=None):
     """Gradients of linear_fwd from that of ``y``: ``dx`` [T, K], ``dw`` [N, K] and ``db`` (fp32 [N]), each of which may be
     None. ``z`` is the forward's (None without an activation); the gradient of ``res`` is ``g``. ``ws`` is a workspace of
@@ -965,6 +970,11 @@ def linear_gated_fwd(x, wg, wu, h, gate=None, up=None, act: str = "silu", stream
 
 def linear_gated_bwd_workspace_bytes(T: int, N: int, K: int) -> int:
     return int(load().linear_gated_bwd_workspace_bytes(int(T), int(N), int(K)))
+
+
+def linear_gated_bwd_workspace_bytes_max(T_max: int, N: int, K: int) -> int:
+    """Bytes of one workspace that serves every T up to T_max (the per-T size is not monotone in T)."""
+    return int(load().linear_gated_bwd_workspace_bytes_max(int(T_max), int(N), int(K)))
 
 
 def linear_gated_bwd(g, x, wg, wu, gate, up, dx, dwg, dwu, ws, act: str = "silu", stream=None):

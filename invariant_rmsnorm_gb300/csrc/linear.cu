@@ -180,16 +180,23 @@ int check_in_place(const void* res, int64_t ldr, const void* y, int64_t ldy, int
 constexpr size_t kAlign = 256;
 size_t padded(size_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 
+// A weight gradient's cycles by the tiles' model, its rows in s ranges, for which the join costs a launch (5000) and the
+// partial sums' way to L2 and back (3000 bytes a cycle). It does not fall with `blocks`, of 64 rows.
+int64_t split_cycles(int64_t blocks, int64_t N, int64_t K, int64_t outputs, int64_t s) {
+    return linear_tiling(kGradW, N, K, (blocks + s - 1) / s, outputs * s, true).cycles + (s > 1 ? 5000 + 8 * s * outputs * N * K / 3000 : 0);
+}
+
+constexpr int kMostSplits = 64;
+constexpr int64_t kSplitRows = 512;  // of a range, at least
+
 // Ranges of rows that a weight gradient is split into, where its tiles leave SMs without one:
-// the power of two, of 512 rows at least a range, with the fewest cycles by the tiles' model, in which the join
-// costs a launch (5000) and the partial sums' way to L2 and back (3000 bytes a cycle). A function of the sizes alone.
+// the power of two with the fewest cycles. A function of the sizes alone.
 int weight_splits(int64_t T, int64_t N, int64_t K, int outputs) {
     const int64_t blocks = (T + 63) / 64;
     int best = 1;
-    int64_t least = linear_tiling(kGradW, N, K, blocks, outputs, true).cycles;
-    for (int s = 2; s <= 64 && T / s >= 512; s *= 2) {
-        const int64_t cycles = linear_tiling(kGradW, N, K, (blocks + s - 1) / s, static_cast<int64_t>(outputs) * s, true).cycles +
-                               5000 + 8 * s * outputs * N * K / 3000;
+    int64_t least = split_cycles(blocks, N, K, outputs, 1);
+    for (int s = 2; s <= kMostSplits && T / s >= kSplitRows; s *= 2) {
+        const int64_t cycles = split_cycles(blocks, N, K, outputs, s);
         if (cycles < least) {
             least = cycles;
             best = s;
@@ -198,9 +205,49 @@ int weight_splits(int64_t T, int64_t N, int64_t K, int outputs) {
     return best;
 }
 
-size_t split_bytes(int64_t T, int64_t N, int64_t K, int outputs) {
-    const int s = weight_splits(T, N, K, outputs);
-    return s > 1 ? padded(static_cast<size_t>(s) * outputs * N * K * 4u) : 0;
+// Whether s ranges cost less than any fewer at some count of blocks from lo to hi. Both sides do not fall with
+// the blocks, so an interval whose cheapest s is no cheaper than its dearest of the others holds none; the rest is halved. `nodes`
+// bounds the intervals looked at (near ties of long axes): past it the answer is yes, which costs bytes alone.
+bool splits_pay(int64_t lo, int64_t hi, int64_t N, int64_t K, int64_t outputs, int64_t s, int& nodes) {
+    const auto others = [&](int64_t blocks) {
+        int64_t least = split_cycles(blocks, N, K, outputs, 1);
+        for (int64_t f = 2; f < s; f *= 2) least = std::min(least, split_cycles(blocks, N, K, outputs, f));
+        return least;
+    };
+    if (--nodes < 0) return true;
+    const int64_t at_lo = split_cycles(lo, N, K, outputs, s), at_hi = split_cycles(hi, N, K, outputs, s), of_hi = others(hi);
+    if (at_lo >= of_hi) return false;
+    if (at_hi < of_hi || at_lo < others(lo)) return true;
+    if (hi - lo < 2) return false;
+    const int64_t mid = lo + (hi - lo) / 2;
+    return splits_pay(mid, hi, N, K, outputs, s, nodes) || splits_pay(lo, mid, N, K, outputs, s, nodes);
+}
+
+// The most ranges of any T up to T_max: nearly equal costs make them fall and rise with T. (Whole blocks: a T within one
+// has its ranges, or fewer.)
+int most_splits(int64_t T_max, int64_t N, int64_t K, int outputs) {
+    const int at_max = weight_splits(T_max, N, K, outputs);
+    for (int64_t s = kMostSplits; s > at_max; s /= 2) {
+        const int64_t lo = kSplitRows / 64 * s, hi = T_max / 64;
+        int nodes = 2048;
+        if (lo <= hi && splits_pay(lo, hi, N, K, outputs, s, nodes)) return static_cast<int>(s);
+    }
+    return at_max;
+}
+
+size_t split_bytes(int splits, int64_t N, int64_t K, int outputs) {
+    return splits > 1 ? padded(static_cast<size_t>(splits) * outputs * N * K * 4u) : 0;
+}
+
+// linear_bwd's: dz; the partial sums of db; those of dw.
+size_t bwd_bytes(int64_t T, int64_t N, int64_t K, int act, int splits) {
+    return (act == LINEAR_ACT_NONE ? 0 : padded(static_cast<size_t>(T) * N * 2u)) +
+           padded(static_cast<size_t>(slope_ranges(T, N)) * N * 4u) + split_bytes(splits, N, K, 1);
+}
+
+// linear_gated_bwd's: dgate and dup; the partial sums of dwg, then dwu.
+size_t gated_bwd_bytes(int64_t T, int64_t N, int64_t K, int splits) {
+    return 2 * padded(static_cast<size_t>(T) * N * 2u) + split_bytes(splits, N, K, 2);
 }
 
 cudaError_t grad(bool f16, ProductKind kind, const Product& p, cudaStream_t s) {
@@ -285,11 +332,14 @@ int linear_fwd(const rmsn_act16* x, int64_t ldx, const rmsn_act16* w, int64_t ld
     return cuda_status(flags ? launch_linear_fwd_f16(kForward, p, stream) : launch_linear_fwd(kForward, p, stream));
 }
 
-// The workspace: dz; the partial sums of db; those of dw.
 size_t linear_bwd_workspace_bytes(int64_t T, int64_t N, int64_t K, int act) {
     if (check_sizes(T, N, K, act) != RMSN_OK || T == 0) return 0;
-    return (act == LINEAR_ACT_NONE ? 0 : padded(static_cast<size_t>(T) * N * 2u)) +
-           padded(static_cast<size_t>(slope_ranges(T, N)) * N * 4u) + split_bytes(T, N, K, 1);
+    return bwd_bytes(T, N, K, act, weight_splits(T, N, K, 1));
+}
+
+size_t linear_bwd_workspace_bytes_max(int64_t T_max, int64_t N, int64_t K, int act) {
+    if (check_sizes(T_max, N, K, act) != RMSN_OK || T_max == 0) return 0;
+    return bwd_bytes(T_max, N, K, act, most_splits(T_max, N, K, 1));
 }
 
 int linear_bwd(const rmsn_act16* g, int64_t ldg, const rmsn_act16* x, int64_t ldx, const rmsn_act16* w, int64_t ldw,
@@ -363,10 +413,14 @@ int linear_gated_fwd(const rmsn_act16* x, int64_t ldx, const rmsn_act16* wg, int
     return cuda_status(flags ? launch_linear_fwd_f16(kGatedFwd, p, stream) : launch_linear_fwd(kGatedFwd, p, stream));
 }
 
-// The workspace: dgate and dup; the partial sums of dwg, then dwu.
 size_t linear_gated_bwd_workspace_bytes(int64_t T, int64_t N, int64_t K) {
     if (check_sizes(T, N, K, LINEAR_ACT_NONE) != RMSN_OK || T == 0) return 0;
-    return 2 * padded(static_cast<size_t>(T) * N * 2u) + split_bytes(T, N, K, 2);
+    return gated_bwd_bytes(T, N, K, weight_splits(T, N, K, 2));
+}
+
+size_t linear_gated_bwd_workspace_bytes_max(int64_t T_max, int64_t N, int64_t K) {
+    if (check_sizes(T_max, N, K, LINEAR_ACT_NONE) != RMSN_OK || T_max == 0) return 0;
+    return gated_bwd_bytes(T_max, N, K, most_splits(T_max, N, K, 2));
 }
 
 int linear_gated_bwd(const rmsn_act16* g, int64_t ldg, const rmsn_act16* x, int64_t ldx, const rmsn_act16* wg, int64_t ldwg,
