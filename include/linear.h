@@ -65,7 +65,7 @@ int linear_fwd(const rmsn_act16* x, int64_t ldx, const rmsn_act16* w, int64_t ld
                const rmsn_act16* res, int64_t ldr, rmsn_act16* y, int64_t ldy, rmsn_act16* z, int64_t ldz,
                int64_t T, int64_t N, int64_t K, int act, int dtype, rmsn_stream stream);
 
-/* Bytes of workspace linear_bwd needs (0 for T == 0 and unsupported sizes). They are not monotone in T:
+/* Bytes of workspace linear_bwd needs for all of its outputs (0 for T == 0 and unsupported sizes). They are not monotone in T:
  * rows are split for the weights' gradient where that pays, and a larger T can need far fewer bytes than a
  * smaller one (N = K = 4096, no activation: 136 MB at T = 23680, 2 MB at 23681). To size one buffer for every T up to
  * a maximum, use linear_bwd_workspace_bytes_max. */
@@ -76,7 +76,9 @@ size_t linear_bwd_workspace_bytes_max(int64_t T_max, int64_t N, int64_t K, int a
 
 /* g [T][ldg] is the gradient of y. z is read where there is an activation (else it may
  * be NULL). dx [T][lddx], dw [N][lddw] and db [N] may each be NULL: not wanted. x is read
- * for dw, w for dx alone, and may be NULL without them. ws: contents never read back after the call. */
+ * for dw, w for dx alone, and may be NULL without them. ws: contents never read back after the call. Of its bytes
+ * a call asks for what its outputs take: 2 T N (to a multiple of 256) for dx or dw with an activation, db's partial rows for db, the split sums
+ * for dw. Without any of these (dx alone and no activation, say) ws may be NULL. */
 int linear_bwd(const rmsn_act16* g, int64_t ldg, const rmsn_act16* x, int64_t ldx, const rmsn_act16* w, int64_t ldw,
                const rmsn_act16* z, int64_t ldz, rmsn_act16* dx, int64_t lddx, rmsn_act16* dw, int64_t lddw, float* db,
                void* ws, size_t ws_bytes, int64_t T, int64_t N, int64_t K, int act, int dtype, rmsn_stream stream);
@@ -86,13 +88,14 @@ int linear_gated_fwd(const rmsn_act16* x, int64_t ldx, const rmsn_act16* wg, int
                      rmsn_act16* h, int64_t ldh, rmsn_act16* gate, int64_t ldgate, rmsn_act16* up, int64_t ldup,
                      int64_t T, int64_t N, int64_t K, int act, int dtype, rmsn_stream stream);
 
-/* Bytes of workspace linear_gated_bwd needs (0 for T == 0 and unsupported sizes); not monotone in T either. */
+/* Bytes of workspace linear_gated_bwd needs for all of its outputs (0 for T == 0 and unsupported sizes); not monotone in T either. */
 size_t linear_gated_bwd_workspace_bytes(int64_t T, int64_t N, int64_t K);
 
 /* One size that serves every T up to T_max (0 for T_max <= 0 and unsupported sizes). */
 size_t linear_gated_bwd_workspace_bytes_max(int64_t T_max, int64_t N, int64_t K);
 
-/* g [T][ldg] is the gradient of h. dx may be NULL, and dwg and dwu together. */
+/* g [T][ldg] is the gradient of h. dx may be NULL, and dwg and dwu together; without these two the call asks for no
+ * split sums (4 T N bytes, each half of them to a multiple of 256, are enough). */
 int linear_gated_bwd(const rmsn_act16* g, int64_t ldg, const rmsn_act16* x, int64_t ldx,
                      const rmsn_act16* wg, int64_t ldwg, const rmsn_act16* wu, int64_t ldwu,
                      const rmsn_act16* gate, int64_t ldgate, const rmsn_act16* up, int64_t ldup,

@@ -905,6 +905,11 @@ def _x_w(x, w, xn: str = "x", wn: str = "w"):
     return x.shape[0], x.shape[1], w.shape[0]
 
 
+def _scratch(ws, index: int):
+    """A workspace that may be None where the call takes nothing of it."""
+    return (0, 0) if ws is None else _bytes_of(ws, index)
+
+
 def linear_fwd(x, w, b, res, y, z=None, act: str = "none", stream=None):
     """``y = act(x @ w.T + b) + res`` of ``x`` [T, K] and ``w`` [N, K], one rounding. ``b`` (fp32 [N]) and ``res`` [T, N]
     may be None; ``y`` may be ``res``. ``z`` [T, N], unless None, keeps the pre-activation for the backward."""
@@ -933,7 +938,8 @@ def linear_bwd_workspace_bytes_max(T_max: int, N: int, K: int, act: str = "none"
 def linear_bwd(g, x, w, z, dx, dw, db, ws, act: str = "none", stream=None):
     """Gradients of linear_fwd from that of ``y``: ``dx`` [T, K], ``dw`` [N, K] and ``db`` (fp32 [N]), each of which may be
     None. ``z`` is the forward's (None without an activation); the gradient of ``res`` is ``g``. ``ws`` is a workspace of
-    ``linear_bwd_workspace_bytes(T, N, K, act)`` bytes."""
+    ``linear_bwd_workspace_bytes(T, N, K, act)`` bytes, or of what the wanted outputs take of them (None for ``dx`` alone
+    without an activation)."""
     i, code = _index_and_code(x, "x")
     dt = x.dtype
     T, K, N = _x_w(x, w)
@@ -946,7 +952,7 @@ def linear_bwd(g, x, w, z, dx, dw, db, ws, act: str = "none", stream=None):
     zp, ldz = _rows(z, "z", (T, N), dt, i) if a else (0, N)
     dxp, lddx = (0, K) if dx is None else _rows(dx, "dx", (T, K), dt, i)
     dwp, lddw = (0, K) if dw is None else _rows(dw, "dw", (N, K), dt, i)
-    sp, sb = _bytes_of(ws, i)
+    sp, sb = _scratch(ws, i)
     _call("linear_bwd", i, stream, gp, ldg, xp, ldx, wp, ldw, zp, ldz, dxp, lddx, dwp, lddw,
           0 if db is None else _vec(db, "db", (N,), i), sp, sb, T, N, K, a, code)
 
@@ -979,7 +985,8 @@ def linear_gated_bwd_workspace_bytes_max(T_max: int, N: int, K: int) -> int:
 
 def linear_gated_bwd(g, x, wg, wu, gate, up, dx, dwg, dwu, ws, act: str = "silu", stream=None):
     """Gradients of linear_gated_fwd from that of ``h``: ``dx`` [T, K] (or None), ``dwg`` and ``dwu`` [N, K] (or both None).
-    ``gate`` and ``up`` are the forward's. ``ws`` is a workspace of ``linear_gated_bwd_workspace_bytes(T, N, K)`` bytes."""
+    ``gate`` and ``up`` are the forward's. ``ws`` is a workspace of ``linear_gated_bwd_workspace_bytes(T, N, K)`` bytes
+    (``dx`` alone takes the first 4 T N, to a multiple of 512)."""
     i, code = _index_and_code(x, "x")
     dt = x.dtype
     T, K, N = _x_w(x, wg, wn="wg")
@@ -989,7 +996,7 @@ def linear_gated_bwd(g, x, wg, wu, gate, up, dx, dwg, dwu, ws, act: str = "silu"
     dxp, lddx = (0, K) if dx is None else _rows(dx, "dx", (T, K), dt, i)
     dgp, lddg = (0, K) if dwg is None else _rows(dwg, "dwg", nk, dt, i)
     dup, lddu = (0, K) if dwu is None else _rows(dwu, "dwu", nk, dt, i)
-    sp, sb = _bytes_of(ws, i)
+    sp, sb = _scratch(ws, i)
     _call("linear_gated_bwd", i, stream, *_rows(g, "g", tn, dt, i), *_rows(x, "x", (T, K), dt, i), *_rows(wg, "wg", nk, dt, i),
           *_rows(wu, "wu", nk, dt, i), *_rows(gate, "gate", tn, dt, i), *_rows(up, "up", tn, dt, i), dxp, lddx, dgp, lddg, dup,
           lddu, sp, sb, T, N, K, _linear_act(act), code)

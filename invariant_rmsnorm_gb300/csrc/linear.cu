@@ -174,6 +174,13 @@ int check_in_place(const void* res, int64_t ldr, const void* y, int64_t ldy, int
     return res == y && T > 1 && ldr != ldy ? RMSN_EINVAL : RMSN_OK;
 }
 
+// A workspace of which a call takes `need` bytes (none: it may be anything).
+int check_ws(const void* ws, size_t ws_bytes, size_t need) {
+    if (need == 0) return RMSN_OK;
+    if (ws == nullptr || ws_bytes < need) return RMSN_EWORKSPACE;
+    return aligned16(ws) ? RMSN_OK : RMSN_EALIGN;
+}
+
 // ---------------------------------------------------------------------------
 // Workspaces
 // ---------------------------------------------------------------------------
@@ -239,13 +246,13 @@ size_t split_bytes(int splits, int64_t N, int64_t K, int outputs) {
     return splits > 1 ? padded(static_cast<size_t>(splits) * outputs * N * K * 4u) : 0;
 }
 
-// linear_bwd's: dz; the partial sums of db; those of dw.
+// linear_bwd's with every output: dz; the partial sums of db; those of dw.
 size_t bwd_bytes(int64_t T, int64_t N, int64_t K, int act, int splits) {
     return (act == LINEAR_ACT_NONE ? 0 : padded(static_cast<size_t>(T) * N * 2u)) +
            padded(static_cast<size_t>(slope_ranges(T, N)) * N * 4u) + split_bytes(splits, N, K, 1);
 }
 
-// linear_gated_bwd's: dgate and dup; the partial sums of dwg, then dwu.
+// linear_gated_bwd's with every output: dgate and dup; the partial sums of dwg, then dwu.
 size_t gated_bwd_bytes(int64_t T, int64_t N, int64_t K, int splits) {
     return 2 * padded(static_cast<size_t>(T) * N * 2u) + split_bytes(splits, N, K, 2);
 }
@@ -362,21 +369,22 @@ int linear_bwd(const rmsn_act16* g, int64_t ldg, const rmsn_act16* x, int64_t ld
     }
     if (dw != nullptr) RMSN_TRY(check_mat(x, ldx, K));
     if (act != LINEAR_ACT_NONE) RMSN_TRY(check_mat(z, ldz, N));
-    const size_t need = linear_bwd_workspace_bytes(T, N, K, act);
-    if (ws == nullptr || ws_bytes < need) return RMSN_EWORKSPACE;
-    if (!aligned16(ws)) return RMSN_EALIGN;
+    // Of the workspace, what the wanted outputs take.
+    Slopes a{};
+    a.g = {g, ldg}; a.z = {z, ldz}; a.T = T; a.N = N; a.ranges = slope_ranges(T, N); a.act = act;
+    const size_t of_dz = act != LINEAR_ACT_NONE && (dx != nullptr || dw != nullptr) ? padded(static_cast<size_t>(T) * N * 2u) : 0;
+    const size_t of_db = db != nullptr ? padded(static_cast<size_t>(a.ranges) * N * 4u) : 0;
+    const size_t need = of_dz + of_db + (dw != nullptr ? split_bytes(weight_splits(T, N, K, 1), N, K, 1) : 0);
+    RMSN_TRY(check_ws(ws, ws_bytes, need));
     const bool f16 = flags != 0;
     unsigned char* at = static_cast<unsigned char*>(ws);
     MatIn dz{g, ldg};
-    Slopes a{};
-    a.g = {g, ldg}; a.z = {z, ldz}; a.T = T; a.N = N; a.ranges = slope_ranges(T, N); a.act = act;
-    if (act != LINEAR_ACT_NONE) {
-        if (dx != nullptr || dw != nullptr) a.out[0] = {reinterpret_cast<uint16_t*>(at), N};
+    if (of_dz > 0) {
+        a.out[0] = {reinterpret_cast<uint16_t*>(at), N};
         dz = {reinterpret_cast<uint16_t*>(at), N};
-        at += padded(static_cast<size_t>(T) * N * 2u);
     }
-    if (db != nullptr) a.partials = reinterpret_cast<float*>(at);
-    at += padded(static_cast<size_t>(a.ranges) * N * 4u);
+    if (db != nullptr) a.partials = reinterpret_cast<float*>(at + of_dz);
+    at += of_dz + of_db;
     if (a.out[0].p != nullptr || a.partials != nullptr) RMSN_TRY(cuda_status(launch_linear_slopes(a, f16, stream)));
     if (db != nullptr)
         RMSN_TRY(cuda_status(launch_reduce_columns({a.partials, a.ranges, db}, {nullptr, 0, nullptr}, static_cast<int>(N), stream)));
@@ -450,9 +458,8 @@ int linear_gated_bwd(const rmsn_act16* g, int64_t ldg, const rmsn_act16* x, int6
     }
     if (weights) RMSN_TRY(check_mat(x, ldx, K));
     if (dx == nullptr && !weights) return RMSN_OK;
-    const size_t need = linear_gated_bwd_workspace_bytes(T, N, K), each = padded(static_cast<size_t>(T) * N * 2u);
-    if (ws == nullptr || ws_bytes < need) return RMSN_EWORKSPACE;
-    if (!aligned16(ws)) return RMSN_EALIGN;
+    const size_t each = padded(static_cast<size_t>(T) * N * 2u);
+    RMSN_TRY(check_ws(ws, ws_bytes, 2 * each + (weights ? split_bytes(weight_splits(T, N, K, 2), N, K, 2) : 0)));
     const bool f16 = flags != 0;
     unsigned char* at = static_cast<unsigned char*>(ws);
     uint16_t *dgate = reinterpret_cast<uint16_t*>(at), *dup = reinterpret_cast<uint16_t*>(at + each);

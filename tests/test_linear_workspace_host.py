@@ -68,3 +68,40 @@ def test_the_longest_axes_and_refusals():
         assert rn.linear_bwd_workspace_bytes_max(T, N, K) == rn.linear_gated_bwd_workspace_bytes_max(T, N, K) == 0
     with pytest.raises(ValueError):
         rn.linear_bwd_workspace_bytes_max(8, 8, 8, "swish")
+
+
+# --------------------------------------------------------------------------
+# what a call asks for (a workspace at an odd address: its size is looked at first, and nothing is launched)
+# --------------------------------------------------------------------------
+A = 1 << 20
+EALIGN, EWORKSPACE = -2, -5
+
+
+def _pad(n):
+    return -(-n // 256) * 256
+
+
+@pytest.mark.parametrize("T,N,K", [(4, 40, 64), (9000, 136, 264), (23680, 4096, 4096)])
+@pytest.mark.parametrize("act", [0, 3])
+@pytest.mark.parametrize("dx,dw,db", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0), (1, 0, 1), (1, 1, 1)])
+def test_linear_bwd_asks_for_what_its_outputs_take(lib, T, N, K, act, dx, dw, db):
+    rows = _pad(4 * N * max(1, min(-(-1824 // -(-N // 256)), -(-T // 32))))
+    dz = _pad(2 * T * N) if act else 0
+    sums = rn.linear_bwd_workspace_bytes(T, N, K, "gelu" if act else "none") - dz - rows
+    need = (dz if dx or dw else 0) + (rows if db else 0) + (sums if dw else 0)
+
+    def call(ws, size):
+        return lib.linear_bwd(A, N, A, K, A, K, A, N, A if dx else 0, K, A if dw else 0, K, A if db else 0, ws, size, T, N, K, act, 0,
+                              None)
+
+    if need:
+        assert call(A + 8, need) == EALIGN and call(A + 8, need - 1) == call(0, need) == EWORKSPACE
+
+
+def test_linear_gated_bwd_asks_for_no_sums_without_weights(lib):
+    T, N, K = 18432, 1032, 520
+    for dw, need in ((0, 2 * _pad(2 * T * N)), (A, rn.linear_gated_bwd_workspace_bytes(T, N, K))):
+        def call(ws, size):
+            return lib.linear_gated_bwd(A, N, A, K, A, K, A, K, A, N, A, N, A, K, dw, K, dw, K, ws, size, T, N, K, 1, 0, None)
+
+        assert call(A + 8, need) == EALIGN and call(A + 8, need - 1) == call(0, need) == EWORKSPACE
