@@ -36,8 +36,9 @@
  * independent of T, of the row's position and of the other rows: every value is
  * one chain of sums over the reduced axis in ascending order, at every tile size.
  * The weights' gradients are summed with no atomics, over ranges of rows that
- * depend on T, N and K alone: the same bits from run to run. (Every kernel's tiles are
- * chosen by the sizes alone, whatever the GPU's SM count.)
+ * depend on T, N and K alone: the same bits from run to run. (Tiles are chosen by the sizes, as of a GPU of 152
+ * SMs, and by whether every operand's rows start on lines of 128 bytes; no bits depend on them, so a view between
+ * other columns has those of a matrix of its own.)
  *
  * Calls that may run at the same time (on two streams, in two graphs) need
  * workspaces of their own.
