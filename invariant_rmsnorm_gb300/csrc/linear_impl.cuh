@@ -29,6 +29,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "activation.cuh"
@@ -86,10 +87,13 @@ struct ProductArgs {
     uint32_t staging;         // offset of the epilogue's staging from the ring's start
 };
 
-// Device error word of the including translation unit.
+// Device error word of the including translation unit, and whether any of its kernels was launched (or captured): a
+// word that nothing can have set is not read, nor its kernels' module loaded for it.
 __device__ unsigned int g_linear_error;
+std::atomic<bool> g_linear_launched{false};
 
 cudaError_t read_linear_error_word(unsigned* flags, bool clear) {
+    if (!g_linear_launched.load()) return cudaSuccess;
     unsigned v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_linear_error, sizeof(v));
     if (e != cudaSuccess) return e;
@@ -669,6 +673,7 @@ cudaError_t product_run(const Product& p, const Tiling& tile, cudaStream_t st) {
     } else {
         grid = std::min<int64_t>(tiles, sm_count());
     }
+    g_linear_launched.store(true);
     return launch_kernel_clustered(kern, static_cast<unsigned>(CTAS), static_cast<unsigned>(grid), kProductThreads, smem, st, g);
 }
 

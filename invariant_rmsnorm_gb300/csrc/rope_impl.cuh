@@ -35,6 +35,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "f32x2.cuh"
@@ -56,10 +57,13 @@ __device__ __forceinline__ long long axis_position(const RopeArgs& a, int axis, 
     return a.pos64 ? __ldg(static_cast<const long long*>(a.pos) + i) : __ldg(static_cast<const int*>(a.pos) + i);
 }
 
-// Device error word of the including translation unit.
+// Device error word of the including translation unit, and whether any of its kernels was launched (or captured): a
+// word that nothing can have set is not read, nor its kernels' module loaded for it.
 __device__ unsigned int g_rope_error;
+std::atomic<bool> g_rope_launched{false};
 
 cudaError_t read_rope_error_word(unsigned* flags, bool clear) {
+    if (!g_rope_launched.load()) return cudaSuccess;
     unsigned v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_rope_error, sizeof(v));
     if (e != cudaSuccess) return e;
@@ -776,6 +780,7 @@ cudaError_t rope_run_as(const RopeArgs& a, int* ctas_q, cudaStream_t st) {
         b.ctas_q = static_cast<int>(grid);
     }
     *ctas_q = b.ctas_q;
+    g_rope_launched.store(true);
     return launch_kernel(kern, static_cast<unsigned>(grid), threads, smem, st, b);
 }
 
