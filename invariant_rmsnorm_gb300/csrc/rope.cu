@@ -121,8 +121,8 @@ int check_in_out(const RopeArgs& a, int64_t T, int64_t D) {
 }
 
 int turn_impl(bool back, const HeadsIn& q, const HeadsIn& k, const double* inv_freq, const Axes* axes,
-              const void* positions, int pos_dtype, const HeadsOut& qo, const HeadsOut& ko, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
-              int64_t R, float scale, int layout, int dtype, cudaStream_t stream) {
+              const void* positions, int pos_dtype, const HeadsOut& qo, const HeadsOut& ko, int64_t T, int64_t Hq,
+              int64_t Hk, int64_t D, int64_t R, float scale, int layout, int dtype, cudaStream_t stream) {
     int flags = 0;
     RMSN_TRY(dtype_flags(dtype, &flags));
     RMSN_TRY(check_sizes(T, Hq, Hk, D));
@@ -289,9 +289,10 @@ int rope_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head, const rmsn
 }
 
 int rope_axes_fwd(const rmsn_act16* q, int64_t q_token, int64_t q_head, const rmsn_act16* k, int64_t k_token,
-             int64_t k_head, const double* inv_freq, const uint8_t* axis, int64_t axes, const void* positions, int64_t pos_axis, int64_t pos_token, int pos_dtype, rmsn_act16* q_out,
-             int64_t qo_token, int64_t qo_head, rmsn_act16* k_out, int64_t ko_token, int64_t ko_head, int64_t T,
-             int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale, int layout, int dtype, rmsn_stream stream) {
+                  int64_t k_head, const double* inv_freq, const uint8_t* axis, int64_t axes, const void* positions,
+                  int64_t pos_axis, int64_t pos_token, int pos_dtype, rmsn_act16* q_out, int64_t qo_token, int64_t qo_head,
+                  rmsn_act16* k_out, int64_t ko_token, int64_t ko_head, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                  int64_t R, float scale, int layout, int dtype, rmsn_stream stream) {
     const Axes x{axis, axes, pos_axis, pos_token};
     return turn_impl(false, {q, q_token, q_head}, {k, k_token, k_head}, inv_freq, &x, positions, pos_dtype,
                      {q_out, qo_token, qo_head}, {k_out, ko_token, ko_head}, T, Hq, Hk, D, R, scale, layout, dtype,
@@ -299,9 +300,10 @@ int rope_axes_fwd(const rmsn_act16* q, int64_t q_token, int64_t q_head, const rm
 }
 
 int rope_axes_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head, const rmsn_act16* gk, int64_t gk_token,
-             int64_t gk_head, const double* inv_freq, const uint8_t* axis, int64_t axes, const void* positions, int64_t pos_axis, int64_t pos_token, int pos_dtype, rmsn_act16* dq,
-             int64_t dq_token, int64_t dq_head, rmsn_act16* dk, int64_t dk_token, int64_t dk_head, int64_t T,
-             int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale, int layout, int dtype, rmsn_stream stream) {
+                  int64_t gk_head, const double* inv_freq, const uint8_t* axis, int64_t axes, const void* positions,
+                  int64_t pos_axis, int64_t pos_token, int pos_dtype, rmsn_act16* dq, int64_t dq_token, int64_t dq_head,
+                  rmsn_act16* dk, int64_t dk_token, int64_t dk_head, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                  int64_t R, float scale, int layout, int dtype, rmsn_stream stream) {
     const Axes x{axis, axes, pos_axis, pos_token};
     return turn_impl(true, {gq, gq_token, gq_head}, {gk, gk_token, gk_head}, inv_freq, &x, positions, pos_dtype,
                      {dq, dq_token, dq_head}, {dk, dk_token, dk_head}, T, Hq, Hk, D, R, scale, layout, dtype, stream);
@@ -319,11 +321,12 @@ int rmsnorm_rope_fwd(const rmsn_act16* q, int64_t q_token, int64_t q_head, const
 }
 
 int rmsnorm_rope_axes_fwd(const rmsn_act16* q, int64_t q_token, int64_t q_head, const rmsn_act16* k, int64_t k_token,
-                     int64_t k_head, const float* wq, const float* wk, const double* inv_freq, const uint8_t* axis, int64_t axes, const void* positions, int64_t pos_axis, int64_t pos_token,
-                     int pos_dtype, rmsn_act16* q_out, int64_t qo_token, int64_t qo_head, rmsn_act16* k_out,
-                     int64_t ko_token, int64_t ko_head, float* rstd_q, float* rstd_k, int64_t T, int64_t Hq,
-                     int64_t Hk, int64_t D, int64_t R, float scale, int layout, float eps, int zero_centered_gamma,
-                     int dtype, rmsn_stream stream) {
+                          int64_t k_head, const float* wq, const float* wk, const double* inv_freq, const uint8_t* axis,
+                          int64_t axes, const void* positions, int64_t pos_axis, int64_t pos_token, int pos_dtype,
+                          rmsn_act16* q_out, int64_t qo_token, int64_t qo_head, rmsn_act16* k_out, int64_t ko_token,
+                          int64_t ko_head, float* rstd_q, float* rstd_k, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                          int64_t R, float scale, int layout, float eps, int zero_centered_gamma, int dtype,
+                          rmsn_stream stream) {
     const Axes x{axis, axes, pos_axis, pos_token};
     return norm_fwd_impl({q, q_token, q_head}, {k, k_token, k_head}, wq, wk, inv_freq, &x, positions, pos_dtype,
                          {q_out, qo_token, qo_head}, {k_out, ko_token, ko_head}, rstd_q, rstd_k, T, Hq, Hk, D, R, scale, layout,
@@ -343,12 +346,13 @@ int rmsnorm_rope_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head, co
 }
 
 int rmsnorm_rope_axes_bwd(const rmsn_act16* gq, int64_t gq_token, int64_t gq_head, const rmsn_act16* gk, int64_t gk_token,
-                     int64_t gk_head, const rmsn_act16* q, int64_t q_token, int64_t q_head, const rmsn_act16* k,
-                     int64_t k_token, int64_t k_head, const float* wq, const float* wk, const double* inv_freq,
-                     const uint8_t* axis, int64_t axes, const void* positions, int64_t pos_axis, int64_t pos_token, int pos_dtype, const float* rstd_q, const float* rstd_k, rmsn_act16* dq,
-                     int64_t dq_token, int64_t dq_head, rmsn_act16* dk, int64_t dk_token, int64_t dk_head, float* dwq,
-                     float* dwk, void* ws, size_t ws_bytes, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R,
-                     float scale, int layout, int zero_centered_gamma, int dtype, rmsn_stream stream) {
+                          int64_t gk_head, const rmsn_act16* q, int64_t q_token, int64_t q_head, const rmsn_act16* k,
+                          int64_t k_token, int64_t k_head, const float* wq, const float* wk, const double* inv_freq,
+                          const uint8_t* axis, int64_t axes, const void* positions, int64_t pos_axis, int64_t pos_token,
+                          int pos_dtype, const float* rstd_q, const float* rstd_k, rmsn_act16* dq, int64_t dq_token,
+                          int64_t dq_head, rmsn_act16* dk, int64_t dk_token, int64_t dk_head, float* dwq, float* dwk,
+                          void* ws, size_t ws_bytes, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale,
+                          int layout, int zero_centered_gamma, int dtype, rmsn_stream stream) {
     const Axes x{axis, axes, pos_axis, pos_token};
     return norm_bwd_impl({gq, gq_token, gq_head}, {gk, gk_token, gk_head}, {q, q_token, q_head}, {k, k_token, k_head}, wq, wk,
                          inv_freq, &x, positions, pos_dtype, rstd_q, rstd_k, {dq, dq_token, dq_head}, {dk, dk_token, dk_head},
