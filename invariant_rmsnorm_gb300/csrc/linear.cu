@@ -17,7 +17,8 @@ constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements: a tensor map's st
 
 // ---------------------------------------------------------------------------
 // Gradients of the activations: dz = g act'(z), and with a second projection
-// dgate = g up act'(gate), dup = g act(gate), in fp32, rounded once.
+// dgate = g up act'(gate), dup = g act(gate), in fp32, rounded once: to 16 bits, as the tensor cores' operands. (The products'
+// error is 1.4 times that of one rounding so; a high and a low part of each would keep them whole for twice the products.)
 //
 // Bound by HBM where the activation is cheap: 6 bytes a value (10 with `up`, 2 for the sums alone). A thread takes 8
 // adjacent columns of every 8th row of its CTA's range, a CTA 256 columns; the columns' sums (of dz before it
