@@ -57,3 +57,40 @@ def test_dq_and_dk(D, R, interleaved, T, Hq, Hk, A, cycled, dtype, layout, zc):
     rn.rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, f, norm[2], norm[3], *one[:2], *one[4:], ws, p, SCALE, interleaved, zc)
     for i in (0, 1) if Hk else (0,):
         assert torch.equal(_bits(several[i]), _bits(one[i])) and torch.equal(several[4 + i], one[4 + i])
+
+
+@pytest.mark.parametrize("D,R", [(64, 64), (80, 72), (128, 78), (256, 64)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,Hq,Hk", [(50, 8, 2), (6001, 2, 1)])
+def test_in_place_and_beside_other_columns(D, R, interleaved, T, Hq, Hk):
+    """Gradients written over those of the outputs, and every output as part of one projection's buffer whose
+    other columns stay as they were: the bits of outputs of their own."""
+    q, k = _heads(T, Hq, Hk, D, 41)
+    gq, gk = _heads(T, Hq, Hk, D, 42)
+    w = synth.gamma_f32(D, 43, DEV)
+    f, axis, pos = rn.rope_frequencies(R).to(DEV), rn.rope_axes_map(_sections(R // 2, 3)).to(DEV), _pos(3, T, 44)
+    ws = torch.full((max(rn.rmsnorm_rope_bwd_workspace_bytes(T, Hq, Hk, D) // 4, 4),), float("nan"), device=DEV)
+    rq, rk, dw = torch.empty((T, Hq), device=DEV), torch.empty((T, Hk), device=DEV), [torch.empty(D, device=DEV) for _ in range(2)]
+    calls = (lambda a, b: rn.rope_axes_fwd(q, k, f, axis, a, b, pos, SCALE, interleaved),
+             lambda a, b: rn.rope_axes_bwd(gq, gk, f, axis, a, b, pos, SCALE, interleaved),
+             lambda a, b: rn.rmsnorm_rope_axes_fwd(q, k, w, w, f, axis, a, b, rq, rk, pos, SCALE, interleaved, EPS),
+             lambda a, b: rn.rmsnorm_rope_axes_bwd(gq, gk, q, k, w, w, f, axis, rq, rk, a, b, *dw, ws, pos, SCALE, interleaved))
+    for call in calls:
+        own = _buffers(q, k)[:2]
+        call(*own)
+        base = torch.full((T, (Hq + 2 * Hk) * D + 16), 3.0, dtype=BF16, device=DEV)
+        a, b = base[:, 8:8 + Hq * D].view(T, Hq, D), base[:, 8 + (Hq + Hk) * D:8 + (Hq + 2 * Hk) * D].view(T, Hk, D)
+        call(a, b)
+        assert torch.equal(_bits(a), _bits(own[0])) and torch.equal(_bits(b), _bits(own[1]))
+        rest = torch.cat((base[:, :8], base[:, 8 + Hq * D:8 + (Hq + Hk) * D], base[:, -8:]), 1)
+        assert bool((rest == 3.0).all())
+    want, turned = _buffers(q, k)[:2], _buffers(q, k)[:2]
+    calls[3](*want)
+    sums = [t.clone() for t in dw]
+    calls[1](*turned)
+    pq, pk = gq.clone(), gk.clone()
+    rn.rope_axes_bwd(pq, pk, f, axis, pq, pk, pos, SCALE, interleaved)
+    assert torch.equal(_bits(pq), _bits(turned[0])) and torch.equal(_bits(pk), _bits(turned[1]))
+    calls[3](gq, gk)  # over the gradients themselves
+    assert torch.equal(_bits(gq), _bits(want[0])) and torch.equal(_bits(gk), _bits(want[1]))
+    assert torch.equal(dw[0], sums[0]) and torch.equal(dw[1], sums[1])

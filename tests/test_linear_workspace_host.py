@@ -1,5 +1,5 @@
 """Host checks (no GPU) of the projections' workspaces: one size for every T up to a
-maximum, although the size of a T may fall as T grows."""
+maximum, although the size of a T may fall as T grows, and what a call asks for."""
 from __future__ import annotations
 
 import random
